@@ -73,7 +73,11 @@ typedef enum pa_status {
   PA_ERR_DEVICE_TIMEOUT = 6,      /* device status: a bounded wait gave up    */
   PA_ERR_BAD_BLOCK_ID = 7,        /* device status: block id outside the pool */
   PA_ERR_BAD_SEQ_LEN = 8,         /* device status: seq_len outside 0..max    */
-  PA_ERR_WORKSPACE_NOT_INIT = 9   /* device status: pa_workspace_init missing */
+  PA_ERR_WORKSPACE_NOT_INIT = 9,  /* device status: pa_workspace_init missing */
+  PA_ERR_NO_ROOM = 10,            /* device status: pa_plan_step refused requests:
+                                     free blocks or rows ran out              */
+  PA_ERR_BAD_SLOT = 11,           /* device status: slot outside the pool     */
+  PA_ERR_BAD_POSITION = 12        /* device status: position outside the table */
 } pa_status_t;
 
 typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_F16 = 2 } pa_dtype_t;
@@ -397,6 +401,192 @@ PA_API pa_status_t pa_prefill(const pa_prefill_params_t* params, const void* q, 
                               const void* v, const void* k_cache, const void* v_cache,
                               const int32_t* block_tables, const int32_t* query_start,
                               const int32_t* ctx_lens, void* out, cudaStream_t stream);
+
+/*
+ * The step plan: block tables, slots, positions and row starts of one serving
+ * step, built on the GPU from the requests' lengths.  Request b has
+ * C_b = ctx_lens[b] tokens in the cache (its first ceil(C_b / block_size)
+ * table entries hold their blocks) and appends n_b = new_lens[b] tokens (1 for
+ * a decode, a chunk for a prefill, 0 to sit the step out).
+ *   - The blocks the new tokens need beyond those the request has are taken
+ *     from the END of the free list, request by request: the i-th new block
+ *     of the step is free_blocks[*free_count - 1 - i].  They are written into
+ *     the request's row of block_tables; no other entry is touched.
+ *   - query_start [num_seqs + 1] is the running sum of n_b, seq_lens[b] =
+ *     C_b + n_b; row r = query_start[b] + i is new token i of request b, with
+ *     positions[r] = *base_len + C_b + i (base_len may be null: 0; tokens of
+ *     a shared prefix that the tables do not hold) and
+ *     slots[r] = block * block_size + (C_b + i) % block_size, the place of its
+ *     key and value in the cache pool.
+ *   - Rows from the step's total up to max_tokens (a padded batch) get slot
+ *     -1 and position 0.  *free_left = *free_count less the blocks taken: the
+ *     next step's free_count (released blocks go on the end of the list).
+ *   - Requests are admitted in order: the first one whose blocks or rows do
+ *     not fit, and all after it, are left as they are (no rows, no blocks,
+ *     seq_lens[b] = C_b), and the status reads PA_ERR_NO_ROOM.  A request
+ *     with a negative length, or with C_b + n_b > max_blocks_per_seq *
+ *     block_size, gets no rows and no blocks and seq_lens[b] = max(C_b, 0)
+ *     (at most the row's capacity), and the status reads PA_ERR_BAD_SEQ_LEN.
+ *     A block id outside 0..num_blocks-1 (table or free list) gives its
+ *     tokens slot -1 and PA_ERR_BAD_BLOCK_ID; a *free_count outside
+ *     0..max_free counts as 0.
+ *   - An output must not overlap an input (PA_ERR_INVALID_ARG): other CTAs
+ *     still read the inputs.  Steps captured into a graph use two sets of
+ *     buffers in turn.
+ * status (may be null): one int32 word, as the first word of a workspace;
+ * device errors are stored there and stay until read.  One launch; no
+ * workspace.
+ */
+typedef struct pa_plan_params {
+  int32_t num_seqs;           /* B >= 0                                      */
+  int32_t block_size;         /* tokens per cache block                      */
+  int32_t num_blocks;         /* blocks in the pool (block ids below it)     */
+  int32_t max_blocks_per_seq; /* row length of block_tables                  */
+  int32_t max_tokens;         /* rows of positions and slots                 */
+  int32_t max_free;           /* entries of free_blocks                      */
+} pa_plan_params_t;
+
+PA_API pa_status_t pa_plan_step(const pa_plan_params_t* params, const int32_t* ctx_lens,
+                                const int32_t* new_lens, const int32_t* free_blocks,
+                                const int32_t* free_count, const int32_t* base_len,
+                                int32_t* block_tables, int32_t* query_start, int32_t* seq_lens,
+                                int32_t* positions, int64_t* slots, int32_t* free_left,
+                                int32_t* status, cudaStream_t stream);
+
+/*
+ * Norm of each query and key head, rotation by position, and the write of
+ * keys and values into the paged cache, in one pass over the projections.
+ * For row t and head h, x the head_dim elements of q[t,h] (or k[t,h]):
+ *   y = x * (1 / sqrt(mean(x^2) + eps)) * (weight + weight_offset)
+ * (no norm where the weight is null), then the first rotary_dim elements are
+ * rotated in pairs (a, b) by the row's angles, c_j = cos_sin[pos][j] and
+ * s_j = cos_sin[pos][rotary_dim / 2 + j]:
+ *   (a, b) -> (a c_j - b s_j, b c_j + a s_j),
+ * pair j being elements (j, j + rotary_dim / 2), or (2j, 2j + 1) with
+ * PA_ROPE_INTERLEAVED.  Sums and products are float32, rounded once.
+ *   q [T, num_heads, head_dim], k, v [T, num_kv_heads, head_dim]: rows
+ *        q_stride / k_stride / v_stride elements apart (slices of one fused
+ *        projection), heads contiguous within a row; 16-byte aligned rows
+ *   q_out [T, num_heads, head_dim], contiguous; may be q itself when
+ *        q is contiguous
+ *   k_out, v_out [T, num_kv_heads, head_dim], contiguous, may be null: the
+ *        normed and rotated keys, and the values, as pa_prefill takes them
+ *   k_cache, v_cache: the pools (standard layout, or PA_FLAG_SPLIT_X); row t
+ *        is stored at slot slots[t] = block * block_size + place.  Both may
+ *        be null (slots then only marks padding).
+ *   q_weight, k_weight [head_dim], element type as q; both null: no norm
+ *   cos_sin float32 [max_position, rotary_dim]
+ *   positions int32 [T], slots int64 [T]
+ * A row with slot -1 is padding: nothing of it is read or written.  A slot
+ * outside the pool (below -1, or past num_blocks * block_size) writes no cache
+ * and reads PA_ERR_BAD_SLOT in the status; a position outside
+ * 0..max_position-1 makes the row's q_out and k_out NaN, writes no cache and
+ * reads PA_ERR_BAD_POSITION.  Rows must have distinct slots: where two rows
+ * share one, what it holds afterwards is some mix of the two.
+ * rotary_dim is a multiple of 16, at most head_dim (0: no rotation).  One
+ * launch; no workspace; status as for pa_plan_step.
+ */
+#define PA_ROPE_INTERLEAVED 256 /* pa_rope_params_t.flags, beside PA_FLAG_SPLIT_X */
+typedef struct pa_rope_params {
+  int32_t num_tokens;   /* T >= 0                                            */
+  int32_t num_heads;    /* Hq >= 1                                           */
+  int32_t num_kv_heads; /* Hkv >= 1                                          */
+  int32_t head_dim;     /* D: 64, 128 or 256                                 */
+  int32_t block_size;   /* tokens per cache block                            */
+  int32_t num_blocks;   /* blocks in each cache pool                         */
+  int32_t rotary_dim;   /* elements rotated                                  */
+  int32_t max_position; /* rows of cos_sin                                   */
+  int64_t q_stride;     /* elements from one row of q to the next            */
+  int64_t k_stride;
+  int64_t v_stride;
+  pa_dtype_t dtype;     /* q, k, v, weights, caches and outputs              */
+  int32_t flags;        /* PA_ROPE_INTERLEAVED, PA_FLAG_SPLIT_X              */
+  float eps;
+  float weight_offset;  /* added to the weights (0, or 1 for weights around 0) */
+} pa_rope_params_t;
+
+PA_API pa_status_t pa_qk_norm_rope(const pa_rope_params_t* params, const void* q, const void* k,
+                                   const void* v, const void* q_weight, const void* k_weight,
+                                   const float* cos_sin, const int32_t* positions,
+                                   const int64_t* slots, void* q_out, void* k_out, void* v_out,
+                                   void* k_cache, void* v_cache, int32_t* status,
+                                   cudaStream_t stream);
+
+/*
+ * Attention with a sliding window and sinks.  A query at position p (0-based)
+ * sees token t <= p when t < num_sinks (the sequence's first tokens, which stay
+ * visible) or t > p - window (the last `window` tokens, itself included).
+ * Tokens outside are not read: block-table entries of blocks that hold no
+ * visible token may say anything (blocks given back to the pool).
+ */
+typedef struct pa_window {
+  int32_t window;    /* >= 1                                                 */
+  int32_t num_sinks; /* >= 0                                                 */
+} pa_window_t;
+
+/*
+ * Decode: the step of pa_decode (same tensors, layouts, flags and checks; the
+ * query sits at position seq_lens[b] - 1) over the visible tokens.  The
+ * workspace holds pa_window_workspace_size() bytes, its control block
+ * initialised by pa_workspace_init; partition_size tokens (a multiple of
+ * block_size, as for pa_decode_v2) are one partial of a row.  Tensor-core
+ * kernel where pa_decode_kernel() says 2 and the layout is the standard one,
+ * else CUDA cores.  v1_max_seq_len is not used.  What the pools hold for
+ * invisible tokens does not matter (NaN included).
+ */
+PA_API size_t pa_window_workspace_size(const pa_params_t* params, const pa_window_t* window);
+PA_API pa_status_t pa_decode_window(const pa_params_t* params, const pa_window_t* window,
+                                    const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, const int32_t* seq_lens,
+                                    void* workspace, size_t workspace_bytes, void* out,
+                                    cudaStream_t stream);
+
+/*
+ * Prefill: the chunk of pa_prefill (same tensors and device-side checks) with
+ * the same mask; row i of sequence b sits at position ctx_lens[b] + i.  Every
+ * dtype, head_dim (64, 128, 256) and block size the decode calls take:
+ * tensor-core kernel for bf16 / f16, head_dim 128 (block_size 16, 32, 64) or
+ * 256 (16, 32) and at most 64 query heads per KV head, else CUDA cores
+ * (flags: PA_FLAG_PORTABLE, PA_FLAG_SPLIT_X for the caches,
+ * PA_FLAG_SELFTEST_STALL).  Of the tokens that at least one row of the call
+ * sees, values must be finite (a weight of zero times infinity is NaN).
+ */
+PA_API pa_status_t pa_prefill_window(const pa_prefill_params_t* params, const pa_window_t* window,
+                                     const void* q, const void* k, const void* v,
+                                     const void* k_cache, const void* v_cache,
+                                     const int32_t* block_tables, const int32_t* query_start,
+                                     const int32_t* ctx_lens, void* out, cudaStream_t stream);
+
+/*
+ * Decode of a batch that shares a prefix.  Every sequence attends to the
+ * *prefix_len tokens of one shared prefix (blocks prefix_blocks[0 ..], the
+ * last one possibly part full) and then to its own seq_lens[b] tokens (blocks
+ * block_tables[b], which hold nothing of the prefix):
+ *   out[b,h] = softmax over both lists of scale * q[b,h] . k, applied to v.
+ * The prefix is read once for all sequences and heads of a KV group, as one
+ * matrix product over the rows (b, h); the own tokens go through the paged
+ * decode pass; a last kernel joins the partial results.
+ *   prefix_blocks [int32] [max_prefix_blocks], prefix_len [int32] [1], on the
+ *   device; seq_lens[b] in 0..max_seq_len, and both lists may be empty (a row
+ *   with no token at all is zeros).
+ * A prefix length outside 0..max_prefix_len, or a prefix block id outside the
+ * pool, makes every row NaN; a sequence's own bad length or block id its rows.
+ * workspace: pa_prefix_workspace_size() bytes, initialised once by
+ * pa_workspace_init.  Tensor-core kernel for the prefix where pa_decode_kernel()
+ * says 2 and the layout is the standard one, else CUDA cores.
+ */
+typedef struct pa_prefix {
+  int32_t max_prefix_len;    /* host-known bound of *prefix_len              */
+  int32_t max_prefix_blocks; /* entries of prefix_blocks                     */
+} pa_prefix_t;
+
+PA_API size_t pa_prefix_workspace_size(const pa_params_t* params, const pa_prefix_t* prefix);
+PA_API pa_status_t pa_decode_prefix(const pa_params_t* params, const pa_prefix_t* prefix,
+                                    const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* prefix_blocks, const int32_t* prefix_len,
+                                    const int32_t* block_tables, const int32_t* seq_lens,
+                                    void* workspace, size_t workspace_bytes, void* out,
+                                    cudaStream_t stream);
 
 /* ABI version: major * 10000 + minor * 100 + patch. */
 PA_API int pa_version(void);

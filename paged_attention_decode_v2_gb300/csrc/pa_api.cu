@@ -59,6 +59,8 @@ int64_t num_partitions(const pa_params_t* p) {
   return n > 0 ? n : 1;
 }
 
+}  // namespace
+
 pa_status_t check_tensors(const void* q, const void* k, const void* v, const int32_t* bt,
                           const int32_t* sl, const void* out) {
   if (!q || !k || !v || !bt || !sl || !out) return PA_ERR_INVALID_ARG;
@@ -105,8 +107,6 @@ cudaError_t launch_pass(const pa_params_t* p, const KernelArgs& a, bool v2, cuda
     default: return launch_generic_f16(a, v2, s);
   }
 }
-
-}  // namespace
 
 WorkspaceLayout workspace_layout(int64_t num_seqs, int64_t num_heads, int64_t head_dim,
                                  int64_t np) {
@@ -278,6 +278,9 @@ const char* pa_status_string(pa_status_t s) {
     case PA_ERR_BAD_BLOCK_ID: return "block id outside the pool";
     case PA_ERR_BAD_SEQ_LEN: return "sequence length outside 0..max_seq_len";
     case PA_ERR_WORKSPACE_NOT_INIT: return "workspace not initialised (pa_workspace_init)";
+    case PA_ERR_NO_ROOM: return "no room: free blocks or rows ran out";
+    case PA_ERR_BAD_SLOT: return "slot outside the pool";
+    case PA_ERR_BAD_POSITION: return "position outside the table";
   }
   return "unknown status";
 }

@@ -111,11 +111,74 @@ struct PrefillArgs {
   int32_t selftest_stall;
 };
 
+// CUDA-core attention over a list of tokens (pa_portable.cuh).
+enum ListMode { kDecodeWindow = 0, kPrefillWindow = 1, kPrefix = 2 };
+struct ListArgs {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const void* k_new;            // kPrefillWindow: the chunk's keys and values
+  const void* v_new;
+  const int32_t* block_tables;  // kPrefix: the prefix's blocks
+  const int32_t* lens;          // seq_lens / ctx_lens / prefix_len
+  const int32_t* query_start;   // kPrefillWindow
+  void* out;
+  float* part_max;
+  float* part_sum;
+  float* part_out;
+  int32_t* status;
+  int64_t rows;                 // sequences, or tokens of the chunks
+  int32_t mode;
+  int32_t num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int32_t max_blocks_per_seq, max_len, total_tokens, max_query_len;
+  int32_t window, num_sinks;
+  int32_t part_size, num_parts; // num_parts 1: no split
+  int32_t always_partial;       // partials even where there is one part
+  int32_t group, out_dtype, split_x;
+  float scale_log2;
+};
+cudaError_t launch_portable_f32(const ListArgs& a, cudaStream_t s);
+cudaError_t launch_portable_bf16(const ListArgs& a, cudaStream_t s);
+cudaError_t launch_portable_f16(const ListArgs& a, cudaStream_t s);
+
+// The join of up to two lists of partials of each row (pa_join.cu).  Row r of
+// a list has `stride` slots from r * stride on; how many hold a partial
+// follows from the row's length in the list.
+struct JoinList {
+  const float* m;               // null: no such list
+  const float* s;
+  const float* o;
+  const int32_t* lens;          // [num_seqs], or [1] when shared
+  int32_t shared;
+  int32_t max_len;
+  int32_t stride;
+  int32_t part_size;            // tokens of a partial, unless key_blocks > 0
+  int32_t window, num_sinks;    // window > 0: the length is the visible list's
+  int32_t block_list;           //   the block list's (pa_span.cuh), else the plain list's
+  int32_t block_size;
+  int32_t key_blocks;           // > 0: the tensor-core prefix pass's segments,
+  int32_t lanes;                //   each with this many partials
+};
+struct JoinArgs {
+  JoinList list[2];
+  void* out;
+  int64_t num_rows;             // num_seqs * num_heads
+  int32_t num_heads, head_dim, group, out_dtype;
+};
+cudaError_t launch_join(const JoinArgs& a, cudaStream_t s, bool pdl);
+
 // Launchers return cudaSuccess or the launch error.
 cudaError_t launch_generic_f32(const KernelArgs& a, bool v2, cudaStream_t s);
 cudaError_t launch_generic_bf16(const KernelArgs& a, bool v2, cudaStream_t s);
 cudaError_t launch_generic_f16(const KernelArgs& a, bool v2, cudaStream_t s);
 cudaError_t launch_reduce(const KernelArgs& a, cudaStream_t s, bool pdl);
+// Pass 1 of V2 (or V1) on the kernels these parameters choose.
+cudaError_t launch_pass(const pa_params_t* p, const KernelArgs& a, bool v2, cudaStream_t s);
+// Pointer checks of the decode tensors, and the kernel arguments of a step.
+pa_status_t check_tensors(const void* q, const void* k, const void* v, const int32_t* bt,
+                          const int32_t* sl, const void* out);
+KernelArgs make_args(const pa_params_t* p, const void* q, const void* k, const void* v,
+                     const int32_t* bt, const int32_t* sl, void* out);
 // Parameter checks of every decode entry point (`v2`: the partition rules too).
 pa_status_t check_params(const pa_params_t* p, bool v2);
 

@@ -1,0 +1,253 @@
+// pa_plan.cu -- pa_plan_step: block tables, slots, positions and row starts
+// of one serving step, from the requests' lengths.
+//
+// With have_b = ceil(C_b / BS) and need_b = ceil((C_b + n_b) / BS), the step
+// is two running sums over the requests, of n_b (rows) and of need_b - have_b
+// (blocks taken), and then one independent piece of work per row:
+//   row r of request b: i = r - start_b, place t = C_b + i;
+//   block = t / BS < have_b ? the table's entry : the free list's, counted
+//   from its end by the request's block offset; slot = block * BS + t % BS.
+// A new block always begins with one of the step's tokens, so the thread of
+// the token at t % BS == 0 also writes the table entry.
+//
+// Both sums cost less than a launch: every CTA makes them for itself (64-bit,
+// over chunks of 1024 requests, in shared memory) and then takes 2048 rows,
+// finding a row's request by a binary search of the chunk's starts.  Nothing
+// passes between CTAs, so one launch does it all.  Bound by latency: one load
+// of the lengths, the scan, one dependent load of a block id, the stores.
+#include <cstdint>
+
+#include <cuda_runtime_api.h>
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kNT = 512;       // threads: two requests each in a chunk
+constexpr int kChunk = 2 * kNT;
+constexpr int kRows = 4 * kNT;  // rows of a CTA
+
+struct PlanArgs {
+  const int32_t* ctx_lens;
+  const int32_t* new_lens;
+  const int32_t* free_blocks;
+  const int32_t* free_count;
+  const int32_t* base_len;
+  int32_t* block_tables;
+  int32_t* query_start;
+  int32_t* seq_lens;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* free_left;
+  int32_t* status;
+  int32_t num_seqs, block_size, num_blocks, max_blocks, max_tokens, max_free;
+};
+
+struct Request {
+  int32_t C, n;      // cached and new tokens (n 0 where the lengths are refused)
+  int32_t have, d;   // blocks it has, blocks it takes
+  bool ok;
+};
+
+__device__ __forceinline__ Request request(const PlanArgs& a, int b) {
+  Request r{0, 0, 0, 0, true};
+  if (b >= a.num_seqs) return r;
+  const int32_t C = __ldg(a.ctx_lens + b), n = __ldg(a.new_lens + b);
+  const int64_t cap = static_cast<int64_t>(a.max_blocks) * a.block_size;
+  r.ok = C >= 0 && n >= 0 && static_cast<int64_t>(C) + n <= cap;
+  r.C = r.ok ? C : static_cast<int32_t>(min(static_cast<int64_t>(max(C, 0)), cap));
+  r.n = r.ok ? n : 0;
+  const int64_t bs = a.block_size;
+  r.have = static_cast<int32_t>((r.C + bs - 1) / bs);
+  r.d = static_cast<int32_t>((static_cast<int64_t>(r.C) + r.n + bs - 1) / bs) - r.have;
+  return r;
+}
+
+__global__ void __launch_bounds__(kNT) pa_plan_kernel(const PlanArgs a) {
+  __shared__ int64_t row_s[kChunk + 1];  // rows before each request of the chunk
+  __shared__ int64_t blk_s[kChunk + 1];  // blocks taken before it
+  __shared__ int32_t ctx_s[kChunk];
+  __shared__ int64_t wsum[2][kNT / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int64_t r1 = min(r0 + kRows, static_cast<int64_t>(a.max_tokens));
+  const int32_t given = __ldg(a.free_count);
+  const int64_t count = given >= 0 && given <= a.max_free ? given : 0;
+  const int32_t base = a.base_len ? __ldg(a.base_len) : 0;
+  int64_t carry_row = 0, carry_blk = 0;  // totals over the chunks so far
+  int64_t stop_row = 0, stop_blk = 0;    // totals over the admitted requests
+
+  for (int c0 = 0; c0 < a.num_seqs; c0 += kChunk) {
+    const Request q[2] = {request(a, c0 + 2 * tid), request(a, c0 + 2 * tid + 1)};
+    // inclusive scan of the threads' pairs over the CTA
+    const int64_t mr = static_cast<int64_t>(q[0].n) + q[1].n;
+    const int64_t mb = static_cast<int64_t>(q[0].d) + q[1].d;
+    int64_t xr = mr, xb = mb;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t yr = __shfl_up_sync(0xffffffffu, xr, o);
+      const int64_t yb = __shfl_up_sync(0xffffffffu, xb, o);
+      if (lane >= o) {
+        xr += yr;
+        xb += yb;
+      }
+    }
+    __syncthreads();  // the previous chunk's shared values are no longer read
+    if (lane == 31) {
+      wsum[0][warp] = xr;
+      wsum[1][warp] = xb;
+    }
+    __syncthreads();
+    int64_t row = carry_row + xr - mr, blk = carry_blk + xb - mb;
+#pragma unroll
+    for (int w = 0; w < kNT / 32; ++w) {
+      carry_row += wsum[0][w];
+      carry_blk += wsum[1][w];
+      if (w < warp) {
+        row += wsum[0][w];
+        blk += wsum[1][w];
+      }
+    }
+    bool admitted[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = 2 * tid + e;
+      row_s[j] = row;
+      blk_s[j] = blk;
+      ctx_s[j] = q[e].C;
+      row += q[e].n;
+      blk += q[e].d;
+      // both sums only grow, so the admitted requests are the first ones
+      admitted[e] = row <= a.max_tokens && blk <= count;
+    }
+    if (tid == kNT - 1) {
+      row_s[kChunk] = row;
+      blk_s[kChunk] = blk;
+    }
+    // how many of the chunk's are admitted (both counts are barriers too)
+    const int m0 = __syncthreads_count(admitted[0]);
+    const int m = m0 + __syncthreads_count(admitted[1]);
+    if (m > 0) {
+      stop_row = row_s[m];
+      stop_blk = blk_s[m];
+    }
+    if (blockIdx.x == (c0 / kChunk) % gridDim.x) {  // one CTA writes the chunk's requests
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int b = c0 + 2 * tid + e;
+        if (b >= a.num_seqs) break;
+        a.query_start[b + 1] =
+            static_cast<int32_t>(admitted[e] ? row_s[2 * tid + e + 1] : stop_row);
+        a.seq_lens[b] = q[e].C + (admitted[e] ? q[e].n : 0);
+        if (!q[e].ok) set_status(a.status, PA_ERR_BAD_SEQ_LEN);
+        if (!admitted[e]) set_status(a.status, PA_ERR_NO_ROOM);
+      }
+    }
+    // this CTA's rows that belong to the chunk
+    const int64_t lo = max(r0, row_s[0]), hi = min(min(r1, row_s[kChunk]), stop_row);
+    for (int64_t r = lo + tid; r < hi; r += kNT) {
+      int p = 0, z = kChunk;  // the last request that starts at or before r has rows
+      while (z - p > 1) {
+        const int mid = (p + z) >> 1;
+        if (row_s[mid] <= r) p = mid;
+        else z = mid;
+      }
+      const int b = c0 + p;
+      const int32_t C = ctx_s[p];
+      const int32_t t = C + static_cast<int32_t>(r - row_s[p]);
+      const int32_t idx = t / a.block_size, at = t - idx * a.block_size;
+      const int32_t have = static_cast<int32_t>((static_cast<int64_t>(C) + a.block_size - 1) /
+                                                a.block_size);
+      int32_t* entry = a.block_tables + static_cast<int64_t>(b) * a.max_blocks + idx;
+      int32_t id;
+      if (idx < have) {
+        id = *entry;
+      } else {
+        id = __ldg(a.free_blocks + (count - 1 - (blk_s[p] + idx - have)));
+        if (at == 0) *entry = id;
+      }
+      const bool bad = id < 0 || id >= a.num_blocks;
+      if (bad) set_status(a.status, PA_ERR_BAD_BLOCK_ID);
+      a.positions[r] = base + t;
+      a.slots[r] = bad ? -1 : static_cast<int64_t>(id) * a.block_size + at;
+    }
+  }
+  for (int64_t r = max(r0, stop_row) + tid; r < r1; r += kNT) {  // padding
+    a.positions[r] = 0;
+    a.slots[r] = -1;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.query_start[0] = 0;
+    *a.free_left = static_cast<int32_t>(count - stop_blk);
+  }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status_t pa_plan_step(const pa_plan_params_t* p, const int32_t* ctx_lens,
+                                    const int32_t* new_lens, const int32_t* free_blocks,
+                                    const int32_t* free_count, const int32_t* base_len,
+                                    int32_t* block_tables, int32_t* query_start,
+                                    int32_t* seq_lens, int32_t* positions, int64_t* slots,
+                                    int32_t* free_left, int32_t* status, cudaStream_t stream) {
+  using namespace pa;
+  if (!p || p->num_seqs < 0 || p->block_size < 1 || p->num_blocks < 1) return PA_ERR_INVALID_ARG;
+  if (p->max_blocks_per_seq < 1 || p->max_tokens < 0 || p->max_free < 0) return PA_ERR_INVALID_ARG;
+  // token places are int32
+  if (static_cast<int64_t>(p->max_blocks_per_seq) * p->block_size >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;
+  if (p->num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+  if (!free_count || !query_start || !free_left) return PA_ERR_INVALID_ARG;
+  if (p->num_seqs && (!ctx_lens || !new_lens || !block_tables || !seq_lens))
+    return PA_ERR_INVALID_ARG;
+  if (p->max_tokens && (!positions || !slots)) return PA_ERR_INVALID_ARG;
+  if (p->max_free && !free_blocks) return PA_ERR_INVALID_ARG;
+  for (const void* x : {static_cast<const void*>(ctx_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(free_count), static_cast<const void*>(base_len),
+                        static_cast<const void*>(block_tables),
+                        static_cast<const void*>(query_start), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(positions), static_cast<const void*>(free_left),
+                        static_cast<const void*>(status)})
+    if (!aligned(x, 4)) return PA_ERR_MISALIGNED;
+  if (!aligned(slots, 8)) return PA_ERR_MISALIGNED;
+  {  // no output over an input, nor over another output
+    const size_t B = static_cast<size_t>(p->num_seqs), T = static_cast<size_t>(p->max_tokens);
+    const struct { const void* p; size_t n; bool out; } r[] = {
+        {ctx_lens, 4 * B, false},
+        {new_lens, 4 * B, false},
+        {free_blocks, 4 * static_cast<size_t>(p->max_free), false},
+        {free_count, 4, false},
+        {base_len, 4, false},
+        {block_tables, 4 * B * static_cast<size_t>(p->max_blocks_per_seq), true},
+        {query_start, 4 * (B + 1), true},
+        {seq_lens, 4 * B, true},
+        {positions, 4 * T, true},
+        {slots, 8 * T, true},
+        {free_left, 4, true},
+        {status, 4, true}};
+    constexpr int n = sizeof r / sizeof r[0];
+    for (int i = 0; i < n; ++i)
+      for (int j = i + 1; j < n; ++j)
+        if ((r[i].out || r[j].out) && r[i].n && r[j].n && overlap(r[i].p, r[i].n, r[j].p, r[j].n))
+          return PA_ERR_INVALID_ARG;
+  }
+  PlanArgs a{ctx_lens,  new_lens,      free_blocks,   free_count,    base_len,
+             block_tables, query_start, seq_lens,     positions,     slots,
+             free_left, status,        p->num_seqs,   p->block_size, p->num_blocks,
+             p->max_blocks_per_seq, p->max_tokens, p->max_free};
+  int64_t grid = (static_cast<int64_t>(p->max_tokens) + kRows - 1) / kRows;
+  if (grid < 1) grid = 1;
+  pa_plan_kernel<<<static_cast<unsigned>(grid), kNT, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}

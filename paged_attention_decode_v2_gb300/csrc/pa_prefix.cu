@@ -1,0 +1,166 @@
+// pa_prefix.cu -- pa_decode_prefix: a batch that shares a prefix.
+//
+// Three kernels: the sequences' own tokens (pass 1 of V2 over their block
+// tables, as in pa_decode_v2_partitions), the prefix (one product over all
+// rows of a KV head, split over keys), and the join of both lists of partials
+// (pa_join.cu).
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "pa.h"
+#include "pa_internal.h"
+#include "pa_span.cuh"
+
+namespace pa {
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int64_t kPortablePart = 1024;  // prefix tokens of a partial on the CUDA cores
+
+size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+pa_status_t check_prefix(const pa_params_t* p, const pa_prefix_t* x) {
+  if (pa_status_t st = check_params(p, true)) return st;
+  if (!x || x->max_prefix_len < 0 || x->max_prefix_blocks < 0) return PA_ERR_INVALID_ARG;
+  if (x->max_prefix_len > static_cast<int64_t>(x->max_prefix_blocks) * p->block_size)
+    return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(p->max_seq_len) + p->partition_size + 256 >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(x->max_prefix_len) + 2048 >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+// Control block | prefix partials (max, sum, output) | own partials.
+struct PrefixLayout {
+  int64_t np_prefix, np_own;  // slots of a row in each list
+  size_t m[2], s[2], o[2], total;
+};
+
+PrefixLayout layout_of(const pa_params_t* p, const pa_prefix_t* x) {
+  PrefixLayout w;
+  w.np_prefix = std::max<int64_t>(1, ceil_div(x->max_prefix_len, kPortablePart));
+  w.np_own = std::max<int64_t>(1, ceil_div(p->max_seq_len, p->partition_size));
+  const size_t rows = static_cast<size_t>(p->num_seqs) * p->num_heads;
+  size_t at = kCtrlBytes;
+  const int64_t np[2] = {w.np_prefix, w.np_own};
+  for (int i = 0; i < 2; ++i) {
+    w.m[i] = at;
+    at += up(rows * np[i] * 4);
+    w.s[i] = at;
+    at += up(rows * np[i] * 4);
+    w.o[i] = at;
+    at += up(rows * np[i] * p->head_dim * 4);
+  }
+  w.total = at;
+  return w;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+size_t pa_prefix_workspace_size(const pa_params_t* p, const pa_prefix_t* prefix) {
+  if (check_prefix(p, prefix) != PA_OK) return 0;
+  return layout_of(p, prefix).total;
+}
+
+pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, const void* q,
+                             const void* k_cache, const void* v_cache,
+                             const int32_t* prefix_blocks, const int32_t* prefix_len,
+                             const int32_t* block_tables, const int32_t* seq_lens,
+                             void* workspace, size_t workspace_bytes, void* out,
+                             cudaStream_t stream) {
+  if (pa_status_t st = check_prefix(p, prefix)) return st;
+  if (p->num_seqs == 0) return PA_OK;
+  if (pa_status_t st = check_tensors(q, k_cache, v_cache, block_tables, seq_lens, out)) return st;
+  if (!prefix_len || (prefix->max_prefix_len && !prefix_blocks)) return PA_ERR_INVALID_ARG;
+  if (!aligned(prefix_len, 4) || !aligned(prefix_blocks, 4)) return PA_ERR_MISALIGNED;
+  if (!workspace) return PA_ERR_INVALID_ARG;
+  if (!aligned(workspace, kAlign)) return PA_ERR_MISALIGNED;
+  const PrefixLayout w = layout_of(p, prefix);
+  if (workspace_bytes < w.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  char* base = static_cast<char*>(workspace);
+  int32_t* status = reinterpret_cast<int32_t*>(base);
+  const auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
+  JoinArgs j{};
+
+  // the sequences' own tokens
+  if (p->max_seq_len > 0) {
+    KernelArgs a = make_args(p, q, k_cache, v_cache, block_tables, seq_lens, out);
+    a.status = status;
+    a.max_logits = at(w.m[1]);
+    a.exp_sums = at(w.s[1]);
+    a.tmp_out = at(w.o[1]);
+    a.num_partitions = static_cast<int32_t>(w.np_own);
+    if (launch_pass(p, a, true, stream) != cudaSuccess) return PA_ERR_CUDA;
+    JoinList& l = j.list[1];
+    l.m = a.max_logits;
+    l.s = a.exp_sums;
+    l.o = a.tmp_out;
+    l.part_size = p->partition_size;
+  }
+  j.list[1].lens = seq_lens;
+  j.list[1].max_len = p->max_seq_len;
+  j.list[1].stride = static_cast<int32_t>(w.np_own);
+
+  // the shared prefix
+  if (prefix->max_prefix_len > 0) {
+    if (w.np_prefix > 65535) return PA_ERR_UNSUPPORTED;
+    ListArgs a{};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = prefix_blocks;
+    a.lens = prefix_len;
+    a.part_max = at(w.m[0]);
+    a.part_sum = at(w.s[0]);
+    a.part_out = at(w.o[0]);
+    a.status = status;
+    a.rows = p->num_seqs;
+    a.mode = kPrefix;
+    a.num_seqs = p->num_seqs;
+    a.num_heads = p->num_heads;
+    a.num_kv_heads = p->num_kv_heads;
+    a.head_dim = p->head_dim;
+    a.block_size = p->block_size;
+    a.num_blocks = p->num_blocks;
+    a.max_len = prefix->max_prefix_len;
+    a.part_size = static_cast<int32_t>(kPortablePart);
+    a.num_parts = static_cast<int32_t>(w.np_prefix);
+    a.always_partial = 1;
+    a.group = p->num_heads / p->num_kv_heads;
+    a.split_x = (p->flags & PA_FLAG_SPLIT_X) ? 1 : 0;
+    a.scale_log2 = p->scale * 1.442695040888963407360f;
+    cudaError_t e;
+    switch (p->kv_dtype) {
+      case PA_F32: e = launch_portable_f32(a, stream); break;
+      case PA_BF16: e = launch_portable_bf16(a, stream); break;
+      default: e = launch_portable_f16(a, stream); break;
+    }
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    JoinList& l = j.list[0];
+    l.m = a.part_max;
+    l.s = a.part_sum;
+    l.o = a.part_out;
+    l.part_size = a.part_size;
+  }
+  j.list[0].lens = prefix_len;
+  j.list[0].shared = 1;
+  j.list[0].max_len = prefix->max_prefix_len;
+  j.list[0].stride = static_cast<int32_t>(w.np_prefix);
+  j.out = out;
+  j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;
+  j.num_heads = p->num_heads;
+  j.head_dim = p->head_dim;
+  j.group = p->num_heads / p->num_kv_heads;
+  j.out_dtype = p->out_dtype;
+  return launch_join(j, stream, false) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"
