@@ -141,6 +141,45 @@ cudaError_t launch_portable_f32(const ListArgs& a, cudaStream_t s);
 cudaError_t launch_portable_bf16(const ListArgs& a, cudaStream_t s);
 cudaError_t launch_portable_f16(const ListArgs& a, cudaStream_t s);
 
+// Attention of many query rows over key tiles on the tensor cores
+// (pa_rows.cuh): the windowed prefill and the shared-prefix pass.
+constexpr int kRowsMaxCompact = 1024;  // sequences whose row groups are walked compactly
+struct RowsArgs {
+  const int32_t* block_tables;  // prefix: the prefix's blocks
+  const int32_t* query_start;   // windowed prefill
+  const int32_t* lens;          // ctx_lens [num_seqs], or prefix_len [1]
+  void* out;                    // windowed prefill
+  float* part_max;              // prefix: partials, num_parts slots per row
+  float* part_sum;
+  float* part_out;
+  int32_t* status;
+  int32_t num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int32_t max_blocks_per_seq;
+  int32_t num_tokens;           // rows of q: tokens of the chunks, or sequences
+  int32_t max_query_len, max_ctx_len;
+  int32_t window, num_sinks;
+  int32_t group;                // query heads per KV head
+  int32_t row_tokens;           // tokens of a row tile: 128 / group
+  int32_t group_tokens;         // tokens of a unit: one or two row tiles
+  int32_t row_groups;           // prefix: units' row groups; else those of the longest chunk
+  int32_t dual;                 // head_dim 128: two row tiles per unit
+  int32_t key_blocks;           // prefix (pa_span.cuh)
+  int32_t num_parts;
+  int32_t out_dtype;
+  int32_t selftest_stall;
+  float scale_log2;
+};
+// The q, k, v and cache tensors of a row attention; k and v null for a prefix.
+struct RowsTensors {
+  const void *q, *k, *v, *k_cache, *v_cache;
+};
+// Whether the kernel serves these shapes on the current device (its SMs then,
+// else 0), and its launch (pa_rows_host.cu).
+int rows_applicable(pa_dtype_t t, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                    int64_t num_blocks, int64_t num_tokens, float scale);
+cudaError_t launch_rows(RowsArgs a, pa_dtype_t t, const RowsTensors& x, int sms, bool pdl,
+                        cudaStream_t s);
+
 // The join of up to two lists of partials of each row (pa_join.cu).  Row r of
 // a list has `stride` slots from r * stride on; how many hold a partial
 // follows from the row's length in the list.

@@ -33,6 +33,44 @@ pa_status_t check_prefix(const pa_params_t* p, const pa_prefix_t* x) {
   return PA_OK;
 }
 
+// The tensor-core prefix pass's plan for these shapes, whatever the device:
+// rows of a row tile and of a unit, and the number of key blocks.  Row groups x
+// key blocks are the units; with k rounds of 152 CTAs there is room for
+// floor(152 k / groups) key blocks, and a round costs as much as its key block
+// is long, so k minimises k / key blocks (and a little per round).
+struct RowsPlan {
+  bool shape;  // served by the tensor-core kernel as far as shapes go
+  int row_tokens, group_tokens, row_groups, dual, lanes, key_blocks;
+  int64_t np;  // partials of a row
+};
+
+RowsPlan rows_plan(const pa_params_t* p, const pa_prefix_t* x) {
+  constexpr int kSms = 152;
+  RowsPlan r{};
+  const int G = p->num_heads / p->num_kv_heads;
+  r.shape = G <= 64 && (p->head_dim == 128 || p->head_dim == 256) && p->num_seqs > 0 &&
+            !(p->flags & (PA_FLAG_PORTABLE | PA_FLAG_SPLIT_X)) && x->max_prefix_len > 0;
+  if (!r.shape) return r;
+  r.row_tokens = 128 / G;
+  r.dual = p->head_dim == 128 && p->num_seqs > r.row_tokens;
+  r.lanes = p->head_dim == 128 && !r.dual ? 2 : 1;
+  r.group_tokens = r.row_tokens * (r.dual ? 2 : 1);
+  r.row_groups = static_cast<int>(ceil_div(p->num_seqs, r.group_tokens));
+  const int k0 = static_cast<int>(ceil_div(r.row_groups, kSms));
+  double best = 0;
+  for (int k = k0; k < k0 + 4; ++k) {
+    const int blocks = k * kSms / r.row_groups;
+    const double cost = static_cast<double>(k) / blocks * (1.0 + 0.02 * k);
+    if (k == k0 || cost < best) {
+      best = cost;
+      r.key_blocks = blocks;
+    }
+  }
+  const int64_t tiles = ceil_div(x->max_prefix_len, 128);
+  r.np = r.lanes * std::min<int64_t>(tiles, r.key_blocks / p->num_kv_heads + 2);
+  return r;
+}
+
 // Control block | prefix partials (max, sum, output) | own partials.
 struct PrefixLayout {
   int64_t np_prefix, np_own;  // slots of a row in each list
@@ -41,7 +79,8 @@ struct PrefixLayout {
 
 PrefixLayout layout_of(const pa_params_t* p, const pa_prefix_t* x) {
   PrefixLayout w;
-  w.np_prefix = std::max<int64_t>(1, ceil_div(x->max_prefix_len, kPortablePart));
+  w.np_prefix = std::max<int64_t>(std::max<int64_t>(1, ceil_div(x->max_prefix_len, kPortablePart)),
+                                  rows_plan(p, x).np);
   w.np_own = std::max<int64_t>(1, ceil_div(p->max_seq_len, p->partition_size));
   const size_t rows = static_cast<size_t>(p->num_seqs) * p->num_heads;
   size_t at = kCtrlBytes;
@@ -111,56 +150,96 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
 
   // the shared prefix
   if (prefix->max_prefix_len > 0) {
-    if (w.np_prefix > 65535) return PA_ERR_UNSUPPORTED;
-    ListArgs a{};
-    a.q = q;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.block_tables = prefix_blocks;
-    a.lens = prefix_len;
-    a.part_max = at(w.m[0]);
-    a.part_sum = at(w.s[0]);
-    a.part_out = at(w.o[0]);
-    a.status = status;
-    a.rows = p->num_seqs;
-    a.mode = kPrefix;
-    a.num_seqs = p->num_seqs;
-    a.num_heads = p->num_heads;
-    a.num_kv_heads = p->num_kv_heads;
-    a.head_dim = p->head_dim;
-    a.block_size = p->block_size;
-    a.num_blocks = p->num_blocks;
-    a.max_len = prefix->max_prefix_len;
-    a.part_size = static_cast<int32_t>(kPortablePart);
-    a.num_parts = static_cast<int32_t>(w.np_prefix);
-    a.always_partial = 1;
-    a.group = p->num_heads / p->num_kv_heads;
-    a.split_x = (p->flags & PA_FLAG_SPLIT_X) ? 1 : 0;
-    a.scale_log2 = p->scale * 1.442695040888963407360f;
-    cudaError_t e;
-    switch (p->kv_dtype) {
-      case PA_F32: e = launch_portable_f32(a, stream); break;
-      case PA_BF16: e = launch_portable_bf16(a, stream); break;
-      default: e = launch_portable_f16(a, stream); break;
-    }
-    if (e != cudaSuccess) return PA_ERR_CUDA;
+    const RowsPlan r = rows_plan(p, prefix);
+    const int sms = r.shape ? rows_applicable(p->kv_dtype, p->num_heads, p->num_kv_heads,
+                                              p->head_dim, p->block_size, p->num_blocks,
+                                              p->num_seqs, p->scale)
+                            : 0;
     JoinList& l = j.list[0];
-    l.m = a.part_max;
-    l.s = a.part_sum;
-    l.o = a.part_out;
-    l.part_size = a.part_size;
+    l.m = at(w.m[0]);
+    l.s = at(w.s[0]);
+    l.o = at(w.o[0]);
+    if (sms > 0) {
+      RowsArgs a{};
+      a.block_tables = prefix_blocks;
+      a.lens = prefix_len;
+      a.part_max = at(w.m[0]);
+      a.part_sum = at(w.s[0]);
+      a.part_out = at(w.o[0]);
+      a.status = status;
+      a.num_seqs = p->num_seqs;
+      a.num_heads = p->num_heads;
+      a.num_kv_heads = p->num_kv_heads;
+      a.head_dim = p->head_dim;
+      a.block_size = p->block_size;
+      a.num_blocks = p->num_blocks;
+      a.num_tokens = p->num_seqs;
+      a.max_ctx_len = prefix->max_prefix_len;
+      a.group = p->num_heads / p->num_kv_heads;
+      a.row_tokens = r.row_tokens;
+      a.group_tokens = r.group_tokens;
+      a.row_groups = r.row_groups;
+      a.dual = r.dual;
+      a.key_blocks = r.key_blocks;
+      a.num_parts = static_cast<int32_t>(r.np);
+      a.selftest_stall = (p->flags & PA_FLAG_SELFTEST_STALL) ? 1 : 0;
+      a.scale_log2 = p->scale * 1.442695040888963407360f;
+      const RowsTensors t{q, nullptr, nullptr, k_cache, v_cache};
+      // may start while the pass above still runs; it ends after it
+      if (launch_rows(a, p->kv_dtype, t, sms, p->max_seq_len > 0, stream) != cudaSuccess)
+        return PA_ERR_CUDA;
+      l.stride = a.num_parts;
+      l.key_blocks = r.key_blocks;
+      l.lanes = r.lanes;
+    } else {
+      const int64_t parts = std::max<int64_t>(1, ceil_div(prefix->max_prefix_len, kPortablePart));
+      if (parts > 65535) return PA_ERR_UNSUPPORTED;
+      ListArgs a{};
+      a.q = q;
+      a.k_cache = k_cache;
+      a.v_cache = v_cache;
+      a.block_tables = prefix_blocks;
+      a.lens = prefix_len;
+      a.part_max = at(w.m[0]);
+      a.part_sum = at(w.s[0]);
+      a.part_out = at(w.o[0]);
+      a.status = status;
+      a.rows = p->num_seqs;
+      a.mode = kPrefix;
+      a.num_seqs = p->num_seqs;
+      a.num_heads = p->num_heads;
+      a.num_kv_heads = p->num_kv_heads;
+      a.head_dim = p->head_dim;
+      a.block_size = p->block_size;
+      a.num_blocks = p->num_blocks;
+      a.max_len = prefix->max_prefix_len;
+      a.part_size = static_cast<int32_t>(kPortablePart);
+      a.num_parts = static_cast<int32_t>(parts);
+      a.always_partial = 1;
+      a.group = p->num_heads / p->num_kv_heads;
+      a.split_x = (p->flags & PA_FLAG_SPLIT_X) ? 1 : 0;
+      a.scale_log2 = p->scale * 1.442695040888963407360f;
+      cudaError_t e;
+      switch (p->kv_dtype) {
+        case PA_F32: e = launch_portable_f32(a, stream); break;
+        case PA_BF16: e = launch_portable_bf16(a, stream); break;
+        default: e = launch_portable_f16(a, stream); break;
+      }
+      if (e != cudaSuccess) return PA_ERR_CUDA;
+      l.stride = a.num_parts;
+      l.part_size = a.part_size;
+    }
   }
   j.list[0].lens = prefix_len;
   j.list[0].shared = 1;
   j.list[0].max_len = prefix->max_prefix_len;
-  j.list[0].stride = static_cast<int32_t>(w.np_prefix);
   j.out = out;
   j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;
   j.num_heads = p->num_heads;
   j.head_dim = p->head_dim;
   j.group = p->num_heads / p->num_kv_heads;
   j.out_dtype = p->out_dtype;
-  return launch_join(j, stream, false) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch_join(j, stream, true) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"

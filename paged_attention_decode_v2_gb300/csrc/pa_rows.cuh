@@ -1,0 +1,912 @@
+// pa_rows.cuh -- attention of many query rows over a list of key tiles on the
+// tensor cores (tcgen05): the windowed prefill and the shared-prefix pass.
+//
+// Rows.  The G query heads of one KV head share its keys, so a tile of up to
+// 128 rows holds nq = 128 / G tokens (prefill) or sequences (prefix) times G
+// heads: row r is token r / G, head r % G, and one TMA copy with box (64
+// elements, G heads, nq tokens) brings a 64-element slice of all of them.
+// Keys and values are read once for the G heads.
+//
+// Work unit: the rows of one or two tiles against a run of 128-key tiles.
+//   * windowed prefill: (sequence, KV head, group of tokens); the key tiles
+//     are those that hold a token some row sees: the sinks' tiles, then the
+//     window's, context tiles from the paged cache and chunk tiles from the
+//     dense tensors; rows are masked in the tiles that need it;
+//   * prefix: (key block, row group): the key tiles of all KV heads are one
+//     line cut into key blocks (pa_span.cuh); the row groups of one key block
+//     run side by side on neighbouring CTAs, so a key tile comes from HBM once
+//     and from L2 for the others.  Results are partials (max, sum, output)
+//     that pa_join.cu joins.
+//
+// Steps.  A unit is a sequence of steps, each one product of a row tile with
+// a key tile: QK^T into one of two tensor-memory buffers ("slots"), softmax
+// of that slot by its own four warps, one thread per row, P written over the
+// logits in 16 bits, and P.V from tensor memory.  The MMA warp issues
+// QK^T(k), P.V(k - 1), so the tensor core works on one slot while the warps of
+// the other run their softmax.
+//   head_dim 128, two row tiles ("dual"): slot s is row tile s, both against
+//     the same key tile, which is read from shared memory twice and copied
+//     once; each slot has its own output accumulator.
+//   head_dim 128, one row tile (prefix of a small batch): slots take the key
+//     tiles in turn, each with its own accumulator, maximum and sum: two
+//     partials for the join.
+//   head_dim 256: one row tile and one accumulator (256 of the 512 columns);
+//     slots take the key tiles in turn and hand the row's reference maximum
+//     from one to the other through shared memory as soon as it is known.
+// The reference maximum moves only when a tile's maximum exceeds it by more
+// than 2^8 (then the sum and the accumulator are rescaled), so p <= 2^8.  Sums
+// and accumulators are float32; p alone is rounded to 16 bits (the operand
+// type of the MMA): at most half a step each, the sum adds the unrounded p.
+//
+// Bound by the tensor core for many rows (4 * head_dim flops per row and key)
+// and by HBM for few.  Every wait is bounded; one that gives up makes the
+// CTA's results NaN.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include <cuda.h>
+
+#include "pa_device.cuh"
+#include "pa_sm100.cuh"
+#include "pa_span.cuh"
+
+namespace pa {
+
+namespace rw {
+
+constexpr int kProducers = 3;
+constexpr int kMmaWarp = 8;          // warps 0-7 softmax, 9 .. 8 + kProducers producers
+constexpr int kThreads = 32 * (kMmaWarp + 1 + kProducers);
+constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
+constexpr int kStage = 16384;
+constexpr int kMaxStages = 12;
+constexpr int kTmemCols = 512;       // S slot 0 | S slot 1 | O (two of 128, or one of 256)
+constexpr int kOCol = 256;
+constexpr float kRescaleLog2 = 8.f;
+constexpr long long kWaitBudget = 4000000000LL;    // cycles (about 2 s)
+constexpr long long kSelftestBudget = 20000000LL;  // cycles (about 10 ms)
+constexpr int kSmemLimit = 227 * 1024;
+// register shares: the launch gives kThreads * 168; the softmax warps hold a
+// row's 128 logits, the other warpgroup needs few (256 * 208 + 128 * 88)
+constexpr int kSoftmaxRegs = 208;
+constexpr int kOtherRegs = 88;
+
+template <int D>
+struct Layout {
+  static constexpr int kSlices = D / 64;
+  static constexpr int kVTokens = kStage / (D * 2);    // keys of a value stage
+  static constexpr int kQBytes = 65536;                // D 128: two row tiles, D 256: one
+  static constexpr int kPrefixBytes = ((kRowsMaxCompact + 1) * 4 + 63) / 64 * 64;
+  static constexpr int kStages =
+      std::min(kMaxStages, (kSmemLimit - kQBytes - 4096 - kPrefixBytes) / kStage);
+  static constexpr int kRingOff = kQBytes;
+  static constexpr int kCtrlOff = kRingOff + kStages * kStage;
+  static constexpr int kPrefixOff = kCtrlOff + 3072;
+  static constexpr int kSmem = kPrefixOff + kPrefixBytes + 1024;  // + room to align to 1024
+  static_assert(kSmem <= kSmemLimit, "shared memory");
+  static_assert(kStages >= 8, "a key tile and a value tile in flight");
+};
+
+struct Ctrl {
+  uint64_t full[kMaxStages];   // stage landed
+  uint64_t empty[kMaxStages];  // stage consumed by its MMAs
+  uint64_t qfull, qempty;      // row tiles landed / no longer read
+  uint64_t s_full[2];          // a slot's logits ready
+  uint64_t p_ready[2];         // a slot's P written (its 128 threads arrive)
+  uint64_t o_done[2];          // the P.V of a slot's step completed
+  uint64_t m_next[2];          // D 256: the slot's step has published the reference maximum
+  uint64_t o_free;             // D 256: the accumulator has been read (256 threads arrive)
+  uint64_t tail[kProducers];   // producer-private: a value stage to be cleared landed
+  uint64_t drain;              // abort path: all issued MMAs finished
+  uint64_t never;              // self-test: nothing ever arrives here
+  uint32_t tmem;
+  int abort;
+  int total_groups;            // row groups of the batch (windowed prefill, compact list)
+  float mref[kTile];           // D 256: a row's reference maximum, handed from slot to slot
+  float lsum[2][kTile];        // D 256: the slots' sums at the end of a unit
+};
+static_assert(sizeof(Ctrl) <= 3072, "control block");
+
+// One work unit, decoded the same way by every role.
+struct Unit {
+  int kvh;
+  int seq;           // block-table row
+  int32_t i0, n;     // first token (sequence of the batch), tokens of the sequence (batch)
+  int64_t row0;      // tensor row of token 0
+  int32_t ctx;       // positions from here on are chunk rows
+  int32_t lo_min;    // the first row's window begins here: [sinks, lo_min) is seen by no row
+  int32_t pmax;      // last position that a row sees
+  int tiles;         // key tiles of the unit
+  int low, skip;     // tile j < low is tile j, else tile j + skip
+  int nctx;          // context key tiles of the sequence
+  bool poison;
+  bool run;          // false: nothing to do (a segment list's end)
+  int part;          // prefix: the partial's segment
+};
+
+struct Tile {
+  int32_t pos0;      // position of its first key
+  int nk;            // keys
+  bool ctx;          // from the cache
+  int32_t chunk;     // chunk row of its first key (dense tiles)
+};
+
+__device__ __forceinline__ Tile tile_of(const Unit& u, int j) {
+  Tile t;
+  const int x = j < u.low ? j : j + u.skip;
+  t.ctx = x < u.nctx;
+  if (t.ctx) {
+    t.pos0 = x * kTile;
+    t.nk = min(kTile, u.ctx - t.pos0);
+    t.chunk = 0;
+  } else {
+    t.chunk = (x - u.nctx) * kTile;
+    t.pos0 = u.ctx + t.chunk;
+    t.nk = min(kTile, u.pmax + 1 - t.pos0);
+  }
+  return t;
+}
+
+// The units of one CTA, in order; every role walks the same sequence.
+struct Walk {
+  int64_t k;         // next unit (windowed prefill) or next item (prefix)
+  int64_t x, end;    // prefix: rest of the item's key tiles on the line
+  int rt;            // prefix: its row group
+};
+
+__device__ __forceinline__ Walk walk_begin() { return Walk{blockIdx.x, 0, 0, 0}; }
+
+// Windowed prefill: row groups of sequence b are ceil(n_b / a.group_tokens).
+__device__ __forceinline__ bool chunk_ok(const RowsArgs& a, int b, int32_t& s0, int32_t& n) {
+  s0 = __ldg(a.query_start + b);
+  const int32_t s1 = __ldg(a.query_start + b + 1);
+  n = s1 - s0;
+  return s0 >= 0 && s1 >= s0 && n <= a.max_query_len && s1 <= a.num_tokens;
+}
+
+template <bool kPrefix>
+__device__ __forceinline__ bool walk_next(const RowsArgs& a, const int32_t* groups_before,
+                                          int total_groups, Walk& w, Unit& u) {
+  if constexpr (kPrefix) {
+    const int32_t len = __ldg(a.lens);
+    if (len < 1 || len > a.max_ctx_len) return false;  // the join reports it
+    const PrefixSplit sp = prefix_split(len, a.num_kv_heads, a.key_blocks);
+    const int64_t all = sp.tiles * a.num_kv_heads;
+    if (w.x >= w.end) {
+      const int64_t kb = w.k / a.row_groups;
+      if (kb * sp.block >= all) return false;
+      w.rt = static_cast<int>(w.k % a.row_groups);
+      w.x = kb * sp.block;
+      w.end = min(all, w.x + sp.block);
+      w.k += gridDim.x;
+    }
+    u.kvh = static_cast<int>(w.x / sp.tiles);
+    const int j0 = static_cast<int>(w.x % sp.tiles);
+    const int n = static_cast<int>(min(w.end, (u.kvh + 1) * sp.tiles) - w.x);
+    u.part = static_cast<int>(w.x / sp.block) - sp.first(u.kvh);
+    w.x += n;
+    u.seq = 0;
+    u.i0 = w.rt * a.group_tokens;
+    u.n = a.num_tokens;
+    u.row0 = 0;
+    u.ctx = len;
+    u.lo_min = 0;
+    u.pmax = len - 1;
+    u.tiles = n;
+    u.low = 0;
+    u.skip = j0;
+    u.nctx = static_cast<int>(sp.tiles);
+    u.poison = false;
+    return true;
+  } else {
+    int32_t s0, n;
+    while (true) {
+      int b, g;
+      if (groups_before) {
+        const int64_t units = static_cast<int64_t>(total_groups) * a.num_kv_heads;
+        if (w.k >= units) return false;
+        const int x = static_cast<int>(w.k / a.num_kv_heads);
+        u.kvh = static_cast<int>(w.k % a.num_kv_heads);
+        w.k += gridDim.x;
+        int lo = 0, hi = a.num_seqs;  // largest lo with groups_before[lo] <= x
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (groups_before[mid] <= x) lo = mid;
+          else hi = mid;
+        }
+        b = lo;
+        g = x - groups_before[lo];
+        chunk_ok(a, b, s0, n);
+      } else {
+        const int64_t per = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+        if (w.k >= per * a.row_groups) return false;
+        g = static_cast<int>(w.k / per);
+        const int64_t rem = w.k % per;
+        w.k += gridDim.x;
+        b = static_cast<int>(rem / a.num_kv_heads);
+        u.kvh = static_cast<int>(rem % a.num_kv_heads);
+        if (!chunk_ok(a, b, s0, n) || static_cast<int64_t>(g) * a.group_tokens >= n) continue;
+      }
+      const int32_t C = __ldg(a.lens + b);
+      u.poison = !(C >= 0 && C <= a.max_ctx_len &&
+                   C <= static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size);
+      u.ctx = u.poison ? 0 : C;
+      u.seq = b;
+      // later tokens first: their lists are the longest
+      const int groups = (n + a.group_tokens - 1) / a.group_tokens;
+      u.i0 = (groups - 1 - g) * a.group_tokens;
+      u.n = n;
+      u.row0 = s0;
+      const int32_t last = min(n, u.i0 + a.group_tokens) - 1;
+      u.pmax = u.ctx + last;
+      u.lo_min = max(0, u.ctx + u.i0 - a.window + 1);
+      u.nctx = (u.ctx + kTile - 1) / kTile;
+      const int total = u.nctx + last / kTile + 1;
+      const int sinks = a.num_sinks <= u.ctx
+                            ? (a.num_sinks + kTile - 1) / kTile
+                            : u.nctx + (a.num_sinks - u.ctx + kTile - 1) / kTile;
+      const int first = u.lo_min < u.ctx ? u.lo_min / kTile
+                                         : u.nctx + (u.lo_min - u.ctx) / kTile;
+      u.low = min(sinks, first);
+      u.skip = first - u.low;
+      u.tiles = total - u.skip;
+      return true;
+    }
+  }
+}
+
+// 2^x by the hardware's approximate exponential: relative error well below the
+// 16-bit rounding that p goes through; inputs are at most 8 here.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Bits e of [lo, hi) within a 32-key word that starts at key c0.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) {
+  const int a = max(lo - c0, 0), b = min(hi - c0, 32);
+  if (a >= b) return 0u;
+  const uint32_t up = b >= 32 ? 0xffffffffu : ((1u << b) - 1u);
+  return up & (0xffffffffu << a);
+}
+
+// Each thread reads 32 consecutive columns of its tensor-memory lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void sync256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+}  // namespace rw
+
+// qmap: q as (64, Hq, rows, D / 64), box (64, G, nq, 1); knmap / vnmap: the
+// chunk's keys and values as (64, Hkv, T, D / 64), boxes (64, 1, 128, 1) and
+// (64, 1, 16, D / 64) (windowed prefill only); kcmap / vcmap: the caches as
+// rows of head_dim (box 64 x BS, and a whole block slice-major).
+template <typename T, int D, int BS, bool kPrefix>
+__global__ void __launch_bounds__(rw::kThreads, 1)
+    pa_rows_kernel(const RowsArgs a, const __grid_constant__ CUtensorMap qmap,
+                   const __grid_constant__ CUtensorMap knmap,
+                   const __grid_constant__ CUtensorMap vnmap,
+                   const __grid_constant__ CUtensorMap kcmap,
+                   const __grid_constant__ CUtensorMap vcmap, long long budget) {
+  using namespace rw;
+  using Lay = Layout<D>;
+  constexpr int NST = Lay::kStages;
+  constexpr int kSl = Lay::kSlices;
+  constexpr int kVT = Lay::kVTokens;
+  constexpr bool kChain = D == 256;   // one accumulator, the maximum handed on
+  static_assert(D == 128 || D == 256, "head_dim");
+  static_assert(BS % 16 == 0 && kTile % BS == 0 && kVT % BS == 0, "block size");
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr unsigned kAll = 0xffffffffu;
+
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* qs = smem;
+  uint8_t* ring = smem + Lay::kRingOff;
+  Ctrl& c = *reinterpret_cast<Ctrl*>(smem + Lay::kCtrlOff);
+  int32_t* prefix_s = reinterpret_cast<int32_t*>(smem + Lay::kPrefixOff);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool dual = D == 128 && a.dual;
+
+  if constexpr (kPrefix) asm volatile("griddepcontrol.launch_dependents;");
+
+  if (tid == 0) {
+    for (int s = 0; s < NST; ++s) {
+      sm100::mbar_init(&c.full[s], 1);
+      sm100::mbar_init(&c.empty[s], 1);
+    }
+    sm100::mbar_init(&c.qfull, 1);
+    sm100::mbar_init(&c.qempty, 1);
+    for (int s = 0; s < 2; ++s) {
+      sm100::mbar_init(&c.s_full[s], 1);
+      sm100::mbar_init(&c.p_ready[s], 128);
+      sm100::mbar_init(&c.o_done[s], 1);
+      sm100::mbar_init(&c.m_next[s], 128);
+    }
+    sm100::mbar_init(&c.o_free, 256);
+    for (int p = 0; p < kProducers; ++p) sm100::mbar_init(&c.tail[p], 1);
+    sm100::mbar_init(&c.drain, 1);
+    sm100::mbar_init(&c.never, 1);
+    c.abort = 0;
+    if (kPrefix && blockIdx.x == 0) {
+      const int32_t len = __ldg(a.lens);
+      if (len < 0 || len > a.max_ctx_len) set_status(a.status, PA_ERR_BAD_SEQ_LEN);
+    }
+  }
+  if (warp == kMmaWarp) {
+    sm100::tmem_alloc(&c.tmem, kTmemCols);
+    sm100::tmem_relinquish();
+  }
+  if (warp == kMmaWarp + 1 && lane == 0) {
+    sm100::tma_prefetch_desc(&qmap);
+    sm100::tma_prefetch_desc(&kcmap);
+    sm100::tma_prefetch_desc(&vcmap);
+    if (!kPrefix) {
+      sm100::tma_prefetch_desc(&knmap);
+      sm100::tma_prefetch_desc(&vnmap);
+    }
+  }
+  // windowed prefill of up to kRowsMaxCompact sequences: row groups before
+  // each sequence, so that only existing groups are walked
+  const bool compact = !kPrefix && a.num_seqs <= kRowsMaxCompact;
+  if (compact && warp == 0) {
+    int carry = 0;
+    for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
+      const int b = b0 + lane;
+      int x = 0;
+      if (b < a.num_seqs) {
+        int32_t s0, n;
+        if (chunk_ok(a, b, s0, n)) x = (n + a.group_tokens - 1) / a.group_tokens;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < a.num_seqs) prefix_s[b + 1] = carry + x;
+      carry += __shfl_sync(kAll, x, 31);
+    }
+    if (lane == 0) {
+      prefix_s[0] = 0;
+      c.total_groups = carry;
+    }
+  }
+  sm100::fence_proxy_async_smem();
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  const int32_t* before = compact ? prefix_s : nullptr;
+  const int total_groups = compact ? c.total_groups : 0;
+  volatile int* abort_flag = &c.abort;
+
+  if (warp >= kMmaWarp) {
+    // one instruction for the whole warpgroup, before its roles part
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp > kMmaWarp) {
+    // ========================= producers ==========================================
+    // Every producer warp walks the stages in the order the MMA warp takes
+    // them -- dual: keys, values of each tile; else keys 0, then (keys j,
+    // values j - 1), then the last values -- and fills those with
+    // g % kProducers == pid (producer 0 loads the rows too).
+    const uint32_t pid = static_cast<uint32_t>(warp - kMmaWarp - 1);
+    uint64_t* my_tail = &c.tail[pid];
+    uint64_t keep;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+    uint32_t g = 0, un = 0, tn = 0;
+    int tail_pending = -1;
+    bool ok = true;
+
+    // Block id of each lane's block of a context tile; loaded a tile ahead.
+    auto ctx_id = [&](const Unit& u, int j) -> int32_t {
+      if (j >= u.tiles) return -1;
+      const Tile t = tile_of(u, j);
+      if (!t.ctx || lane >= (t.nk + BS - 1) / BS) return -1;
+      return __ldg(a.block_tables + static_cast<int64_t>(u.seq) * a.max_blocks_per_seq +
+                   t.pos0 / BS + lane);
+    };
+    // Its TMA row; a block outside the pool, or one that no row sees, becomes
+    // a negative row, which TMA fills with zeros instead of reading memory.
+    auto ctx_row = [&](const Unit& u, const Tile& t, int32_t id) -> int32_t {
+      const int32_t p = t.pos0 + lane * BS;
+      const bool seen = kPrefix || p < a.num_sinks || p + BS > u.lo_min;
+      return (!seen || id < 0 || id >= a.num_blocks) ? -BS : (id * a.num_kv_heads + u.kvh) * BS;
+    };
+    auto wait_empty = [&](int slot) {
+      return __all_sync(kAll, sm100::mbar_wait(&c.empty[slot], ((g / NST) & 1) ^ 1, budget,
+                                               abort_flag)) != 0;
+    };
+
+    auto issue_k = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
+      const int nblk = (t.nk + BS - 1) / BS;
+      for (int sl = 0; sl < kSl; ++sl, ++g) {
+        if (g % kProducers != pid) continue;
+        const int slot = g % NST;
+        if (!wait_empty(slot)) return false;
+        uint8_t* st = ring + slot * kStage;
+        if (t.ctx) {
+          if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], nblk * BS * 128);
+          __syncwarp();
+          if (lane < nblk)
+            sm100::tma_load_2d(st + lane * BS * 128, &kcmap, &c.full[slot], sl * 64, y, keep);
+        } else if (lane == 0) {
+          sm100::mbar_arrive_expect_tx(&c.full[slot], kStage);
+          sm100::tma_load_4d(st, &knmap, &c.full[slot], 0, u.kvh,
+                             static_cast<int32_t>(u.row0) + t.chunk, sl, keep);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+
+    // Values of a tile.  Keys that no row sees -- past the tile's last key up
+    // to the end of its 16-key MMA step, and the run between the sinks and
+    // the first row's window -- are cleared before the stage is handed on:
+    // their p is zero, but 0 * NaN would be NaN.  Such a stage lands on the
+    // producer's own barrier first.
+    auto issue_v = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
+      const int vbs = t.ctx ? BS : 16;  // rows per copy
+      const int nv = (t.nk + kVT - 1) / kVT;
+      const int h0 = kPrefix ? 0 : max(0, a.num_sinks - t.pos0);
+      const int h1 = kPrefix ? 0 : min(t.nk, u.lo_min - t.pos0);
+      for (int v = 0; v < nv; ++v, ++g) {
+        if (g % kProducers != pid) continue;
+        const int slot = g % NST;
+        if (!wait_empty(slot)) return false;
+        const int toks = min(kVT, t.nk - v * kVT);
+        const int ncp = (toks + vbs - 1) / vbs;
+        const int a0 = max(h0 - v * kVT, 0), a1 = min(h1 - v * kVT, toks);  // the unseen run
+        const int z1 = (toks + 15) / 16 * 16;
+        const bool clear = a0 < a1 || toks < z1;
+        uint64_t* land = clear ? my_tail : &c.full[slot];
+        uint8_t* st = ring + slot * kStage;
+        if (lane == 0) sm100::mbar_arrive_expect_tx(land, ncp * vbs * D * 2);
+        __syncwarp();
+        if (t.ctx) {
+          const int32_t yj = __shfl_sync(kAll, y, (v * kVT / BS + lane) & 31);
+          if (lane < ncp) sm100::tma_load_3d(st + lane * BS * D * 2, &vcmap, land, 0, yj, 0, keep);
+        } else if (lane < ncp) {
+          sm100::tma_load_4d(st + lane * 16 * D * 2, &vnmap, land, 0, u.kvh,
+                             static_cast<int32_t>(u.row0) + t.chunk + v * kVT + lane * 16, 0, keep);
+        }
+        __syncwarp();
+        if (clear) {
+          tail_pending = slot;
+          if (!__all_sync(kAll, sm100::mbar_wait(my_tail, tn & 1, budget, abort_flag)))
+            return false;
+          ++tn;
+          tail_pending = -1;
+          const int n0 = a0 < a1 ? a1 - a0 : 0;
+          const int pieces = (n0 + z1 - toks) * kSl * 8;
+          for (int i = lane; i < pieces; i += 32) {
+            const int line = i / 8, piece = i % 8;
+            const int x = line / kSl, sl = line % kSl;
+            const int r = x < n0 ? a0 + x : toks + x - n0;
+            *reinterpret_cast<uint4*>(st + (r / vbs) * vbs * D * 2 + sl * vbs * 128 +
+                                      (r % vbs) * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          sm100::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&c.full[slot]);
+        }
+      }
+      return true;
+    };
+
+    Walk wk = walk_begin();
+    Unit u;
+    while (ok && walk_next<kPrefix>(a, before, total_groups, wk, u)) {
+      if (pid == 0) {
+        ok = __all_sync(kAll, sm100::mbar_wait(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
+        if (!ok) break;
+        // rows past the sequence belong to others or are filled with zeros;
+        // their results are never stored
+        const int copies = dual ? 2 * kSl : kSl;
+        if (lane == 0) sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
+        __syncwarp();
+        if (lane < copies)
+          sm100::tma_load_4d(qs + lane * kStage, &qmap, &c.qfull, 0, u.kvh * a.group,
+                             static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
+                             lane % kSl, keep);
+        ++un;
+      }
+      int32_t yprev = 0;
+      Tile tprev{};
+      int32_t id = ctx_id(u, 0);
+      for (int j = 0; j < u.tiles && ok; ++j) {
+        const Tile t = tile_of(u, j);
+        const int32_t y = t.ctx ? ctx_row(u, t, id) : 0;
+        id = ctx_id(u, j + 1);
+        ok = issue_k(u, t, y);
+        if (dual) {
+          if (ok) ok = issue_v(u, t, y);
+        } else {
+          if (ok && j > 0) ok = issue_v(u, tprev, yprev);
+          yprev = y;
+          tprev = t;
+        }
+      }
+      if (ok && !dual) ok = issue_v(u, tprev, yprev);
+    }
+    if (!ok) {
+      if (lane == 0) c.abort = 1;
+      // copies already issued must land before the CTA may exit
+      for (uint32_t gg = g > NST ? g - NST : 0; gg < g; ++gg)
+        if (gg % kProducers == pid && static_cast<int>(gg % NST) != tail_pending)
+          sm100::mbar_wait(&c.full[gg % NST], (gg / NST) & 1, budget, nullptr);
+      if (tail_pending >= 0) sm100::mbar_wait(my_tail, tn & 1, budget, nullptr);
+      if (un > 0) sm100::mbar_wait(&c.qfull, (un - 1) & 1, budget, nullptr);
+    }
+    } else {
+    // ========================= MMA issuer =========================================
+    constexpr uint32_t id_qk = sm100::idesc_f16(kBf16, false, false, 128, kTile);
+    constexpr uint32_t id_pv = sm100::idesc_f16(kBf16, false, true, 128, D);
+    const uint32_t q_base = sm100::smem_u32(qs);
+    const uint32_t ring_base = sm100::smem_u32(ring);
+    uint32_t g = 0, un = 0;     // ring stages, units
+    uint32_t steps[2] = {0, 0}; // P.V issued in each slot
+    uint32_t gk = 0, gv = 0;    // first stages of the current key and value tiles
+    bool ok = true;
+    if (a.selftest_stall) ok = __all_sync(kAll, sm100::mbar_wait(&c.never, 0, budget, abort_flag));
+    auto wait_full = [&](uint32_t gg) {
+      const bool r = __all_sync(kAll, sm100::mbar_wait(&c.full[gg % NST], (gg / NST) & 1, budget,
+                                                       abort_flag)) != 0;
+      sm100::tc_fence_after();
+      return r;
+    };
+
+    // logits of step k: fresh keys unless the other slot has just used them
+    auto qk = [&](int k, bool last) -> bool {
+      const int slot = k & 1;
+      const bool fresh = !dual || slot == 0, done = !dual || slot == 1;
+      if (fresh) {
+        gk = g;
+        g += kSl;
+      }
+      const uint32_t qt = q_base + (dual && slot ? kSl * kStage : 0);
+      for (int sl = 0; sl < kSl; ++sl) {
+        if (fresh && !wait_full(gk + sl)) return false;
+        const uint32_t st = ring_base + ((gk + sl) % NST) * kStage;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t ad = sm100::smem_desc(qt + sl * kStage + kk * 32, 16, 1024, sm100::kSw128);
+          const uint64_t bd = sm100::smem_desc(st + kk * 32, 16, 1024, sm100::kSw128);
+          sm100::mma_f16_elect(tmem + slot * kTile, ad, bd, id_qk, (sl | kk) != 0);
+        }
+        if (done) sm100::mma_commit_elect(&c.empty[(gk + sl) % NST]);
+      }
+      if (last) sm100::mma_commit_elect(&c.qempty);
+      sm100::mma_commit_elect(&c.s_full[slot]);
+      return true;
+    };
+    auto pv = [&](const Unit& u, int k) -> bool {
+      const int slot = k & 1;
+      const Tile t = tile_of(u, dual ? k >> 1 : k);
+      const int vbs = t.ctx ? BS : 16;
+      const int nv = (t.nk + kVT - 1) / kVT;
+      const bool fresh = !dual || slot == 0, done = !dual || slot == 1;
+      if (fresh) {
+        gv = g;
+        g += nv;
+      }
+      if (kChain && k == 0 && un > 1 &&
+          !__all_sync(kAll, sm100::mbar_wait(&c.o_free, un & 1, budget, abort_flag)))
+        return false;
+      if (!__all_sync(kAll, sm100::mbar_wait(&c.p_ready[slot], steps[slot] & 1, budget,
+                                             abort_flag)))
+        return false;
+      sm100::tc_fence_after();
+      ++steps[slot];
+      const uint32_t o = tmem + kOCol + (kChain ? 0 : slot * 128);
+      const bool first = kChain ? k == 0 : k < 2;
+      for (int v = 0; v < nv; ++v) {
+        if (fresh && !wait_full(gv + v)) return false;
+        const uint32_t st = ring_base + ((gv + v) % NST) * kStage;
+        const int toks = min(kVT, t.nk - v * kVT);
+        for (int r = 0; r < toks; r += 16) {
+          const uint32_t at = tmem + slot * kTile + (v * kVT + r) / 2;
+          const uint64_t bd = sm100::smem_desc(st + (r / vbs) * vbs * D * 2 + (r % vbs) * 128,
+                                               vbs * 128, 1024, sm100::kSw128);
+          sm100::mma_f16_ts_elect(o, at, bd, id_pv, !first || (v | r) != 0);
+        }
+        if (done) sm100::mma_commit_elect(&c.empty[(gv + v) % NST]);
+      }
+      sm100::mma_commit_elect(&c.o_done[slot]);
+      return true;
+    };
+
+    Walk wk = walk_begin();
+    Unit u;
+    while (ok && walk_next<kPrefix>(a, before, total_groups, wk, u)) {
+      ok = __all_sync(kAll, sm100::mbar_wait(&c.qfull, un & 1, budget, abort_flag));
+      if (!ok) break;
+      ++un;
+      sm100::tc_fence_after();
+      const int K = dual ? 2 * u.tiles : u.tiles;
+      for (int k = 0; k < K && ok; ++k) {
+        ok = qk(k, k == K - 1);
+        if (ok && k > 0) ok = pv(u, k - 1);
+      }
+      if (ok) ok = pv(u, K - 1);
+    }
+    if (!ok) {
+      if (lane == 0) c.abort = 1;
+      // no MMA may still be running when tensor memory is released
+      sm100::mma_commit_elect(&c.drain);
+      sm100::mbar_wait(&c.drain, 0, budget, nullptr);
+    }
+    __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ========================= softmax + epilogue =================================
+    // Slot = warpgroup; thread r of it owns row r of the slot's row tile
+    // (tensor-memory lane r).  Every thread runs the same iterations and
+    // barriers whatever happens; a failed wait only marks the abort, which
+    // ends later waits.
+    const int slot = warp >> 2;
+    const int r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t sbuf = tmem + lane_base + slot * kTile;
+    const uint32_t obuf = tmem + lane_base + kOCol + (kChain ? 0 : slot * 128);
+    const float sl2 = a.scale_log2;
+    uint32_t done[2] = {0, 0};  // steps of each slot in the units before
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!sm100::mbar_wait(bar, parity & 1, budget, abort_flag)) c.abort = 1;
+    };
+    // token and head of this row within the unit
+    const int tile = dual ? slot : 0;
+    const int tok = r / a.group, head = r - tok * a.group;
+    const bool row_in = tok < a.row_tokens;
+    Walk wk = walk_begin();
+    Unit u;
+    while (walk_next<kPrefix>(a, before, total_groups, wk, u)) {
+      const int K = dual ? 2 * u.tiles : u.tiles;
+      const int32_t i = u.i0 + tile * a.row_tokens + tok;
+      const bool row_ok = row_in && i < u.n;
+      // window of the row (rows that are not stored take the first one's)
+      const int32_t p = u.ctx + (row_ok ? i : u.i0);
+      const int32_t lo = p - a.window + 1;
+      float m_ref = -INFINITY, lsum = 0.f;
+      bool bad = u.poison;
+      for (int k = slot; k < K; k += 2) {
+        const Tile t = tile_of(u, dual ? k >> 1 : k);
+        // a context block outside the pool poisons the unit (blocks that no
+        // row sees are not looked at); tested after P is written
+        int32_t blk_id = 0;
+        if (t.ctx && lane < (t.nk + BS - 1) / BS) {
+          const int32_t bp = t.pos0 + lane * BS;
+          if (kPrefix || bp < a.num_sinks || bp + BS > u.lo_min)
+            blk_id = __ldg(a.block_tables + static_cast<int64_t>(u.seq) * a.max_blocks_per_seq +
+                           t.pos0 / BS + lane);
+        }
+        wait(&c.s_full[slot], done[slot] + (k >> 1));
+        sm100::tc_fence_after();
+        __syncwarp();
+        float s[kTile];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(sbuf + 32 * q, s + 32 * q);
+        sm100::tmem_wait_ld();
+        // rows see all of the tile, or the keys of a mask
+        const bool whole =
+            kPrefix ? t.nk == kTile
+                    : t.nk == kTile && t.pos0 + kTile - 1 <= u.ctx + u.i0 &&
+                          (t.pos0 >= u.pmax - a.window + 1 || t.pos0 + kTile <= a.num_sinks);
+        if (!whole) {
+          const int hi = kPrefix ? t.nk : min(t.nk, p - t.pos0 + 1);
+          const int from = kPrefix ? 0 : lo - t.pos0;
+          const int sk = kPrefix ? 0 : a.num_sinks - t.pos0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t bits = range_bits(0, hi, 32 * q) &
+                                  (range_bits(from, kTile, 32 * q) | range_bits(0, sk, 32 * q));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1u)) s[32 * q + e] = -INFINITY;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < kTile; e += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], fmaxf(s[e + 2 * x], s[e + 2 * x + 1]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        // the row's reference maximum
+        const float m_old = m_ref;
+        float m_in = m_ref;     // before this step (from the other slot, if handed on)
+        if constexpr (kChain) {
+          if (k > 0) {
+            const int o = slot ^ 1;
+            wait(&c.m_next[o], done[o] + ((k - 1) >> 1));
+            m_in = c.mref[r];
+          }
+        }
+        const bool move = mt > m_in + kRescaleLog2 || (m_in == -INFINITY && mt > -INFINITY);
+        m_ref = move ? mt : m_in;
+        if constexpr (kChain) {
+          c.mref[r] = m_ref;
+          sm100::mbar_arrive(&c.m_next[slot]);
+        }
+        if (m_ref != m_old) lsum *= m_old == -INFINITY ? 0.f : exp2f(m_old - m_ref);
+        const bool has_o = kChain ? k > 0 : k >= 2;
+        if (has_o && __any_sync(kAll, move)) {
+          // the accumulator must hold every step before this one
+          const float corr = move ? (m_in == -INFINITY ? 0.f : exp2f(m_in - m_ref)) : 1.f;
+          const int o = kChain ? slot ^ 1 : slot;
+          wait(&c.o_done[o], done[o] + (kChain ? (k - 1) >> 1 : (k >> 1) - 1));
+          sm100::tc_fence_after();
+          __syncwarp();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            float ov[16];
+            sm100::tmem_ld16(obuf + c0, ov);
+            sm100::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] *= corr;
+            sm100::tmem_st16(obuf + c0, ov);
+          }
+          sm100::tmem_wait_st();
+        }
+        // p = 2^(s * scale * log2(e) - m), two keys per 32-bit column over the
+        // logits this thread has read
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = ex2_approx(fmaf(s[32 * q + e], sl2, neg_m));
+            const float p1 = ex2_approx(fmaf(s[32 * q + e + 1], sl2, neg_m));
+            add[(e >> 1) & 3] += p0 + p1;
+            w[e / 2] = __uint_as_float(pack16(p0, p1, static_cast<T*>(nullptr)));
+          }
+          sm100::tmem_st16(sbuf + 16 * q, w);
+        }
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        sm100::mbar_arrive(&c.p_ready[slot]);
+        lsum += (add[0] + add[1]) + (add[2] + add[3]);
+        bad |= __any_sync(kAll, blk_id < 0 || blk_id >= a.num_blocks) != 0;
+      }
+      // ---- epilogue: the row's accumulator over its sum ----------------------------
+      const int mine = slot == 0 ? (K + 1) >> 1 : K >> 1;  // this slot's steps
+      float total = lsum, m_end = m_ref;
+      int c_lo = 0, c_hi = D;
+      if constexpr (kChain) {
+        // both slots' sums at the last reference; each slot stores half the columns
+        sync256();
+        m_end = c.mref[r];
+        if (m_end != m_ref) lsum *= m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_end);
+        c.lsum[slot][r] = bad ? qnan() : lsum;
+        sync256();
+        total = c.lsum[0][r] + c.lsum[1][r];
+        bad |= isnan(total);
+        c_lo = slot * (D / 2);
+        c_hi = c_lo + D / 2;
+        const int o = (K - 1) & 1;
+        wait(&c.o_done[o], done[o] + ((K - 1) >> 1));
+      } else if (mine > 0) {
+        wait(&c.o_done[slot], done[slot] + mine - 1);
+      }
+      sm100::tc_fence_after();
+      __syncwarp();
+      const bool poison = bad || *abort_flag != 0;
+      const float inv = poison ? qnan() : total > 0.f ? 1.f / total : 0.f;
+      const int64_t orow = (u.row0 + i) * a.num_heads + u.kvh * a.group + head;
+      const bool empty = !kChain && mine == 0;
+      int64_t at = orow;
+      if constexpr (kPrefix) at = orow * a.num_parts + (D == 128 && !dual ? 2 * u.part + slot : u.part);
+#pragma unroll 1
+      for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
+        float ov[16];
+        sm100::tmem_ld16(obuf + c0, ov);
+        sm100::tmem_wait_ld();
+        if (row_ok) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ov[e] = empty ? 0.f : ov[e] * inv;
+          if constexpr (kPrefix)
+            store_row16(a.part_out, at * D + c0, PA_F32, ov);
+          else
+            store_row16(a.out, at * D + c0, a.out_dtype, ov);
+        }
+      }
+      if constexpr (kPrefix) {
+        if (row_ok && c_lo == 0) {
+          a.part_max[at] = poison ? qnan() : m_end * kLn2;
+          a.part_sum[at] = total;
+          if (poison) set_status(a.status, *abort_flag ? PA_ERR_DEVICE_TIMEOUT : PA_ERR_BAD_BLOCK_ID);
+        }
+      }
+      sm100::tc_fence_before();
+      if constexpr (kChain) sm100::mbar_arrive(&c.o_free);
+      done[0] += (K + 1) >> 1;
+      done[1] += K >> 1;
+    }
+  }
+
+  // ---- teardown -------------------------------------------------------------------
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  if (warp == kMmaWarp) sm100::tmem_dealloc(tmem, kTmemCols);
+  // the join, a dependent of this grid, reads what the pass before it wrote
+  if constexpr (kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Persistent launch: one CTA per SM (it takes nearly all shared memory and all
+// tensor-memory columns).
+template <typename T, int D, int BS, bool kPrefix>
+cudaError_t launch_rows_v(const RowsArgs& a, const CUtensorMap (&m)[5], int grid, bool pdl,
+                          cudaStream_t s) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  auto kern = pa_rows_kernel<T, D, BS, kPrefix>;
+  // set once per device; concurrent first calls set the same attribute
+  static std::atomic<bool> configured[128];
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             rw::Layout<D>::kSmem))
+      return e;
+    configured[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(rw::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = rw::Layout<D>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  const long long budget = a.selftest_stall ? rw::kSelftestBudget : rw::kWaitBudget;
+  return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1], m[2], m[3], m[4], budget);
+}
+
+template <typename T, bool kPrefix>
+cudaError_t launch_rows_t(const RowsArgs& a, const CUtensorMap (&m)[5], int grid, bool pdl,
+                          cudaStream_t s) {
+  if (a.head_dim == 256 && a.block_size == 16)
+    return launch_rows_v<T, 256, 16, kPrefix>(a, m, grid, pdl, s);
+  if (a.head_dim == 256 && a.block_size == 32)
+    return launch_rows_v<T, 256, 32, kPrefix>(a, m, grid, pdl, s);
+  if (a.head_dim == 128 && a.block_size == 16)
+    return launch_rows_v<T, 128, 16, kPrefix>(a, m, grid, pdl, s);
+  if (a.head_dim == 128 && a.block_size == 32)
+    return launch_rows_v<T, 128, 32, kPrefix>(a, m, grid, pdl, s);
+  if (a.head_dim == 128 && a.block_size == 64)
+    return launch_rows_v<T, 128, 64, kPrefix>(a, m, grid, pdl, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -1,0 +1,11 @@
+// pa_rows_prefix_bf16.cu -- bf16 instantiations of the row attention kernel (prefix).
+#include "pa_rows.cuh"
+
+namespace pa {
+
+cudaError_t launch_rows_prefix_bf16(const RowsArgs& a, const CUtensorMap (&m)[5], int grid, bool pdl,
+                                cudaStream_t s) {
+  return launch_rows_t<__nv_bfloat16, true>(a, m, grid, pdl, s);
+}
+
+}  // namespace pa

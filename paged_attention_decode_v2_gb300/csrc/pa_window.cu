@@ -134,7 +134,7 @@ pa_status_t pa_decode_window(const pa_params_t* p, const pa_window_t* window, co
   j.head_dim = p->head_dim;
   j.group = a.group;
   j.out_dtype = p->out_dtype;
-  return launch_join(j, stream, false) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch_join(j, stream, true) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status_t pa_prefill_window(const pa_prefill_params_t* p, const pa_window_t* window,
@@ -172,6 +172,39 @@ pa_status_t pa_prefill_window(const pa_prefill_params_t* p, const pa_window_t* w
   if (!aligned(block_tables, 4) || !aligned(query_start, 4) || !aligned(ctx_lens, 4))
     return PA_ERR_MISALIGNED;
   const pa_window_t w = clamped(window, p->max_ctx_len + p->max_query_len);
+  const int sms = (p->flags & (PA_FLAG_PORTABLE | PA_FLAG_SPLIT_X))
+                      ? 0
+                      : rows_applicable(p->kv_dtype, p->num_heads, p->num_kv_heads, p->head_dim,
+                                        p->block_size, p->num_blocks, p->total_tokens, p->scale);
+  if (sms > 0) {
+    RowsArgs a{};
+    a.block_tables = block_tables;
+    a.query_start = query_start;
+    a.lens = ctx_lens;
+    a.out = out;
+    a.num_seqs = p->num_seqs;
+    a.num_heads = p->num_heads;
+    a.num_kv_heads = p->num_kv_heads;
+    a.head_dim = p->head_dim;
+    a.block_size = p->block_size;
+    a.num_blocks = p->num_blocks;
+    a.max_blocks_per_seq = p->max_blocks_per_seq;
+    a.num_tokens = p->total_tokens;
+    a.max_query_len = p->max_query_len;
+    a.max_ctx_len = p->max_ctx_len;
+    a.window = w.window;
+    a.num_sinks = w.num_sinks;
+    a.group = p->num_heads / p->num_kv_heads;
+    a.row_tokens = 128 / a.group;
+    a.dual = p->head_dim == 128;
+    a.group_tokens = a.row_tokens * (a.dual ? 2 : 1);
+    a.row_groups = (p->max_query_len + a.group_tokens - 1) / a.group_tokens;
+    a.out_dtype = p->out_dtype;
+    a.selftest_stall = (p->flags & PA_FLAG_SELFTEST_STALL) ? 1 : 0;
+    a.scale_log2 = p->scale * 1.442695040888963407360f;
+    const RowsTensors x{q, k, v, k_cache, v_cache};
+    return launch_rows(a, p->kv_dtype, x, sms, false, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
 
   ListArgs a{};
   a.q = q;
