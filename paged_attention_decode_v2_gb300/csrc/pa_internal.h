@@ -43,6 +43,9 @@ struct KernelArgs {
                            // straight into out) and the reduce skips its rows
   int32_t fused;           // V2 in one launch: the pass-1 grid runs pass 2 itself
                            // after its streaming (pa_grid_reduce.cuh)
+  int32_t window;          // > 0: windowed decode (pa_span.cuh), with
+  int32_t num_sinks;       //   this many sinks, and
+  int32_t max_list;        //   block lists of at most this many tokens
 };
 
 // The workspace starts with a control block of fixed size: the status word,

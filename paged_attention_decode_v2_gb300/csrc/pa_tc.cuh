@@ -39,6 +39,13 @@
 // with whole tiles staged by bulk asynchronous copies (the SM90+ tier of the
 // same page's BlockLoadToShared notes) and the dot products on tensor cores.
 //
+// Windowed decode (kWin).  The item's range runs over the sequence's block
+// list instead of its tokens: the blocks that hold a sink or a token of the
+// window (pa_span.cuh).  Token places, chunks and tiles are list places; only
+// the block-table entry of a list block is shifted, and the list's unseen run
+// is masked in the softmax and its value rows are cleared like those past the
+// end (0 * NaN would be NaN).
+//
 // Every wait is bounded.  A wait that gives up sets the status word to
 // PA_ERR_DEVICE_TIMEOUT and an abort flag that ends every other wait at
 // once; issued copies and MMAs are drained (again with a bound) before
@@ -54,6 +61,7 @@
 #include "pa_device.cuh"
 #include "pa_grid_reduce.cuh"
 #include "pa_sm100.cuh"
+#include "pa_span.cuh"
 
 namespace pa {
 
@@ -123,6 +131,8 @@ struct Item {
   int32_t t0, t1;  // this CTA's token range; empty when t0 >= t1
   bool len_ok;     // 0 <= seq_len <= max_seq_len
   bool any;        // the item's whole range (over all CTAs of a cluster) has tokens
+  int32_t sinks, shift;  // windowed: list blocks from `sinks` on are shifted by this
+  int32_t h0, h1;        // windowed: list tokens that are not seen
   bool direct;     // V2 with single_direct: the sequence fits this one partition, so
                    // the item's result is the final output (written straight to out)
 };
@@ -159,16 +169,28 @@ __device__ __forceinline__ Item item_coords(const KernelArgs& a, const int32_t* 
   it.len_ok = false;
   it.any = false;
   it.direct = false;
+  it.sinks = it.shift = it.h0 = it.h1 = 0;
   return it;
 }
 
 // The item's token range, given its sequence's length L, and the share of
 // it that CTA `rank` of a cluster of `cs` CTAs streams: a balanced run of
 // the range's 128-token tiles (the whole range when cs == 1).
+template <bool kWin>
 __device__ __forceinline__ void item_range(const KernelArgs& a, Item& it, int32_t L, bool v2,
                                            int rank, int cs) {
   it.L = L;
   it.len_ok = seq_len_ok(a, L);
+  if constexpr (kWin) {
+    if (it.len_ok) {
+      const WindowSpan w = window_span(L, a.window, a.num_sinks, a.block_size);
+      L = w.len;
+      it.sinks = w.sinks;
+      it.shift = w.shift;
+      it.h0 = w.h0;
+      it.h1 = w.h1;
+    }
+  }
   it.t1 = !it.len_ok ? it.t0 : (v2 ? min(L, it.t0 + a.partition_size) : L);
   it.any = it.t0 < it.t1;
   it.direct = v2 && a.single_direct && it.len_ok && L <= a.partition_size;
@@ -180,10 +202,11 @@ __device__ __forceinline__ void item_range(const KernelArgs& a, Item& it, int32_
   }
 }
 
+template <bool kWin>
 __device__ __forceinline__ Item item_at(const KernelArgs& a, const int32_t* prefix, int64_t k,
                                         bool v2, int rank, int cs) {
   Item it = item_coords(a, prefix, k, v2);
-  item_range(a, it, __ldg(a.seq_lens + it.b), v2, rank, cs);
+  item_range<kWin>(a, it, __ldg(a.seq_lens + it.b), v2, rank, cs);
   return it;
 }
 
@@ -198,6 +221,18 @@ __device__ __forceinline__ int32_t load_block_id(const KernelArgs& a, int b, int
              : 0;
 }
 
+// Windowed: the entry of list block c0 / BS + lane of an item whose range is
+// known (lanes past the list: 0, never used).
+template <int BS>
+__device__ __forceinline__ int32_t load_list_id(const KernelArgs& a, const Item& it, int c0,
+                                                int lane) {
+  int idx = c0 / BS + lane;
+  if (idx >= it.sinks) idx += it.shift;
+  return idx < a.max_blocks_per_seq
+             ? __ldg(a.block_tables + static_cast<int64_t>(it.b) * a.max_blocks_per_seq + idx)
+             : 0;
+}
+
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ void fail(Ctrl& c, int32_t* status) {
@@ -208,7 +243,7 @@ __device__ __forceinline__ void fail(Ctrl& c, int32_t* status) {
 
 }  // namespace tc
 
-template <typename T, int D, int BS, bool kV2, int NST, int CPS>
+template <typename T, int D, int BS, bool kV2, int NST, int CPS, bool kWin>
 __global__ void __launch_bounds__(tc::kThreads, CPS)
     pa_tc_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap,
@@ -251,7 +286,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
   // set-up writes: its length and first block ids are loaded now, so the
   // load latency overlaps the set-up below.
   int32_t pre_L = 0, pre_raw = 0;
-  const bool pre = warp == 4 && !compact && cid < grid_items;
+  const bool pre = !kWin && warp == 4 && !compact && cid < grid_items;
   if (pre) {
     const Item it0 = item_coords(a, nullptr, cid, kV2);
     pre_L = __ldg(a.seq_lens + it0.b);
@@ -279,7 +314,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
     c.abort = 0;
     // one-launch V2: the counters are usable only in an initialised workspace;
     // the CTA counts itself started (the result is first used at the end)
-    if (kV2 && a.fused) {
+    if (kV2 && !kWin && a.fused) {
       sm100::mbar_init(&c.red_bar, 1);
       c.ws_ok = __ldcg(a.status + kMarkerOffset / 4) == kMarker;
       if (c.ws_ok)
@@ -293,7 +328,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
     sm100::tmem_relinquish();
   }
   if (warp == 4 && lane == 0) {
-    if (kV2 && a.fused) sm100::tma_prefetch_desc(&pmap);
+    if (kV2 && !kWin && a.fused) sm100::tma_prefetch_desc(&pmap);
     sm100::tma_prefetch_desc(&kmap);
     sm100::tma_prefetch_desc(&vmap);
     sm100::tma_prefetch_desc(&qmap);
@@ -310,7 +345,8 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
       if (b < a.num_seqs) {
         const int32_t L = __ldg(a.seq_lens + b);
         if (seq_len_ok(a, L))
-          n = (L + a.partition_size - 1) / a.partition_size;
+          n = ((kWin ? window_span(L, a.window, a.num_sinks, BS).len : L) + a.partition_size - 1) /
+              a.partition_size;
         else if (blockIdx.x == 0)
           set_status(a.status, PA_ERR_BAD_SEQ_LEN);
       }
@@ -362,7 +398,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
     // next chunk are loaded while the current one streams.
     auto next_active = [&](int64_t k, Item& it) -> int64_t {
       for (; k < total_items; k += stride) {
-        it = item_at(a, prefix, k, kV2, rank, cs);
+        it = item_at<kWin>(a, prefix, k, kV2, rank, cs);
         if (it.t0 < it.t1) return k;
       }
       return total_items;
@@ -385,13 +421,20 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
     if (k < total_items) {
       it = item_coords(a, prefix, k, kV2);
       const int32_t L = pre ? pre_L : __ldg(a.seq_lens + it.b);
-      const int32_t t_spec = it.t0;
-      raw = pre ? pre_raw : load_block_id<BS>(a, it.b, t_spec, lane);
-      item_range(a, it, L, kV2, rank, cs);
-      if (it.t0 < it.t1 && it.t0 != t_spec) raw = load_block_id<BS>(a, it.b, it.t0, lane);
-      if (it.t0 >= it.t1) {
-        k = next_active(k + stride, it);
-        if (k < total_items) raw = load_block_id<BS>(a, it.b, it.t0, lane);
+      if constexpr (kWin) {
+        // which blocks the list holds follows from the length
+        item_range<kWin>(a, it, L, kV2, rank, cs);
+        if (it.t0 >= it.t1) k = next_active(k + stride, it);
+        if (k < total_items) raw = load_list_id<BS>(a, it, it.t0, lane);
+      } else {
+        const int32_t t_spec = it.t0;
+        raw = pre ? pre_raw : load_block_id<BS>(a, it.b, t_spec, lane);
+        item_range<kWin>(a, it, L, kV2, rank, cs);
+        if (it.t0 < it.t1 && it.t0 != t_spec) raw = load_block_id<BS>(a, it.b, it.t0, lane);
+        if (it.t0 >= it.t1) {
+          k = next_active(k + stride, it);
+          if (k < total_items) raw = load_block_id<BS>(a, it.b, it.t0, lane);
+        }
       }
     }
     int ci = 0;
@@ -413,6 +456,10 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
                              it.b * Hq + it.kvh * G, keep);
         ++qn;
       }
+      // windowed: the next item's length, ahead of its block ids
+      int32_t L_ahead = 0;
+      if (kWin && ci == nchunks - 1 && k + stride < total_items)
+        L_ahead = __ldg(a.seq_lens + item_coords(a, prefix, k + stride, kV2).b);
       const bool tail_fix = (it.t1 % 16) != 0;
       const int c0 = it.t0 + ci * kChunk;
       const int n = min(kChunk, it.t1 - c0);
@@ -447,12 +494,15 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
         ci2 = 0;
         if (k2 < total_items) {
           it2 = item_coords(a, prefix, k2, kV2);
-          L2 = __ldg(a.seq_lens + it2.b);
+          L2 = kWin ? L_ahead : __ldg(a.seq_lens + it2.b);
+          if constexpr (kWin) item_range<kWin>(a, it2, L2, kV2, rank, cs);
         }
       }
       int32_t raw2 = 0;
       const int32_t t2_spec = it2.t0 + ci2 * kChunk;
-      if (k2 < total_items) raw2 = load_block_id<BS>(a, it2.b, t2_spec, lane);
+      if (k2 < total_items)
+        raw2 = kWin ? load_list_id<BS>(a, it2, t2_spec, lane)
+                    : load_block_id<BS>(a, it2.b, t2_spec, lane);
       const int nv = (n + Lay::kVTokens - 1) / Lay::kVTokens;
       for (int v = 0; v < nv && ok; ++v) {
         const int jb0 = v * Lay::kVTokens / BS;
@@ -464,7 +514,15 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
         // 16-token MMA step, lands on the producer's own barrier first: the
         // rows past the end are cleared (P^T is zero there, but 0 * NaN
         // would be NaN) and only then is the stage handed to the MMA warp.
-        const bool tail = tail_fix && ci == nchunks - 1 && v == nv - 1;
+        bool tail = tail_fix && ci == nchunks - 1 && v == nv - 1;
+        // windowed: the stage's part of the list's unseen run, cleared too
+        int u0 = 0, u1 = 0;
+        if constexpr (kWin) {
+          u0 = max(it.h0 - c0 - v * Lay::kVTokens, 0);
+          u1 = min(min(it.h1 - c0, n) - v * Lay::kVTokens, Lay::kVTokens);
+          u1 = max(u0, u1);
+          tail = tail || u0 < u1;
+        }
         uint64_t* land = tail ? &c.tail : &c.full[slot];
         if (lane == 0) sm100::mbar_arrive_expect_tx(land, (jb1 - jb0) * BS * D * 2);
         __syncwarp();
@@ -479,13 +537,15 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
           if (!ok) break;
           ++tn;
           tail_pending = -1;
-          const int r0 = n - v * Lay::kVTokens;  // first row past the end
+          int r0 = n - v * Lay::kVTokens;  // first row past the end
+          if (kWin) r0 = min(r0, Lay::kVTokens);
           const int r1 = (r0 + 15) / 16 * 16;    // end of its 16-token step
           uint8_t* st = ring + slot * kStageBytes;
-          const int pieces = (r1 - r0) * Lay::kSlices * 8;  // 16-byte pieces
+          const int pieces = (r1 - r0 + u1 - u0) * Lay::kSlices * 8;  // 16-byte pieces
           for (int i = lane; i < pieces; i += 32) {
             const int line = i / 8, piece = i % 8;
-            const int r = r0 + line / Lay::kSlices, sl = line % Lay::kSlices;
+            const int x = line / Lay::kSlices, sl = line % Lay::kSlices;
+            const int r = !kWin || x < r1 - r0 ? r0 + x : u0 + x - (r1 - r0);
             *reinterpret_cast<uint4*>(st + (r / BS) * BS * D * 2 + sl * BS * 128 + (r % BS) * 128 +
                                       piece * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -495,11 +555,16 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
         }
       }
       if (!same_item && k2 < total_items) {
-        item_range(a, it2, L2, kV2, rank, cs);
-        if (it2.t0 < it2.t1 && it2.t0 != t2_spec) raw2 = load_block_id<BS>(a, it2.b, it2.t0, lane);
+        if constexpr (!kWin) {
+          item_range<kWin>(a, it2, L2, kV2, rank, cs);
+          if (it2.t0 < it2.t1 && it2.t0 != t2_spec)
+            raw2 = load_block_id<BS>(a, it2.b, it2.t0, lane);
+        }
         if (it2.t0 >= it2.t1) {  // an empty item: find the next one with tokens
           k2 = next_active(k2 + stride, it2);
-          if (k2 < total_items) raw2 = load_block_id<BS>(a, it2.b, it2.t0, lane);
+          if (k2 < total_items)
+            raw2 = kWin ? load_list_id<BS>(a, it2, it2.t0, lane)
+                        : load_block_id<BS>(a, it2.b, it2.t0, lane);
         }
       }
       k = k2;
@@ -536,7 +601,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
       // wait runs out and the abort path is exercised
       if (a.selftest_stall) ok = __all_sync(kAll, sm100::mbar_wait(&c.never, 0, budget, abort_flag));
       for (int64_t k = cid; k < total_items && ok; k += stride) {
-        const Item it = item_at(a, prefix, k, kV2, rank, cs);
+        const Item it = item_at<kWin>(a, prefix, k, kV2, rank, cs);
         if (it.t0 >= it.t1) continue;
         const int qb = qn & 1;
         ok = __all_sync(kAll, sm100::mbar_wait(&c.qfull[qb], (qn >> 1) & 1, budget, abort_flag));
@@ -696,7 +761,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
     // effects, scratch in the still unused P^T buffer), while the first keys
     // land, so its code is in the instruction cache when the reduce runs.
     static_assert(gridred::kDryBytes <= (kChunk / 16) * 512, "dry run within the P^T buffer");
-    if (kV2 && !kClusters && a.fused && c.ws_ok) {
+    if (kV2 && !kClusters && !kWin && a.fused && c.ws_ok) {
       uint32_t dry_phase = 0;
       gridred::grid_reduce<D>(a, true, started, c.red_word,
                               *reinterpret_cast<gridred::UnitScratch*>(pt), &pmap, &c.red_bar,
@@ -707,7 +772,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
     }
     uint32_t cc = 0, ic = 0;  // chunks / cluster combines so far
     for (int64_t k = cid; k < total_items; k += stride) {
-      const Item it = item_at(a, prefix, k, kV2, rank, cs);
+      const Item it = item_at<kWin>(a, prefix, k, kV2, rank, cs);
       const int64_t row0 = static_cast<int64_t>(it.b) * Hq + it.kvh * G;
       if (!it.any) {  // nothing to attend to in the whole item
         if (rank == 0) {
@@ -740,7 +805,9 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
           const int nblk = (n + BS - 1) / BS;
           bool bl = false;
           if (lane < nblk) {
-            const int32_t id = __ldg(bt + c0 / BS + lane);
+            int idx = c0 / BS + lane;
+            if (kWin && idx >= it.sinks) idx += it.shift;
+            const int32_t id = __ldg(bt + idx);
             bl = id < 0 || id >= a.num_blocks;
           }
           bad |= __any_sync(0xffffffffu, bl);
@@ -755,7 +822,9 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
           float s[16];
           sm100::tmem_ld16(tmem + lane_base + tt * 16, s);
           sm100::tmem_wait_ld();
-          if (tt * kTile + r < n) {
+          // windowed: list tokens between the sinks and the window are not seen
+          const int lt = c0 + tt * kTile + r;
+          if (tt * kTile + r < n && !(kWin && lt >= it.h0 && lt < it.h1)) {
 #pragma unroll
             for (int h = 0; h < 8; ++h)
               if (h < G) mx[h] = fmaxf(mx[h], s[h] * sl2);
@@ -782,7 +851,8 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
           sm100::tmem_wait_ld();
           const int tok = tt * kTile + r;
           if (tok < n16) {
-            const bool valid = tok < n;
+            const bool valid =
+                tok < n && !(kWin && c0 + tok >= it.h0 && c0 + tok < it.h1);
             // P^T element (tok, col): 16-token step, 8-token core, column
             // group col / 8, column col % 8, token tok % 8 (no-swizzle
             // K-major core matrices of 8 x 16 bytes)
@@ -881,7 +951,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
   // CTA has stored its partials; the ring is free scratch now
   static_assert(sizeof(gridred::UnitScratch) <= NST * kStageBytes, "reduce scratch in the ring");
   static_assert(alignof(gridred::UnitScratch) <= 1024, "the ring starts 1024-byte aligned");
-  if (kV2 && !kClusters && a.fused && warp < 4)
+  if (kV2 && !kClusters && !kWin && a.fused && warp < 4)
     gridred::grid_reduce<D>(a, c.ws_ok != 0, started, c.red_word,
                             *reinterpret_cast<gridred::UnitScratch*>(ring), &pmap, &c.red_bar, tid,
                             budget, false);
@@ -891,12 +961,12 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
 
 // Kernel attributes, set once per device: the dynamic shared memory, and for
 // the one-CTA-per-SM variant clusters of up to 16 CTAs.
-template <typename T, int D, int BS, bool V2, int NST, int CPS>
+template <typename T, int D, int BS, bool V2, int NST, int CPS, bool kWin>
 cudaError_t configure_tc(int dev) {
   // set once per device; concurrent first calls set the same attributes
   static std::atomic<bool> configured[128];
   if (configured[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  auto kern = pa_tc_kernel<T, D, BS, V2, NST, CPS>;
+  auto kern = pa_tc_kernel<T, D, BS, V2, NST, CPS, kWin>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        tc::Layout<D, NST>::kSmemCompact);
   if (e == cudaSuccess && NST == tc::kDeepStages)
@@ -905,18 +975,18 @@ cudaError_t configure_tc(int dev) {
   return e;
 }
 
-template <typename T, int D, int BS, bool V2, int NST, int CPS>
+template <typename T, int D, int BS, bool V2, int NST, int CPS, bool kWin>
 cudaError_t launch_tc_variant(const KernelArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                               const CUtensorMap& qm, const CUtensorMap& pm, int64_t items,
                               unsigned grid, int compact, int cs, cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-  auto kern = pa_tc_kernel<T, D, BS, V2, NST, CPS>;
+  auto kern = pa_tc_kernel<T, D, BS, V2, NST, CPS, kWin>;
   using Lay = tc::Layout<D, NST>;
   // the compact work list's prefix table only takes shared memory when used,
   // which leaves room on each SM for the reduce kernel's waiting CTAs
   const int smem = compact ? Lay::kSmemCompact : Lay::kSmem;
-  if (cudaError_t e = configure_tc<T, D, BS, V2, NST, CPS>(dev)) return e;
+  if (cudaError_t e = configure_tc<T, D, BS, V2, NST, CPS, kWin>(dev)) return e;
   const long long budget = a.selftest_stall ? tc::kSelftestWaitBudget : tc::kDefaultWaitBudget;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
@@ -936,14 +1006,14 @@ cudaError_t launch_tc_variant(const KernelArgs& a, const CUtensorMap& km, const 
 // Largest cluster size <= want (a power of two) of which at least `need`
 // clusters of the one-CTA-per-SM variant can be resident at once.  The
 // resident-cluster counts are queried once per device and size.
-template <typename T, int D, int BS, bool V2>
+template <typename T, int D, int BS, bool V2, bool kWin>
 int fit_cluster(int want, int64_t need) {
   // [device][log2 size], 0 = not queried yet; concurrent first calls store the same count
   static std::atomic<int> resident[128][5];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 1;
-  if (configure_tc<T, D, BS, V2, tc::kDeepStages, 1>(dev) != cudaSuccess) return 1;
-  auto kern = pa_tc_kernel<T, D, BS, V2, tc::kDeepStages, 1>;
+  if (configure_tc<T, D, BS, V2, tc::kDeepStages, 1, kWin>(dev) != cudaSuccess) return 1;
+  auto kern = pa_tc_kernel<T, D, BS, V2, tc::kDeepStages, 1, kWin>;
   int lg = 0;
   while ((2 << lg) <= want && lg < 4) ++lg;  // log2 of the largest power of two <= want
   for (; lg >= 1; --lg) {
@@ -974,7 +1044,7 @@ int fit_cluster(int want, int64_t need) {
   return 1;
 }
 
-template <typename T, int D, int BS>
+template <typename T, int D, int BS, bool kWin>
 cudaError_t launch_tc_t(const KernelArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                         const CUtensorMap& qm, const CUtensorMap& pm, bool v2, int num_sms,
                         cudaStream_t s) {
@@ -990,39 +1060,40 @@ cudaError_t launch_tc_t(const KernelArgs& a, const CUtensorMap& km, const CUtens
     // that split its 128-token tiles and merge their partial results -- as
     // long as every CTA keeps at least four tiles (512 tokens), below which
     // the merge costs more than the split saves.
-    const int range = v2 ? std::min(a.partition_size, a.max_seq_len) : a.max_seq_len;
+    const int longest = kWin ? a.max_list : a.max_seq_len;
+    const int range = v2 ? std::min(a.partition_size, longest) : longest;
     const int tiles = (range + tc::kTile - 1) / tc::kTile;
     int want = 1;
     while (want < 16 && items * want * 2 <= num_sms && want * 2 * 4 <= tiles) want *= 2;
-    const int cs = want > 1 ? (v2 ? fit_cluster<T, D, BS, true>(want, items)
-                                  : fit_cluster<T, D, BS, false>(want, items))
+    const int cs = want > 1 ? (v2 ? fit_cluster<T, D, BS, true, kWin>(want, items)
+                                  : fit_cluster<T, D, BS, false, kWin>(want, items))
                             : 1;
     const unsigned grid = static_cast<unsigned>(items * cs);
-    return v2 ? launch_tc_variant<T, D, BS, true, tc::kDeepStages, 1>(a, km, vm, qm, pm, items, grid, compact, cs, s)
-              : launch_tc_variant<T, D, BS, false, tc::kDeepStages, 1>(a, km, vm, qm, pm, items, grid, compact, cs,
+    return v2 ? launch_tc_variant<T, D, BS, true, tc::kDeepStages, 1, kWin>(a, km, vm, qm, pm, items, grid, compact, cs, s)
+              : launch_tc_variant<T, D, BS, false, tc::kDeepStages, 1, kWin>(a, km, vm, qm, pm, items, grid, compact, cs,
                                                           s);
   }
   // Persistent grid: at most two CTAs per SM, every CTA doing the same number
   // of rounds when the items are all the same size (tc_persistent_grid).
   const unsigned grid = static_cast<unsigned>(persistent);
-  return v2 ? launch_tc_variant<T, D, BS, true, 5, 2>(a, km, vm, qm, pm, items, grid, compact, 1, s)
-            : launch_tc_variant<T, D, BS, false, 5, 2>(a, km, vm, qm, pm, items, grid, compact, 1, s);
+  return v2 ? launch_tc_variant<T, D, BS, true, 5, 2, kWin>(a, km, vm, qm, pm, items, grid, compact, 1, s)
+            : launch_tc_variant<T, D, BS, false, 5, 2, kWin>(a, km, vm, qm, pm, items, grid, compact, 1, s);
 }
 
-template <typename T>
+template <typename T, bool kWin>
 cudaError_t launch_tc_dtype(const KernelArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                             const CUtensorMap& qm, const CUtensorMap& pm, bool v2, int num_sms,
                             cudaStream_t s) {
   if (a.head_dim == 256 && a.block_size == 16)
-    return launch_tc_t<T, 256, 16>(a, km, vm, qm, pm, v2, num_sms, s);
+    return launch_tc_t<T, 256, 16, kWin>(a, km, vm, qm, pm, v2, num_sms, s);
   if (a.head_dim == 256 && a.block_size == 32)
-    return launch_tc_t<T, 256, 32>(a, km, vm, qm, pm, v2, num_sms, s);
+    return launch_tc_t<T, 256, 32, kWin>(a, km, vm, qm, pm, v2, num_sms, s);
   if (a.head_dim == 128 && a.block_size == 16)
-    return launch_tc_t<T, 128, 16>(a, km, vm, qm, pm, v2, num_sms, s);
+    return launch_tc_t<T, 128, 16, kWin>(a, km, vm, qm, pm, v2, num_sms, s);
   if (a.head_dim == 128 && a.block_size == 32)
-    return launch_tc_t<T, 128, 32>(a, km, vm, qm, pm, v2, num_sms, s);
+    return launch_tc_t<T, 128, 32, kWin>(a, km, vm, qm, pm, v2, num_sms, s);
   if (a.head_dim == 128 && a.block_size == 64)
-    return launch_tc_t<T, 128, 64>(a, km, vm, qm, pm, v2, num_sms, s);
+    return launch_tc_t<T, 128, 64, kWin>(a, km, vm, qm, pm, v2, num_sms, s);
   return cudaErrorInvalidValue;
 }
 

@@ -7,7 +7,7 @@ namespace pa {
 cudaError_t launch_tc_f16(const KernelArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                          const CUtensorMap& qmap, const CUtensorMap& pmap, bool v2, int num_sms,
                          cudaStream_t s) {
-  return launch_tc_dtype<__half>(a, kmap, vmap, qmap, pmap, v2, num_sms, s);
+  return launch_tc_dtype<__half, false>(a, kmap, vmap, qmap, pmap, v2, num_sms, s);
 }
 
 }  // namespace pa

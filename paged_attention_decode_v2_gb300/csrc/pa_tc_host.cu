@@ -26,6 +26,12 @@ cudaError_t launch_tc_bf16(const KernelArgs& a, const CUtensorMap& kmap, const C
 cudaError_t launch_tc_f16(const KernelArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const CUtensorMap& qmap, const CUtensorMap& pmap, bool v2, int num_sms,
                           cudaStream_t s);
+cudaError_t launch_tcw_bf16(const KernelArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                            const CUtensorMap& qmap, const CUtensorMap& pmap, bool v2, int num_sms,
+                            cudaStream_t s);
+cudaError_t launch_tcw_f16(const KernelArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                           const CUtensorMap& qmap, const CUtensorMap& pmap, bool v2, int num_sms,
+                           cudaStream_t s);
 cudaError_t launch_sx_bf16(const KernelArgs& a, const CUtensorMap& pmap, bool v2, cudaStream_t s);
 cudaError_t launch_sx_f16(const KernelArgs& a, const CUtensorMap& pmap, bool v2, cudaStream_t s);
 
@@ -196,6 +202,9 @@ cudaError_t launch_tc(const KernelArgs& a, pa_dtype_t kv, bool v2, cudaStream_t 
   CUtensorMap pmap = qmap;
   if (a.fused && !encode_partials_map(enc, a, &pmap)) return cudaErrorInvalidValue;
   const int sms = device_info().num_sms;
+  if (a.window > 0)
+    return kv == PA_BF16 ? launch_tcw_bf16(a, kmap, vmap, qmap, pmap, v2, sms, s)
+                         : launch_tcw_f16(a, kmap, vmap, qmap, pmap, v2, sms, s);
   return kv == PA_BF16 ? launch_tc_bf16(a, kmap, vmap, qmap, pmap, v2, sms, s)
                        : launch_tc_f16(a, kmap, vmap, qmap, pmap, v2, sms, s);
 }

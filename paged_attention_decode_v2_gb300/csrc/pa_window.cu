@@ -80,6 +80,44 @@ pa_status_t pa_decode_window(const pa_params_t* p, const pa_window_t* window, co
   float* part_sum = reinterpret_cast<float*>(base + lay.exp_sums_off);
   float* part_out = reinterpret_cast<float*>(base + lay.tmp_out_off);
 
+  JoinArgs j{};
+  JoinList& l = j.list[0];
+  l.m = part_max;
+  l.s = part_sum;
+  l.o = part_out;
+  l.lens = seq_lens;
+  l.max_len = p->max_seq_len;
+  l.part_size = p->partition_size;
+  l.window = w.window;
+  l.num_sinks = w.num_sinks;
+  l.block_size = p->block_size;
+  j.out = out;
+  j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;
+  j.num_heads = p->num_heads;
+  j.head_dim = p->head_dim;
+  j.group = p->num_heads / p->num_kv_heads;
+  j.out_dtype = p->out_dtype;
+
+  if (tc_applicable(p)) {
+    KernelArgs a = make_args(p, q, k_cache, v_cache, block_tables, seq_lens, out);
+    a.status = reinterpret_cast<int32_t*>(base);
+    a.max_logits = part_max;
+    a.exp_sums = part_sum;
+    a.tmp_out = part_out;
+    a.window = w.window;
+    a.num_sinks = w.num_sinks;
+    a.max_list = static_cast<int32_t>(
+        window_max_len(p->max_seq_len, w.window, w.num_sinks, p->block_size));
+    const int64_t parts = parts_of(a.max_list, p->partition_size);
+    a.num_partitions = static_cast<int32_t>(parts);
+    const bool v2 = parts > 1;
+    if (launch_tc(a, p->kv_dtype, v2, stream) != cudaSuccess) return PA_ERR_CUDA;
+    if (!v2) return PA_OK;
+    l.stride = a.num_partitions;
+    l.block_list = 1;
+    return launch_join(j, stream, true) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+
   ListArgs a{};
   a.q = q;
   a.k_cache = k_cache;
@@ -115,25 +153,7 @@ pa_status_t pa_decode_window(const pa_params_t* p, const pa_window_t* window, co
   a.scale_log2 = p->scale * 1.442695040888963407360f;
   if (launch_list(a, p->kv_dtype, stream) != cudaSuccess) return PA_ERR_CUDA;
   if (parts == 1) return PA_OK;
-
-  JoinArgs j{};
-  JoinList& l = j.list[0];
-  l.m = part_max;
-  l.s = part_sum;
-  l.o = part_out;
-  l.lens = seq_lens;
-  l.max_len = p->max_seq_len;
   l.stride = a.num_parts;
-  l.part_size = p->partition_size;
-  l.window = w.window;
-  l.num_sinks = w.num_sinks;
-  l.block_size = p->block_size;
-  j.out = out;
-  j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;
-  j.num_heads = p->num_heads;
-  j.head_dim = p->head_dim;
-  j.group = a.group;
-  j.out_dtype = p->out_dtype;
   return launch_join(j, stream, true) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
