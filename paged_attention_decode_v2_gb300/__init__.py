@@ -549,33 +549,22 @@ def prefill(q, k, v, k_cache, v_cache, block_tables, query_start, ctx_lens, out,
 
 
 # ---- the serving step around the attention -----------------------------------------------------
+#
+# These calls go through _marshal.so, which reads the tensors, checks them and
+# calls the C entry points; a refused argument raises PaError.
 
-def _refuse(ok: bool, why: str):
-    if not ok:
-        raise PaError(PA_ERR_INVALID_ARG, why)
-
-
-def _launch_stream(first, stream):
-    """The stream handle to launch on; the current device must be the tensors'."""
-    import torch
-    _refuse(first.is_cuda and first.device.index == torch.cuda.current_device(),
-            "the tensors must be on the current CUDA device")
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream
+_marshal_mod = None
 
 
-def _check(device, contiguous, **tensors):
-    """Every tensor given (None is skipped) is on ``device``, and contiguous if asked."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise PaError(PA_ERR_INVALID_ARG, f"{name} must be on {device}")
-        if contiguous and not t.is_contiguous():
-            raise PaError(PA_ERR_INVALID_ARG, f"{name} must be contiguous")
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _binding():
+    global _marshal_mod
+    if _marshal_mod is None:
+        lib()  # names what is missing where nothing has been built
+        import torch  # noqa: F401  (the module links against its libraries)
+        from . import _marshal as m
+        m.set_error(PaError)
+        _marshal_mod = m
+    return _marshal_mod
 
 
 def _done(status: int, where: str):
@@ -583,10 +572,8 @@ def _done(status: int, where: str):
         raise PaError(status, where)
 
 
-def _check_status_word(status):
-    import torch
-    if status is not None:
-        _refuse(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32")
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def plan_step(ctx_lens, new_lens, free_blocks, free_count, block_tables, query_start, seq_lens,
@@ -603,34 +590,9 @@ def plan_step(ctx_lens, new_lens, free_blocks, free_count, block_tables, query_s
     ``positions`` int32 [T], ``slots`` int64 [T] (rows past the step's total:
     0 and -1), ``free_left`` [1].  ``status``: an int32 tensor whose first
     element receives device errors."""
-    import torch
-    i32 = torch.int32
-    B, T = ctx_lens.shape[0], slots.shape[0]
-    _check(ctx_lens.device, True, ctx_lens=ctx_lens, new_lens=new_lens, free_blocks=free_blocks,
-           free_count=free_count, block_tables=block_tables, query_start=query_start,
-           seq_lens=seq_lens, positions=positions, slots=slots, free_left=free_left,
-           base_len=base_len, status=status)
-    _check_status_word(status)
-    for t in (ctx_lens, new_lens, free_blocks, free_count, block_tables, query_start, seq_lens,
-              positions, free_left):
-        _refuse(t.dtype == i32, "lengths, tables, positions and counts must be int32")
-    _refuse(slots.dtype == torch.int64, "slots must be int64")
-    _refuse(base_len is None or (base_len.dtype == i32 and base_len.numel() == 1),
-            "base_len must be one int32")
-    _refuse(ctx_lens.dim() == 1 and new_lens.shape == ctx_lens.shape == seq_lens.shape and
-            query_start.shape == (B + 1,), "lengths must be [B] and query_start [B + 1]")
-    _refuse(block_tables.dim() == 2 and block_tables.shape[0] == B, "block_tables must be [B, ..]")
-    _refuse(free_blocks.dim() == 1 and free_count.numel() == 1 and free_left.numel() == 1,
-            "free_blocks must be 1-D, free_count and free_left one element")
-    _refuse(slots.dim() == 1 and positions.shape == slots.shape,
-            "positions and slots must be [T]")
-    p = PlanParams(B, int(block_size), int(num_blocks), block_tables.shape[1], T,
-                   free_blocks.shape[0])
-    _done(lib().pa_plan_step(
-        ctypes.byref(p), _addr(ctx_lens), _addr(new_lens), _addr(free_blocks), _addr(free_count),
-        _addr(base_len), _addr(block_tables), _addr(query_start), _addr(seq_lens),
-        _addr(positions), _addr(slots), _addr(free_left), _addr(status),
-        _launch_stream(ctx_lens, stream)), "pa_plan_step")
+    _done(_binding().plan_step(ctx_lens, new_lens, free_blocks, free_count, block_tables,
+                                query_start, seq_lens, positions, slots, free_left, block_size,
+                                num_blocks, base_len, status, _handle(stream)), "pa_plan_step")
 
 
 def qk_norm_rope(q, k, v, positions, slots, cos_sin, q_out, k_cache=None, v_cache=None, *,
@@ -647,53 +609,10 @@ def qk_norm_rope(q, k, v, positions, slots, cos_sin, q_out, k_cache=None, v_cach
     ``k_out`` and ``v_out`` [T, Hkv, D] contiguous.  ``block_size`` and
     ``num_blocks`` are read off ``k_cache``; without caches they only bound
     the slots."""
-    import torch
-    T, hq, d = q.shape
-    hkv = k.shape[1]
-    dev, dt = q.device, q.dtype
-    _check(dev, False, q=q, k=k, v=v)
-    _check(dev, True, positions=positions, slots=slots, cos_sin=cos_sin, q_out=q_out,
-           k_cache=k_cache, v_cache=v_cache, q_weight=q_weight, k_weight=k_weight, k_out=k_out,
-           v_out=v_out, status=status)
-    _check_status_word(status)
-    _refuse(k.dim() == 3 and k.shape == (T, hkv, d) and v.shape == k.shape and
-            q_out.shape == q.shape, "q, q_out must be [T, Hq, D] and k, v [T, Hkv, D]")
-    for t in (q, k, v):
-        _refuse(t.stride(2) == 1 and (t.stride(1) == d or t.shape[1] == 1),
-                "heads must be contiguous within a row")
-    for t in (k, v, q_out, k_cache, v_cache, q_weight, k_weight, k_out, v_out):
-        _refuse(t is None or t.dtype == dt, "q, k, v, weights, caches and outputs share one dtype")
-    _refuse(slots.dtype == torch.int64 and slots.shape == (T,), "slots must be int64 [T]")
-    _refuse(positions is None or (positions.dtype == torch.int32 and positions.shape == (T,)),
-            "positions must be int32 [T]")
-    _refuse((q_weight is None) == (k_weight is None), "give both weights or neither")
-    for t in (q_weight, k_weight):
-        _refuse(t is None or t.shape == (d,), "weights must be [D]")
-    for t in (k_out, v_out):
-        _refuse(t is None or t.shape == k.shape, "k_out and v_out must be [T, Hkv, D]")
-    rot = max_pos = 0
-    if cos_sin is not None:
-        _refuse(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and positions is not None,
-                "cos_sin must be float32 [max_position, rotary_dim], with positions")
-        max_pos, rot = cos_sin.shape
-    _refuse((k_cache is None) == (v_cache is None), "give both caches or neither")
-    if k_cache is not None:
-        nb, h2, bs, d2 = cache_dims(k_cache, split_x)
-        v_shape = (nb, h2, d2, bs) if split_x else (nb, h2, bs, d2)
-        _refuse(h2 == hkv and d2 == d and v_cache.shape == v_shape,
-                "the caches' heads and head_dim must be k's")
-        _refuse(not split_x or k_cache.shape[4] * k_cache.element_size() == 16,
-                "split-x key groups are 16 bytes")
-        num_blocks, block_size = nb, bs
-    p = RopeParams(T, hq, hkv, d, int(block_size) or 1, int(num_blocks) or (1 << 30), rot, max_pos,
-                   q.stride(0), k.stride(0), v.stride(0), _dtype_code(dt),
-                   (PA_ROPE_INTERLEAVED if interleaved else 0) |
-                   (PA_FLAG_SPLIT_X if split_x else 0), eps, weight_offset)
-    _done(lib().pa_qk_norm_rope(
-        ctypes.byref(p), _addr(q), _addr(k), _addr(v), _addr(q_weight), _addr(k_weight),
-        _addr(cos_sin), _addr(positions), _addr(slots), _addr(q_out), _addr(k_out), _addr(v_out),
-        _addr(k_cache), _addr(v_cache), _addr(status), _launch_stream(q, stream)),
-        "pa_qk_norm_rope")
+    _done(_binding().qk_norm_rope(q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache,
+                                   q_weight, k_weight, eps, weight_offset, interleaved, block_size,
+                                   num_blocks, k_out, v_out, split_x, status, _handle(stream)),
+          "pa_qk_norm_rope")
     return q_out
 
 
@@ -706,27 +625,8 @@ def _alloc(n: int, where: str, device):
     return ws
 
 
-def _step_params(q, k_cache, block_tables, out_dtype, max_seq_len, scale, partition_size,
-                 portable, split_x, flags):
-    return make_params(q, k_cache, block_tables, max_seq_len=max_seq_len, scale=scale,
-                       partition_size=partition_size, out_dtype=out_dtype, portable=portable,
-                       split_x=split_x, flags=flags)
-
-
-def _check_step(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, split_x):
-    """The checks of the decode calls, and of tensors on different devices."""
-    import torch
-    _check(q.device, True, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-           seq_lens=seq_lens, out=out, workspace=workspace)
-    _refuse(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32,
-            "block_tables and seq_lens must be int32")
-    nb, hkv, bs, d = cache_dims(k_cache, split_x)
-    _refuse(v_cache.shape == ((nb, hkv, d, bs) if split_x else (nb, hkv, bs, d)) and
-            v_cache.dtype == k_cache.dtype == q.dtype,
-            "q, k_cache and v_cache must agree in dtype/shape")
-    _refuse(out.shape == q.shape, "out must have q's shape")
-    _refuse(block_tables.dim() == 2 and block_tables.shape[0] == q.shape[0] and
-            seq_lens.shape == (q.shape[0],), "block_tables must be [B, ..] and seq_lens [B]")
+def _flags(portable, split_x, flags):
+    return (PA_FLAG_PORTABLE if portable else 0) | (PA_FLAG_SPLIT_X if split_x else 0) | flags
 
 
 def window_workspace_size(params: Params, window: int, num_sinks: int = 0) -> int:
@@ -737,8 +637,8 @@ def window_workspace_size(params: Params, window: int, num_sinks: int = 0) -> in
 def alloc_window_workspace(q, k_cache, block_tables, *, window: int, num_sinks: int = 0,
                            max_seq_len: int, partition_size: int = 512, split_x: bool = False):
     """A workspace for :func:`decode_window` with these shapes, initialised."""
-    p = _step_params(q, k_cache, block_tables, None, max_seq_len, 1.0, partition_size, False,
-                     split_x, 0)
+    p = make_params(q, k_cache, block_tables, max_seq_len=max_seq_len, scale=1.0,
+                    partition_size=partition_size, split_x=split_x)
     return _alloc(window_workspace_size(p, window, num_sinks), "pa_window_workspace_size",
                   q.device)
 
@@ -749,15 +649,10 @@ def decode_window(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, *
     """``pa_decode_window``: decode where a query sees the last ``window``
     tokens (itself included) and the first ``num_sinks``.  Table entries of
     blocks that hold none of these are not read."""
-    _check_step(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, split_x)
-    p = _step_params(q, k_cache, block_tables, out.dtype, max_seq_len, scale, partition_size,
-                     portable, split_x, flags)
-    w = WindowParams(int(window), int(num_sinks))
-    _done(lib().pa_decode_window(
-        ctypes.byref(p), ctypes.byref(w), _addr(q), _addr(k_cache), _addr(v_cache),
-        _addr(block_tables), _addr(seq_lens), _addr(workspace),
-        workspace.numel() * workspace.element_size(), _addr(out), _launch_stream(q, stream)),
-        "pa_decode_window")
+    _done(_binding().decode_window(q, k_cache, v_cache, block_tables, seq_lens, out, workspace,
+                                    max_seq_len, scale, partition_size,
+                                    _flags(portable, split_x, flags), window, num_sinks,
+                                    _handle(stream)), "pa_decode_window")
     return out
 
 
@@ -767,30 +662,10 @@ def prefill_window(q, k, v, k_cache, v_cache, block_tables, query_start, ctx_len
                    stream=None):
     """``pa_prefill_window``: :func:`prefill` where the query at position p sees
     tokens t <= p with t > p - ``window`` or t < ``num_sinks``."""
-    import torch
-    _check(q.device, True, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache,
-           block_tables=block_tables, query_start=query_start, ctx_lens=ctx_lens, out=out)
-    for t in (block_tables, query_start, ctx_lens):
-        _refuse(t.dtype == torch.int32, "block_tables, query_start and ctx_lens must be int32")
-    T, hq, d = q.shape
-    nb, hkv, bs, d2 = cache_dims(k_cache, split_x)
-    _refuse(k.shape == (T, hkv, d) and v.shape == (T, hkv, d) and d2 == d and
-            v_cache.shape == ((nb, hkv, d, bs) if split_x else (nb, hkv, bs, d)) and
-            out.shape == q.shape, "prefill tensor shapes disagree")
-    _refuse(q.dtype == k.dtype == v.dtype == k_cache.dtype == v_cache.dtype,
-            "q, k, v and the caches must share one dtype")
-    B = block_tables.shape[0]
-    _refuse(query_start.shape == (B + 1,) and ctx_lens.shape == (B,),
-            "query_start must be [B + 1] and ctx_lens [B]")
-    p = PrefillParams(B, hq, hkv, d, bs, nb, block_tables.shape[1], T, int(max_query_len),
-                      int(max_ctx_len), _dtype_code(k_cache.dtype), _dtype_code(out.dtype),
-                      float(scale), (PA_FLAG_PORTABLE if portable else 0) |
-                      (PA_FLAG_SPLIT_X if split_x else 0) | int(flags))
-    w = WindowParams(int(window), int(num_sinks))
-    _done(lib().pa_prefill_window(
-        ctypes.byref(p), ctypes.byref(w), _addr(q), _addr(k), _addr(v), _addr(k_cache),
-        _addr(v_cache), _addr(block_tables), _addr(query_start), _addr(ctx_lens), _addr(out),
-        _launch_stream(q, stream)), "pa_prefill_window")
+    _done(_binding().prefill_window(q, k, v, k_cache, v_cache, block_tables, query_start, ctx_lens,
+                                     out, max_query_len, max_ctx_len, scale,
+                                     _flags(portable, split_x, flags), window, num_sinks,
+                                     _handle(stream)), "pa_prefill_window")
     return out
 
 
@@ -802,10 +677,10 @@ def prefix_workspace_size(params: Params, max_prefix_len: int, max_prefix_blocks
 def alloc_prefix_workspace(q, k_cache, block_tables, *, max_seq_len: int, max_prefix_len: int,
                            partition_size: int = 512, split_x: bool = False):
     """A workspace for :func:`decode_prefix` with these shapes, initialised."""
-    p = _step_params(q, k_cache, block_tables, None, max_seq_len, 1.0, partition_size, False,
-                     split_x, 0)
-    bs = p.block_size
-    return _alloc(prefix_workspace_size(p, max_prefix_len, -(-int(max_prefix_len) // bs)),
+    p = make_params(q, k_cache, block_tables, max_seq_len=max_seq_len, scale=1.0,
+                    partition_size=partition_size, split_x=split_x)
+    return _alloc(prefix_workspace_size(p, max_prefix_len, -(-int(max_prefix_len) //
+                                                             p.block_size)),
                   "pa_prefix_workspace_size", q.device)
 
 
@@ -817,18 +692,8 @@ def decode_prefix(q, k_cache, v_cache, prefix_blocks, prefix_len, block_tables, 
     ``prefix_len`` [1] tokens in ``prefix_blocks`` [.] and own ``seq_lens`` [B]
     further tokens in ``block_tables`` [B, .].  The prefix is read once for
     the whole batch."""
-    import torch
-    _check_step(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, split_x)
-    _check(q.device, True, prefix_blocks=prefix_blocks, prefix_len=prefix_len)
-    _refuse(prefix_blocks.dtype == torch.int32 and prefix_blocks.dim() == 1 and
-            prefix_len.dtype == torch.int32 and prefix_len.numel() == 1,
-            "prefix_blocks must be int32 [.] and prefix_len one int32")
-    p = _step_params(q, k_cache, block_tables, out.dtype, max_seq_len, scale, partition_size,
-                     portable, split_x, flags)
-    x = PrefixParams(int(max_prefix_len), prefix_blocks.shape[0])
-    _done(lib().pa_decode_prefix(
-        ctypes.byref(p), ctypes.byref(x), _addr(q), _addr(k_cache), _addr(v_cache),
-        _addr(prefix_blocks), _addr(prefix_len), _addr(block_tables), _addr(seq_lens),
-        _addr(workspace), workspace.numel() * workspace.element_size(), _addr(out),
-        _launch_stream(q, stream)), "pa_decode_prefix")
+    _done(_binding().decode_prefix(q, k_cache, v_cache, block_tables, seq_lens, out, workspace,
+                                    max_seq_len, scale, partition_size,
+                                    _flags(portable, split_x, flags), prefix_blocks, prefix_len,
+                                    max_prefix_len, _handle(stream)), "pa_decode_prefix")
     return out

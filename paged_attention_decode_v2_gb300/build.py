@@ -1,4 +1,5 @@
-"""Build ``libpa.so`` (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build ``libpa.so`` (the C-ABI library) in-tree with nvcc for sm_103a, and
+``_marshal.so`` (its torch argument marshalling, host code) with g++.
 
 Each ``csrc/*.cu`` file is compiled in parallel into ``_build/``, then the
 objects are linked into ``paged_attention_decode_v2_gb300/libpa.so``.  A file
@@ -23,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,6 +46,35 @@ def _flags(verbose: bool):
     if verbose:
         f += ["-Xptxas", "-v"]
     return f
+
+
+def _build_marshal(force: bool) -> None:
+    """Compile and link ``csrc/marshal.cpp`` against torch's headers and libpa."""
+    import sysconfig
+
+    import torch
+
+    src, header = os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "pa.h")
+    newest = max(os.path.getmtime(src), os.path.getmtime(header))
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
+           "-fvisibility=hidden", src, "-o", tmp, "-I", INCLUDE,
+           "-isystem", os.path.join(troot, "include"),
+           "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-L", os.path.join(troot, "lib"), f"-Wl,-rpath,{os.path.join(troot, 'lib')}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-L", PKG, "-l:libpa.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"build of _marshal.so failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
@@ -76,11 +107,13 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(map(os.path.getmtime, objs)):
         tmp = LIB + f".tmp{os.getpid()}"
         r = subprocess.run([exe, "-shared", *ARCH, *objs, "-o", tmp, "-cudart", "static",
+                            "-Xlinker", "-soname=libpa.so",
                             "-Xlinker", "-Bsymbolic", "-Xlinker", "--exclude-libs,ALL"],
                            capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link of libpa.so failed:\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_marshal(force)
     return LIB
 
 
