@@ -1,17 +1,20 @@
 // pa_rope.cu -- pa_qk_norm_rope: norm of each query and key head, rotation by
 // position, and the write of keys and values into the paged cache.
 //
-// Row t has R = Hq + 2 Hkv head rows of D elements: queries, keys, values.  A
-// group of LPR lanes (a row's 16-byte pieces, at most a warp) holds one head
-// row in registers: sum of squares by shuffles, y = x * r * w in float32, the
-// rotation of the pair (i, i + rot / 2) by one shuffle with the lane that
-// holds the partner (pairs (2i, 2i + 1) are within a lane), one rounding, one
+// Row t has R = Hq + 2 Hkv head rows of D elements: queries, keys, values.  D / 8
+// lanes hold a head row in registers, each lane four pairs of the rotation:
+// elements (j, j + rot / 2) or (2j, 2j + 1), and runs of the tail where
+// rotary_dim < D, so a pair never leaves its lane.  The sum of squares is a
+// shuffle reduction; y = x * r * w in float32, the rotation, one rounding, one
 // store: queries to q_out, keys and values to their slot (and k_out / v_out).
 //
-// Bound by memory: every element is read and written once.  A group takes
-// kHeads head rows of one row t, so the row's angles (4 bytes per rotated
-// element, as many bytes as two 16-bit head rows) are loaded once for all of
-// them and several 16-byte loads are in flight.
+// Bound by memory where there are many rows: every element is read and written
+// once.  What stands in the way is issuing instructions and waiting: so the
+// arithmetic is in pairs of floats (one instruction for two), and a warp takes
+// a run of head rows of one kind and one row t (two or four side by side where
+// D < 256), everything that does not depend on the head -- the slot's place,
+// the angles, the weights -- done once per run, kUnroll rows loaded before the
+// first is used.
 #include <cstdint>
 
 #include <cuda_runtime_api.h>
@@ -42,29 +45,89 @@ struct RopeArgs {
   int64_t q_stride, k_stride, v_stride;
   int64_t pool;  // slots of the pool
   int32_t num_tokens, num_heads, num_kv_heads, block_size, rot, max_position;
-  int32_t interleaved, split_x, head_groups;
+  int32_t interleaved, split_x;
+  int32_t block_shift;         // log2 of block_size, or -1
+  int32_t run;                 // head rows of a run
+  int32_t q_runs, kv_runs;     // runs of a row t: queries; keys, and as many values
+  int64_t items;
   float eps, weight_offset;
 };
 
-// Round E values to T and store them at p (aligned to their size).
-template <typename T, int E>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[E]) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i)
-      reinterpret_cast<float4*>(p)[i] =
-          make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-  } else {
-    static_assert(E == 8, "16-byte pieces");
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const T a = round16(f[2 * i], static_cast<T*>(nullptr));
-      const T b = round16(f[2 * i + 1], static_cast<T*>(nullptr));
-      w[i] = bits16(a) | (static_cast<uint32_t>(bits16(b)) << 16);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+// Two floats in one 64-bit register, for the packed float32 instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(F2 v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 swapped(F2 v) {
+  float x, y;
+  unpair(v, x, y);
+  return pair(y, x);
+}
+
+// Four elements as they are in memory, and widened.
+template <typename T>
+struct Raw4 {
+  uint2 v;
+  __device__ __forceinline__ void load(const T* p) {
+    v = __ldcs(reinterpret_cast<const uint2*>(p));
   }
+  __device__ __forceinline__ void widen(F2* f) const {
+    float x, y;
+    widen2(static_cast<const T*>(nullptr), v.x, x, y);
+    f[0] = pair(x, y);
+    widen2(static_cast<const T*>(nullptr), v.y, x, y);
+    f[1] = pair(x, y);
+  }
+};
+template <>
+struct Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) {
+    v = __ldcs(reinterpret_cast<const float4*>(p));
+  }
+  __device__ __forceinline__ void widen(F2* f) const {
+    f[0] = pair(v.x, v.y);
+    f[1] = pair(v.z, v.w);
+  }
+};
+
+// Round four values to the element type and store them at p.
+__device__ __forceinline__ void store4(float* p, const F2* f) {
+  float4 v;
+  unpair(f[0], v.x, v.y);
+  unpair(f[1], v.z, v.w);
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ uint32_t round2(F2 f, __nv_bfloat16*) {
+  float x, y;
+  unpair(f, x, y);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t round2(F2 f, __half*) {
+  float x, y;
+  unpair(f, x, y);
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const F2* f) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(round2(f[0], p), round2(f[1], p));
 }
 
 __device__ __forceinline__ float round_elem(float x, float*) { return x; }
@@ -73,157 +136,202 @@ __device__ __forceinline__ __nv_bfloat16 round_elem(float x, __nv_bfloat16* p) {
 }
 __device__ __forceinline__ __half round_elem(float x, __half* p) { return round16(x, p); }
 
-template <typename T, int D, int kHeads>
-__global__ void __launch_bounds__(kNT) pa_rope_kernel(const RopeArgs a) {
-  constexpr int X = 16 / sizeof(T);                   // elements of a 16-byte piece
-  constexpr int LPR = D / X < 32 ? D / X : 32;        // lanes of a head row
-  constexpr int E = D / LPR;                          // elements a lane holds
-  constexpr int kGroups = kNT / LPR;
-  static_assert(E == X || E == 2 * X, "pieces of a lane");
-  const int lane = threadIdx.x % LPR;                 // within the group
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LPR;
-  const int64_t t = item / a.head_groups;
-  if (t >= a.num_tokens) return;                      // whole groups leave together
-  const unsigned mask = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u))
-                        << (threadIdx.x % 32 / LPR * LPR);
-  const int Hq = a.num_heads, Hkv = a.num_kv_heads, R = Hq + 2 * Hkv;
-  const int first = static_cast<int>(item % a.head_groups) * kHeads;
+// What a lane needs to norm and rotate its eight elements of any head row.
+// Element pairs y[0..3] hold elements oa .. oa + 3 and ob .. ob + 3; out =
+// y * c + other * s with `other` the pairs' other sides: y[2], y[3], y[0], y[1]
+// (halves), or each pair swapped (interleaved).  Lanes that do not rotate have
+// c = 1, s = 0.
+struct Lane {
+  F2 w[4], c[4], s[4];
+};
+
+template <int LPR, bool kInter>
+__device__ __forceinline__ void norm_rotate(F2 (&y)[4], const Lane& l, bool norm, float eps,
+                                            unsigned mask) {
+  constexpr int D = LPR * 8;
+  if (norm) {
+    F2 q = mul2(y[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) q = fma2(y[i], y[i], q);
+    float x, z;
+    unpair(q, x, z);
+    float ss = x + z;
+#pragma unroll
+    for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+    const float rn = rsqrtf(fmaf(ss, 1.f / D, eps));
+    const F2 r2 = pair(rn, rn);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(y[i], r2), l.w[i]);
+  }
+  const F2 t[4] = {kInter ? swapped(y[0]) : y[2], kInter ? swapped(y[1]) : y[3],
+                   kInter ? swapped(y[2]) : y[0], kInter ? swapped(y[3]) : y[1]};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = fma2(y[i], l.c[i], mul2(t[i], l.s[i]));
+}
+
+// Head rows loaded at once, per side of the warp, and CTAs per SM that the
+// register budget is set for (64 registers, no spills).  Measured on GB300,
+// 8192 rows of 24 / 4 heads of 256, bf16: 4 rows and 4 CTAs 55 us, 4 and 3
+// 64 us, 2 and 5 58 us, 8 and 3 70 us.
+constexpr int kUnroll = 4;
+constexpr int kCtas = 4;
+
+template <typename T, int D, bool kInter>
+__global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
+  constexpr int X = 16 / sizeof(T);                   // elements of a split-x key group
+  constexpr int LPR = D / 8;                          // lanes of a head row
+  constexpr int kSide = 32 / LPR;                     // head rows side by side in a warp
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x % LPR, side = threadIdx.x % 32 / LPR;
+  const uint32_t item = blockIdx.x * (kNT / 32) + threadIdx.x / 32;
+  if (item >= a.items) return;
+  const uint32_t per_row = a.q_runs + 2 * a.kv_runs;
+  const int32_t t = static_cast<int32_t>(item / per_row);
+  const int k = static_cast<int>(item - t * per_row);
   const int64_t slot = __ldg(a.slots + t);
   const int32_t pos = a.rot ? __ldg(a.positions + t) : 0;
+  const int kind = k < a.q_runs ? 0 : k < a.q_runs + a.kv_runs ? 1 : 2;
+  const int h0 = (kind == 0 ? k : kind == 1 ? k - a.q_runs : k - a.q_runs - a.kv_runs) * a.run;
+  const int heads = kind == 0 ? a.num_heads : a.num_kv_heads;
+  const int h1 = min(h0 + a.run, heads);
+  // this lane's two runs of four elements
+  const int half = a.rot / 2, j0 = lane * 4;
+  const bool rotates = j0 < half;                     // half is a multiple of 8
+  const int oa = kInter ? lane * 8 : rotates ? j0 : half + j0;
+  const int ob = kInter ? lane * 8 + 4 : rotates ? j0 + half : D / 2 + j0;
+
+  const T* src = (kind == 0   ? static_cast<const T*>(a.q) + t * a.q_stride
+                  : kind == 1 ? static_cast<const T*>(a.k) + t * a.k_stride
+                              : static_cast<const T*>(a.v) + t * a.v_stride) +
+                 (h0 + side) * D;
+  Raw4<T> raw[kUnroll][2];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + side + u * kSide < h1) {
+        raw[u][0].load(src + u * kSide * D + oa);
+        raw[u][1].load(src + u * kSide * D + ob);
+      }
+    src += kUnroll * kSide * D;
+  };
+  load(h0);
   if (slot == -1) return;                             // padding
   const bool pos_ok = !a.rot || (pos >= 0 && pos < a.max_position);
   const bool slot_ok = slot >= 0 && slot < a.pool;
-  if (first == 0 && lane == 0) {
+  if (k == 0 && threadIdx.x % 32 == 0) {
     if (!slot_ok) set_status(a.status, PA_ERR_BAD_SLOT);
     if (!pos_ok) set_status(a.status, PA_ERR_BAD_POSITION);
   }
-  const bool cache = a.k_cache && slot_ok && pos_ok;
-  const int64_t block = slot_ok ? slot / a.block_size : 0;
-  const int at = slot_ok ? static_cast<int>(slot % a.block_size) : 0;
-
-  float x[kHeads][E];
-#pragma unroll
-  for (int j = 0; j < kHeads; ++j) {
-    const int r = first + j;
-    if (r >= R) break;
-    const T* src = r < Hq ? static_cast<const T*>(a.q) + t * a.q_stride + r * D
-                   : r < Hq + Hkv
-                       ? static_cast<const T*>(a.k) + t * a.k_stride + (r - Hq) * D
-                       : static_cast<const T*>(a.v) + t * a.v_stride + (r - Hq - Hkv) * D;
-    load_row<T, E>(src + lane * E, x[j]);
-  }
-  // the angles of this lane's elements: pair j of the row at table column j
-  const int half = a.rot / 2;
-  const bool rotates = a.rot && lane * E < a.rot;     // rot is a multiple of 2 E
-  float cs[E], sn[E];
-  if (rotates && pos_ok) {
-    const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
-    if (a.interleaved) {
-      const int c0 = lane * E / 2;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        cs[e] = __ldg(row + c0 + e / 2);
-        sn[e] = __ldg(row + half + c0 + e / 2);
-        if (e % 2 == 0) sn[e] = -sn[e];
-      }
+  Lane l;
+  const bool norm = a.qw != nullptr;
+  if (kind < 2) {
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (rotates && pos_ok) {
+      const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot + j0;
+      c = __ldg(reinterpret_cast<const float4*>(row));
+      s = __ldg(reinterpret_cast<const float4*>(row + half));
+    }
+    if (!pos_ok) c.x = c.y = c.z = c.w = qnan();      // the rows come out NaN
+    if (kInter) {
+      l.c[0] = pair(c.x, c.x), l.c[1] = pair(c.y, c.y);
+      l.c[2] = pair(c.z, c.z), l.c[3] = pair(c.w, c.w);
+      l.s[0] = pair(-s.x, s.x), l.s[1] = pair(-s.y, s.y);
+      l.s[2] = pair(-s.z, s.z), l.s[3] = pair(-s.w, s.w);
     } else {
-      const bool low = lane * E < half;
-      const int c0 = lane * E - (low ? 0 : half);
-      load_row<float, E>(row + c0, cs);
-      load_row<float, E>(row + half + c0, sn);
+      l.c[0] = l.c[2] = pair(c.x, c.y);
+      l.c[1] = l.c[3] = pair(c.z, c.w);
+      l.s[0] = pair(-s.x, -s.y), l.s[1] = pair(-s.z, -s.w);
+      l.s[2] = pair(s.x, s.y), l.s[3] = pair(s.z, s.w);
+    }
+    if (norm) {
+      const T* w = static_cast<const T*>(kind == 0 ? a.qw : a.kw);
+      float f[8];
+      load_row<T, 4>(w + oa, *reinterpret_cast<float(*)[4]>(&f[0]));
+      load_row<T, 4>(w + ob, *reinterpret_cast<float(*)[4]>(&f[4]));
 #pragma unroll
-      for (int e = 0; e < E; ++e) sn[e] = low ? -sn[e] : sn[e];
+      for (int i = 0; i < 4; ++i)
+        l.w[i] = pair(f[2 * i] + a.weight_offset, f[2 * i + 1] + a.weight_offset);
     }
   }
-  const int base = threadIdx.x % 32 - lane;           // the group's first lane of the warp
-  const int away = half / E;                          // lanes between a pair's halves
-  const int partner = base + (!rotates || a.interleaved ? lane
-                              : lane < away ? lane + away : lane - away);
-#pragma unroll
-  for (int j = 0; j < kHeads; ++j) {
-    const int r = first + j;
-    if (r >= R) break;
-    const bool value = r >= Hq + Hkv;
-    if (!value) {
-      const T* w = static_cast<const T*>(r < Hq ? a.qw : a.kw);
-      if (w) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(x[j][e], x[j][e], ss);
-#pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-        const float rn = rsqrtf(ss * (1.f / D) + a.eps);
-        float wf[E];
-        load_row<T, E>(w + lane * E, wf);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[j][e] = x[j][e] * rn * (wf[e] + a.weight_offset);
-      }
-      if (a.rot) {
-        if (a.interleaved) {
-          if (rotates) {
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const float p = x[j][e], b = x[j][e + 1];
-              x[j][e] = fmaf(p, cs[e], b * sn[e]);
-              x[j][e + 1] = fmaf(b, cs[e + 1], p * sn[e + 1]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float o = __shfl_sync(mask, x[j][e], partner);
-            if (rotates) x[j][e] = fmaf(x[j][e], cs[e], o * sn[e]);
-          }
-        }
-        if (!pos_ok) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[j][e] = qnan();
-        }
-      }
-    }
-    if (r < Hq) {
-      store_vec<T, E>(static_cast<T*>(a.q_out) + (t * Hq + r) * D + lane * E, x[j]);
-      continue;
-    }
-    const int h = value ? r - Hq - Hkv : r - Hq;
-    T* dense = static_cast<T*>(value ? a.v_out : a.k_out);
-    if (dense) store_vec<T, E>(dense + (t * Hkv + h) * D + lane * E, x[j]);
-    if (!cache) continue;
-    T* pool = static_cast<T*>(value ? a.v_cache : a.k_cache) +
-              (block * Hkv + h) * static_cast<int64_t>(a.block_size) * D;
+  // where the rows go: q_out, or dense and the slot's place in the pool
+  const bool cache = kind > 0 && a.k_cache && slot_ok && pos_ok;
+  T* dense = static_cast<T*>(kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out);
+  if (dense) dense += static_cast<int64_t>(t) * heads * D;
+  T* pool = nullptr;
+  const int64_t head = static_cast<int64_t>(a.block_size) * D;  // a head's part of a block
+  int64_t pa = 0, pb = 0;
+  if (cache) {
+    const int64_t block = a.block_shift >= 0 ? slot >> a.block_shift : slot / a.block_size;
+    const int at = static_cast<int>(slot - block * a.block_size);
+    pool = static_cast<T*>(kind == 1 ? a.k_cache : a.v_cache) + block * heads * head;
     if (!a.split_x) {
-      store_vec<T, E>(pool + static_cast<int64_t>(at) * D + lane * E, x[j]);
-    } else if (!value) {  // 16-byte pieces [D / X][block_size][X]
-#pragma unroll
-      for (int g = 0; g < E / X; ++g) {
-        float f[X];
-#pragma unroll
-        for (int e = 0; e < X; ++e) f[e] = x[j][g * X + e];
-        store_vec<T, X>(pool + (static_cast<int64_t>(lane * (E / X) + g) * a.block_size + at) * X,
-                        f);
-      }
-    } else {              // [D][block_size]
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        pool[static_cast<int64_t>(lane * E + e) * a.block_size + at] =
-            round_elem(x[j][e], static_cast<T*>(nullptr));
+      pa = static_cast<int64_t>(at) * D + oa;
+      pb = static_cast<int64_t>(at) * D + ob;
+    } else if (kind == 1) {  // 16-byte groups [D / X][block_size][X]
+      pa = (static_cast<int64_t>(oa / X) * a.block_size + at) * X + oa % X;
+      pb = (static_cast<int64_t>(ob / X) * a.block_size + at) * X + ob % X;
+    } else {                 // [D][block_size]
+      pa = static_cast<int64_t>(oa) * a.block_size + at;
+      pb = static_cast<int64_t>(ob) * a.block_size + at;
     }
+  }
+  for (int h = h0;;) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = h + side + u * kSide;
+      if (h + u * kSide >= h1) break;
+      F2 y[4];
+      raw[u][0].widen(&y[0]);
+      raw[u][1].widen(&y[2]);
+      if (kind < 2) norm_rotate<LPR, kInter>(y, l, norm, a.eps, kAll);
+      if (x >= h1) continue;
+      if (dense) {
+        store4(dense + x * D + oa, y);
+        store4(dense + x * D + ob, y + 2);
+      }
+      if (!cache) continue;
+      if (!a.split_x || kind == 1) {
+        store4(pool + x * head + pa, y);
+        store4(pool + x * head + pb, y + 2);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float f[2];
+          unpair(y[e / 2], f[0], f[1]);
+          pool[x * head + (e < 4 ? pa : pb) + static_cast<int64_t>(e % 4) * a.block_size] =
+              round_elem(f[e % 2], static_cast<T*>(nullptr));
+        }
+      }
+    }
+    h += kUnroll * kSide;
+    if (h >= h1) break;
+    load(h);
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_d(RopeArgs a, int sms, cudaStream_t s) {
-  constexpr int X = 16 / sizeof(T);
-  constexpr int LPR = D / X < 32 ? D / X : 32;
-  const int R = a.num_heads + 2 * a.num_kv_heads;
-  constexpr int kHeads = 4;
-  (void)sms;
-  a.head_groups = (R + kHeads - 1) / kHeads;
-  const int64_t items = static_cast<int64_t>(a.num_tokens) * a.head_groups;
-  const int64_t grid = (items + kNT / LPR - 1) / (kNT / LPR);
-  if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  pa_rope_kernel<T, D, kHeads><<<static_cast<unsigned>(grid), kNT, 0, s>>>(a);
+template <typename T, int D, bool kInter>
+cudaError_t launch_i(RopeArgs a, int sms, cudaStream_t s) {
+  constexpr int kWarps = kNT / 32;
+  constexpr int kSide = 32 / (D / 8);
+  // two loads' worth of head rows a run, fewer while the runs do not fill the
+  // GPU twice (16 warps an SM)
+  a.run = 2 * kUnroll * kSide;
+  while (a.run > kSide &&
+         static_cast<int64_t>(a.num_tokens) * (a.num_heads + 2 * a.num_kv_heads) / a.run <
+             static_cast<int64_t>(sms > 0 ? sms : 152) * 16)
+    a.run = a.run / 2 > kSide ? a.run / 2 : kSide;
+  a.q_runs = (a.num_heads + a.run - 1) / a.run;
+  a.kv_runs = (a.num_kv_heads + a.run - 1) / a.run;
+  a.items = static_cast<int64_t>(a.num_tokens) * (a.q_runs + 2 * a.kv_runs);
+  if (a.items + kWarps >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  pa_rope_kernel<T, D, kInter>
+      <<<static_cast<unsigned>((a.items + kWarps - 1) / kWarps), kNT, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const RopeArgs& a, int sms, cudaStream_t s) {
+  return a.interleaved ? launch_i<T, D, true>(a, sms, s) : launch_i<T, D, false>(a, sms, s);
 }
 
 template <typename T>
@@ -301,6 +409,7 @@ extern "C" pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q,
   a.num_heads = p->num_heads;
   a.num_kv_heads = p->num_kv_heads;
   a.block_size = p->block_size;
+  a.block_shift = (p->block_size & (p->block_size - 1)) ? -1 : __builtin_ctz(p->block_size);
   a.rot = p->rotary_dim;
   a.max_position = p->max_position;
   a.interleaved = (p->flags & PA_ROPE_INTERLEAVED) ? 1 : 0;
