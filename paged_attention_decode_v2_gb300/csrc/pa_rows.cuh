@@ -301,6 +301,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// x of lane 0, for values that all lanes hold alike.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ void sync256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 }  // namespace rw
@@ -334,7 +337,10 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
   Ctrl& c = *reinterpret_cast<Ctrl*>(smem + Lay::kCtrlOff);
   int32_t* prefix_s = reinterpret_cast<int32_t*>(smem + Lay::kPrefixOff);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The warp index and what the MMA warp branches on or addresses with go
+  // through uniform(): known to be the same in all lanes, they stay in uniform
+  // registers, where the MMA instruction takes its operands from.
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const bool dual = D == 128 && a.dual;
 
   if constexpr (kPrefix) asm volatile("griddepcontrol.launch_dependents;");
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
-  const uint32_t tmem = c.tmem;
+  const uint32_t tmem = uniform(c.tmem);
   const int32_t* before = compact ? prefix_s : nullptr;
   const int total_groups = compact ? c.total_groups : 0;
   volatile int* abort_flag = &c.abort;
@@ -568,56 +574,80 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     }
     } else {
     // ========================= MMA issuer =========================================
+    // One MMA occupies the tensor core for 64 (N = 128) or 128 cycles, so
+    // issuing it must not take longer: ring slots and phases are counted, not
+    // divided out, and descriptors are a base plus compile-time offsets.
     constexpr uint32_t id_qk = sm100::idesc_f16(kBf16, false, false, 128, kTile);
     constexpr uint32_t id_pv = sm100::idesc_f16(kBf16, false, true, 128, D);
-    const uint32_t q_base = sm100::smem_u32(qs);
-    const uint32_t ring_base = sm100::smem_u32(ring);
-    uint32_t g = 0, un = 0;     // ring stages, units
+    const uint64_t q_desc = sm100::smem_desc(sm100::smem_u32(qs), 16, 1024, sm100::kSw128);
+    const uint64_t k_desc = sm100::smem_desc(sm100::smem_u32(ring), 16, 1024, sm100::kSw128);
+    // values: rows of `vbs` (block or 16) per slice
+    const uint64_t vc_desc = sm100::smem_desc(sm100::smem_u32(ring), BS * 128, 1024, sm100::kSw128);
+    const uint64_t vn_desc = sm100::smem_desc(sm100::smem_u32(ring), 16 * 128, 1024, sm100::kSw128);
+    struct Ring {
+      uint32_t slot, phase;
+      __device__ __forceinline__ void next() {
+        if (++slot == NST) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    };
+    Ring rg{0, 0};              // next stage of the ring
+    Ring rk{0, 0}, rv{0, 0};    // first stages of the current key and value tiles
+    uint32_t un = 0;            // units
     uint32_t steps[2] = {0, 0}; // P.V issued in each slot
-    uint32_t gk = 0, gv = 0;    // first stages of the current key and value tiles
     bool ok = true;
     if (a.selftest_stall) ok = __all_sync(kAll, sm100::mbar_wait(&c.never, 0, budget, abort_flag));
-    auto wait_full = [&](uint32_t gg) {
-      const bool r = __all_sync(kAll, sm100::mbar_wait(&c.full[gg % NST], (gg / NST) & 1, budget,
-                                                       abort_flag)) != 0;
+    auto wait_full = [&](const Ring& r) {
+      const bool done = __all_sync(kAll, sm100::mbar_wait(&c.full[r.slot], r.phase, budget,
+                                                          abort_flag)) != 0;
       sm100::tc_fence_after();
-      return r;
+      return done;
     };
 
     // logits of step k: fresh keys unless the other slot has just used them
     auto qk = [&](int k, bool last) -> bool {
       const int slot = k & 1;
       const bool fresh = !dual || slot == 0, done = !dual || slot == 1;
-      if (fresh) {
-        gk = g;
-        g += kSl;
-      }
-      const uint32_t qt = q_base + (dual && slot ? kSl * kStage : 0);
-      for (int sl = 0; sl < kSl; ++sl) {
-        if (fresh && !wait_full(gk + sl)) return false;
-        const uint32_t st = ring_base + ((gk + sl) % NST) * kStage;
+      if (fresh) rk = rg;
+      Ring r = rk;
+      const uint64_t qd = q_desc + (dual && slot ? kSl * kStage / 16 : 0);
+      const uint32_t d = tmem + slot * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t ad = sm100::smem_desc(qt + sl * kStage + kk * 32, 16, 1024, sm100::kSw128);
-          const uint64_t bd = sm100::smem_desc(st + kk * 32, 16, 1024, sm100::kSw128);
-          sm100::mma_f16_elect(tmem + slot * kTile, ad, bd, id_qk, (sl | kk) != 0);
-        }
-        if (done) sm100::mma_commit_elect(&c.empty[(gk + sl) % NST]);
+      for (int sl = 0; sl < kSl; ++sl) {
+        if (fresh && !wait_full(r)) return false;
+        const uint64_t kd = k_desc + r.slot * (kStage / 16);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          sm100::mma_f16_elect(d, qd + sl * (kStage / 16) + kk * 2, kd + kk * 2, id_qk,
+                               (sl | kk) != 0);
+        if (done) sm100::mma_commit_elect(&c.empty[r.slot]);
+        r.next();
       }
+      if (fresh) rg = r;
       if (last) sm100::mma_commit_elect(&c.qempty);
       sm100::mma_commit_elect(&c.s_full[slot]);
       return true;
     };
+    // the MMAs of one value stage (rows of VB per slice), `toks` keys of it
+    auto pv_stage = [&](auto vb, uint64_t vd, uint32_t at, uint32_t o, int toks, bool first) {
+      constexpr int VB = decltype(vb)::value;
+#pragma unroll
+      for (int r = 0; r < kVT; r += 16)
+        if (r < toks)
+          sm100::mma_f16_ts_elect(o, at + r / 2, vd + ((r / VB) * VB * D * 2 + (r % VB) * 128) / 16,
+                                  id_pv, !first || r != 0);
+    };
     auto pv = [&](const Unit& u, int k) -> bool {
       const int slot = k & 1;
       const Tile t = tile_of(u, dual ? k >> 1 : k);
-      const int vbs = t.ctx ? BS : 16;
-      const int nv = (t.nk + kVT - 1) / kVT;
+      const int nk = uniform(t.nk);
+      const bool ctx = kPrefix || uniform(t.ctx) != 0;
+      const int nv = (nk + kVT - 1) / kVT;
       const bool fresh = !dual || slot == 0, done = !dual || slot == 1;
-      if (fresh) {
-        gv = g;
-        g += nv;
-      }
+      if (fresh) rv = rg;
+      Ring r = rv;
       if (kChain && k == 0 && un > 1 &&
           !__all_sync(kAll, sm100::mbar_wait(&c.o_free, un & 1, budget, abort_flag)))
         return false;
@@ -628,30 +658,35 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       ++steps[slot];
       const uint32_t o = tmem + kOCol + (kChain ? 0 : slot * 128);
       const bool first = kChain ? k == 0 : k < 2;
+#pragma unroll 1
       for (int v = 0; v < nv; ++v) {
-        if (fresh && !wait_full(gv + v)) return false;
-        const uint32_t st = ring_base + ((gv + v) % NST) * kStage;
-        const int toks = min(kVT, t.nk - v * kVT);
-        for (int r = 0; r < toks; r += 16) {
-          const uint32_t at = tmem + slot * kTile + (v * kVT + r) / 2;
-          const uint64_t bd = sm100::smem_desc(st + (r / vbs) * vbs * D * 2 + (r % vbs) * 128,
-                                               vbs * 128, 1024, sm100::kSw128);
-          sm100::mma_f16_ts_elect(o, at, bd, id_pv, !first || (v | r) != 0);
-        }
-        if (done) sm100::mma_commit_elect(&c.empty[(gv + v) % NST]);
+        if (fresh && !wait_full(r)) return false;
+        const uint32_t at = tmem + slot * kTile + v * (kVT / 2);
+        const int toks = min(kVT, nk - v * kVT);
+        if (ctx)
+          pv_stage(std::integral_constant<int, BS>{}, vc_desc + r.slot * (kStage / 16), at, o, toks,
+                   first && v == 0);
+        else
+          pv_stage(std::integral_constant<int, 16>{}, vn_desc + r.slot * (kStage / 16), at, o, toks,
+                   first && v == 0);
+        if (done) sm100::mma_commit_elect(&c.empty[r.slot]);
+        r.next();
       }
+      if (fresh) rg = r;
       sm100::mma_commit_elect(&c.o_done[slot]);
       return true;
     };
 
     Walk wk = walk_begin();
     Unit u;
-    while (ok && walk_next<kPrefix>(a, before, total_groups, wk, u)) {
+    while (ok) {
+      const bool more = walk_next<kPrefix>(a, before, total_groups, wk, u);
+      if (!__all_sync(kAll, more)) break;
       ok = __all_sync(kAll, sm100::mbar_wait(&c.qfull, un & 1, budget, abort_flag));
       if (!ok) break;
       ++un;
       sm100::tc_fence_after();
-      const int K = dual ? 2 * u.tiles : u.tiles;
+      const int K = uniform(dual ? 2 * u.tiles : u.tiles);
       for (int k = 0; k < K && ok; ++k) {
         ok = qk(k, k == K - 1);
         if (ok && k > 0) ok = pv(u, k - 1);
