@@ -146,7 +146,7 @@ cudaError_t launch_portable_f16(const ListArgs& a, cudaStream_t s);
 
 // Attention of many query rows over key tiles on the tensor cores
 // (pa_rows.cuh): the windowed prefill and the shared-prefix pass.
-constexpr int kRowsMaxCompact = 1024;  // sequences whose row groups are walked compactly
+constexpr int kRowsMaxCompact = 2048;  // sequences whose row groups are walked compactly
 struct RowsArgs {
   const int32_t* block_tables;  // prefix: the prefix's blocks
   const int32_t* query_start;   // windowed prefill

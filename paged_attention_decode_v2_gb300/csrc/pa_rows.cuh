@@ -21,7 +21,8 @@
 // Steps.  A unit is a sequence of steps, each one product of a row tile with
 // a key tile: QK^T into one of two tensor-memory buffers ("slots"), softmax
 // of that slot by its own four warps, one thread per row, P written over the
-// logits in 16 bits, and P.V from tensor memory.  The MMA warp issues
+// logits in 16 bits (keys 0-63 handed on before 64-127), and P.V from tensor
+// memory.  The MMA warp issues
 // QK^T(k), P.V(k - 1), so the tensor core works on one slot while the warps of
 // the other run their softmax.
 //   head_dim 128, two row tiles ("dual"): slot s is row tile s, both against
@@ -61,8 +62,9 @@ constexpr int kProducers = 3;
 constexpr int kMmaWarp = 8;          // warps 0-7 softmax, 9 .. 8 + kProducers producers
 constexpr int kThreads = 32 * (kMmaWarp + 1 + kProducers);
 constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
-constexpr int kStage = 16384;
-constexpr int kMaxStages = 12;
+constexpr int kStage = 32768;        // ring stage: two 64-element slices of a key tile, or values
+constexpr int kSliceBytes = 16384;   // a 64-element slice of 128 rows
+constexpr int kMaxStages = 5;
 constexpr int kTmemCols = 512;       // S slot 0 | S slot 1 | O (two of 128, or one of 256)
 constexpr int kOCol = 256;
 constexpr float kRescaleLog2 = 8.f;
@@ -77,17 +79,14 @@ constexpr int kOtherRegs = 88;
 template <int D>
 struct Layout {
   static constexpr int kSlices = D / 64;
+  static constexpr int kKStages = kSlices / 2;         // ring stages of a key tile
   static constexpr int kVTokens = kStage / (D * 2);    // keys of a value stage
   static constexpr int kQBytes = 65536;                // D 128: two row tiles, D 256: one
-  static constexpr int kPrefixBytes = ((kRowsMaxCompact + 1) * 4 + 63) / 64 * 64;
-  static constexpr int kStages =
-      std::min(kMaxStages, (kSmemLimit - kQBytes - 4096 - kPrefixBytes) / kStage);
+  static constexpr int kStages = kMaxStages;
   static constexpr int kRingOff = kQBytes;
   static constexpr int kCtrlOff = kRingOff + kStages * kStage;
-  static constexpr int kPrefixOff = kCtrlOff + 3072;
-  static constexpr int kSmem = kPrefixOff + kPrefixBytes + 1024;  // + room to align to 1024
+  static constexpr int kSmem = kCtrlOff + 2048 + 1024; // + room to align to 1024
   static_assert(kSmem <= kSmemLimit, "shared memory");
-  static_assert(kStages >= 8, "a key tile and a value tile in flight");
 };
 
 struct Ctrl {
@@ -95,8 +94,8 @@ struct Ctrl {
   uint64_t empty[kMaxStages];  // stage consumed by its MMAs
   uint64_t qfull, qempty;      // row tiles landed / no longer read
   uint64_t s_full[2];          // a slot's logits ready
-  uint64_t p_ready[2];         // a slot's P written (its 128 threads arrive)
-  uint64_t o_done[2];          // the P.V of a slot's step completed
+  uint64_t p_ready[2][2];      // a slot's P written, keys 0-63 and 64-127 (128 threads arrive)
+  uint64_t o_done[2];          // the P.V of a slot's step (D 256), of its last step completed
   uint64_t m_next[2];          // D 256: the slot's step has published the reference maximum
   uint64_t o_free;             // D 256: the accumulator has been read (256 threads arrive)
   uint64_t tail[kProducers];   // producer-private: a value stage to be cleared landed
@@ -104,11 +103,11 @@ struct Ctrl {
   uint64_t never;              // self-test: nothing ever arrives here
   uint32_t tmem;
   int abort;
-  int total_groups;            // row groups of the batch (windowed prefill, compact list)
+  int before[kRowsMaxCompact / 32 + 1];  // row groups before each 32 sequences (windowed prefill)
   float mref[kTile];           // D 256: a row's reference maximum, handed from slot to slot
   float lsum[2][kTile];        // D 256: the slots' sums at the end of a unit
 };
-static_assert(sizeof(Ctrl) <= 3072, "control block");
+static_assert(sizeof(Ctrl) <= 2048, "control block");
 
 // One work unit, decoded the same way by every role.
 struct Unit {
@@ -167,9 +166,22 @@ __device__ __forceinline__ bool chunk_ok(const RowsArgs& a, int b, int32_t& s0, 
   return s0 >= 0 && s1 >= s0 && n <= a.max_query_len && s1 <= a.num_tokens;
 }
 
+// Row groups of sequences up to and including b (a lane each, from a multiple
+// of 32), and of b alone.
+__device__ __forceinline__ int groups_scan(const RowsArgs& a, int b, int& mine) {
+  int32_t s0, n;
+  mine = b < a.num_seqs && chunk_ok(a, b, s0, n) ? (n + a.group_tokens - 1) / a.group_tokens : 0;
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (static_cast<int>(threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
+}
+
 template <bool kPrefix>
-__device__ __forceinline__ bool walk_next(const RowsArgs& a, const int32_t* groups_before,
-                                          int total_groups, Walk& w, Unit& u) {
+__device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, Walk& w, Unit& u) {
   if constexpr (kPrefix) {
     const int32_t len = __ldg(a.lens);
     if (len < 1 || len > a.max_ctx_len) return false;  // the join reports it
@@ -205,20 +217,26 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int32_t* grou
     int32_t s0, n;
     while (true) {
       int b, g;
-      if (groups_before) {
-        const int64_t units = static_cast<int64_t>(total_groups) * a.num_kv_heads;
+      if (before) {
+        const int blocks = (a.num_seqs + 31) / 32;
+        const int64_t units = static_cast<int64_t>(before[blocks]) * a.num_kv_heads;
         if (w.k >= units) return false;
         const int x = static_cast<int>(w.k / a.num_kv_heads);
         u.kvh = static_cast<int>(w.k % a.num_kv_heads);
         w.k += gridDim.x;
-        int lo = 0, hi = a.num_seqs;  // largest lo with groups_before[lo] <= x
+        int lo = 0, hi = blocks;  // the 32 sequences: largest lo with before[lo] <= x
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (groups_before[mid] <= x) lo = mid;
+          if (before[mid] <= x) lo = mid;
           else hi = mid;
         }
-        b = lo;
-        g = x - groups_before[lo];
+        // the sequence among them: a lane each (the whole warp walks together)
+        const int lane = threadIdx.x & 31;
+        int mine;
+        const int upto = groups_scan(a, lo * 32 + lane, mine) + before[lo];
+        const int at = __ffs(__ballot_sync(0xffffffffu, upto > x)) - 1;
+        b = lo * 32 + at;
+        g = x - __shfl_sync(0xffffffffu, upto - mine, at);
         chunk_ok(a, b, s0, n);
       } else {
         const int64_t per = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
@@ -275,6 +293,26 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two floats in one 64-bit register, for the packed float32 instructions.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Bits e of [lo, hi) within a 32-key word that starts at key c0.
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) {
   const int a = max(lo - c0, 0), b = min(hi - c0, 32);
@@ -301,6 +339,44 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Four MMAs of one 64-element slice (descriptors 32 bytes apart), or of 64 keys
+// (P 8 columns apart), issued by one elected lane: one election for the four.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, e, t;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "setp.ne.b32 p, %10, 0;\n"
+      "setp.eq.b32 t, 0, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, t;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(a + 2), "l"(a + 4), "l"(a + 6), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6),
+      "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uint64_t b1,
+                                        uint64_t b2, uint64_t b3, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, e, t;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "setp.ne.b32 p, %10, 0;\n"
+      "setp.eq.b32 t, 0, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b0), "l"(b1), "l"(b2), "l"(b3),
+      "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
 // x of lane 0, for values that all lanes hold alike.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -312,7 +388,7 @@ __device__ __forceinline__ void sync256() { asm volatile("bar.sync 1, 256;" ::: 
 // chunk's keys and values as (64, Hkv, T, D / 64), boxes (64, 1, 128, 1) and
 // (64, 1, 16, D / 64) (windowed prefill only); kcmap / vcmap: the caches as
 // rows of head_dim (box 64 x BS, and a whole block slice-major).
-template <typename T, int D, int BS, bool kPrefix>
+template <typename T, int D, int BS, bool kPrefix, bool kDual>
 __global__ void __launch_bounds__(rw::kThreads, 1)
     pa_rows_kernel(const RowsArgs a, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap knmap,
@@ -335,13 +411,13 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
   uint8_t* qs = smem;
   uint8_t* ring = smem + Lay::kRingOff;
   Ctrl& c = *reinterpret_cast<Ctrl*>(smem + Lay::kCtrlOff);
-  int32_t* prefix_s = reinterpret_cast<int32_t*>(smem + Lay::kPrefixOff);
 
   // The warp index and what the MMA warp branches on or addresses with go
   // through uniform(): known to be the same in all lanes, they stay in uniform
   // registers, where the MMA instruction takes its operands from.
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const bool dual = D == 128 && a.dual;
+  static_assert(!kDual || D == 128, "two row tiles");
+  constexpr bool dual = kDual;
 
   if constexpr (kPrefix) asm volatile("griddepcontrol.launch_dependents;");
 
@@ -354,7 +430,8 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     sm100::mbar_init(&c.qempty, 1);
     for (int s = 0; s < 2; ++s) {
       sm100::mbar_init(&c.s_full[s], 1);
-      sm100::mbar_init(&c.p_ready[s], 128);
+      sm100::mbar_init(&c.p_ready[s][0], 128);
+      sm100::mbar_init(&c.p_ready[s][1], 128);
       sm100::mbar_init(&c.o_done[s], 1);
       sm100::mbar_init(&c.m_next[s], 128);
     }
@@ -381,38 +458,23 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       sm100::tma_prefetch_desc(&vnmap);
     }
   }
-  // windowed prefill of up to kRowsMaxCompact sequences: row groups before
-  // each sequence, so that only existing groups are walked
+  // windowed prefill of up to kRowsMaxCompact sequences: only row groups that
+  // exist are walked
   const bool compact = !kPrefix && a.num_seqs <= kRowsMaxCompact;
   if (compact && warp == 0) {
-    int carry = 0;
+    int carry = 0, mine;
     for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
-      const int b = b0 + lane;
-      int x = 0;
-      if (b < a.num_seqs) {
-        int32_t s0, n;
-        if (chunk_ok(a, b, s0, n)) x = (n + a.group_tokens - 1) / a.group_tokens;
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAll, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b < a.num_seqs) prefix_s[b + 1] = carry + x;
-      carry += __shfl_sync(kAll, x, 31);
+      if (lane == 0) c.before[b0 / 32] = carry;
+      carry += __shfl_sync(kAll, groups_scan(a, b0 + lane, mine), 31);
     }
-    if (lane == 0) {
-      prefix_s[0] = 0;
-      c.total_groups = carry;
-    }
+    if (lane == 0) c.before[(a.num_seqs + 31) / 32] = carry;
   }
   sm100::fence_proxy_async_smem();
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
   const uint32_t tmem = uniform(c.tmem);
-  const int32_t* before = compact ? prefix_s : nullptr;
-  const int total_groups = compact ? c.total_groups : 0;
+  const int* before = compact ? c.before : nullptr;
   volatile int* abort_flag = &c.abort;
 
   if (warp >= kMmaWarp) {
@@ -453,21 +515,28 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     };
 
     auto issue_k = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
+      constexpr int kMaxBlk = kTile / BS;
       const int nblk = (t.nk + BS - 1) / BS;
-      for (int sl = 0; sl < kSl; ++sl, ++g) {
+      for (int sl = 0; sl < kSl; sl += 2, ++g) {
         if (g % kProducers != pid) continue;
         const int slot = g % NST;
         if (!wait_empty(slot)) return false;
         uint8_t* st = ring + slot * kStage;
         if (t.ctx) {
-          if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], nblk * BS * 128);
+          // one lane per block and slice
+          const int blk = lane % kMaxBlk, half = lane / kMaxBlk;
+          const int32_t yj = __shfl_sync(kAll, y, blk);
+          if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], 2 * nblk * BS * 128);
           __syncwarp();
-          if (lane < nblk)
-            sm100::tma_load_2d(st + lane * BS * 128, &kcmap, &c.full[slot], sl * 64, y, keep);
-        } else if (lane == 0) {
-          sm100::mbar_arrive_expect_tx(&c.full[slot], kStage);
-          sm100::tma_load_4d(st, &knmap, &c.full[slot], 0, u.kvh,
-                             static_cast<int32_t>(u.row0) + t.chunk, sl, keep);
+          if (half < 2 && blk < nblk)
+            sm100::tma_load_2d(st + half * kSliceBytes + blk * BS * 128, &kcmap, &c.full[slot],
+                               (sl + half) * 64, yj, keep);
+        } else {
+          if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], kStage);
+          __syncwarp();
+          if (lane < 2)
+            sm100::tma_load_4d(st + lane * kSliceBytes, &knmap, &c.full[slot], 0, u.kvh,
+                               static_cast<int32_t>(u.row0) + t.chunk, sl + lane, keep);
         }
         __syncwarp();
       }
@@ -530,7 +599,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
 
     Walk wk = walk_begin();
     Unit u;
-    while (ok && walk_next<kPrefix>(a, before, total_groups, wk, u)) {
+    while (ok && walk_next<kPrefix>(a, before, wk, u)) {
       if (pid == 0) {
         ok = __all_sync(kAll, sm100::mbar_wait(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
         if (!ok) break;
@@ -540,7 +609,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         if (lane == 0) sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
         __syncwarp();
         if (lane < copies)
-          sm100::tma_load_4d(qs + lane * kStage, &qmap, &c.qfull, 0, u.kvh * a.group,
+          sm100::tma_load_4d(qs + lane * kSliceBytes, &qmap, &c.qfull, 0, u.kvh * a.group,
                              static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
                              lane % kSl, keep);
         ++un;
@@ -574,9 +643,11 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     }
     } else {
     // ========================= MMA issuer =========================================
-    // One MMA occupies the tensor core for 64 (N = 128) or 128 cycles, so
-    // issuing it must not take longer: ring slots and phases are counted, not
-    // divided out, and descriptors are a base plus compile-time offsets.
+    // One MMA occupies the tensor core for 64 (N = 128) or 128 cycles and this
+    // warp issues in order, one instruction every few cycles, so every
+    // instruction between MMAs counts: slots are compile-time, ring positions
+    // are counted, descriptors are a base plus constants, four MMAs share an
+    // election, and nothing is waited for that an earlier wait implies.
     constexpr uint32_t id_qk = sm100::idesc_f16(kBf16, false, false, 128, kTile);
     constexpr uint32_t id_pv = sm100::idesc_f16(kBf16, false, true, 128, D);
     const uint64_t q_desc = sm100::smem_desc(sm100::smem_u32(qs), 16, 1024, sm100::kSw128);
@@ -594,104 +665,160 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       }
     };
     Ring rg{0, 0};              // next stage of the ring
-    Ring rk{0, 0}, rv{0, 0};    // first stages of the current key and value tiles
+    Ring rk{0, 0}, rv{0, 0};    // dual: stages of the current key and value tiles
     uint32_t un = 0;            // units
-    uint32_t steps[2] = {0, 0}; // P.V issued in each slot
+    uint32_t parity[2] = {0, 0};  // of the P.V in each slot
     bool ok = true;
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
     if (a.selftest_stall) ok = __all_sync(kAll, sm100::mbar_wait(&c.never, 0, budget, abort_flag));
-    auto wait_full = [&](const Ring& r) {
-      const bool done = __all_sync(kAll, sm100::mbar_wait(&c.full[r.slot], r.phase, budget,
-                                                          abort_flag)) != 0;
+    auto wait_for = [&](uint64_t* bar, uint32_t phase) {
+      const bool r = __all_sync(kAll, sm100::mbar_wait(bar, phase, budget, abort_flag)) != 0;
       sm100::tc_fence_after();
-      return done;
+      return r;
     };
-
-    // logits of step k: fresh keys unless the other slot has just used them
-    auto qk = [&](int k, bool last) -> bool {
-      const int slot = k & 1;
-      const bool fresh = !dual || slot == 0, done = !dual || slot == 1;
-      if (fresh) rk = rg;
+    // logits into slot S: keys from the ring, or (dual, slot 1) those in hand
+    auto qk = [&](auto slot) -> bool {
+      constexpr int S = decltype(slot)::value;
+      constexpr bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
+      if constexpr (kFresh) rk = rg;
       Ring r = rk;
-      const uint64_t qd = q_desc + (dual && slot ? kSl * kStage / 16 : 0);
-      const uint32_t d = tmem + slot * kTile;
+      const uint32_t d = tmem + S * kTile;
+      const uint64_t qd = q_desc + (kDual && S ? kSl * kSliceBytes / 16 : 0);
 #pragma unroll
-      for (int sl = 0; sl < kSl; ++sl) {
-        if (fresh && !wait_full(r)) return false;
+      for (int st = 0; st < Lay::kKStages; ++st) {
+        if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
         const uint64_t kd = k_desc + r.slot * (kStage / 16);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          sm100::mma_f16_elect(d, qd + sl * (kStage / 16) + kk * 2, kd + kk * 2, id_qk,
-                               (sl | kk) != 0);
-        if (done) sm100::mma_commit_elect(&c.empty[r.slot]);
+        mma4_ss(d, qd + 2 * st * (kSliceBytes / 16), kd, id_qk, st != 0);
+        mma4_ss(d, qd + (2 * st + 1) * (kSliceBytes / 16), kd + kSliceBytes / 16, id_qk, true);
+        if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
         r.next();
       }
-      if (fresh) rg = r;
-      if (last) sm100::mma_commit_elect(&c.qempty);
-      sm100::mma_commit_elect(&c.s_full[slot]);
+      if constexpr (kFresh) rg = r;
       return true;
     };
-    // the MMAs of one value stage (rows of VB per slice), `toks` keys of it
-    auto pv_stage = [&](auto vb, uint64_t vd, uint32_t at, uint32_t o, int toks, bool first) {
-      constexpr int VB = decltype(vb)::value;
+    // the MMAs of keys r0 .. r0 + 63 of one value stage (rows of VB per slice),
+    // as many as the stage's `toks` keys reach
+    auto pv_part = [&](auto vb, auto from, uint64_t vd, uint32_t at, uint32_t o, int toks,
+                       bool first) {
+      constexpr int VB = decltype(vb)::value, r0 = decltype(from)::value;
+      constexpr auto off = [](int r) {
+        return static_cast<uint64_t>(((r / VB) * VB * D * 2 + (r % VB) * 128) / 16);
+      };
+      if (toks >= r0 + 64) {
+        mma4_ts(o, at + r0 / 2, vd + off(r0), vd + off(r0 + 16), vd + off(r0 + 32),
+                vd + off(r0 + 48), id_pv, !first || r0 != 0);
+        return;
+      }
 #pragma unroll
-      for (int r = 0; r < kVT; r += 16)
-        if (r < toks)
-          sm100::mma_f16_ts_elect(o, at + r / 2, vd + ((r / VB) * VB * D * 2 + (r % VB) * 128) / 16,
-                                  id_pv, !first || r != 0);
+      for (int r = r0; r < r0 + 64; r += 16)
+        if (r < toks) sm100::mma_f16_ts_elect(o, at + r / 2, vd + off(r), id_pv, !first || r != 0);
     };
-    auto pv = [&](const Unit& u, int k) -> bool {
-      const int slot = k & 1;
-      const Tile t = tile_of(u, dual ? k >> 1 : k);
-      const int nk = uniform(t.nk);
-      const bool ctx = kPrefix || uniform(t.ctx) != 0;
-      const int nv = (nk + kVT - 1) / kVT;
-      const bool fresh = !dual || slot == 0, done = !dual || slot == 1;
-      if (fresh) rv = rg;
+    auto pv_keys = [&](bool ctx, auto from, uint32_t slot, uint32_t at, uint32_t o, int toks,
+                       bool first) {
+      if (kPrefix || ctx)
+        pv_part(std::integral_constant<int, BS>{}, from, vc_desc + slot * (kStage / 16), at, o,
+                toks, first);
+      else
+        pv_part(std::integral_constant<int, 16>{}, from, vn_desc + slot * (kStage / 16), at, o,
+                toks, first);
+    };
+    // P.V of slot S over a tile of nk keys; `first`: the accumulator starts anew
+    auto pv = [&](auto slot, int nk, bool ctx, bool first) -> bool {
+      constexpr int S = decltype(slot)::value;
+      constexpr bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
+      if constexpr (kFresh) rv = rg;
       Ring r = rv;
-      if (kChain && k == 0 && un > 1 &&
-          !__all_sync(kAll, sm100::mbar_wait(&c.o_free, un & 1, budget, abort_flag)))
-        return false;
-      if (!__all_sync(kAll, sm100::mbar_wait(&c.p_ready[slot], steps[slot] & 1, budget,
-                                             abort_flag)))
-        return false;
-      sm100::tc_fence_after();
-      ++steps[slot];
-      const uint32_t o = tmem + kOCol + (kChain ? 0 : slot * 128);
-      const bool first = kChain ? k == 0 : k < 2;
-#pragma unroll 1
-      for (int v = 0; v < nv; ++v) {
-        if (fresh && !wait_full(r)) return false;
-        const uint32_t at = tmem + slot * kTile + v * (kVT / 2);
-        const int toks = min(kVT, nk - v * kVT);
-        if (ctx)
-          pv_stage(std::integral_constant<int, BS>{}, vc_desc + r.slot * (kStage / 16), at, o, toks,
-                   first && v == 0);
-        else
-          pv_stage(std::integral_constant<int, 16>{}, vn_desc + r.slot * (kStage / 16), at, o, toks,
-                   first && v == 0);
-        if (done) sm100::mma_commit_elect(&c.empty[r.slot]);
+      if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
+      if (!wait_for(&c.p_ready[S][0], parity[S])) return false;
+      const uint32_t o = tmem + kOCol + (kChain ? 0 : S * 128);
+      const uint32_t at = tmem + S * kTile;
+      // keys 0-63, then, when their P is there too, keys 64-127
+      pv_keys(ctx, S0{}, r.slot, at, o, nk, first);
+      if constexpr (kVT == 64) {
+        if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
         r.next();
       }
-      if (fresh) rg = r;
-      sm100::mma_commit_elect(&c.o_done[slot]);
+      if (!wait_for(&c.p_ready[S][1], parity[S])) return false;
+      parity[S] ^= 1;
+      if constexpr (kVT == 64) {
+        if (nk > 64) {
+          if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
+          pv_keys(ctx, S0{}, r.slot, at + 32, o, nk - 64, false);
+          if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
+          r.next();
+        }
+      } else {
+        if (nk > 64) pv_keys(ctx, std::integral_constant<int, 64>{}, r.slot, at, o, nk, false);
+        if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
+        r.next();
+      }
+      if constexpr (kFresh) rg = r;
+      // a step's softmax may have to rescale the accumulator: with one
+      // accumulator per slot, the logits it has waited for imply that the
+      // slot's last P.V is done; with one for both slots they do not
+      if constexpr (kChain) sm100::mma_commit_elect(&c.o_done[S]);
       return true;
     };
 
     Walk wk = walk_begin();
     Unit u;
     while (ok) {
-      const bool more = walk_next<kPrefix>(a, before, total_groups, wk, u);
+      const bool more = walk_next<kPrefix>(a, before, wk, u);
       if (!__all_sync(kAll, more)) break;
-      ok = __all_sync(kAll, sm100::mbar_wait(&c.qfull, un & 1, budget, abort_flag));
+      ok = wait_for(&c.qfull, un & 1);
       if (!ok) break;
       ++un;
-      sm100::tc_fence_after();
-      const int K = uniform(dual ? 2 * u.tiles : u.tiles);
-      for (int k = 0; k < K && ok; ++k) {
-        ok = qk(k, k == K - 1);
-        if (ok && k > 0) ok = pv(u, k - 1);
+      const int tiles = uniform(u.tiles);
+      int nk = 0, nk_prev = 0;
+      bool ctx = true, ctx_prev = true;
+      for (int j = 0; j < tiles && ok; ++j) {
+        {
+          const Tile t = tile_of(u, j);
+          const int both = uniform(t.nk | (t.ctx ? 256 : 0));
+          nk = both & 255;
+          ctx = (both & 256) != 0;
+        }
+        if constexpr (kDual) {
+          ok = qk(S0{});
+          if (!ok) break;
+          sm100::mma_commit_elect(&c.s_full[0]);
+          if (j > 0 && !(ok = pv(S1{}, nk_prev, ctx_prev, j == 1))) break;
+          ok = qk(S1{});
+          if (!ok) break;
+          if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
+          sm100::mma_commit_elect(&c.s_full[1]);
+          ok = pv(S0{}, nk, ctx, j == 0);
+        } else {
+          ok = j & 1 ? qk(S1{}) : qk(S0{});
+          if (!ok) break;
+          if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
+          sm100::mma_commit_elect(&c.s_full[j & 1]);
+          if (j > 0) {
+            // one accumulator: not before the last unit's has been read
+            if (kChain && j == 1 && un > 1) ok = wait_for(&c.o_free, un & 1);
+            if (ok)
+              ok = j & 1 ? pv(S0{}, nk_prev, ctx_prev, kChain ? j == 1 : j <= 2)
+                         : pv(S1{}, nk_prev, ctx_prev, kChain ? j == 1 : j <= 2);
+          }
+        }
+        nk_prev = nk;
+        ctx_prev = ctx;
       }
-      if (ok) ok = pv(u, K - 1);
+      if (!ok) break;
+      if constexpr (kDual) {
+        sm100::mma_commit_elect(&c.o_done[0]);
+        ok = pv(S1{}, nk_prev, ctx_prev, tiles == 1);
+        sm100::mma_commit_elect(&c.o_done[1]);
+      } else {
+        if (kChain && tiles == 1 && un > 1) ok = wait_for(&c.o_free, un & 1);
+        // the slot before the last is done with its accumulator
+        if (!kChain && tiles > 1) sm100::mma_commit_elect(&c.o_done[tiles & 1]);
+        if (ok)
+          ok = tiles & 1 ? pv(S0{}, nk_prev, ctx_prev, kChain ? tiles == 1 : tiles <= 2)
+                         : pv(S1{}, nk_prev, ctx_prev, kChain ? tiles == 1 : tiles <= 2);
+        if (!kChain) sm100::mma_commit_elect(&c.o_done[(tiles - 1) & 1]);
+      }
     }
     if (!ok) {
       if (lane == 0) c.abort = 1;
@@ -715,6 +842,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     const uint32_t obuf = tmem + lane_base + kOCol + (kChain ? 0 : slot * 128);
     const float sl2 = a.scale_log2;
     uint32_t done[2] = {0, 0};  // steps of each slot in the units before
+    uint32_t units = 0;         // units in which this slot had a step
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!sm100::mbar_wait(bar, parity & 1, budget, abort_flag)) c.abort = 1;
     };
@@ -724,7 +852,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     const bool row_in = tok < a.row_tokens;
     Walk wk = walk_begin();
     Unit u;
-    while (walk_next<kPrefix>(a, before, total_groups, wk, u)) {
+    while (walk_next<kPrefix>(a, before, wk, u)) {
       const int K = dual ? 2 * u.tiles : u.tiles;
       const int32_t i = u.i0 + tile * a.row_tokens + tok;
       const bool row_ok = row_in && i < u.n;
@@ -796,10 +924,12 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         if (has_o && __any_sync(kAll, move)) {
           // the accumulator must hold every step before this one
           const float corr = move ? (m_in == -INFINITY ? 0.f : exp2f(m_in - m_ref)) : 1.f;
-          const int o = kChain ? slot ^ 1 : slot;
-          wait(&c.o_done[o], done[o] + (kChain ? (k - 1) >> 1 : (k >> 1) - 1));
-          sm100::tc_fence_after();
-          __syncwarp();
+          // (one accumulator per slot: it does, see the MMA warp)
+          if constexpr (kChain) {
+            wait(&c.o_done[slot ^ 1], done[slot ^ 1] + ((k - 1) >> 1));
+            sm100::tc_fence_after();
+            __syncwarp();
+          }
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
             float ov[16];
@@ -814,23 +944,30 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         // p = 2^(s * scale * log2(e) - m), two keys per 32-bit column over the
         // logits this thread has read
         const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-        float add[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sc2 = pair(sl2, sl2), neg2 = pair(neg_m, neg_m);
+        uint64_t add[2] = {0, 0};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float p0 = ex2_approx(fmaf(s[32 * q + e], sl2, neg_m));
-            const float p1 = ex2_approx(fmaf(s[32 * q + e + 1], sl2, neg_m));
-            add[(e >> 1) & 3] += p0 + p1;
+            float p0, p1;
+            unpair(fma2(pair(s[32 * q + e], s[32 * q + e + 1]), sc2, neg2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            add[(e >> 1) & 1] = add2(add[(e >> 1) & 1], pair(p0, p1));
             w[e / 2] = __uint_as_float(pack16(p0, p1, static_cast<T*>(nullptr)));
           }
           sm100::tmem_st16(sbuf + 16 * q, w);
+          if (q & 1) {
+            sm100::tmem_wait_st();
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(&c.p_ready[slot][q >> 1]);
+          }
         }
-        sm100::tmem_wait_st();
-        sm100::tc_fence_before();
-        sm100::mbar_arrive(&c.p_ready[slot]);
-        lsum += (add[0] + add[1]) + (add[2] + add[3]);
+        float sum0, sum1;
+        unpair(add2(add[0], add[1]), sum0, sum1);
+        lsum += sum0 + sum1;
         bad |= __any_sync(kAll, blk_id < 0 || blk_id >= a.num_blocks) != 0;
       }
       // ---- epilogue: the row's accumulator over its sum ----------------------------
@@ -851,7 +988,8 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         const int o = (K - 1) & 1;
         wait(&c.o_done[o], done[o] + ((K - 1) >> 1));
       } else if (mine > 0) {
-        wait(&c.o_done[slot], done[slot] + mine - 1);
+        wait(&c.o_done[slot], units);
+        ++units;
       }
       sm100::tc_fence_after();
       __syncwarp();
@@ -900,12 +1038,12 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
 
 // Persistent launch: one CTA per SM (it takes nearly all shared memory and all
 // tensor-memory columns).
-template <typename T, int D, int BS, bool kPrefix>
+template <typename T, int D, int BS, bool kPrefix, bool kDual>
 cudaError_t launch_rows_v(const RowsArgs& a, const CUtensorMap (&m)[5], int grid, bool pdl,
                           cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-  auto kern = pa_rows_kernel<T, D, BS, kPrefix>;
+  auto kern = pa_rows_kernel<T, D, BS, kPrefix, kDual>;
   // set once per device; concurrent first calls set the same attribute
   static std::atomic<bool> configured[128];
   if (!configured[dev].load(std::memory_order_acquire)) {
@@ -928,19 +1066,26 @@ cudaError_t launch_rows_v(const RowsArgs& a, const CUtensorMap (&m)[5], int grid
   return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1], m[2], m[3], m[4], budget);
 }
 
+template <typename T, int BS, bool kPrefix>
+cudaError_t launch_rows_128(const RowsArgs& a, const CUtensorMap (&m)[5], int grid, bool pdl,
+                            cudaStream_t s) {
+  // a windowed prefill always takes two row tiles
+  if constexpr (kPrefix)
+    if (!a.dual) return launch_rows_v<T, 128, BS, kPrefix, false>(a, m, grid, pdl, s);
+  return launch_rows_v<T, 128, BS, kPrefix, true>(a, m, grid, pdl, s);
+}
+
 template <typename T, bool kPrefix>
 cudaError_t launch_rows_t(const RowsArgs& a, const CUtensorMap (&m)[5], int grid, bool pdl,
                           cudaStream_t s) {
   if (a.head_dim == 256 && a.block_size == 16)
-    return launch_rows_v<T, 256, 16, kPrefix>(a, m, grid, pdl, s);
+    return launch_rows_v<T, 256, 16, kPrefix, false>(a, m, grid, pdl, s);
   if (a.head_dim == 256 && a.block_size == 32)
-    return launch_rows_v<T, 256, 32, kPrefix>(a, m, grid, pdl, s);
-  if (a.head_dim == 128 && a.block_size == 16)
-    return launch_rows_v<T, 128, 16, kPrefix>(a, m, grid, pdl, s);
-  if (a.head_dim == 128 && a.block_size == 32)
-    return launch_rows_v<T, 128, 32, kPrefix>(a, m, grid, pdl, s);
-  if (a.head_dim == 128 && a.block_size == 64)
-    return launch_rows_v<T, 128, 64, kPrefix>(a, m, grid, pdl, s);
+    return launch_rows_v<T, 256, 32, kPrefix, false>(a, m, grid, pdl, s);
+  if (a.head_dim != 128) return cudaErrorInvalidValue;
+  if (a.block_size == 16) return launch_rows_128<T, 16, kPrefix>(a, m, grid, pdl, s);
+  if (a.block_size == 32) return launch_rows_128<T, 32, kPrefix>(a, m, grid, pdl, s);
+  if (a.block_size == 64) return launch_rows_128<T, 64, kPrefix>(a, m, grid, pdl, s);
   return cudaErrorInvalidValue;
 }
 
