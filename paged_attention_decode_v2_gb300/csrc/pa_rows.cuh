@@ -293,6 +293,13 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The largest of three in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Two floats in one 64-bit register, for the packed float32 instructions.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t r;
@@ -897,39 +904,57 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
               if (!(bits >> e & 1u)) s[32 * q + e] = -INFINITY;
           }
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < kTile; e += 8)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], fmaxf(s[e + 2 * x], s[e + 2 * x + 1]));
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-        // the row's reference maximum
+        // The row's reference maximum before this step: the slot's own, or the
+        // other slot's after the step before.  P is computed against it at once,
+        // while the tile's maximum is still being found; only when that exceeds
+        // the reference by more than 2^8 (the first tile, rarely later) the
+        // reference moves, what the sum and the accumulator hold is rescaled, and
+        // the first keys are taken again.
         const float m_old = m_ref;
-        float m_in = m_ref;     // before this step (from the other slot, if handed on)
         if constexpr (kChain) {
           if (k > 0) {
             const int o = slot ^ 1;
             wait(&c.m_next[o], done[o] + ((k - 1) >> 1));
-            m_in = c.mref[r];
+            m_ref = c.mref[r];
           }
         }
-        const bool move = mt > m_in + kRescaleLog2 || (m_in == -INFINITY && mt > -INFINITY);
-        m_ref = move ? mt : m_in;
+        const float m_in = m_ref;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < kTile; e += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[e + 2 * x], s[e + 2 * x + 1]);
+        const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;
+        const bool move = mt > m_in + kRescaleLog2;  // also from -inf
+        if (move) m_ref = mt;
         if constexpr (kChain) {
           c.mref[r] = m_ref;
           sm100::mbar_arrive(&c.m_next[slot]);
         }
-        if (m_ref != m_old) lsum *= m_old == -INFINITY ? 0.f : exp2f(m_old - m_ref);
-        const bool has_o = kChain ? k > 0 : k >= 2;
-        if (has_o && __any_sync(kAll, move)) {
-          // the accumulator must hold every step before this one
+        // p = 2^(s * scale * log2(e) - m), two keys per 32-bit column over the
+        // logits this thread has read
+        float neg_m = m_in == -INFINITY ? 0.f : -m_in;
+        const uint64_t sc2 = pair(sl2, sl2);
+        uint64_t neg2, add[2];
+        auto exps = [&](int e0, float (&w)[16]) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            unpair(fma2(pair(s[e0 + e], s[e0 + e + 1]), sc2, neg2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            add[(e >> 1) & 1] = add2(add[(e >> 1) & 1], pair(p0, p1));
+            w[e / 2] = __uint_as_float(pack16(p0, p1, static_cast<T*>(nullptr)));
+          }
+        };
+        // what the accumulator holds of the steps before, at the new reference
+        auto rescale = [&]() {
           const float corr = move ? (m_in == -INFINITY ? 0.f : exp2f(m_in - m_ref)) : 1.f;
-          // (one accumulator per slot: it does, see the MMA warp)
           if constexpr (kChain) {
             wait(&c.o_done[slot ^ 1], done[slot ^ 1] + ((k - 1) >> 1));
             sm100::tc_fence_after();
             __syncwarp();
-          }
+          }  // one accumulator per slot is complete: see the MMA warp
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
             float ov[16];
@@ -940,31 +965,35 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
             sm100::tmem_st16(obuf + c0, ov);
           }
           sm100::tmem_wait_st();
-        }
-        // p = 2^(s * scale * log2(e) - m), two keys per 32-bit column over the
-        // logits this thread has read
-        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t sc2 = pair(sl2, sl2), neg2 = pair(neg_m, neg_m);
-        uint64_t add[2] = {0, 0};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float w[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float p0, p1;
-            unpair(fma2(pair(s[32 * q + e], s[32 * q + e + 1]), sc2, neg2), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            add[(e >> 1) & 1] = add2(add[(e >> 1) & 1], pair(p0, p1));
-            w[e / 2] = __uint_as_float(pack16(p0, p1, static_cast<T*>(nullptr)));
+        };
+        // head_dim 256 leaves the softmax twice the time (its products take
+        // twice as long): there the reference is moved first
+        float w0[16], w1[16];
+        for (bool again = kChain;;) {
+          if (again && __any_sync(kAll, move)) {
+            neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+            if (kChain ? k > 0 : k >= 2) rescale();
           }
-          sm100::tmem_st16(sbuf + 16 * q, w);
-          if (q & 1) {
-            sm100::tmem_wait_st();
-            sm100::tc_fence_before();
-            sm100::mbar_arrive(&c.p_ready[slot][q >> 1]);
-          }
+          neg2 = pair(neg_m, neg_m);
+          add[0] = add[1] = 0;
+          exps(0, w0);
+          exps(32, w1);
+          if (again || !__any_sync(kAll, move)) break;
+          again = true;
         }
+        if (m_ref != m_old) lsum *= m_old == -INFINITY ? 0.f : exp2f(m_old - m_ref);
+        sm100::tmem_st16(sbuf, w0);
+        sm100::tmem_st16(sbuf + 16, w1);
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        sm100::mbar_arrive(&c.p_ready[slot][0]);
+        exps(64, w0);
+        sm100::tmem_st16(sbuf + 32, w0);
+        exps(96, w1);
+        sm100::tmem_st16(sbuf + 48, w1);
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        sm100::mbar_arrive(&c.p_ready[slot][1]);
         float sum0, sum1;
         unpair(add2(add[0], add[1]), sum0, sum1);
         lsum += sum0 + sum1;

@@ -264,7 +264,11 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
   int32_t* prefix_s = reinterpret_cast<int32_t*>(smem + Lay::kPrefixOff);
   Ctrl& c = *reinterpret_cast<Ctrl*>(smem + Lay::kCtrlOff);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The warp index, and what the MMA warp branches on or addresses with, come
+  // from one lane: known to be the same in all of them, they stay in uniform
+  // registers, where the MMA instruction takes its operands from.
+  auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int G = a.group, Hq = a.num_heads;
   // Clusters of cs CTAs (cs == 1: none) share each work item: cluster cid
   // takes items cid, cid + clusters, ...; CTA `rank` streams its share of the
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
   sm100::tc_fence_after();
   // peers' barriers must be initialised before any CTA signals them
   if (cs > 1) sm100::cluster_sync_all();
-  const uint32_t tmem = c.tmem;
+  const uint32_t tmem = uniform(c.tmem);
   const int64_t total_items = c.total_items;
   volatile int* abort_flag = &c.abort;
 
@@ -595,40 +599,56 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
       const uint32_t q_base = sm100::smem_u32(qs);
       const uint32_t pt_base = sm100::smem_u32(pt);
       const uint32_t ring_base = sm100::smem_u32(ring);
-      uint32_t g = 0, qn = 0, cc = 0;
+      // Issuing must not take longer than the MMAs: ring slots and phases are
+      // counted, descriptors are a base plus constants.
+      const uint64_t k_desc = sm100::smem_desc(ring_base, 16, 1024, sm100::kSw128);
+      const uint64_t v_desc = sm100::smem_desc(ring_base, BS * 128, 1024, sm100::kSw128);
+      const uint64_t q_desc = sm100::smem_desc(q_base, 16, 1024, sm100::kSw128);
+      const uint64_t p_desc = sm100::smem_desc(pt_base, 256, 128, sm100::kSwNone);
+      uint32_t slot = 0, phase = 0, qn = 0, cc = 0;
+      auto next_slot = [&]() {
+        if (++slot == NST) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      auto wait_full = [&]() {
+        const bool r =
+            __all_sync(kAll, sm100::mbar_wait(&c.full[slot], phase, budget, abort_flag)) != 0;
+        sm100::tc_fence_after();
+        return r;
+      };
       bool ok = true;
       // diagnostic: wait for an event that never happens, so the bounded
       // wait runs out and the abort path is exercised
       if (a.selftest_stall) ok = __all_sync(kAll, sm100::mbar_wait(&c.never, 0, budget, abort_flag));
-      for (int64_t k = cid; k < total_items && ok; k += stride) {
+      const int64_t items = (static_cast<int64_t>(uniform(static_cast<int>(total_items >> 32))) << 32) |
+                            static_cast<uint32_t>(uniform(static_cast<int>(total_items)));
+      for (int64_t k = cid; k < items && ok; k += stride) {
         const Item it = item_at<kWin>(a, prefix, k, kV2, rank, cs);
-        if (it.t0 >= it.t1) continue;
+        const int len = uniform(it.t1 - it.t0);
+        if (len <= 0) continue;
         const int qb = qn & 1;
         ok = __all_sync(kAll, sm100::mbar_wait(&c.qfull[qb], (qn >> 1) & 1, budget, abort_flag));
         if (!ok) break;
         ++qn;
-        const uint32_t qbuf = q_base + qb * Lay::kSlices * 1024;
-        const int nchunks = (it.t1 - it.t0 + kChunk - 1) / kChunk;
+        const uint64_t qd = q_desc + qb * Lay::kSlices * (1024 / 16);
+        const int nchunks = (len + kChunk - 1) / kChunk;
         for (int ci = 0; ci < nchunks && ok; ++ci, ++cc) {
-          const int c0 = it.t0 + ci * kChunk;
-          const int n = min(kChunk, it.t1 - c0);
+          const int n = min(kChunk, len - ci * kChunk);
           const int nt = (n + kTile - 1) / kTile;
           for (int tt = 0; tt < nt && ok; ++tt) {
-            for (int sl = 0; sl < Lay::kSlices; ++sl) {
-              const int slot = g % NST;
-              ok = __all_sync(kAll, sm100::mbar_wait(&c.full[slot], (g / NST) & 1, budget, abort_flag));
-              if (!ok) break;
-              sm100::tc_fence_after();
-              const uint32_t st = ring_base + slot * kStageBytes;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t ad = sm100::smem_desc(st + kk * 32, 16, 1024, sm100::kSw128);
-                const uint64_t bd =
-                    sm100::smem_desc(qbuf + sl * 1024 + kk * 32, 16, 1024, sm100::kSw128);
-                sm100::mma_f16_elect(tmem + tt * 16, ad, bd, id_qk, (sl | kk) != 0);
-              }
+            for (int sl = 0; sl < Lay::kSlices; ++sl) {
+              ok = wait_full();
+              if (!ok) break;
+              const uint64_t kd = k_desc + slot * (kStageBytes / 16);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                sm100::mma_f16_elect(tmem + tt * 16, kd + kk * 2, qd + sl * (1024 / 16) + kk * 2,
+                                     id_qk, (sl | kk) != 0);
               sm100::mma_commit_elect(&c.empty[slot]);
-              ++g;
+              next_slot();
             }
           }
           if (!ok) break;
@@ -638,29 +658,24 @@ __global__ void __launch_bounds__(tc::kThreads, CPS)
           if (!ok) break;
           sm100::tc_fence_after();
           const int nv = (n + Lay::kVTokens - 1) / Lay::kVTokens;
-          bool first = true;
           for (int v = 0; v < nv; ++v) {
-            const int slot = g % NST;
-            ok = __all_sync(kAll, sm100::mbar_wait(&c.full[slot], (g / NST) & 1, budget, abort_flag));
+            ok = wait_full();
             if (!ok) break;
-            sm100::tc_fence_after();
-            const uint32_t st = ring_base + slot * kStageBytes;
+            const uint64_t vd = v_desc + slot * (kStageBytes / 16);
+            const uint64_t pd = p_desc + v * (Lay::kVTokens / 16) * (512 / 16);
             const int toks = min(Lay::kVTokens, n - v * Lay::kVTokens);
-            for (int r = 0; r < toks; r += 16) {
-              const int jb = r / BS, s0 = r % BS;
-              const uint64_t bd = sm100::smem_desc(pt_base + ((v * Lay::kVTokens + r) / 16) * 512,
-                                                   256, 128, sm100::kSwNone);
 #pragma unroll
-              for (int j = 0; j < Lay::kHalves; ++j) {
-                const uint64_t ad =
-                    sm100::smem_desc(st + jb * BS * D * 2 + 2 * j * BS * 128 + s0 * 128, BS * 128,
-                                     1024, sm100::kSw128);
-                sm100::mma_f16_elect(tmem + kOCol + 16 * j, ad, bd, id_pv, !first);
-              }
-              first = false;
+            for (int r = 0; r < Lay::kVTokens; r += 16) {
+              if (r >= toks) break;
+#pragma unroll
+              for (int j = 0; j < Lay::kHalves; ++j)
+                sm100::mma_f16_elect(
+                    tmem + kOCol + 16 * j,
+                    vd + ((r / BS) * BS * D * 2 + 2 * j * BS * 128 + (r % BS) * 128) / 16,
+                    pd + (r / 16) * (512 / 16), id_pv, (v | r) != 0);
             }
             sm100::mma_commit_elect(&c.empty[slot]);
-            ++g;
+            next_slot();
           }
           if (!ok) break;
           sm100::mma_commit_elect(&c.o_full);
