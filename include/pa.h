@@ -528,8 +528,10 @@ typedef struct pa_window {
  * Decode: the step of pa_decode (same tensors, layouts, flags and checks; the
  * query sits at position seq_lens[b] - 1) over the visible tokens.  The
  * workspace holds pa_window_workspace_size() bytes, its control block
- * initialised by pa_workspace_init; partition_size tokens (a multiple of
- * block_size, as for pa_decode_v2) are one partial of a row.  Tensor-core
+ * initialised by pa_workspace_init; partition_size (a multiple of block_size,
+ * as for pa_decode_v2) is the tokens of one partial of a row where there are
+ * many sequences; for few the tensor-core kernel's split is chosen to fill
+ * the GPU.  Tensor-core
  * kernel where pa_decode_kernel() says 2 and the layout is the standard one,
  * else CUDA cores.  v1_max_seq_len is not used.  What the pools hold for
  * invisible tokens does not matter (NaN included).

@@ -11,7 +11,7 @@
 // the token at t % BS == 0 also writes the table entry.
 //
 // Both sums cost less than a launch: every CTA makes them for itself (64-bit,
-// over chunks of 1024 requests, in shared memory) and then takes 2048 rows,
+// over chunks of 1024 requests, in shared memory) and then takes 512 rows,
 // finding a row's request by a binary search of the chunk's starts.  Nothing
 // passes between CTAs, so one launch does it all.  Bound by latency: one load
 // of the lengths, the scan, one dependent load of a block id, the stores.
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kNT = 512;       // threads: two requests each in a chunk
 constexpr int kChunk = 2 * kNT;
-constexpr int kRows = 4 * kNT;  // rows of a CTA
+constexpr int kRows = kNT;      // rows of a CTA
 
 struct PlanArgs {
   const int32_t* ctx_lens;

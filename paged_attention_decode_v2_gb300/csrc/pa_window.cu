@@ -36,10 +36,45 @@ pa_status_t check_decode(const pa_params_t* p, const pa_window_t* w) {
   return PA_OK;
 }
 
+// Tokens of a partial on the tensor-core kernel, whose persistent grid has room
+// for 304 items (two CTAs on each of 152 SMs) at a time.
+//   * Many (sequence, KV head) pairs -- two rounds of them: partition_size,
+//     evened out over the list, so that short lists do not wait for long ones.
+//   * Fewer: the split that takes the least time, a round costing as much as
+//     its part is long plus about 100 tokens (start and hand-over), a partial
+//     about 2 (the join).  One part needs no join at all.
+// Measured (window, heads 24 / 4 x 256, bf16; us with this split against parts of
+// 512): 1 sequence, 4096: 19.8 / 23.2; 4, 4096: 25 / 27; 16, 2048: 36 / 44; 64,
+// 1024: 52 / 55; 256 sequences, 8 KV heads of 128, 1024: 132, and 137 undivided.
+int32_t tc_part(const pa_params_t* p, int64_t len) {
+  constexpr int64_t kRoom = 304, kStart = 100, kJoin = 2, kLeast = 128;
+  const int64_t pairs = static_cast<int64_t>(p->num_seqs) * p->num_kv_heads;
+  int64_t parts = parts_of(len, p->partition_size);
+  if (pairs < 2 * kRoom) {
+    int64_t best = -1;
+    for (int64_t n = 1; n <= 64 && (n == 1 || n * kLeast <= len); ++n) {
+      const int64_t cost = (pairs * n + kRoom - 1) / kRoom * ((len + n - 1) / n + kStart) +
+                           (n > 1 ? n * kJoin : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        parts = n;
+      }
+    }
+  }
+  // whole blocks, of any size the kernel takes
+  return static_cast<int32_t>(((len + parts - 1) / parts + 63) / 64 * 64);
+}
+
+int64_t list_len(const pa_params_t* p, const pa_window_t& w) {
+  return window_max_len(p->max_seq_len, w.window, w.num_sinks, p->block_size);
+}
+
+// Room for the partials of either kernel, whatever the device.
 WorkspaceLayout layout_of(const pa_params_t* p, const pa_window_t& w) {
-  const int64_t len = window_max_len(p->max_seq_len, w.window, w.num_sinks, p->block_size);
+  const int64_t len = list_len(p, w);
   return workspace_layout(p->num_seqs, p->num_heads, p->head_dim,
-                          parts_of(len, p->partition_size));
+                          std::max(parts_of(len, p->partition_size),
+                                   len > 0 ? parts_of(len, tc_part(p, len)) : 1));
 }
 
 cudaError_t launch_list(const ListArgs& a, pa_dtype_t t, cudaStream_t s) {
@@ -106,14 +141,15 @@ pa_status_t pa_decode_window(const pa_params_t* p, const pa_window_t* window, co
     a.tmp_out = part_out;
     a.window = w.window;
     a.num_sinks = w.num_sinks;
-    a.max_list = static_cast<int32_t>(
-        window_max_len(p->max_seq_len, w.window, w.num_sinks, p->block_size));
-    const int64_t parts = parts_of(a.max_list, p->partition_size);
+    a.max_list = static_cast<int32_t>(list_len(p, w));
+    a.partition_size = a.max_list > 0 ? tc_part(p, a.max_list) : p->partition_size;
+    const int64_t parts = parts_of(a.max_list, a.partition_size);
     a.num_partitions = static_cast<int32_t>(parts);
     const bool v2 = parts > 1;
     if (launch_tc(a, p->kv_dtype, v2, stream) != cudaSuccess) return PA_ERR_CUDA;
     if (!v2) return PA_OK;
     l.stride = a.num_partitions;
+    l.part_size = a.partition_size;
     l.block_list = 1;
     return launch_join(j, stream, true) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
