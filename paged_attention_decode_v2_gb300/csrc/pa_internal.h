@@ -208,6 +208,12 @@ struct JoinArgs {
   int32_t num_heads, head_dim, group, out_dtype;
 };
 cudaError_t launch_join(const JoinArgs& a, cudaStream_t s, bool pdl);
+// Attention over the own tokens and the join with the prefix pass's partials,
+// for short own lists (pa_own.cu): whether it serves these parameters on the
+// current device, and its launch (prefix.m null: no partials).
+bool own_applicable(const pa_params_t* p);
+cudaError_t launch_own(const KernelArgs& a, const JoinList& prefix, pa_dtype_t t, bool pdl,
+                       cudaStream_t s);
 
 // Launchers return cudaSuccess or the launch error.
 cudaError_t launch_generic_f32(const KernelArgs& a, bool v2, cudaStream_t s);

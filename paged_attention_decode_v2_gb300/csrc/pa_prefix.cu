@@ -1,12 +1,14 @@
 // pa_prefix.cu -- pa_decode_prefix: a batch that shares a prefix.
 //
-// Three kernels: the sequences' own tokens (pass 1 of V2 over their block
-// tables, as in pa_decode_v2_partitions), the prefix (one product over all
-// rows of a KV head, split over keys), and the join of both lists of partials
-// (pa_join.cu).
+// The prefix is one product over all rows of a KV head, split over keys
+// (pa_rows.cuh; on the CUDA cores pa_portable.cuh).  Own lists of up to 512
+// tokens are then taken by one kernel that joins them with the prefix's
+// partials (pa_own.cu): two launches.  Longer ones go through pass 1 of V2 over
+// their block tables, as in pa_decode_v2_partitions, first, and a third kernel
+// joins both lists of partials (pa_join.cu).
 #include <algorithm>
 #include <cstdint>
-#include <cstring>
+#include <cstdlib>
 
 #include "pa.h"
 #include "pa_internal.h"
@@ -128,9 +130,18 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
   int32_t* status = reinterpret_cast<int32_t*>(base);
   const auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
   JoinArgs j{};
+  const RowsPlan r = rows_plan(p, prefix);
+  const int sms = r.shape ? rows_applicable(p->kv_dtype, p->num_heads, p->num_kv_heads,
+                                            p->head_dim, p->block_size, p->num_blocks, p->num_seqs,
+                                            p->scale)
+                          : 0;
+  // short own lists: one kernel for them and the join, after the prefix
+  const int own_max = getenv("PA_OWN") ? atoi(getenv("PA_OWN")) : 512;
+  const bool fused = own_applicable(p) && p->max_seq_len <= own_max &&
+                     (sms > 0 || prefix->max_prefix_len == 0);
 
   // the sequences' own tokens
-  if (p->max_seq_len > 0) {
+  if (!fused && p->max_seq_len > 0) {
     KernelArgs a = make_args(p, q, k_cache, v_cache, block_tables, seq_lens, out);
     a.status = status;
     a.max_logits = at(w.m[1]);
@@ -150,11 +161,6 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
 
   // the shared prefix
   if (prefix->max_prefix_len > 0) {
-    const RowsPlan r = rows_plan(p, prefix);
-    const int sms = r.shape ? rows_applicable(p->kv_dtype, p->num_heads, p->num_kv_heads,
-                                              p->head_dim, p->block_size, p->num_blocks,
-                                              p->num_seqs, p->scale)
-                            : 0;
     JoinList& l = j.list[0];
     l.m = at(w.m[0]);
     l.s = at(w.s[0]);
@@ -186,7 +192,7 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
       a.scale_log2 = p->scale * 1.442695040888963407360f;
       const RowsTensors t{q, nullptr, nullptr, k_cache, v_cache};
       // may start while the pass above still runs; it ends after it
-      if (launch_rows(a, p->kv_dtype, t, sms, p->max_seq_len > 0, stream) != cudaSuccess)
+      if (launch_rows(a, p->kv_dtype, t, sms, !fused && p->max_seq_len > 0, stream) != cudaSuccess)
         return PA_ERR_CUDA;
       l.stride = a.num_parts;
       l.key_blocks = r.key_blocks;
@@ -233,6 +239,13 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
   j.list[0].lens = prefix_len;
   j.list[0].shared = 1;
   j.list[0].max_len = prefix->max_prefix_len;
+  if (fused) {
+    KernelArgs a = make_args(p, q, k_cache, v_cache, block_tables, seq_lens, out);
+    a.status = status;
+    return launch_own(a, j.list[0], p->kv_dtype, prefix->max_prefix_len > 0, stream) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+  }
   j.out = out;
   j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;
   j.num_heads = p->num_heads;

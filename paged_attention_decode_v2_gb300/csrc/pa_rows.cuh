@@ -58,9 +58,10 @@ namespace pa {
 
 namespace rw {
 
-constexpr int kProducers = 3;
-constexpr int kMmaWarp = 8;          // warps 0-7 softmax, 9 .. 8 + kProducers producers
-constexpr int kThreads = 32 * (kMmaWarp + 1 + kProducers);
+constexpr int kProducers = 2;        // warps that stream keys and values
+constexpr int kMmaWarp = 8;          // warps 0-7 softmax, 9 and 10 producers, 11 the rows
+constexpr int kRowWarp = kMmaWarp + 1 + kProducers;
+constexpr int kThreads = 32 * (kRowWarp + 1);
 constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
 constexpr int kStage = 32768;        // ring stage: two 64-element slices of a key tile, or values
 constexpr int kSliceBytes = 16384;   // a 64-element slice of 128 rows
@@ -320,6 +321,39 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Eight 32-bit words to p (32-byte aligned) in one store: a whole sector.  A
+// thread stores its own row, so a warp's store touches 32 rows, and 16-byte
+// stores would write every sector twice.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// 16 elements of a row, from element i (a multiple of 16) of `out`, which is
+// 16-byte aligned: by sectors where it is 32-byte aligned.
+__device__ __forceinline__ void store_16(void* out, int64_t i, int32_t dtype, bool sectors,
+                                         const float (&v)[16]) {
+  if (!sectors) {
+    store_row16(out, i, dtype, v);
+    return;
+  }
+  uint32_t w[8];
+  if (dtype == PA_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * h + k]);
+      st_sector(static_cast<float*>(out) + i + 8 * h, w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    w[k] = dtype == PA_BF16 ? pack16(v[2 * k], v[2 * k + 1], static_cast<__nv_bfloat16*>(nullptr))
+                            : pack16(v[2 * k], v[2 * k + 1], static_cast<__half*>(nullptr));
+  st_sector(static_cast<uint16_t*>(out) + i, w);
+}
+
 // Bits e of [lo, hi) within a 32-key word that starts at key c0.
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) {
   const int a = max(lo - c0, 0), b = min(hi - c0, 32);
@@ -488,16 +522,41 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     // one instruction for the whole warpgroup, before its roles part
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp > kMmaWarp) {
-    // ========================= producers ==========================================
-    // Every producer warp walks the stages in the order the MMA warp takes
-    // them -- dual: keys, values of each tile; else keys 0, then (keys j,
-    // values j - 1), then the last values -- and fills those with
-    // g % kProducers == pid (producer 0 loads the rows too).
-    const uint32_t pid = static_cast<uint32_t>(warp - kMmaWarp - 1);
-    uint64_t* my_tail = &c.tail[pid];
+    // ========================= row loader =========================================
+    // The unit's row tiles, as soon as the last unit's QK^T are done with theirs.
     uint64_t keep;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
-    uint32_t g = 0, un = 0, tn = 0;
+    if (warp == kRowWarp) {
+    uint32_t un = 0;
+    bool ok = true;
+    Walk wk = walk_begin();
+    Unit u;
+    while (ok && walk_next<kPrefix>(a, before, wk, u)) {
+      ok = __all_sync(kAll, sm100::mbar_wait(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
+      if (!ok) break;
+      // rows past the sequence belong to others or are filled with zeros;
+      // their results are never stored
+      const int copies = dual ? 2 * kSl : kSl;
+      if (lane == 0) sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
+      __syncwarp();
+      if (lane < copies)
+        sm100::tma_load_4d(qs + lane * kSliceBytes, &qmap, &c.qfull, 0, u.kvh * a.group,
+                           static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
+                           lane % kSl, keep);
+      ++un;
+    }
+    if (!ok) {
+      if (lane == 0) c.abort = 1;
+      if (un > 0) sm100::mbar_wait(&c.qfull, (un - 1) & 1, budget, nullptr);
+    }
+    } else {
+    // ========================= producers ==========================================
+    // Both walk the stages in the order the MMA warp takes them -- dual: keys,
+    // values of each tile; else keys 0, then (keys j, values j - 1), then the
+    // last values -- and each fills every other one.
+    const uint32_t pid = static_cast<uint32_t>(warp - kMmaWarp - 1);
+    uint64_t* my_tail = &c.tail[pid];
+    uint32_t g = 0, tn = 0;
     int tail_pending = -1;
     bool ok = true;
 
@@ -558,17 +617,24 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     auto issue_v = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
       const int vbs = t.ctx ? BS : 16;  // rows per copy
       const int nv = (t.nk + kVT - 1) / kVT;
+      // the unseen run [h0, h1) of the tile; of a context tile, blocks inside it
+      // have come as zeros, so only the ends in blocks that are seen remain:
+      // [h0, e0) and [e1, h1)
       const int h0 = kPrefix ? 0 : max(0, a.num_sinks - t.pos0);
-      const int h1 = kPrefix ? 0 : min(t.nk, u.lo_min - t.pos0);
+      const int h1 = kPrefix ? 0 : max(h0, min(t.nk, u.lo_min - t.pos0));
+      const int e0 = t.ctx ? min(h1, (h0 + BS - 1) / BS * BS) : h1;
+      const int e1 = t.ctx && h0 < h1 ? max(e0, h1 / BS * BS) : h1;
       for (int v = 0; v < nv; ++v, ++g) {
         if (g % kProducers != pid) continue;
         const int slot = g % NST;
         if (!wait_empty(slot)) return false;
         const int toks = min(kVT, t.nk - v * kVT);
         const int ncp = (toks + vbs - 1) / vbs;
-        const int a0 = max(h0 - v * kVT, 0), a1 = min(h1 - v * kVT, toks);  // the unseen run
+        // rows of this stage to clear: [a0, a1), [b0, b1) and [toks, z1)
+        const int a0 = max(h0 - v * kVT, 0), a1 = max(a0, min(e0 - v * kVT, toks));
+        const int b0 = max(e1 - v * kVT, 0), b1 = max(b0, min(h1 - v * kVT, toks));
         const int z1 = (toks + 15) / 16 * 16;
-        const bool clear = a0 < a1 || toks < z1;
+        const bool clear = a0 < a1 || b0 < b1 || toks < z1;
         uint64_t* land = clear ? my_tail : &c.full[slot];
         uint8_t* st = ring + slot * kStage;
         if (lane == 0) sm100::mbar_arrive_expect_tx(land, ncp * vbs * D * 2);
@@ -587,15 +653,18 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
             return false;
           ++tn;
           tail_pending = -1;
-          const int n0 = a0 < a1 ? a1 - a0 : 0;
-          const int pieces = (n0 + z1 - toks) * kSl * 8;
-          for (int i = lane; i < pieces; i += 32) {
-            const int line = i / 8, piece = i % 8;
-            const int x = line / kSl, sl = line % kSl;
-            const int r = x < n0 ? a0 + x : toks + x - n0;
-            *reinterpret_cast<uint4*>(st + (r / vbs) * vbs * D * 2 + sl * vbs * 128 +
-                                      (r % vbs) * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
+          const int shift = t.ctx ? 31 - __clz(BS) : 4;  // vbs is a power of two
+          auto zero = [&](int r0, int r1) {
+            for (int i = lane; i < (r1 - r0) * kSl * 8; i += 32) {
+              const int line = i / 8, r = r0 + line / kSl, sl = line % kSl;
+              *reinterpret_cast<uint4*>(st + ((((r >> shift) * kSl + sl) << shift) +
+                                              (r & (vbs - 1))) * 128 + i % 8 * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+          };
+          zero(a0, a1);
+          zero(b0, b1);
+          zero(toks, z1);
           sm100::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) sm100::mbar_arrive(&c.full[slot]);
@@ -607,20 +676,6 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     Walk wk = walk_begin();
     Unit u;
     while (ok && walk_next<kPrefix>(a, before, wk, u)) {
-      if (pid == 0) {
-        ok = __all_sync(kAll, sm100::mbar_wait(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
-        if (!ok) break;
-        // rows past the sequence belong to others or are filled with zeros;
-        // their results are never stored
-        const int copies = dual ? 2 * kSl : kSl;
-        if (lane == 0) sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
-        __syncwarp();
-        if (lane < copies)
-          sm100::tma_load_4d(qs + lane * kSliceBytes, &qmap, &c.qfull, 0, u.kvh * a.group,
-                             static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
-                             lane % kSl, keep);
-        ++un;
-      }
       int32_t yprev = 0;
       Tile tprev{};
       int32_t id = ctx_id(u, 0);
@@ -646,7 +701,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         if (gg % kProducers == pid && static_cast<int>(gg % NST) != tail_pending)
           sm100::mbar_wait(&c.full[gg % NST], (gg / NST) & 1, budget, nullptr);
       if (tail_pending >= 0) sm100::mbar_wait(my_tail, tn & 1, budget, nullptr);
-      if (un > 0) sm100::mbar_wait(&c.qfull, (un - 1) & 1, budget, nullptr);
+    }
     }
     } else {
     // ========================= MMA issuer =========================================
@@ -1028,6 +1083,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       const bool empty = !kChain && mine == 0;
       int64_t at = orow;
       if constexpr (kPrefix) at = orow * a.num_parts + (D == 128 && !dual ? 2 * u.part + slot : u.part);
+      const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
       for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
         float ov[16];
@@ -1037,9 +1093,9 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) ov[e] = empty ? 0.f : ov[e] * inv;
           if constexpr (kPrefix)
-            store_row16(a.part_out, at * D + c0, PA_F32, ov);
+            store_16(a.part_out, at * D + c0, PA_F32, true, ov);
           else
-            store_row16(a.out, at * D + c0, a.out_dtype, ov);
+            store_16(a.out, at * D + c0, a.out_dtype, sectors, ov);
         }
       }
       if constexpr (kPrefix) {
