@@ -51,7 +51,8 @@ RowsPlan rows_plan(const pa_params_t* p, const pa_prefix_t* x) {
   RowsPlan r{};
   const int G = p->num_heads / p->num_kv_heads;
   r.shape = G <= 64 && (p->head_dim == 128 || p->head_dim == 256) && p->num_seqs > 0 &&
-            !(p->flags & (PA_FLAG_PORTABLE | PA_FLAG_SPLIT_X)) && x->max_prefix_len > 0;
+            !(p->flags & (PA_FLAG_PORTABLE | PA_FLAG_SPLIT_X)) && x->max_prefix_len > 0 &&
+            (ceil_div(x->max_prefix_len, 128) + 152) * p->num_kv_heads < (int64_t(1) << 30);
   if (!r.shape) return r;
   r.row_tokens = 128 / G;
   r.dual = p->head_dim == 128 && p->num_seqs > r.row_tokens;

@@ -152,8 +152,8 @@ __device__ __forceinline__ Tile tile_of(const Unit& u, int j) {
 
 // The units of one CTA, in order; every role walks the same sequence.
 struct Walk {
-  int64_t k;         // next unit (windowed prefill) or next item (prefix)
-  int64_t x, end;    // prefix: rest of the item's key tiles on the line
+  uint32_t k;        // next unit (windowed prefill) or next item (prefix)
+  uint32_t x, end;   // prefix: rest of the item's key tiles on the line
   int rt;            // prefix: its row group
 };
 
@@ -186,20 +186,21 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, 
   if constexpr (kPrefix) {
     const int32_t len = __ldg(a.lens);
     if (len < 1 || len > a.max_ctx_len) return false;  // the join reports it
+    // counts of units, tiles and blocks fit 31 bits (checked on the host)
     const PrefixSplit sp = prefix_split(len, a.num_kv_heads, a.key_blocks);
-    const int64_t all = sp.tiles * a.num_kv_heads;
+    const uint32_t tiles = sp.tiles, block = sp.block, all = tiles * a.num_kv_heads;
     if (w.x >= w.end) {
-      const int64_t kb = w.k / a.row_groups;
-      if (kb * sp.block >= all) return false;
-      w.rt = static_cast<int>(w.k % a.row_groups);
-      w.x = kb * sp.block;
-      w.end = min(all, w.x + sp.block);
+      const uint32_t kb = w.k / static_cast<uint32_t>(a.row_groups);
+      if (kb * block >= all) return false;
+      w.rt = static_cast<int>(w.k - kb * a.row_groups);
+      w.x = kb * block;
+      w.end = min(all, w.x + block);
       w.k += gridDim.x;
     }
-    u.kvh = static_cast<int>(w.x / sp.tiles);
-    const int j0 = static_cast<int>(w.x % sp.tiles);
-    const int n = static_cast<int>(min(w.end, (u.kvh + 1) * sp.tiles) - w.x);
-    u.part = static_cast<int>(w.x / sp.block) - sp.first(u.kvh);
+    u.kvh = static_cast<int>(w.x / tiles);
+    const int j0 = static_cast<int>(w.x - u.kvh * tiles);
+    const int n = static_cast<int>(min(w.end, (u.kvh + 1) * tiles) - w.x);
+    u.part = static_cast<int>(w.x / block - u.kvh * tiles / block);
     w.x += n;
     u.seq = 0;
     u.i0 = w.rt * a.group_tokens;
@@ -211,7 +212,7 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, 
     u.tiles = n;
     u.low = 0;
     u.skip = j0;
-    u.nctx = static_cast<int>(sp.tiles);
+    u.nctx = static_cast<int>(tiles);
     u.poison = false;
     return true;
   } else {
@@ -220,10 +221,10 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, 
       int b, g;
       if (before) {
         const int blocks = (a.num_seqs + 31) / 32;
-        const int64_t units = static_cast<int64_t>(before[blocks]) * a.num_kv_heads;
-        if (w.k >= units) return false;
-        const int x = static_cast<int>(w.k / a.num_kv_heads);
-        u.kvh = static_cast<int>(w.k % a.num_kv_heads);
+        const uint32_t heads = a.num_kv_heads;
+        if (w.k >= before[blocks] * heads) return false;
+        const int x = static_cast<int>(w.k / heads);
+        u.kvh = static_cast<int>(w.k - x * heads);
         w.k += gridDim.x;
         int lo = 0, hi = blocks;  // the 32 sequences: largest lo with before[lo] <= x
         while (hi - lo > 1) {
@@ -240,14 +241,14 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, 
         g = x - __shfl_sync(0xffffffffu, upto - mine, at);
         chunk_ok(a, b, s0, n);
       } else {
-        const int64_t per = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+        const uint32_t heads = a.num_kv_heads, per = a.num_seqs * heads;
         if (w.k >= per * a.row_groups) return false;
         g = static_cast<int>(w.k / per);
-        const int64_t rem = w.k % per;
+        const uint32_t rem = w.k - g * per;
         w.k += gridDim.x;
-        b = static_cast<int>(rem / a.num_kv_heads);
-        u.kvh = static_cast<int>(rem % a.num_kv_heads);
-        if (!chunk_ok(a, b, s0, n) || static_cast<int64_t>(g) * a.group_tokens >= n) continue;
+        b = static_cast<int>(rem / heads);
+        u.kvh = static_cast<int>(rem - b * heads);
+        if (!chunk_ok(a, b, s0, n) || g * a.group_tokens >= n) continue;
       }
       const int32_t C = __ldg(a.lens + b);
       u.poison = !(C >= 0 && C <= a.max_ctx_len &&
@@ -275,6 +276,23 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, 
       return true;
     }
   }
+}
+
+// Walking and waiting out of line, for all roles but the softmax (which holds
+// too many registers for a call): the roles must share the instruction cache,
+// there are many waits, and most find their barrier ready.
+template <bool kPrefix>
+__device__ __forceinline__ bool walk_call(const RowsArgs& a, const int* before, Walk& w, Unit& u) {
+  return walk_next<kPrefix>(a, before, w, u);
+}
+__device__ __forceinline__ bool wait_loop(uint64_t* bar, uint32_t parity, long long budget,
+                                       const volatile int* abort) {
+  return sm100::mbar_wait(bar, parity, budget, abort);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long budget,
+                                         const volatile int* abort) {
+  if (sm100::mbar_try_wait(bar, parity)) return true;
+  return wait_loop(bar, parity, budget, abort);
 }
 
 // 2^x by the hardware's approximate exponential: relative error well below the
@@ -319,6 +337,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// Bring a tile's bytes into L2.
+__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int32_t x, int32_t y, int32_t z,
+                                                int32_t w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 // Eight 32-bit words to p (32-byte aligned) in one store: a whole sector.  A
@@ -527,27 +554,40 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     uint64_t keep;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
     if (warp == kRowWarp) {
+    // The rows come from HBM in 128-byte pieces, several microseconds for a
+    // tile: so the next unit's are fetched into L2 while this one runs.
     uint32_t un = 0;
     bool ok = true;
     Walk wk = walk_begin();
     Unit u;
-    while (ok && walk_next<kPrefix>(a, before, wk, u)) {
-      ok = __all_sync(kAll, sm100::mbar_wait(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
-      if (!ok) break;
-      // rows past the sequence belong to others or are filled with zeros;
-      // their results are never stored
-      const int copies = dual ? 2 * kSl : kSl;
-      if (lane == 0) sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
-      __syncwarp();
-      if (lane < copies)
-        sm100::tma_load_4d(qs + lane * kSliceBytes, &qmap, &c.qfull, 0, u.kvh * a.group,
-                           static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
-                           lane % kSl, keep);
-      ++un;
+    const int copies = dual ? 2 * kSl : kSl;
+    bool more = true;
+    for (int i = 0;; ++i) {
+      // i = 0: find the first unit; then load one and find the next
+      if (i > 0) {
+        ok = __all_sync(kAll, wait_bar(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
+        if (!ok) break;
+        // rows past the sequence belong to others or are filled with zeros;
+        // their results are never stored
+        if (lane == 0)
+          sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
+        __syncwarp();
+        if (lane < copies)
+          sm100::tma_load_4d(qs + lane * kSliceBytes, &qmap, &c.qfull, 0, u.kvh * a.group,
+                             static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
+                             lane % kSl, keep);
+        ++un;
+      }
+      more = walk_call<kPrefix>(a, before, wk, u);
+      if (!more) break;
+      if (i > 0 && lane < copies)
+        tma_prefetch_4d(&qmap, 0, u.kvh * a.group,
+                        static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
+                        lane % kSl);
     }
     if (!ok) {
       if (lane == 0) c.abort = 1;
-      if (un > 0) sm100::mbar_wait(&c.qfull, (un - 1) & 1, budget, nullptr);
+      if (un > 0) wait_bar(&c.qfull, (un - 1) & 1, budget, nullptr);
     }
     } else {
     // ========================= producers ==========================================
@@ -576,7 +616,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       return (!seen || id < 0 || id >= a.num_blocks) ? -BS : (id * a.num_kv_heads + u.kvh) * BS;
     };
     auto wait_empty = [&](int slot) {
-      return __all_sync(kAll, sm100::mbar_wait(&c.empty[slot], ((g / NST) & 1) ^ 1, budget,
+      return __all_sync(kAll, wait_bar(&c.empty[slot], ((g / NST) & 1) ^ 1, budget,
                                                abort_flag)) != 0;
     };
 
@@ -649,7 +689,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         __syncwarp();
         if (clear) {
           tail_pending = slot;
-          if (!__all_sync(kAll, sm100::mbar_wait(my_tail, tn & 1, budget, abort_flag)))
+          if (!__all_sync(kAll, wait_bar(my_tail, tn & 1, budget, abort_flag)))
             return false;
           ++tn;
           tail_pending = -1;
@@ -675,7 +715,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
 
     Walk wk = walk_begin();
     Unit u;
-    while (ok && walk_next<kPrefix>(a, before, wk, u)) {
+    while (ok && walk_call<kPrefix>(a, before, wk, u)) {
       int32_t yprev = 0;
       Tile tprev{};
       int32_t id = ctx_id(u, 0);
@@ -699,8 +739,8 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       // copies already issued must land before the CTA may exit
       for (uint32_t gg = g > NST ? g - NST : 0; gg < g; ++gg)
         if (gg % kProducers == pid && static_cast<int>(gg % NST) != tail_pending)
-          sm100::mbar_wait(&c.full[gg % NST], (gg / NST) & 1, budget, nullptr);
-      if (tail_pending >= 0) sm100::mbar_wait(my_tail, tn & 1, budget, nullptr);
+          wait_bar(&c.full[gg % NST], (gg / NST) & 1, budget, nullptr);
+      if (tail_pending >= 0) wait_bar(my_tail, tn & 1, budget, nullptr);
     }
     }
     } else {
@@ -733,17 +773,17 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     bool ok = true;
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
-    if (a.selftest_stall) ok = __all_sync(kAll, sm100::mbar_wait(&c.never, 0, budget, abort_flag));
+    if (a.selftest_stall) ok = __all_sync(kAll, wait_bar(&c.never, 0, budget, abort_flag));
     auto wait_for = [&](uint64_t* bar, uint32_t phase) {
-      const bool r = __all_sync(kAll, sm100::mbar_wait(bar, phase, budget, abort_flag)) != 0;
+      const bool r = __all_sync(kAll, wait_bar(bar, phase, budget, abort_flag)) != 0;
       sm100::tc_fence_after();
       return r;
     };
     // logits into slot S: keys from the ring, or (dual, slot 1) those in hand
     auto qk = [&](auto slot) -> bool {
-      constexpr int S = decltype(slot)::value;
-      constexpr bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
-      if constexpr (kFresh) rk = rg;
+      const int S = slot;
+      const bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
+      if (kFresh) rk = rg;
       Ring r = rk;
       const uint32_t d = tmem + S * kTile;
       const uint64_t qd = q_desc + (kDual && S ? kSl * kSliceBytes / 16 : 0);
@@ -756,7 +796,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
         r.next();
       }
-      if constexpr (kFresh) rg = r;
+      if (kFresh) rg = r;
       return true;
     };
     // the MMAs of keys r0 .. r0 + 63 of one value stage (rows of VB per slice),
@@ -764,7 +804,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     auto pv_part = [&](auto vb, auto from, uint64_t vd, uint32_t at, uint32_t o, int toks,
                        bool first) {
       constexpr int VB = decltype(vb)::value, r0 = decltype(from)::value;
-      constexpr auto off = [](int r) {
+      auto off = [](int r) {
         return static_cast<uint64_t>(((r / VB) * VB * D * 2 + (r % VB) * 128) / 16);
       };
       if (toks >= r0 + 64) {
@@ -772,9 +812,9 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
                 vd + off(r0 + 48), id_pv, !first || r0 != 0);
         return;
       }
-#pragma unroll
-      for (int r = r0; r < r0 + 64; r += 16)
-        if (r < toks) sm100::mma_f16_ts_elect(o, at + r / 2, vd + off(r), id_pv, !first || r != 0);
+#pragma unroll 1
+      for (int r = r0; r < toks; r += 16)
+        sm100::mma_f16_ts_elect(o, at + r / 2, vd + off(r), id_pv, !first || r != 0);
     };
     auto pv_keys = [&](bool ctx, auto from, uint32_t slot, uint32_t at, uint32_t o, int toks,
                        bool first) {
@@ -787,9 +827,9 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     };
     // P.V of slot S over a tile of nk keys; `first`: the accumulator starts anew
     auto pv = [&](auto slot, int nk, bool ctx, bool first) -> bool {
-      constexpr int S = decltype(slot)::value;
-      constexpr bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
-      if constexpr (kFresh) rv = rg;
+      const int S = slot;
+      const bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
+      if (kFresh) rv = rg;
       Ring r = rv;
       if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
       if (!wait_for(&c.p_ready[S][0], parity[S])) return false;
@@ -815,7 +855,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
         r.next();
       }
-      if constexpr (kFresh) rg = r;
+      if (kFresh) rg = r;
       // a step's softmax may have to rescale the accumulator: with one
       // accumulator per slot, the logits it has waited for imply that the
       // slot's last P.V is done; with one for both slots they do not
@@ -826,7 +866,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     Walk wk = walk_begin();
     Unit u;
     while (ok) {
-      const bool more = walk_next<kPrefix>(a, before, wk, u);
+      const bool more = walk_call<kPrefix>(a, before, wk, u);
       if (!__all_sync(kAll, more)) break;
       ok = wait_for(&c.qfull, un & 1);
       if (!ok) break;
@@ -834,59 +874,57 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       const int tiles = uniform(u.tiles);
       int nk = 0, nk_prev = 0;
       bool ctx = true, ctx_prev = true;
-      for (int j = 0; j < tiles && ok; ++j) {
-        {
+      // QK^T of tile j, P.V of the step before; one more round for the last P.V
+#pragma unroll 1
+      for (int j = 0; j <= tiles; ++j) {
+        const bool more_keys = j < tiles;
+        if (more_keys) {
           const Tile t = tile_of(u, j);
           const int both = uniform(t.nk | (t.ctx ? 256 : 0));
           nk = both & 255;
           ctx = (both & 256) != 0;
         }
         if constexpr (kDual) {
-          ok = qk(S0{});
-          if (!ok) break;
-          sm100::mma_commit_elect(&c.s_full[0]);
+          if (more_keys) {
+            if (!(ok = qk(S0{}))) break;
+            sm100::mma_commit_elect(&c.s_full[0]);
+          } else {
+            sm100::mma_commit_elect(&c.o_done[0]);
+          }
           if (j > 0 && !(ok = pv(S1{}, nk_prev, ctx_prev, j == 1))) break;
-          ok = qk(S1{});
-          if (!ok) break;
+          if (!more_keys) {
+            sm100::mma_commit_elect(&c.o_done[1]);
+            break;
+          }
+          if (!(ok = qk(S1{}))) break;
           if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
           sm100::mma_commit_elect(&c.s_full[1]);
-          ok = pv(S0{}, nk, ctx, j == 0);
+          if (!(ok = pv(S0{}, nk, ctx, j == 0))) break;
         } else {
-          ok = j & 1 ? qk(S1{}) : qk(S0{});
-          if (!ok) break;
-          if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
-          sm100::mma_commit_elect(&c.s_full[j & 1]);
+          if (more_keys) {
+            if (!(ok = qk(j & 1))) break;
+            if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
+            sm100::mma_commit_elect(&c.s_full[j & 1]);
+          } else if (!kChain && tiles > 1) {
+            // the slot before the last is done with its accumulator
+            sm100::mma_commit_elect(&c.o_done[j & 1]);
+          }
           if (j > 0) {
             // one accumulator: not before the last unit's has been read
-            if (kChain && j == 1 && un > 1) ok = wait_for(&c.o_free, un & 1);
-            if (ok)
-              ok = j & 1 ? pv(S0{}, nk_prev, ctx_prev, kChain ? j == 1 : j <= 2)
-                         : pv(S1{}, nk_prev, ctx_prev, kChain ? j == 1 : j <= 2);
+            if (kChain && j == 1 && un > 1 && !(ok = wait_for(&c.o_free, un & 1))) break;
+            if (!(ok = pv((j - 1) & 1, nk_prev, ctx_prev, kChain ? j == 1 : j <= 2))) break;
+            if (!kChain && !more_keys) sm100::mma_commit_elect(&c.o_done[(j - 1) & 1]);
           }
         }
         nk_prev = nk;
         ctx_prev = ctx;
-      }
-      if (!ok) break;
-      if constexpr (kDual) {
-        sm100::mma_commit_elect(&c.o_done[0]);
-        ok = pv(S1{}, nk_prev, ctx_prev, tiles == 1);
-        sm100::mma_commit_elect(&c.o_done[1]);
-      } else {
-        if (kChain && tiles == 1 && un > 1) ok = wait_for(&c.o_free, un & 1);
-        // the slot before the last is done with its accumulator
-        if (!kChain && tiles > 1) sm100::mma_commit_elect(&c.o_done[tiles & 1]);
-        if (ok)
-          ok = tiles & 1 ? pv(S0{}, nk_prev, ctx_prev, kChain ? tiles == 1 : tiles <= 2)
-                         : pv(S1{}, nk_prev, ctx_prev, kChain ? tiles == 1 : tiles <= 2);
-        if (!kChain) sm100::mma_commit_elect(&c.o_done[(tiles - 1) & 1]);
       }
     }
     if (!ok) {
       if (lane == 0) c.abort = 1;
       // no MMA may still be running when tensor memory is released
       sm100::mma_commit_elect(&c.drain);
-      sm100::mbar_wait(&c.drain, 0, budget, nullptr);
+      wait_bar(&c.drain, 0, budget, nullptr);
     }
     __syncwarp();
     }
@@ -1085,17 +1123,21 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       if constexpr (kPrefix) at = orow * a.num_parts + (D == 128 && !dual ? 2 * u.part + slot : u.part);
       const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
-      for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
-        float ov[16];
-        sm100::tmem_ld16(obuf + c0, ov);
+      for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+        float ov[32];
+        tmem_ld32(obuf + c0, ov);
         sm100::tmem_wait_ld();
         if (row_ok) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) ov[e] = empty ? 0.f : ov[e] * inv;
-          if constexpr (kPrefix)
-            store_16(a.part_out, at * D + c0, PA_F32, true, ov);
-          else
-            store_16(a.out, at * D + c0, a.out_dtype, sectors, ov);
+          for (int e = 0; e < 32; ++e) ov[e] = empty ? 0.f : ov[e] * inv;
+#pragma unroll
+          for (int e = 0; e < 32; e += 16) {
+            float(&part)[16] = *reinterpret_cast<float(*)[16]>(&ov[e]);
+            if constexpr (kPrefix)
+              store_16(a.part_out, at * D + c0 + e, PA_F32, true, part);
+            else
+              store_16(a.out, at * D + c0 + e, a.out_dtype, sectors, part);
+          }
         }
       }
       if constexpr (kPrefix) {

@@ -51,20 +51,20 @@ inline int64_t window_max_len(int64_t max_len, int64_t window, int64_t num_sinks
 // of `block` tiles, at most `key_blocks` of them.  The part of a head in one
 // key block is a segment: one partial result of the head's rows.
 struct PrefixSplit {
-  int64_t tiles;  // key tiles of a head
-  int64_t block;  // key tiles of a key block (>= 1)
-  // first key block with a tile of head kvh, and how many have one
-  __host__ __device__ int first(int kvh) const { return static_cast<int>(kvh * tiles / block); }
-  __host__ __device__ int segments(int kvh) const {
-    return tiles ? static_cast<int>(((kvh + 1) * tiles - 1) / block) - first(kvh) + 1 : 0;
+  uint32_t tiles;  // key tiles of a head
+  uint32_t block;  // key tiles of a key block (>= 1)
+  // segments of head kvh: the key blocks with a tile of it
+  __host__ __device__ int segments(uint32_t kvh) const {
+    return tiles ? static_cast<int>(((kvh + 1) * tiles - 1) / block - kvh * tiles / block) + 1 : 0;
   }
 };
 
-__host__ __device__ inline PrefixSplit prefix_split(int32_t len, int num_kv_heads,
-                                                    int key_blocks) {
+// The tiles of all heads must number less than 2^31.
+__host__ __device__ inline PrefixSplit prefix_split(int32_t len, uint32_t num_kv_heads,
+                                                    uint32_t key_blocks) {
   PrefixSplit s;
-  s.tiles = (static_cast<int64_t>(len) + 127) / 128;
-  const int64_t all = s.tiles * num_kv_heads;
+  s.tiles = (static_cast<uint32_t>(len) + 127) / 128;
+  const uint32_t all = s.tiles * num_kv_heads;
   s.block = all > key_blocks ? (all + key_blocks - 1) / key_blocks : 1;
   return s;
 }

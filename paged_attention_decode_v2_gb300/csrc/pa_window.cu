@@ -228,7 +228,16 @@ pa_status_t pa_prefill_window(const pa_prefill_params_t* p, const pa_window_t* w
   if (!aligned(block_tables, 4) || !aligned(query_start, 4) || !aligned(ctx_lens, 4))
     return PA_ERR_MISALIGNED;
   const pa_window_t w = clamped(window, p->max_ctx_len + p->max_query_len);
-  const int sms = (p->flags & (PA_FLAG_PORTABLE | PA_FLAG_SPLIT_X))
+  // row tiles of the tensor-core kernel: 128 rows are 128 / G tokens, one or
+  // two tiles to a unit; it counts its units in 31 bits
+  const int G = p->num_heads / p->num_kv_heads;
+  const int dual = p->head_dim == 128, row_tokens = std::max(128 / G, 1);
+  const int group_tokens = row_tokens * (dual ? 2 : 1);
+  const int64_t row_groups = (static_cast<int64_t>(p->max_query_len) + group_tokens - 1) /
+                             group_tokens;
+  const bool counts = static_cast<int64_t>(p->num_seqs) * p->num_kv_heads <
+                      (int64_t(1) << 30) / row_groups;
+  const int sms = (p->flags & (PA_FLAG_PORTABLE | PA_FLAG_SPLIT_X)) || !counts
                       ? 0
                       : rows_applicable(p->kv_dtype, p->num_heads, p->num_kv_heads, p->head_dim,
                                         p->block_size, p->num_blocks, p->total_tokens, p->scale);
@@ -250,11 +259,11 @@ pa_status_t pa_prefill_window(const pa_prefill_params_t* p, const pa_window_t* w
     a.max_ctx_len = p->max_ctx_len;
     a.window = w.window;
     a.num_sinks = w.num_sinks;
-    a.group = p->num_heads / p->num_kv_heads;
-    a.row_tokens = 128 / a.group;
-    a.dual = p->head_dim == 128;
-    a.group_tokens = a.row_tokens * (a.dual ? 2 : 1);
-    a.row_groups = (p->max_query_len + a.group_tokens - 1) / a.group_tokens;
+    a.group = G;
+    a.row_tokens = row_tokens;
+    a.dual = dual;
+    a.group_tokens = group_tokens;
+    a.row_groups = static_cast<int32_t>(row_groups);
     a.out_dtype = p->out_dtype;
     a.selftest_stall = (p->flags & PA_FLAG_SELFTEST_STALL) ? 1 : 0;
     a.scale_log2 = p->scale * 1.442695040888963407360f;
