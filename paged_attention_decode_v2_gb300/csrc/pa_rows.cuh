@@ -454,7 +454,7 @@ __device__ __forceinline__ void sync256() { asm volatile("bar.sync 1, 256;" ::: 
 
 // qmap: q as (64, Hq, rows, D / 64), box (64, G, nq, 1); knmap / vnmap: the
 // chunk's keys and values as (64, Hkv, T, D / 64), boxes (64, 1, 128, 1) and
-// (64, 1, 16, D / 64) (windowed prefill only); kcmap / vcmap: the caches as
+// (64, 1, BS, D / 64) (windowed prefill only); kcmap / vcmap: the caches as
 // rows of head_dim (box 64 x BS, and a whole block slice-major).
 template <typename T, int D, int BS, bool kPrefix, bool kDual>
 __global__ void __launch_bounds__(rw::kThreads, 1)
@@ -655,7 +655,6 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     // their p is zero, but 0 * NaN would be NaN.  Such a stage lands on the
     // producer's own barrier first.
     auto issue_v = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
-      const int vbs = t.ctx ? BS : 16;  // rows per copy
       const int nv = (t.nk + kVT - 1) / kVT;
       // the unseen run [h0, h1) of the tile; of a context tile, blocks inside it
       // have come as zeros, so only the ends in blocks that are seen remain:
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         const int slot = g % NST;
         if (!wait_empty(slot)) return false;
         const int toks = min(kVT, t.nk - v * kVT);
-        const int ncp = (toks + vbs - 1) / vbs;
+        const int ncp = (toks + BS - 1) / BS;  // copies, of BS rows each
         // rows of this stage to clear: [a0, a1), [b0, b1) and [toks, z1)
         const int a0 = max(h0 - v * kVT, 0), a1 = max(a0, min(e0 - v * kVT, toks));
         const int b0 = max(e1 - v * kVT, 0), b1 = max(b0, min(h1 - v * kVT, toks));
@@ -677,14 +676,14 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         const bool clear = a0 < a1 || b0 < b1 || toks < z1;
         uint64_t* land = clear ? my_tail : &c.full[slot];
         uint8_t* st = ring + slot * kStage;
-        if (lane == 0) sm100::mbar_arrive_expect_tx(land, ncp * vbs * D * 2);
+        if (lane == 0) sm100::mbar_arrive_expect_tx(land, ncp * BS * D * 2);
         __syncwarp();
         if (t.ctx) {
           const int32_t yj = __shfl_sync(kAll, y, (v * kVT / BS + lane) & 31);
           if (lane < ncp) sm100::tma_load_3d(st + lane * BS * D * 2, &vcmap, land, 0, yj, 0, keep);
         } else if (lane < ncp) {
-          sm100::tma_load_4d(st + lane * 16 * D * 2, &vnmap, land, 0, u.kvh,
-                             static_cast<int32_t>(u.row0) + t.chunk + v * kVT + lane * 16, 0, keep);
+          sm100::tma_load_4d(st + lane * BS * D * 2, &vnmap, land, 0, u.kvh,
+                             static_cast<int32_t>(u.row0) + t.chunk + v * kVT + lane * BS, 0, keep);
         }
         __syncwarp();
         if (clear) {
@@ -693,18 +692,16 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
             return false;
           ++tn;
           tail_pending = -1;
-          const int shift = t.ctx ? 31 - __clz(BS) : 4;  // vbs is a power of two
           auto zero = [&](int r0, int r1) {
             for (int i = lane; i < (r1 - r0) * kSl * 8; i += 32) {
               const int line = i / 8, r = r0 + line / kSl, sl = line % kSl;
-              *reinterpret_cast<uint4*>(st + ((((r >> shift) * kSl + sl) << shift) +
-                                              (r & (vbs - 1))) * 128 + i % 8 * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(st + ((r / BS * kSl + sl) * BS + r % BS) * 128 +
+                                        i % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
           };
-          zero(a0, a1);
-          zero(b0, b1);
-          zero(toks, z1);
+#pragma unroll 1
+          for (int x = 0; x < 3; ++x)
+            zero(x == 0 ? a0 : x == 1 ? b0 : toks, x == 0 ? a1 : x == 1 ? b1 : z1);
           sm100::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) sm100::mbar_arrive(&c.full[slot]);
@@ -716,23 +713,22 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     Walk wk = walk_begin();
     Unit u;
     while (ok && walk_call<kPrefix>(a, before, wk, u)) {
-      int32_t yprev = 0;
-      Tile tprev{};
-      int32_t id = ctx_id(u, 0);
-      for (int j = 0; j < u.tiles && ok; ++j) {
-        const Tile t = tile_of(u, j);
-        const int32_t y = t.ctx ? ctx_row(u, t, id) : 0;
-        id = ctx_id(u, j + 1);
-        ok = issue_k(u, t, y);
-        if (dual) {
-          if (ok) ok = issue_v(u, t, y);
-        } else {
-          if (ok && j > 0) ok = issue_v(u, tprev, yprev);
+      // j = -1 only looks up tile 0's blocks; the last round has values alone
+      int32_t y = 0, yprev = 0, id = 0;
+      Tile t{}, tprev{};
+#pragma unroll 1
+      for (int j = -1; j <= u.tiles && ok; ++j) {
+        if (j >= 0) {
           yprev = y;
           tprev = t;
+          t = tile_of(u, j);
+          y = t.ctx ? ctx_row(u, t, id) : 0;
         }
+        id = ctx_id(u, j + 1);
+        if (j >= 0 && j < u.tiles) ok = issue_k(u, t, y);
+        if (dual ? j >= 0 && j < u.tiles : j > 0)
+          if (ok) ok = issue_v(u, dual ? t : tprev, dual ? y : yprev);
       }
-      if (ok && !dual) ok = issue_v(u, tprev, yprev);
     }
     if (!ok) {
       if (lane == 0) c.abort = 1;
@@ -754,9 +750,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
     constexpr uint32_t id_pv = sm100::idesc_f16(kBf16, false, true, 128, D);
     const uint64_t q_desc = sm100::smem_desc(sm100::smem_u32(qs), 16, 1024, sm100::kSw128);
     const uint64_t k_desc = sm100::smem_desc(sm100::smem_u32(ring), 16, 1024, sm100::kSw128);
-    // values: rows of `vbs` (block or 16) per slice
-    const uint64_t vc_desc = sm100::smem_desc(sm100::smem_u32(ring), BS * 128, 1024, sm100::kSw128);
-    const uint64_t vn_desc = sm100::smem_desc(sm100::smem_u32(ring), 16 * 128, 1024, sm100::kSw128);
+    const uint64_t v_desc = sm100::smem_desc(sm100::smem_u32(ring), BS * 128, 1024, sm100::kSw128);
     struct Ring {
       uint32_t slot, phase;
       __device__ __forceinline__ void next() {
@@ -799,13 +793,13 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       if (kFresh) rg = r;
       return true;
     };
-    // the MMAs of keys r0 .. r0 + 63 of one value stage (rows of VB per slice),
+    // the MMAs of keys r0 .. r0 + 63 of one value stage (rows of BS per slice),
     // as many as the stage's `toks` keys reach
-    auto pv_part = [&](auto vb, auto from, uint64_t vd, uint32_t at, uint32_t o, int toks,
-                       bool first) {
-      constexpr int VB = decltype(vb)::value, r0 = decltype(from)::value;
+    auto pv_keys = [&](auto from, uint32_t stage, uint32_t at, uint32_t o, int toks, bool first) {
+      constexpr int r0 = decltype(from)::value;
+      const uint64_t vd = v_desc + stage * (kStage / 16);
       auto off = [](int r) {
-        return static_cast<uint64_t>(((r / VB) * VB * D * 2 + (r % VB) * 128) / 16);
+        return static_cast<uint64_t>(((r / BS) * BS * D * 2 + (r % BS) * 128) / 16);
       };
       if (toks >= r0 + 64) {
         mma4_ts(o, at + r0 / 2, vd + off(r0), vd + off(r0 + 16), vd + off(r0 + 32),
@@ -816,17 +810,8 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       for (int r = r0; r < toks; r += 16)
         sm100::mma_f16_ts_elect(o, at + r / 2, vd + off(r), id_pv, !first || r != 0);
     };
-    auto pv_keys = [&](bool ctx, auto from, uint32_t slot, uint32_t at, uint32_t o, int toks,
-                       bool first) {
-      if (kPrefix || ctx)
-        pv_part(std::integral_constant<int, BS>{}, from, vc_desc + slot * (kStage / 16), at, o,
-                toks, first);
-      else
-        pv_part(std::integral_constant<int, 16>{}, from, vn_desc + slot * (kStage / 16), at, o,
-                toks, first);
-    };
     // P.V of slot S over a tile of nk keys; `first`: the accumulator starts anew
-    auto pv = [&](auto slot, int nk, bool ctx, bool first) -> bool {
+    auto pv = [&](auto slot, int nk, bool first) -> bool {
       const int S = slot;
       const bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
       if (kFresh) rv = rg;
@@ -836,7 +821,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       const uint32_t o = tmem + kOCol + (kChain ? 0 : S * 128);
       const uint32_t at = tmem + S * kTile;
       // keys 0-63, then, when their P is there too, keys 64-127
-      pv_keys(ctx, S0{}, r.slot, at, o, nk, first);
+      pv_keys(S0{}, r.slot, at, o, nk, first);
       if constexpr (kVT == 64) {
         if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
         r.next();
@@ -846,12 +831,12 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       if constexpr (kVT == 64) {
         if (nk > 64) {
           if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
-          pv_keys(ctx, S0{}, r.slot, at + 32, o, nk - 64, false);
+          pv_keys(S0{}, r.slot, at + 32, o, nk - 64, false);
           if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
           r.next();
         }
       } else {
-        if (nk > 64) pv_keys(ctx, std::integral_constant<int, 64>{}, r.slot, at, o, nk, false);
+        if (nk > 64) pv_keys(std::integral_constant<int, 64>{}, r.slot, at, o, nk, false);
         if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
         r.next();
       }
@@ -873,16 +858,12 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       ++un;
       const int tiles = uniform(u.tiles);
       int nk = 0, nk_prev = 0;
-      bool ctx = true, ctx_prev = true;
       // QK^T of tile j, P.V of the step before; one more round for the last P.V
 #pragma unroll 1
       for (int j = 0; j <= tiles; ++j) {
         const bool more_keys = j < tiles;
         if (more_keys) {
-          const Tile t = tile_of(u, j);
-          const int both = uniform(t.nk | (t.ctx ? 256 : 0));
-          nk = both & 255;
-          ctx = (both & 256) != 0;
+          nk = uniform(tile_of(u, j).nk);
         }
         if constexpr (kDual) {
           if (more_keys) {
@@ -891,7 +872,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
           } else {
             sm100::mma_commit_elect(&c.o_done[0]);
           }
-          if (j > 0 && !(ok = pv(S1{}, nk_prev, ctx_prev, j == 1))) break;
+          if (j > 0 && !(ok = pv(S1{}, nk_prev, j == 1))) break;
           if (!more_keys) {
             sm100::mma_commit_elect(&c.o_done[1]);
             break;
@@ -899,7 +880,7 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
           if (!(ok = qk(S1{}))) break;
           if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
           sm100::mma_commit_elect(&c.s_full[1]);
-          if (!(ok = pv(S0{}, nk, ctx, j == 0))) break;
+          if (!(ok = pv(S0{}, nk, j == 0))) break;
         } else {
           if (more_keys) {
             if (!(ok = qk(j & 1))) break;
@@ -912,12 +893,11 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
           if (j > 0) {
             // one accumulator: not before the last unit's has been read
             if (kChain && j == 1 && un > 1 && !(ok = wait_for(&c.o_free, un & 1))) break;
-            if (!(ok = pv((j - 1) & 1, nk_prev, ctx_prev, kChain ? j == 1 : j <= 2))) break;
+            if (!(ok = pv((j - 1) & 1, nk_prev, kChain ? j == 1 : j <= 2))) break;
             if (!kChain && !more_keys) sm100::mma_commit_elect(&c.o_done[(j - 1) & 1]);
           }
         }
         nk_prev = nk;
-        ctx_prev = ctx;
       }
     }
     if (!ok) {

@@ -48,7 +48,7 @@ cudaError_t launch_rows(RowsArgs a, pa_dtype_t t, const RowsTensors& x, int sms,
     const uint64_t dims[4] = {64, Hkv, T, D / 64};
     const uint64_t strides[3] = {D * 2, Hkv * D * 2, 128};
     const uint32_t box_k[4] = {64, 1, 128, 1};
-    const uint32_t box_v[4] = {64, 1, 16, static_cast<uint32_t>(D / 64)};
+    const uint32_t box_v[4] = {64, 1, static_cast<uint32_t>(BS), static_cast<uint32_t>(D / 64)};
     if (cudaError_t e = encode_tiled(&m[1], t, 4, x.k, dims, strides, box_k)) return e;
     if (cudaError_t e = encode_tiled(&m[2], t, 4, x.v, dims, strides, box_v)) return e;
   } else {
