@@ -59,7 +59,7 @@ __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uin
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(D, D == 128 ? 3 : 1)
+__global__ void __launch_bounds__(D, 512 / D)
     pa_own_kernel(const KernelArgs a, const JoinList pre) {
   constexpr int kPieces = D / 32;             // 16-byte pieces of a row per thread (QK^T)
   __shared__ float o_s[kGroups][8][D];
@@ -80,15 +80,20 @@ __global__ void __launch_bounds__(D, D == 128 ? 3 : 1)
   const T* __restrict__ vc = static_cast<const T*>(a.v_cache);
   const int32_t* __restrict__ bt = a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq;
 
-  // q of head `row`: pieces at d = 32 i + 8 c
-  uint4 q[kPieces];
-  {
-    const T* src = static_cast<const T*>(a.q) +
-                   (static_cast<int64_t>(b) * Hq + kvh * G + row) * D + 8 * c;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      q[i] = row < G ? __ldg(reinterpret_cast<const uint4*>(src + 32 * i)) : make_uint4(0, 0, 0, 0);
-  }
+  // q of the heads (rows from G on are zero): in shared memory, since how many
+  // warps there are decides more than how long each takes (128 registers: with
+  // q in them, or both halves of the values in flight, 30 % fewer warps fit and
+  // 256 sequences of 32 own tokens took 49 us for 42)
+  __shared__ uint4 q_s[8][D / 8];
+  for (int i = tid; i < 8 * (D / 8); i += D)
+    q_s[i / (D / 8)][i % (D / 8)] =
+        i / (D / 8) < G
+            ? __ldg(reinterpret_cast<const uint4*>(
+                        static_cast<const T*>(a.q) +
+                        (static_cast<int64_t>(b) * Hq + kvh * G + i / (D / 8)) * D) +
+                    i % (D / 8))
+            : make_uint4(0, 0, 0, 0);
+  __syncthreads();
   float m = -INFINITY, sum = 0.f;             // of this thread's head (all four c alike for m)
   float o[2][8][4];                           // [64 columns][element of 8][MMA accumulator]
 #pragma unroll
@@ -119,8 +124,7 @@ __global__ void __launch_bounds__(D, D == 128 ? 3 : 1)
                                                              32 * i))
                       : make_uint4(0, 0, 0, 0);
     uint4 v[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
+    auto load_v = [&](int j) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int t = 2 * c + (x & 1) + 8 * (x >> 1);
@@ -128,14 +132,18 @@ __global__ void __launch_bounds__(D, D == 128 ? 3 : 1)
                                                                   64 * j + 8 * row))
                            : make_uint4(0, 0, 0, 0);
       }
+    };
+    load_v(0);
     float s[2][4] = {};
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        mma16816<T>(s[u], q[i].x, 0u, q[i].y, 0u, k[u][i].x, k[u][i].y);
-        mma16816<T>(s[u], q[i].z, 0u, q[i].w, 0u, k[u][i].z, k[u][i].w);
+        const uint4 q = q_s[row][4 * i + c];
+        mma16816<T>(s[u], q.x, 0u, q.y, 0u, k[u][i].x, k[u][i].y);
+        mma16816<T>(s[u], q.z, 0u, q.w, 0u, k[u][i].z, k[u][i].w);
       }
+    load_v(1);  // into the keys' registers
     // logits of head `row`: tokens 2c, 2c + 1 (u = 0) and + 8 (u = 1)
     float l[4];
 #pragma unroll
@@ -295,9 +303,15 @@ cudaError_t launch_own_d(const KernelArgs& a, const JoinList& pre, bool pdl, cud
 
 }  // namespace
 
+// Measured against pass 1 + join in kernels of their own (prefix of 4096, own
+// lists of n / 2 .. n; us, this kernel / those): 32 heads over 8 of 128: 64
+// sequences, n = 32: 19 / 31, 128: 25 / 33, 256: 33 / 36, 512: 47 / 42; 256
+// sequences: 42 / 60, 56 / 63, 77 / 74, 115 / 100; 8 sequences: 15 / 17, 18 / 17.
+// 24 over 4 of 256: 64 sequences 24 / 30, 30 / 33, 38 / 34; 256: 65 / 70, 84 / 72.
 bool own_applicable(const pa_params_t* p) {
-  return tc_applicable(p) && p->block_size % 16 == 0 &&
-         static_cast<int64_t>(p->num_seqs) * p->num_kv_heads < (int64_t(1) << 31);
+  const int64_t pairs = static_cast<int64_t>(p->num_seqs) * p->num_kv_heads;
+  return tc_applicable(p) && p->block_size % 16 == 0 && pairs >= 128 &&
+         pairs < (int64_t(1) << 31) && p->max_seq_len <= (p->head_dim == 128 ? 256 : 128);
 }
 
 cudaError_t launch_own(const KernelArgs& a, const JoinList& prefix, pa_dtype_t t, bool pdl,

@@ -1,14 +1,13 @@
 // pa_prefix.cu -- pa_decode_prefix: a batch that shares a prefix.
 //
 // The prefix is one product over all rows of a KV head, split over keys
-// (pa_rows.cuh; on the CUDA cores pa_portable.cuh).  Own lists of up to 512
-// tokens are then taken by one kernel that joins them with the prefix's
-// partials (pa_own.cu): two launches.  Longer ones go through pass 1 of V2 over
+// (pa_rows.cuh; on the CUDA cores pa_portable.cuh).  Short own lists of many
+// sequences are then taken by one kernel that joins them with the prefix's
+// partials (pa_own.cu): two launches.  Others go through pass 1 of V2 over
 // their block tables, as in pa_decode_v2_partitions, first, and a third kernel
 // joins both lists of partials (pa_join.cu).
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 
 #include "pa.h"
 #include "pa_internal.h"
@@ -137,9 +136,7 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
                                             p->scale)
                           : 0;
   // short own lists: one kernel for them and the join, after the prefix
-  const int own_max = getenv("PA_OWN") ? atoi(getenv("PA_OWN")) : 512;
-  const bool fused = own_applicable(p) && p->max_seq_len <= own_max &&
-                     (sms > 0 || prefix->max_prefix_len == 0);
+  const bool fused = own_applicable(p) && (sms > 0 || prefix->max_prefix_len == 0);
 
   // the sequences' own tokens
   if (!fused && p->max_seq_len > 0) {
