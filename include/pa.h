@@ -1,6 +1,10 @@
 /*
  * pa.h -- C ABI of libpa: single-token decode attention over a paged KV
- * cache on one GB300 (sm_103a).
+ * cache on one GB300 (sm_103a), and what a serving step needs around it: the
+ * step plan (pa_plan_step), norm, rotation and cache write
+ * (pa_qk_norm_rope), paged prefill (pa_prefill), attention with a sliding
+ * window and sinks (pa_decode_window, pa_prefill_window) and decode of a batch
+ * that shares a prefix (pa_decode_prefix).
  *
  * What the library computes.  For every sequence b < num_seqs and query head
  * h < num_heads, with G = num_heads / num_kv_heads, kvh = h / G and
@@ -415,7 +419,7 @@ PA_API pa_status_t pa_prefill(const pa_prefill_params_t* params, const void* q, 
  *   - query_start [num_seqs + 1] is the running sum of n_b, seq_lens[b] =
  *     C_b + n_b; row r = query_start[b] + i is new token i of request b, with
  *     positions[r] = *base_len + C_b + i (base_len may be null: 0; tokens of
- *     a shared prefix that the tables do not hold) and
+ *     a shared prefix that the tables do not hold; the sum fits 31 bits) and
  *     slots[r] = block * block_size + (C_b + i) % block_size, the place of its
  *     key and value in the cache pool.
  *   - Rows from the step's total up to max_tokens (a padded batch) get slot

@@ -74,14 +74,26 @@ struct Args {
     }
     return static_cast<float>(v);
   }
-  bool flag() { return PyObject_IsTrue(next()) == 1; }
+  bool flag() {
+    const int v = PyObject_IsTrue(next());
+    if (v < 0) {
+      PyErr_Clear();
+      throw Refused("a flag must be true or false");
+    }
+    return v == 1;
+  }
   // a stream handle, or None for the current stream of the tensors' device
   cudaStream_t stream(const at::Tensor& first) {
     require(first.is_cuda() && first.device().index() == c10::cuda::current_device(),
             "the tensors must be on the current CUDA device");
     PyObject* o = next();
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream(first.device().index()).stream();
-    return static_cast<cudaStream_t>(PyLong_AsVoidPtr(o));
+    void* s = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      throw Refused("stream must be a CUDA stream");
+    }
+    return static_cast<cudaStream_t>(s);
   }
 };
 

@@ -313,6 +313,6 @@ pa_status_t pa_read_device_status(const void* workspace, int32_t* status, int cl
   return PA_OK;
 }
 
-int pa_version(void) { return 100; }
+int pa_version(void) { return 200; }
 
 }  // extern "C"

@@ -28,6 +28,8 @@ pa_status_t check_prefix(const pa_params_t* p, const pa_prefix_t* x) {
   if (!x || x->max_prefix_len < 0 || x->max_prefix_blocks < 0) return PA_ERR_INVALID_ARG;
   if (x->max_prefix_len > static_cast<int64_t>(x->max_prefix_blocks) * p->block_size)
     return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(p->num_seqs) * p->num_heads >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;  // a CTA of the join per row
   if (static_cast<int64_t>(p->max_seq_len) + p->partition_size + 256 >= (int64_t(1) << 31) ||
       static_cast<int64_t>(x->max_prefix_len) + 2048 >= (int64_t(1) << 31))
     return PA_ERR_UNSUPPORTED;

@@ -29,6 +29,8 @@ int64_t parts_of(int64_t len, int64_t size) { return std::max<int64_t>(1, (len +
 pa_status_t check_decode(const pa_params_t* p, const pa_window_t* w) {
   if (pa_status_t st = check_params(p, true)) return st;
   if (pa_status_t st = check_window(w)) return st;
+  if (static_cast<int64_t>(p->num_seqs) * p->num_heads >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;  // a CTA of the join per row
   // list positions up to a partition past the longest list are int32
   if (static_cast<int64_t>(p->max_seq_len) + p->partition_size + 2LL * p->block_size >=
       (int64_t(1) << 31))

@@ -202,7 +202,8 @@ def prefix_problem(prefix, lens, hq, hkv, d, bs, dtype, seed):
     tables = torch.full((len(lens), max(1, -(-max(lens) // bs))), -1, dtype=torch.int32)
     q = pg.randn(len(lens), hq, d)
     ref, mag = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape, dtype=torch.float64)
-    kp, vp = paged_rows(pg.k, shared, range(prefix), bs), paged_rows(pg.v, shared, range(prefix), bs)
+    kp = paged_rows(pg.k, shared, range(prefix), bs)
+    vp = paged_rows(pg.v, shared, range(prefix), bs)
     for b, L in enumerate(lens):
         pg.fill(tables[b], range(L))
         k = torch.cat([kp, paged_rows(pg.k, tables[b], range(L), bs)])

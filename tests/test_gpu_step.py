@@ -324,7 +324,8 @@ def test_decode_window_wider_than_everything_is_decode():
 def test_decode_window_bad_inputs():
     lens = [700, 300, 500, 400]
     for kw in (dict(), dict(portable=True)):
-        q, pg, tables, gl, ref, mag = sr.window_decode_problem(lens, 200, 20, 8, 2, 128, 16, BF16, 6)
+        q, pg, tables, gl, ref, mag = sr.window_decode_problem(lens, 200, 20, 8, 2, 128, 16, BF16,
+                                                               6)
         tables[0, 0] = 10 ** 6                              # a sink block
         tables[1, 299 // 16] = -1                           # the last window block
         tables[2, 10] = 10 ** 6                             # between: not read
@@ -332,7 +333,8 @@ def test_decode_window_bad_inputs():
         assert torch.isnan(out[:2]).all()
         sr.assert_within(out[2:], ref[2:], mag[2:], BF16, F32, False)
         assert pa.read_device_status(ws) == pa.PA_ERR_BAD_BLOCK_ID
-        q, pg, tables, gl, ref, mag = sr.window_decode_problem(lens, 200, 20, 8, 2, 128, 16, BF16, 6)
+        q, pg, tables, gl, ref, mag = sr.window_decode_problem(lens, 200, 20, 8, 2, 128, 16, BF16,
+                                                               6)
         gl[1], gl[3] = -1, 701
         out, ws = _run_window(q, pg, tables, gl, 200, 20, check=False, max_len=700, **kw)
         assert torch.isnan(out[1]).all() and torch.isnan(out[3]).all()
@@ -510,6 +512,181 @@ def test_decode_prefix_bad_inputs():
         out, ws = _run_prefix(p, 400, max_len=60, check=False, **kw)
         assert torch.isnan(out[2]).all()
         sr.assert_within(out[:2], ref[:2], mag[:2], BF16, F32, True)
+
+
+def test_decode_prefix_many_short_sequences():
+    """Many sequences with short own lists: the kernel that joins as it goes,
+    at both head_dims, with and without a prefix, and its bad inputs."""
+    for hq, hkv, d, bs, dtype, prefix in ((24, 4, 256, 16, BF16, 500), (7, 4, 128, 64, F16, 131),
+                                          (32, 8, 128, 32, BF16, 0)):
+        hq = hq if hq % hkv == 0 else hkv * 3
+        lens = [int(x) for x in np.random.RandomState(d).randint(0, 100, size=41)]
+        p = sr.prefix_problem(prefix, lens, hq, hkv, d, bs, dtype, seed=11)
+        ref, mag = p[5:]
+        got = _run_prefix(p, prefix)
+        sr.assert_within(got, ref, mag, dtype, F32, True)
+        got = _run_prefix(p, prefix, out_dtype=dtype)
+        sr.assert_within(got, ref, mag, dtype, dtype, True)
+        bad = next(i for i, n in enumerate(lens) if n > 20)
+        p[3][bad, 0] = 10 ** 6
+        p[4][40] = 101
+        out, ws = _run_prefix(p, prefix, max_len=100, check=False)
+        good = [i for i in range(40) if i != bad]
+        assert torch.isnan(out[bad]).all() and torch.isnan(out[40]).all()
+        sr.assert_within(out[good], ref[good], mag[good], dtype, F32, True)
+        assert pa.read_device_status(ws) in (pa.PA_ERR_BAD_BLOCK_ID, pa.PA_ERR_BAD_SEQ_LEN)
+
+
+# ------------------------------------------------------- what is easily missed
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(6, 1, 128, 16), (4, 2, 256, 32)])
+def test_prefill_window_wide_is_prefill(hq, hkv, d, bs):
+    """A window wider than the sequences: the plain prefill's result."""
+    p = sr.window_prefill_problem((200, 0, 33), (70, 150, 1), 10 ** 6, 0, hq, hkv, d, bs, BF16, 3)
+    q, k, v, pg, tables, start, ctx, ref, mag = p
+    got = _run_window_prefill(p, 10 ** 6, 0)
+    out = torch.empty(q.shape, device="cuda")
+    pa.prefill(q.cuda(), k.cuda(), v.cuda(), pg.k.cuda(), pg.v.cuda(), tables.cuda(), start.cuda(),
+               ctx.cuda(), out, max_query_len=150, max_ctx_len=200, scale=d ** -0.5)
+    sr.assert_within(got, ref, mag, BF16, F32, True)
+    sr.assert_within(out, ref, mag, BF16, F32, True)
+
+
+@pytest.mark.parametrize("B,hi", [(70, 40), (2100, 3)])
+def test_prefill_window_many_sequences(B, hi):
+    r = np.random.RandomState(B)
+    ctx = [int(x) for x in r.randint(0, 20, size=B)]
+    new = [int(x) for x in r.randint(0, hi, size=B)]
+    p = sr.window_prefill_problem(ctx, new, 9, 2, 2, 1, 128, 16, BF16, seed=B)
+    sr.assert_within(_run_window_prefill(p, 9, 2), p[7], p[8], BF16, F32, True)
+
+
+def test_prefill_window_output_on_16_bytes():
+    p = sr.window_prefill_problem((100,), (50,), 60, 4, 4, 2, 128, 16, BF16, seed=5)
+    q, k, v, pg, tables, start, ctx, ref, mag = p
+    flat = torch.zeros(q.numel() + 8, dtype=BF16, device="cuda")
+    out = flat[8:].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    pa.prefill_window(q.cuda(), k.cuda(), v.cuda(), pg.k.cuda(), pg.v.cuda(), tables.cuda(),
+                      start.cuda(), ctx.cuda(), out, window=60, num_sinks=4, max_query_len=50,
+                      max_ctx_len=100, scale=128 ** -0.5)
+    sr.assert_within(out, ref, mag, BF16, BF16, True)
+    assert (flat[:8] == 0).all()
+
+
+def test_waits_that_run_out():
+    """The diagnostic flag makes a wait of the tensor-core kernels run out: NaN
+    and the status, and the next call is right."""
+    stall = pa.PA_FLAG_SELFTEST_STALL
+    for d in (128, 256):
+        p = sr.window_prefill_problem((100,), (50,), 60, 4, 4, 2, d, 16, BF16, seed=5)
+        assert torch.isnan(_run_window_prefill(p, 60, 4, flags=stall)).all()
+        sr.assert_within(_run_window_prefill(p, 60, 4), p[7], p[8], BF16, F32, True)
+        p = sr.prefix_problem(300, (5, 40), 4, 2, d, 16, BF16, seed=6)
+        out, ws = _run_prefix(p, 300, flags=stall, check=False)
+        assert torch.isnan(out).all()
+        assert pa.read_device_status(ws) == pa.PA_ERR_DEVICE_TIMEOUT
+        sr.assert_within(_run_prefix(p, 300), p[5], p[6], BF16, F32, True)
+        q, pg, tables, gl, ref, mag = sr.window_decode_problem([700, 90], 300, 4, 4, 2, d, 16, BF16,
+                                                               seed=7)
+        out, ws = _run_window(q, pg, tables, gl, 300, 4, flags=stall, check=False)
+        assert torch.isnan(out).all()
+        assert pa.read_device_status(ws) == pa.PA_ERR_DEVICE_TIMEOUT
+        sr.assert_within(_run_window(q, pg, tables, gl, 300, 4), ref, mag, BF16, F32, False)
+
+
+def test_caches_past_32_bit_offsets():
+    """Blocks whose elements lie past 2^31 in the pool, for every reader and
+    for the writer."""
+    hq, hkv, d, bs = 4, 4, 256, 16
+    blocks = 2 ** 31 // (hkv * bs * d) + 64
+    big_k = torch.empty(blocks, hkv, bs, d, dtype=BF16, device="cuda")
+    big_v = torch.empty_like(big_k)
+    far = blocks - 60                                       # small problems' blocks go here
+
+    def place(pg, *tables):
+        n = pg.k.shape[0]
+        assert n < 60
+        big_k[far:far + n], big_v[far:far + n] = pg.k.cuda(), pg.v.cuda()
+        return [torch.where(t >= 0, t + far, t).cuda() for t in tables]
+
+    q, pg, tables, gl, ref, mag = sr.window_decode_problem([300, 77], 100, 20, hq, hkv, d, bs, BF16,
+                                                           1)
+    gt, = place(pg, tables)
+    out = torch.empty(q.shape, device="cuda")
+    for portable in (False, True):
+        ws = pa.alloc_window_workspace(q.cuda(), big_k, gt, window=100, num_sinks=20,
+                                       max_seq_len=300)
+        pa.decode_window(q.cuda(), big_k, big_v, gt, gl.cuda(), out, ws, window=100, num_sinks=20,
+                         max_seq_len=300, scale=d ** -0.5, portable=portable)
+        sr.assert_within(out, ref, mag, BF16, F32, False)
+    p = sr.window_prefill_problem((150,), (40,), 70, 3, hq, hkv, d, bs, BF16, 2)
+    gt, = place(p[3], p[4])
+    out = torch.empty(p[0].shape, device="cuda")
+    for portable in (False, True):
+        pa.prefill_window(p[0].cuda(), p[1].cuda(), p[2].cuda(), big_k, big_v, gt, p[5].cuda(),
+                          p[6].cuda(), out, window=70, num_sinks=3, max_query_len=40,
+                          max_ctx_len=150, scale=d ** -0.5, portable=portable)
+        sr.assert_within(out, p[7], p[8], BF16, F32, not portable)
+    p = sr.prefix_problem(120, [3] * 40, hq, hkv, d, bs, BF16, 3)
+    gs, gt = place(p[1], p[2], p[3])
+    out = torch.empty(p[0].shape, device="cuda")
+    for portable in (False, True):
+        ws = pa.alloc_prefix_workspace(p[0].cuda(), big_k, gt, max_seq_len=3, max_prefix_len=120)
+        pa.decode_prefix(p[0].cuda(), big_k, big_v, gs, i32([120]), gt, p[4].cuda(), out, ws,
+                         max_seq_len=3, max_prefix_len=120, scale=d ** -0.5, portable=portable)
+        sr.assert_within(out, p[5], p[6], BF16, F32, not portable)
+    T = 20
+    x = torch.randn(T, 3 * hq, d, device="cuda").to(BF16)
+    slots = far * bs + torch.arange(T, device="cuda") * 3
+    q_out = torch.empty(T, hq, d, dtype=BF16, device="cuda")
+    pa.qk_norm_rope(x[:, :hq], x[:, hq:2 * hq], x[:, 2 * hq:], None, slots, None, q_out, big_k,
+                    big_v)
+    assert torch.equal(big_k[slots // bs, :, slots % bs], x[:, hq:2 * hq])
+    assert torch.equal(big_v[slots // bs, :, slots % bs], x[:, 2 * hq:])
+
+
+def test_nothing_to_do():
+    """Empty batches, lists and chunks."""
+    q, pg, tables, gl, ref, mag = sr.window_decode_problem([0, 0], 5, 2, 4, 2, 128, 16, BF16, 1)
+    out = _run_window(q, pg, tables, gl, 5, 2)
+    assert (out == 0).all()
+    e = torch.empty(0, 4, 128, dtype=BF16, device="cuda")
+    kc, vc = pg.k.cuda(), pg.v.cuda()
+    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    bt, sl = torch.zeros(0, 3, dtype=torch.int32, device="cuda"), i32([])
+    pa.decode_window(e, kc, vc, bt, sl, e.clone(), ws, window=5, max_seq_len=9, scale=1.0)
+    pa.decode_prefix(e, kc, vc, i32([0]), i32([3]), bt, sl, e.clone(), ws, max_seq_len=9,
+                     max_prefix_len=16, scale=1.0)
+    z = torch.empty(0, 2, 128, dtype=BF16, device="cuda")
+    pa.prefill_window(e, z, z, kc, vc, torch.zeros(1, 3, dtype=torch.int32, device="cuda"),
+                      i32([0, 0]), i32([0]), e.clone(), window=5, max_query_len=4, max_ctx_len=0,
+                      scale=1.0)
+    pa.qk_norm_rope(e, z, z, None, torch.zeros(0, dtype=torch.int64, device="cuda"), None,
+                    e.clone())
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its own workspace."""
+    probs = [sr.prefix_problem(700 + 100 * i, (30, 5, 60), 8, 2, 128, 16, BF16, seed=20 + i)
+             for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in probs]
+    state = []
+    for p in probs:
+        q, pg, shared, tables, lens = p[:5]
+        g = [t.cuda() for t in (q, pg.k, pg.v, shared, tables, lens)]
+        ws = pa.alloc_prefix_workspace(g[0], g[1], g[4], max_seq_len=60,
+                                       max_prefix_len=shared.shape[0] * 16)
+        state.append((g, ws, torch.empty(q.shape, device="cuda")))
+    torch.cuda.synchronize()
+    plen = [i32([700]), i32([800])]
+    for _ in range(20):
+        for (g, ws, out), s, n in zip(state, streams, plen):
+            pa.decode_prefix(g[0], g[1], g[2], g[3], n, g[4], g[5], out, ws, max_seq_len=60,
+                             max_prefix_len=g[3].shape[0] * 16, scale=128 ** -0.5, stream=s)
+    torch.cuda.synchronize()
+    for (g, ws, out), p in zip(state, probs):
+        sr.assert_within(out, p[5], p[6], BF16, F32, True)
 
 
 # ---------------------------------------------------------------- a run together
