@@ -38,9 +38,9 @@ pa_status_t check_prefix(const pa_params_t* p, const pa_prefix_t* x) {
 
 // The tensor-core prefix pass's plan for these shapes, whatever the device:
 // rows of a row tile and of a unit, and the number of key blocks.  Row groups x
-// key blocks are the units; with k rounds of 152 CTAs there is room for
-// floor(152 k / groups) key blocks, and a round costs as much as its key block
-// is long, so k minimises k / key blocks (and a little per round).
+// key blocks are the units; with k rounds of S CTAs there is room for
+// floor(S k / groups) key blocks, and a round costs as much as its key block is
+// long, so k minimises k / key blocks (and a little per round).
 struct RowsPlan {
   bool shape;  // served by the tensor-core kernel as far as shapes go
   int row_tokens, group_tokens, row_groups, dual, lanes, key_blocks;
@@ -49,6 +49,14 @@ struct RowsPlan {
 
 RowsPlan rows_plan(const pa_params_t* p, const pa_prefix_t* x) {
   constexpr int kSms = 152;
+  // The own lists' pass 1 runs beside this one.  16 to 76 work items of it (half
+  // the SMs) get SMs of their own; fewer delay a few of this pass's CTAs less
+  // than the SMs are worth, more would leave it too few.  Measured, all SMs
+  // against this: 8 sequences, 4 KV heads of 256, prefix 8192 21.4 and 18.4 us,
+  // 32000 41.3 and 34.8 us; with 1 sequence (4 items) 16.9 and 17.9 us.
+  const int64_t own = static_cast<int64_t>(p->num_seqs) * p->num_kv_heads *
+                      ceil_div(p->max_seq_len, p->partition_size);
+  const int room = own >= 16 && own <= kSms / 2 ? kSms - static_cast<int>(own) : kSms;
   RowsPlan r{};
   const int G = p->num_heads / p->num_kv_heads;
   r.shape = G <= 64 && (p->head_dim == 128 || p->head_dim == 256) && p->num_seqs > 0 &&
@@ -60,10 +68,10 @@ RowsPlan rows_plan(const pa_params_t* p, const pa_prefix_t* x) {
   r.lanes = p->head_dim == 128 && !r.dual ? 2 : 1;
   r.group_tokens = r.row_tokens * (r.dual ? 2 : 1);
   r.row_groups = static_cast<int>(ceil_div(p->num_seqs, r.group_tokens));
-  const int k0 = static_cast<int>(ceil_div(r.row_groups, kSms));
+  const int k0 = static_cast<int>(ceil_div(r.row_groups, room));
   double best = 0;
   for (int k = k0; k < k0 + 4; ++k) {
-    const int blocks = k * kSms / r.row_groups;
+    const int blocks = k * room / r.row_groups;
     const double cost = static_cast<double>(k) / blocks * (1.0 + 0.02 * k);
     if (k == k0 || cost < best) {
       best = cost;

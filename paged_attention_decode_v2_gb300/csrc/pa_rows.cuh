@@ -22,9 +22,10 @@
 // a key tile: QK^T into one of two tensor-memory buffers ("slots"), softmax
 // of that slot by its own four warps, one thread per row, P written over the
 // logits in 16 bits (keys 0-63 handed on before 64-127), and P.V from tensor
-// memory.  The MMA warp issues
-// QK^T(k), P.V(k - 1), so the tensor core works on one slot while the warps of
-// the other run their softmax.
+// memory.  The MMA warp issues QK^T(k), P.V(k - 1), so the tensor core works on
+// one slot while the warps of the other run their softmax.  Twelve warps: 0-7
+// softmax, 8 issues the MMAs, 9 and 10 stream keys and values through a ring of
+// five 32 KB stages, 11 loads the next unit's rows.
 //   head_dim 128, two row tiles ("dual"): slot s is row tile s, both against
 //     the same key tile, which is read from shared memory twice and copied
 //     once; each slot has its own output accumulator.
@@ -276,23 +277,6 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, 
       return true;
     }
   }
-}
-
-// Walking and waiting out of line, for all roles but the softmax (which holds
-// too many registers for a call): the roles must share the instruction cache,
-// there are many waits, and most find their barrier ready.
-template <bool kPrefix>
-__device__ __forceinline__ bool walk_call(const RowsArgs& a, const int* before, Walk& w, Unit& u) {
-  return walk_next<kPrefix>(a, before, w, u);
-}
-__device__ __forceinline__ bool wait_loop(uint64_t* bar, uint32_t parity, long long budget,
-                                       const volatile int* abort) {
-  return sm100::mbar_wait(bar, parity, budget, abort);
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long budget,
-                                         const volatile int* abort) {
-  if (sm100::mbar_try_wait(bar, parity)) return true;
-  return wait_loop(bar, parity, budget, abort);
 }
 
 // 2^x by the hardware's approximate exponential: relative error well below the
@@ -548,365 +532,367 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
   if (warp >= kMmaWarp) {
     // one instruction for the whole warpgroup, before its roles part
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp > kMmaWarp) {
-    // ========================= row loader =========================================
-    // The unit's row tiles, as soon as the last unit's QK^T are done with theirs.
     uint64_t keep;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
     if (warp == kRowWarp) {
-    // The rows come from HBM in 128-byte pieces, several microseconds for a
-    // tile: so the next unit's are fetched into L2 while this one runs.
-    uint32_t un = 0;
-    bool ok = true;
-    Walk wk = walk_begin();
-    Unit u;
-    const int copies = dual ? 2 * kSl : kSl;
-    bool more = true;
-    for (int i = 0;; ++i) {
-      // i = 0: find the first unit; then load one and find the next
-      if (i > 0) {
-        ok = __all_sync(kAll, wait_bar(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
-        if (!ok) break;
-        // rows past the sequence belong to others or are filled with zeros;
-        // their results are never stored
-        if (lane == 0)
-          sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
-        __syncwarp();
-        if (lane < copies)
-          sm100::tma_load_4d(qs + lane * kSliceBytes, &qmap, &c.qfull, 0, u.kvh * a.group,
-                             static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
-                             lane % kSl, keep);
-        ++un;
-      }
-      more = walk_call<kPrefix>(a, before, wk, u);
-      if (!more) break;
-      if (i > 0 && lane < copies)
-        tma_prefetch_4d(&qmap, 0, u.kvh * a.group,
-                        static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
-                        lane % kSl);
-    }
-    if (!ok) {
-      if (lane == 0) c.abort = 1;
-      if (un > 0) wait_bar(&c.qfull, (un - 1) & 1, budget, nullptr);
-    }
-    } else {
-    // ========================= producers ==========================================
-    // Both walk the stages in the order the MMA warp takes them -- dual: keys,
-    // values of each tile; else keys 0, then (keys j, values j - 1), then the
-    // last values -- and each fills every other one.
-    const uint32_t pid = static_cast<uint32_t>(warp - kMmaWarp - 1);
-    uint64_t* my_tail = &c.tail[pid];
-    uint32_t g = 0, tn = 0;
-    int tail_pending = -1;
-    bool ok = true;
-
-    // Block id of each lane's block of a context tile; loaded a tile ahead.
-    auto ctx_id = [&](const Unit& u, int j) -> int32_t {
-      if (j >= u.tiles) return -1;
-      const Tile t = tile_of(u, j);
-      if (!t.ctx || lane >= (t.nk + BS - 1) / BS) return -1;
-      return __ldg(a.block_tables + static_cast<int64_t>(u.seq) * a.max_blocks_per_seq +
-                   t.pos0 / BS + lane);
-    };
-    // Its TMA row; a block outside the pool, or one that no row sees, becomes
-    // a negative row, which TMA fills with zeros instead of reading memory.
-    auto ctx_row = [&](const Unit& u, const Tile& t, int32_t id) -> int32_t {
-      const int32_t p = t.pos0 + lane * BS;
-      const bool seen = kPrefix || p < a.num_sinks || p + BS > u.lo_min;
-      return (!seen || id < 0 || id >= a.num_blocks) ? -BS : (id * a.num_kv_heads + u.kvh) * BS;
-    };
-    auto wait_empty = [&](int slot) {
-      return __all_sync(kAll, wait_bar(&c.empty[slot], ((g / NST) & 1) ^ 1, budget,
-                                               abort_flag)) != 0;
-    };
-
-    auto issue_k = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
-      constexpr int kMaxBlk = kTile / BS;
-      const int nblk = (t.nk + BS - 1) / BS;
-      for (int sl = 0; sl < kSl; sl += 2, ++g) {
-        if (g % kProducers != pid) continue;
-        const int slot = g % NST;
-        if (!wait_empty(slot)) return false;
-        uint8_t* st = ring + slot * kStage;
-        if (t.ctx) {
-          // one lane per block and slice
-          const int blk = lane % kMaxBlk, half = lane / kMaxBlk;
-          const int32_t yj = __shfl_sync(kAll, y, blk);
-          if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], 2 * nblk * BS * 128);
+      // ========================= row loader =========================================
+      // The unit's row tiles, as soon as the last unit's QK^T are done with theirs.
+      // The rows come from HBM in 128-byte pieces, several microseconds for a
+      // tile: so the next unit's are fetched into L2 while this one runs.
+      uint32_t un = 0;
+      bool ok = true;
+      Walk wk = walk_begin();
+      Unit u;
+      const int copies = dual ? 2 * kSl : kSl;
+      bool more = true;
+      for (int i = 0;; ++i) {
+        // i = 0: find the first unit; then load one and find the next
+        if (i > 0) {
+          ok = __all_sync(kAll, sm100::mbar_wait(&c.qempty, (un & 1) ^ 1, budget, abort_flag));
+          if (!ok) break;
+          // rows past the sequence belong to others or are filled with zeros;
+          // their results are never stored
+          if (lane == 0)
+            sm100::mbar_arrive_expect_tx(&c.qfull, copies * a.row_tokens * a.group * 128);
           __syncwarp();
-          if (half < 2 && blk < nblk)
-            sm100::tma_load_2d(st + half * kSliceBytes + blk * BS * 128, &kcmap, &c.full[slot],
-                               (sl + half) * 64, yj, keep);
-        } else {
-          if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], kStage);
-          __syncwarp();
-          if (lane < 2)
-            sm100::tma_load_4d(st + lane * kSliceBytes, &knmap, &c.full[slot], 0, u.kvh,
-                               static_cast<int32_t>(u.row0) + t.chunk, sl + lane, keep);
+          if (lane < copies)
+            sm100::tma_load_4d(qs + lane * kSliceBytes, &qmap, &c.qfull, 0, u.kvh * a.group,
+                               static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
+                               lane % kSl, keep);
+          ++un;
         }
-        __syncwarp();
+        more = walk_next<kPrefix>(a, before, wk, u);
+        if (!more) break;
+        if (i > 0 && lane < copies)
+          tma_prefetch_4d(&qmap, 0, u.kvh * a.group,
+                          static_cast<int32_t>(u.row0) + u.i0 + lane / kSl * a.row_tokens,
+                          lane % kSl);
       }
-      return true;
-    };
+      if (!ok) {
+        if (lane == 0) c.abort = 1;
+        if (un > 0) sm100::mbar_wait(&c.qfull, (un - 1) & 1, budget, nullptr);
+      }
+    } else if (warp > kMmaWarp) {
+      // ========================= producers ==========================================
+      // Both walk the stages in the order the MMA warp takes them -- dual: keys,
+      // values of each tile; else keys 0, then (keys j, values j - 1), then the
+      // last values -- and each fills every other one.
+      const uint32_t pid = static_cast<uint32_t>(warp - kMmaWarp - 1);
+      uint64_t* my_tail = &c.tail[pid];
+      uint32_t g = 0, tn = 0;
+      int tail_pending = -1;
+      bool ok = true;
 
-    // Values of a tile.  Keys that no row sees -- past the tile's last key up
-    // to the end of its 16-key MMA step, and the run between the sinks and
-    // the first row's window -- are cleared before the stage is handed on:
-    // their p is zero, but 0 * NaN would be NaN.  Such a stage lands on the
-    // producer's own barrier first.
-    auto issue_v = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
-      const int nv = (t.nk + kVT - 1) / kVT;
-      // the unseen run [h0, h1) of the tile; of a context tile, blocks inside it
-      // have come as zeros, so only the ends in blocks that are seen remain:
-      // [h0, e0) and [e1, h1)
-      const int h0 = kPrefix ? 0 : max(0, a.num_sinks - t.pos0);
-      const int h1 = kPrefix ? 0 : max(h0, min(t.nk, u.lo_min - t.pos0));
-      const int e0 = t.ctx ? min(h1, (h0 + BS - 1) / BS * BS) : h1;
-      const int e1 = t.ctx && h0 < h1 ? max(e0, h1 / BS * BS) : h1;
-      for (int v = 0; v < nv; ++v, ++g) {
-        if (g % kProducers != pid) continue;
-        const int slot = g % NST;
-        if (!wait_empty(slot)) return false;
-        const int toks = min(kVT, t.nk - v * kVT);
-        const int ncp = (toks + BS - 1) / BS;  // copies, of BS rows each
-        // rows of this stage to clear: [a0, a1), [b0, b1) and [toks, z1)
-        const int a0 = max(h0 - v * kVT, 0), a1 = max(a0, min(e0 - v * kVT, toks));
-        const int b0 = max(e1 - v * kVT, 0), b1 = max(b0, min(h1 - v * kVT, toks));
-        const int z1 = (toks + 15) / 16 * 16;
-        const bool clear = a0 < a1 || b0 < b1 || toks < z1;
-        uint64_t* land = clear ? my_tail : &c.full[slot];
-        uint8_t* st = ring + slot * kStage;
-        if (lane == 0) sm100::mbar_arrive_expect_tx(land, ncp * BS * D * 2);
-        __syncwarp();
-        if (t.ctx) {
-          const int32_t yj = __shfl_sync(kAll, y, (v * kVT / BS + lane) & 31);
-          if (lane < ncp) sm100::tma_load_3d(st + lane * BS * D * 2, &vcmap, land, 0, yj, 0, keep);
-        } else if (lane < ncp) {
-          sm100::tma_load_4d(st + lane * BS * D * 2, &vnmap, land, 0, u.kvh,
-                             static_cast<int32_t>(u.row0) + t.chunk + v * kVT + lane * BS, 0, keep);
-        }
-        __syncwarp();
-        if (clear) {
-          tail_pending = slot;
-          if (!__all_sync(kAll, wait_bar(my_tail, tn & 1, budget, abort_flag)))
-            return false;
-          ++tn;
-          tail_pending = -1;
-          auto zero = [&](int r0, int r1) {
-            for (int i = lane; i < (r1 - r0) * kSl * 8; i += 32) {
-              const int line = i / 8, r = r0 + line / kSl, sl = line % kSl;
-              *reinterpret_cast<uint4*>(st + ((r / BS * kSl + sl) * BS + r % BS) * 128 +
-                                        i % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          };
-#pragma unroll 1
-          for (int x = 0; x < 3; ++x)
-            zero(x == 0 ? a0 : x == 1 ? b0 : toks, x == 0 ? a1 : x == 1 ? b1 : z1);
-          sm100::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) sm100::mbar_arrive(&c.full[slot]);
-        }
-      }
-      return true;
-    };
-
-    Walk wk = walk_begin();
-    Unit u;
-    while (ok && walk_call<kPrefix>(a, before, wk, u)) {
-      // j = -1 only looks up tile 0's blocks; the last round has values alone
-      int32_t y = 0, yprev = 0, id = 0;
-      Tile t{}, tprev{};
-#pragma unroll 1
-      for (int j = -1; j <= u.tiles && ok; ++j) {
-        if (j >= 0) {
-          yprev = y;
-          tprev = t;
-          t = tile_of(u, j);
-          y = t.ctx ? ctx_row(u, t, id) : 0;
-        }
-        id = ctx_id(u, j + 1);
-        if (j >= 0 && j < u.tiles) ok = issue_k(u, t, y);
-        if (dual ? j >= 0 && j < u.tiles : j > 0)
-          if (ok) ok = issue_v(u, dual ? t : tprev, dual ? y : yprev);
-      }
-    }
-    if (!ok) {
-      if (lane == 0) c.abort = 1;
-      // copies already issued must land before the CTA may exit
-      for (uint32_t gg = g > NST ? g - NST : 0; gg < g; ++gg)
-        if (gg % kProducers == pid && static_cast<int>(gg % NST) != tail_pending)
-          wait_bar(&c.full[gg % NST], (gg / NST) & 1, budget, nullptr);
-      if (tail_pending >= 0) wait_bar(my_tail, tn & 1, budget, nullptr);
-    }
-    }
-    } else {
-    // ========================= MMA issuer =========================================
-    // One MMA occupies the tensor core for 64 (N = 128) or 128 cycles and this
-    // warp issues in order, one instruction every few cycles, so every
-    // instruction between MMAs counts: slots are compile-time, ring positions
-    // are counted, descriptors are a base plus constants, four MMAs share an
-    // election, and nothing is waited for that an earlier wait implies.
-    constexpr uint32_t id_qk = sm100::idesc_f16(kBf16, false, false, 128, kTile);
-    constexpr uint32_t id_pv = sm100::idesc_f16(kBf16, false, true, 128, D);
-    const uint64_t q_desc = sm100::smem_desc(sm100::smem_u32(qs), 16, 1024, sm100::kSw128);
-    const uint64_t k_desc = sm100::smem_desc(sm100::smem_u32(ring), 16, 1024, sm100::kSw128);
-    const uint64_t v_desc = sm100::smem_desc(sm100::smem_u32(ring), BS * 128, 1024, sm100::kSw128);
-    struct Ring {
-      uint32_t slot, phase;
-      __device__ __forceinline__ void next() {
-        if (++slot == NST) {
-          slot = 0;
-          phase ^= 1;
-        }
-      }
-    };
-    Ring rg{0, 0};              // next stage of the ring
-    Ring rk{0, 0}, rv{0, 0};    // dual: stages of the current key and value tiles
-    uint32_t un = 0;            // units
-    uint32_t parity[2] = {0, 0};  // of the P.V in each slot
-    bool ok = true;
-    using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
-    if (a.selftest_stall) ok = __all_sync(kAll, wait_bar(&c.never, 0, budget, abort_flag));
-    auto wait_for = [&](uint64_t* bar, uint32_t phase) {
-      const bool r = __all_sync(kAll, wait_bar(bar, phase, budget, abort_flag)) != 0;
-      sm100::tc_fence_after();
-      return r;
-    };
-    // logits into slot S: keys from the ring, or (dual, slot 1) those in hand
-    auto qk = [&](auto slot) -> bool {
-      const int S = slot;
-      const bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
-      if (kFresh) rk = rg;
-      Ring r = rk;
-      const uint32_t d = tmem + S * kTile;
-      const uint64_t qd = q_desc + (kDual && S ? kSl * kSliceBytes / 16 : 0);
-#pragma unroll
-      for (int st = 0; st < Lay::kKStages; ++st) {
-        if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
-        const uint64_t kd = k_desc + r.slot * (kStage / 16);
-        mma4_ss(d, qd + 2 * st * (kSliceBytes / 16), kd, id_qk, st != 0);
-        mma4_ss(d, qd + (2 * st + 1) * (kSliceBytes / 16), kd + kSliceBytes / 16, id_qk, true);
-        if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
-        r.next();
-      }
-      if (kFresh) rg = r;
-      return true;
-    };
-    // the MMAs of keys r0 .. r0 + 63 of one value stage (rows of BS per slice),
-    // as many as the stage's `toks` keys reach
-    auto pv_keys = [&](auto from, uint32_t stage, uint32_t at, uint32_t o, int toks, bool first) {
-      constexpr int r0 = decltype(from)::value;
-      const uint64_t vd = v_desc + stage * (kStage / 16);
-      auto off = [](int r) {
-        return static_cast<uint64_t>(((r / BS) * BS * D * 2 + (r % BS) * 128) / 16);
+      // Block id of each lane's block of a context tile; loaded a tile ahead.
+      auto ctx_id = [&](const Unit& u, int j) -> int32_t {
+        if (j >= u.tiles) return -1;
+        const Tile t = tile_of(u, j);
+        if (!t.ctx || lane >= (t.nk + BS - 1) / BS) return -1;
+        return __ldg(a.block_tables + static_cast<int64_t>(u.seq) * a.max_blocks_per_seq +
+                     t.pos0 / BS + lane);
       };
-      if (toks >= r0 + 64) {
-        mma4_ts(o, at + r0 / 2, vd + off(r0), vd + off(r0 + 16), vd + off(r0 + 32),
-                vd + off(r0 + 48), id_pv, !first || r0 != 0);
-        return;
-      }
+      // Its TMA row; a block outside the pool, or one that no row sees, becomes
+      // a negative row, which TMA fills with zeros instead of reading memory.
+      auto ctx_row = [&](const Unit& u, const Tile& t, int32_t id) -> int32_t {
+        const int32_t p = t.pos0 + lane * BS;
+        const bool seen = kPrefix || p < a.num_sinks || p + BS > u.lo_min;
+        return (!seen || id < 0 || id >= a.num_blocks) ? -BS : (id * a.num_kv_heads + u.kvh) * BS;
+      };
+      auto wait_empty = [&](int slot) {
+        return __all_sync(kAll, sm100::mbar_wait(&c.empty[slot], ((g / NST) & 1) ^ 1, budget,
+                                                 abort_flag)) != 0;
+      };
+
+      auto issue_k = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
+        constexpr int kMaxBlk = kTile / BS;
+        const int nblk = (t.nk + BS - 1) / BS;
+        for (int sl = 0; sl < kSl; sl += 2, ++g) {
+          if (g % kProducers != pid) continue;
+          const int slot = g % NST;
+          if (!wait_empty(slot)) return false;
+          uint8_t* st = ring + slot * kStage;
+          if (t.ctx) {
+            // one lane per block and slice
+            const int blk = lane % kMaxBlk, half = lane / kMaxBlk;
+            const int32_t yj = __shfl_sync(kAll, y, blk);
+            if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], 2 * nblk * BS * 128);
+            __syncwarp();
+            if (half < 2 && blk < nblk)
+              sm100::tma_load_2d(st + half * kSliceBytes + blk * BS * 128, &kcmap, &c.full[slot],
+                                 (sl + half) * 64, yj, keep);
+          } else {
+            if (lane == 0) sm100::mbar_arrive_expect_tx(&c.full[slot], kStage);
+            __syncwarp();
+            if (lane < 2)
+              sm100::tma_load_4d(st + lane * kSliceBytes, &knmap, &c.full[slot], 0, u.kvh,
+                                 static_cast<int32_t>(u.row0) + t.chunk, sl + lane, keep);
+          }
+          __syncwarp();
+        }
+        return true;
+      };
+
+      // Values of a tile.  Keys that no row sees -- past the tile's last key up
+      // to the end of its 16-key MMA step, and the run between the sinks and
+      // the first row's window -- are cleared before the stage is handed on:
+      // their p is zero, but 0 * NaN would be NaN.  Such a stage lands on the
+      // producer's own barrier first.
+      auto issue_v = [&](const Unit& u, const Tile& t, int32_t y) -> bool {
+        const int nv = (t.nk + kVT - 1) / kVT;
+        // the unseen run [h0, h1) of the tile; of a context tile, blocks inside it
+        // have come as zeros, so only the ends in blocks that are seen remain:
+        // [h0, e0) and [e1, h1)
+        const int h0 = kPrefix ? 0 : max(0, a.num_sinks - t.pos0);
+        const int h1 = kPrefix ? 0 : max(h0, min(t.nk, u.lo_min - t.pos0));
+        const int e0 = t.ctx ? min(h1, (h0 + BS - 1) / BS * BS) : h1;
+        const int e1 = t.ctx && h0 < h1 ? max(e0, h1 / BS * BS) : h1;
+        for (int v = 0; v < nv; ++v, ++g) {
+          if (g % kProducers != pid) continue;
+          const int slot = g % NST;
+          if (!wait_empty(slot)) return false;
+          const int toks = min(kVT, t.nk - v * kVT);
+          const int ncp = (toks + BS - 1) / BS;  // copies, of BS rows each
+          // rows of this stage to clear: [a0, a1), [b0, b1) and [toks, z1)
+          const int a0 = max(h0 - v * kVT, 0), a1 = max(a0, min(e0 - v * kVT, toks));
+          const int b0 = max(e1 - v * kVT, 0), b1 = max(b0, min(h1 - v * kVT, toks));
+          const int z1 = (toks + 15) / 16 * 16;
+          const bool clear = a0 < a1 || b0 < b1 || toks < z1;
+          uint64_t* land = clear ? my_tail : &c.full[slot];
+          uint8_t* st = ring + slot * kStage;
+          if (lane == 0) sm100::mbar_arrive_expect_tx(land, ncp * BS * D * 2);
+          __syncwarp();
+          if (t.ctx) {
+            const int32_t yj = __shfl_sync(kAll, y, (v * kVT / BS + lane) & 31);
+            if (lane < ncp)
+              sm100::tma_load_3d(st + lane * BS * D * 2, &vcmap, land, 0, yj, 0, keep);
+          } else if (lane < ncp) {
+            sm100::tma_load_4d(st + lane * BS * D * 2, &vnmap, land, 0, u.kvh,
+                               static_cast<int32_t>(u.row0) + t.chunk + v * kVT + lane * BS, 0,
+                               keep);
+          }
+          __syncwarp();
+          if (clear) {
+            tail_pending = slot;
+            if (!__all_sync(kAll, sm100::mbar_wait(my_tail, tn & 1, budget, abort_flag)))
+              return false;
+            ++tn;
+            tail_pending = -1;
+            auto zero = [&](int r0, int r1) {
+              for (int i = lane; i < (r1 - r0) * kSl * 8; i += 32) {
+                const int line = i / 8, r = r0 + line / kSl, sl = line % kSl;
+                *reinterpret_cast<uint4*>(st + ((r / BS * kSl + sl) * BS + r % BS) * 128 +
+                                          i % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
+            };
 #pragma unroll 1
-      for (int r = r0; r < toks; r += 16)
-        sm100::mma_f16_ts_elect(o, at + r / 2, vd + off(r), id_pv, !first || r != 0);
-    };
-    // P.V of slot S over a tile of nk keys; `first`: the accumulator starts anew
-    auto pv = [&](auto slot, int nk, bool first) -> bool {
-      const int S = slot;
-      const bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
-      if (kFresh) rv = rg;
-      Ring r = rv;
-      if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
-      if (!wait_for(&c.p_ready[S][0], parity[S])) return false;
-      const uint32_t o = tmem + kOCol + (kChain ? 0 : S * 128);
-      const uint32_t at = tmem + S * kTile;
-      // keys 0-63, then, when their P is there too, keys 64-127
-      pv_keys(S0{}, r.slot, at, o, nk, first);
-      if constexpr (kVT == 64) {
-        if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
-        r.next();
+            for (int x = 0; x < 3; ++x)
+              zero(x == 0 ? a0 : x == 1 ? b0 : toks, x == 0 ? a1 : x == 1 ? b1 : z1);
+            sm100::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&c.full[slot]);
+          }
+        }
+        return true;
+      };
+
+      Walk wk = walk_begin();
+      Unit u;
+      while (ok && walk_next<kPrefix>(a, before, wk, u)) {
+        // j = -1 only looks up tile 0's blocks; the last round has values alone
+        int32_t y = 0, yprev = 0, id = 0;
+        Tile t{}, tprev{};
+#pragma unroll 1
+        for (int j = -1; j <= u.tiles && ok; ++j) {
+          if (j >= 0) {
+            yprev = y;
+            tprev = t;
+            t = tile_of(u, j);
+            y = t.ctx ? ctx_row(u, t, id) : 0;
+          }
+          id = ctx_id(u, j + 1);
+          if (j >= 0 && j < u.tiles) ok = issue_k(u, t, y);
+          if (dual ? j >= 0 && j < u.tiles : j > 0)
+            if (ok) ok = issue_v(u, dual ? t : tprev, dual ? y : yprev);
+        }
       }
-      if (!wait_for(&c.p_ready[S][1], parity[S])) return false;
-      parity[S] ^= 1;
-      if constexpr (kVT == 64) {
-        if (nk > 64) {
+      if (!ok) {
+        if (lane == 0) c.abort = 1;
+        // copies already issued must land before the CTA may exit
+        for (uint32_t gg = g > NST ? g - NST : 0; gg < g; ++gg)
+          if (gg % kProducers == pid && static_cast<int>(gg % NST) != tail_pending)
+            sm100::mbar_wait(&c.full[gg % NST], (gg / NST) & 1, budget, nullptr);
+        if (tail_pending >= 0) sm100::mbar_wait(my_tail, tn & 1, budget, nullptr);
+      }
+    } else {
+      // ========================= MMA issuer =========================================
+      // One MMA occupies the tensor core for 64 (N = 128) or 128 cycles and this
+      // warp issues in order, one instruction every few cycles, so every
+      // instruction between MMAs counts: slots are compile-time, ring positions
+      // are counted, descriptors are a base plus constants, four MMAs share an
+      // election, and nothing is waited for that an earlier wait implies.
+      constexpr uint32_t id_qk = sm100::idesc_f16(kBf16, false, false, 128, kTile);
+      constexpr uint32_t id_pv = sm100::idesc_f16(kBf16, false, true, 128, D);
+      const uint64_t q_desc = sm100::smem_desc(sm100::smem_u32(qs), 16, 1024, sm100::kSw128);
+      const uint64_t k_desc = sm100::smem_desc(sm100::smem_u32(ring), 16, 1024, sm100::kSw128);
+      const uint64_t v_desc =
+          sm100::smem_desc(sm100::smem_u32(ring), BS * 128, 1024, sm100::kSw128);
+      struct Ring {
+        uint32_t slot, phase;
+        __device__ __forceinline__ void next() {
+          if (++slot == NST) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      };
+      Ring rg{0, 0};              // next stage of the ring
+      Ring rk{0, 0}, rv{0, 0};    // dual: stages of the current key and value tiles
+      uint32_t un = 0;            // units
+      uint32_t parity[2] = {0, 0};  // of the P.V in each slot
+      bool ok = true;
+      using S0 = std::integral_constant<int, 0>;
+      using S1 = std::integral_constant<int, 1>;
+      if (a.selftest_stall)
+        ok = __all_sync(kAll, sm100::mbar_wait(&c.never, 0, budget, abort_flag));
+      auto wait_for = [&](uint64_t* bar, uint32_t phase) {
+        const bool r = __all_sync(kAll, sm100::mbar_wait(bar, phase, budget, abort_flag)) != 0;
+        sm100::tc_fence_after();
+        return r;
+      };
+      // logits into slot S: keys from the ring, or (dual, slot 1) those in hand
+      auto qk = [&](auto slot) -> bool {
+        const int S = slot;
+        const bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
+        if (kFresh) rk = rg;
+        Ring r = rk;
+        const uint32_t d = tmem + S * kTile;
+        const uint64_t qd = q_desc + (kDual && S ? kSl * kSliceBytes / 16 : 0);
+#pragma unroll
+        for (int st = 0; st < Lay::kKStages; ++st) {
           if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
-          pv_keys(S0{}, r.slot, at + 32, o, nk - 64, false);
+          const uint64_t kd = k_desc + r.slot * (kStage / 16);
+          mma4_ss(d, qd + 2 * st * (kSliceBytes / 16), kd, id_qk, st != 0);
+          mma4_ss(d, qd + (2 * st + 1) * (kSliceBytes / 16), kd + kSliceBytes / 16, id_qk, true);
           if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
           r.next();
         }
-      } else {
-        if (nk > 64) pv_keys(std::integral_constant<int, 64>{}, r.slot, at, o, nk, false);
-        if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
-        r.next();
-      }
-      if (kFresh) rg = r;
-      // a step's softmax may have to rescale the accumulator: with one
-      // accumulator per slot, the logits it has waited for imply that the
-      // slot's last P.V is done; with one for both slots they do not
-      if constexpr (kChain) sm100::mma_commit_elect(&c.o_done[S]);
-      return true;
-    };
-
-    Walk wk = walk_begin();
-    Unit u;
-    while (ok) {
-      const bool more = walk_call<kPrefix>(a, before, wk, u);
-      if (!__all_sync(kAll, more)) break;
-      ok = wait_for(&c.qfull, un & 1);
-      if (!ok) break;
-      ++un;
-      const int tiles = uniform(u.tiles);
-      int nk = 0, nk_prev = 0;
-      // QK^T of tile j, P.V of the step before; one more round for the last P.V
+        if (kFresh) rg = r;
+        return true;
+      };
+      // the MMAs of keys r0 .. r0 + 63 of one value stage (rows of BS per slice),
+      // as many as the stage's `toks` keys reach
+      auto pv_keys = [&](auto from, uint32_t stage, uint32_t at, uint32_t o, int toks, bool first) {
+        constexpr int r0 = decltype(from)::value;
+        const uint64_t vd = v_desc + stage * (kStage / 16);
+        auto off = [](int r) {
+          return static_cast<uint64_t>(((r / BS) * BS * D * 2 + (r % BS) * 128) / 16);
+        };
+        if (toks >= r0 + 64) {
+          mma4_ts(o, at + r0 / 2, vd + off(r0), vd + off(r0 + 16), vd + off(r0 + 32),
+                  vd + off(r0 + 48), id_pv, !first || r0 != 0);
+          return;
+        }
 #pragma unroll 1
-      for (int j = 0; j <= tiles; ++j) {
-        const bool more_keys = j < tiles;
-        if (more_keys) {
-          nk = uniform(tile_of(u, j).nk);
+        for (int r = r0; r < toks; r += 16)
+          sm100::mma_f16_ts_elect(o, at + r / 2, vd + off(r), id_pv, !first || r != 0);
+      };
+      // P.V of slot S over a tile of nk keys; `first`: the accumulator starts anew
+      auto pv = [&](auto slot, int nk, bool first) -> bool {
+        const int S = slot;
+        const bool kFresh = !kDual || S == 0, kDone = !kDual || S == 1;
+        if (kFresh) rv = rg;
+        Ring r = rv;
+        if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
+        if (!wait_for(&c.p_ready[S][0], parity[S])) return false;
+        const uint32_t o = tmem + kOCol + (kChain ? 0 : S * 128);
+        const uint32_t at = tmem + S * kTile;
+        // keys 0-63, then, when their P is there too, keys 64-127
+        pv_keys(S0{}, r.slot, at, o, nk, first);
+        if constexpr (kVT == 64) {
+          if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
+          r.next();
         }
-        if constexpr (kDual) {
-          if (more_keys) {
-            if (!(ok = qk(S0{}))) break;
-            sm100::mma_commit_elect(&c.s_full[0]);
-          } else {
-            sm100::mma_commit_elect(&c.o_done[0]);
+        if (!wait_for(&c.p_ready[S][1], parity[S])) return false;
+        parity[S] ^= 1;
+        if constexpr (kVT == 64) {
+          if (nk > 64) {
+            if (kFresh && !wait_for(&c.full[r.slot], r.phase)) return false;
+            pv_keys(S0{}, r.slot, at + 32, o, nk - 64, false);
+            if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
+            r.next();
           }
-          if (j > 0 && !(ok = pv(S1{}, nk_prev, j == 1))) break;
-          if (!more_keys) {
-            sm100::mma_commit_elect(&c.o_done[1]);
-            break;
-          }
-          if (!(ok = qk(S1{}))) break;
-          if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
-          sm100::mma_commit_elect(&c.s_full[1]);
-          if (!(ok = pv(S0{}, nk, j == 0))) break;
         } else {
-          if (more_keys) {
-            if (!(ok = qk(j & 1))) break;
-            if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
-            sm100::mma_commit_elect(&c.s_full[j & 1]);
-          } else if (!kChain && tiles > 1) {
-            // the slot before the last is done with its accumulator
-            sm100::mma_commit_elect(&c.o_done[j & 1]);
-          }
-          if (j > 0) {
-            // one accumulator: not before the last unit's has been read
-            if (kChain && j == 1 && un > 1 && !(ok = wait_for(&c.o_free, un & 1))) break;
-            if (!(ok = pv((j - 1) & 1, nk_prev, kChain ? j == 1 : j <= 2))) break;
-            if (!kChain && !more_keys) sm100::mma_commit_elect(&c.o_done[(j - 1) & 1]);
-          }
+          if (nk > 64) pv_keys(std::integral_constant<int, 64>{}, r.slot, at, o, nk, false);
+          if (kDone) sm100::mma_commit_elect(&c.empty[r.slot]);
+          r.next();
         }
-        nk_prev = nk;
+        if (kFresh) rg = r;
+        // a step's softmax may have to rescale the accumulator: with one
+        // accumulator per slot, the logits it has waited for imply that the
+        // slot's last P.V is done; with one for both slots they do not
+        if constexpr (kChain) sm100::mma_commit_elect(&c.o_done[S]);
+        return true;
+      };
+
+      Walk wk = walk_begin();
+      Unit u;
+      while (ok) {
+        const bool more = walk_next<kPrefix>(a, before, wk, u);
+        if (!__all_sync(kAll, more)) break;
+        ok = wait_for(&c.qfull, un & 1);
+        if (!ok) break;
+        ++un;
+        const int tiles = uniform(u.tiles);
+        int nk = 0, nk_prev = 0;
+        // QK^T of tile j, P.V of the step before; one more round for the last P.V
+#pragma unroll 1
+        for (int j = 0; j <= tiles; ++j) {
+          const bool more_keys = j < tiles;
+          if (more_keys) {
+            nk = uniform(tile_of(u, j).nk);
+          }
+          if constexpr (kDual) {
+            if (more_keys) {
+              if (!(ok = qk(S0{}))) break;
+              sm100::mma_commit_elect(&c.s_full[0]);
+            } else {
+              sm100::mma_commit_elect(&c.o_done[0]);
+            }
+            if (j > 0 && !(ok = pv(S1{}, nk_prev, j == 1))) break;
+            if (!more_keys) {
+              sm100::mma_commit_elect(&c.o_done[1]);
+              break;
+            }
+            if (!(ok = qk(S1{}))) break;
+            if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
+            sm100::mma_commit_elect(&c.s_full[1]);
+            if (!(ok = pv(S0{}, nk, j == 0))) break;
+          } else {
+            if (more_keys) {
+              if (!(ok = qk(j & 1))) break;
+              if (j == tiles - 1) sm100::mma_commit_elect(&c.qempty);
+              sm100::mma_commit_elect(&c.s_full[j & 1]);
+            } else if (!kChain && tiles > 1) {
+              // the slot before the last is done with its accumulator
+              sm100::mma_commit_elect(&c.o_done[j & 1]);
+            }
+            if (j > 0) {
+              // one accumulator: not before the last unit's has been read
+              if (kChain && j == 1 && un > 1 && !(ok = wait_for(&c.o_free, un & 1))) break;
+              if (!(ok = pv((j - 1) & 1, nk_prev, kChain ? j == 1 : j <= 2))) break;
+              if (!kChain && !more_keys) sm100::mma_commit_elect(&c.o_done[(j - 1) & 1]);
+            }
+          }
+          nk_prev = nk;
+        }
       }
-    }
-    if (!ok) {
-      if (lane == 0) c.abort = 1;
-      // no MMA may still be running when tensor memory is released
-      sm100::mma_commit_elect(&c.drain);
-      wait_bar(&c.drain, 0, budget, nullptr);
-    }
-    __syncwarp();
+      if (!ok) {
+        if (lane == 0) c.abort = 1;
+        // no MMA may still be running when tensor memory is released
+        sm100::mma_commit_elect(&c.drain);
+        sm100::mbar_wait(&c.drain, 0, budget, nullptr);
+      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -1100,7 +1086,8 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
       const int64_t orow = (u.row0 + i) * a.num_heads + u.kvh * a.group + head;
       const bool empty = !kChain && mine == 0;
       int64_t at = orow;
-      if constexpr (kPrefix) at = orow * a.num_parts + (D == 128 && !dual ? 2 * u.part + slot : u.part);
+      if constexpr (kPrefix)
+        at = orow * a.num_parts + (D == 128 && !dual ? 2 * u.part + slot : u.part);
       const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
       for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
@@ -1124,7 +1111,8 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         if (row_ok && c_lo == 0) {
           a.part_max[at] = poison ? qnan() : m_end * kLn2;
           a.part_sum[at] = total;
-          if (poison) set_status(a.status, *abort_flag ? PA_ERR_DEVICE_TIMEOUT : PA_ERR_BAD_BLOCK_ID);
+          if (poison)
+            set_status(a.status, *abort_flag ? PA_ERR_DEVICE_TIMEOUT : PA_ERR_BAD_BLOCK_ID);
         }
       }
       sm100::tc_fence_before();
