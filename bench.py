@@ -58,7 +58,7 @@ L2_BYTES = 129 << 20
 # figure stale, and the bench then reports null.
 KERNEL_SOURCES = {
     "pa_tc_kernel": ("pa_tc.cuh", "pa_tc_host.cu", "pa_tc_bf16.cu", "pa_sm100.cuh",
-                     "pa_device.cuh", "pa_internal.h", "pa_grid_reduce.cuh"),
+                     "pa_device.cuh", "pa_internal.h", "pa_grid_reduce.cuh", "pa_span.cuh"),
     "pa_generic_kernel": ("pa_generic.cuh", "pa_generic_bf16.cu", "pa_generic_f32.cu",
                           "pa_device.cuh", "pa_internal.h"),
     "pa_prefill_kernel": ("pa_prefill.cuh", "pa_prefill_host.cu", "pa_prefill_bf16.cu",
@@ -69,11 +69,11 @@ KERNEL_SOURCES = {
 NCU_TRAFFIC = {
     # (kernel, source hash, workload, partition size, path): bytes per launch
     # the one-launch V2 kernel (pass 1 and the in-grid reduce)
-    ("pa_tc_kernel", "c6cec55e5b4e9c57", "long_100k", 512, "v2"): 409_757_440 + 3_322_880,
+    ("pa_tc_kernel", "8a5045d97b123fcf", "long_100k", 512, "v2"): 409_753_856 + 3_017_728,
     # the split-x kernel in one launch (its own pass 1 and the same in-grid reduce)
-    ("pa_sx_kernel", "b9d31cdbf8604998", "long_100k", 512, "v2"): 409_761_280 + 4_934_400,
-    ("pa_prefill_kernel", "fb27f3351a287baf", "prefill_32k", 0, "prefill"):
-        1_358_718_464 + 194_669_824,
+    ("pa_sx_kernel", "c34260bcc25f78e6", "long_100k", 512, "v2"): 409_794_304 + 4_820_736,
+    ("pa_prefill_kernel", "805b531535404f7f", "prefill_32k", 0, "prefill"):
+        1_356_391_168 + 194_315_776,
 }
 
 
