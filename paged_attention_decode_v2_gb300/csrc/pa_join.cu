@@ -11,7 +11,10 @@
 // One CTA of `warps` warps per row; a warp folds every warps-th partial, four
 // loads in flight, D / 32 output elements a lane, and the warps are joined in
 // shared memory.  The sums run in a fixed order.  Bound by the partials' bytes
-// (they are in L2, written just before) or, for short rows, by latency.
+// (they are in L2, written just before) or, for few rows, by latency.  Measured
+// alone with cold caches (in the calls they are warm and the launch overlaps):
+// 8192 rows of 128 with 28 MB of partials 17.7 us, 24 rows of 256 6.5 us.  Two,
+// four or eight rows in a CTA changed whole calls by less than 1.5 %.
 #include "pa_device.cuh"
 #include "pa_span.cuh"
 

@@ -16,6 +16,11 @@
 //
 // A row of one part writes its output; longer rows write partials
 // (max in natural-log units, sum, normalised output) that pa_join.cu joins.
+// Bound by instructions, 4 D operations a token and head on the CUDA cores, as
+// the decode calls' portable kernel is.  Measured, bf16 on the cases that the
+// tensor-core kernels serve: 256 sequences, 8 KV heads of 128, window 1024
+// 757 us (tensor cores 125); a windowed chunk of 4096 tokens, 24 / 4 heads of
+// 256, 15.8 ms (174 us).
 #pragma once
 
 #include "pa_generic.cuh"

@@ -14,7 +14,10 @@
 // a run of head rows of one kind and one row t (two or four side by side where
 // D < 256), everything that does not depend on the head -- the slot's place,
 // the angles, the weights -- done once per run, kUnroll rows loaded before the
-// first is used.
+// first is used.  Measured on the device, bf16: 8192 rows of 24 / 4 heads of 256
+// (277 MB) 54 us = 5.1 TB/s, 76 % of the copy rate (115 us with one lane per 16
+// bytes, pairs in two lanes and the set-up per head row); 32 rows of 32 / 8
+// heads of 128 2.4 us, a launch's latency.
 #include <cstdint>
 
 #include <cuda_runtime_api.h>

