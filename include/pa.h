@@ -535,9 +535,9 @@ typedef struct pa_window {
  * initialised by pa_workspace_init; partition_size (a multiple of block_size,
  * as for pa_decode_v2) is the tokens of one partial of a row where there are
  * many sequences; for few the tensor-core kernel's split is chosen to fill
- * the GPU.  Tensor-core
- * kernel where pa_decode_kernel() says 2 and the layout is the standard one,
- * else CUDA cores.  v1_max_seq_len is not used.  What the pools hold for
+ * the GPU.  A workspace for some num_seqs and max_seq_len serves smaller ones.
+ * Tensor-core kernel where pa_decode_kernel() says 2 and the layout is the
+ * standard one, else CUDA cores.  v1_max_seq_len is not used.  What the pools hold for
  * invisible tokens does not matter (NaN included).
  */
 PA_API size_t pa_window_workspace_size(const pa_params_t* params, const pa_window_t* window);
@@ -578,7 +578,8 @@ PA_API pa_status_t pa_prefill_window(const pa_prefill_params_t* params, const pa
  * A prefix length outside 0..max_prefix_len, or a prefix block id outside the
  * pool, makes every row NaN; a sequence's own bad length or block id its rows.
  * workspace: pa_prefix_workspace_size() bytes, initialised once by
- * pa_workspace_init.  Tensor-core kernel for the prefix where pa_decode_kernel()
+ * pa_workspace_init; one for some num_seqs, max_seq_len and max_prefix_len
+ * serves smaller ones.  Tensor-core kernel for the prefix where pa_decode_kernel()
  * says 2 and the layout is the standard one, else CUDA cores.
  */
 typedef struct pa_prefix {

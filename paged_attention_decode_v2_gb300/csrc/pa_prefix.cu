@@ -47,37 +47,46 @@ struct RowsPlan {
   int64_t np;  // partials of a row
 };
 
-RowsPlan rows_plan(const pa_params_t* p, const pa_prefix_t* x) {
-  constexpr int kSms = 152;
+constexpr int kSms = 152;
+
+int key_blocks(int row_groups, int room) {
+  const int k0 = static_cast<int>(ceil_div(row_groups, room));
+  double best = 0;
+  int got = 1;
+  for (int k = k0; k < k0 + 4; ++k) {
+    const int blocks = k * room / row_groups;
+    const double cost = static_cast<double>(k) / blocks * (1.0 + 0.02 * k);
+    if (k == k0 || cost < best) {
+      best = cost;
+      got = blocks;
+    }
+  }
+  return got;
+}
+
+// For `seqs` sequences; on all SMs, or with room for the own lists.
+RowsPlan rows_plan(const pa_params_t* p, const pa_prefix_t* x, int seqs, bool all) {
   // The own lists' pass 1 runs beside this one.  16 to 76 work items of it (half
   // the SMs) get SMs of their own; fewer delay a few of this pass's CTAs less
   // than the SMs are worth, more would leave it too few.  Measured, all SMs
   // against this: 8 sequences, 4 KV heads of 256, prefix 8192 21.4 and 18.4 us,
   // 32000 41.3 and 34.8 us; with 1 sequence (4 items) 16.9 and 17.9 us.
-  const int64_t own = static_cast<int64_t>(p->num_seqs) * p->num_kv_heads *
+  const int64_t own = static_cast<int64_t>(seqs) * p->num_kv_heads *
                       ceil_div(p->max_seq_len, p->partition_size);
-  const int room = own >= 16 && own <= kSms / 2 ? kSms - static_cast<int>(own) : kSms;
+  const int room = !all && own >= 16 && own <= kSms / 2 ? kSms - static_cast<int>(own) : kSms;
   RowsPlan r{};
   const int G = p->num_heads / p->num_kv_heads;
-  r.shape = G <= 64 && (p->head_dim == 128 || p->head_dim == 256) && p->num_seqs > 0 &&
+  r.shape = G <= 64 && (p->head_dim == 128 || p->head_dim == 256) && seqs > 0 &&
             !(p->flags & (PA_FLAG_PORTABLE | PA_FLAG_SPLIT_X)) && x->max_prefix_len > 0 &&
             (ceil_div(x->max_prefix_len, 128) + 152) * p->num_kv_heads < (int64_t(1) << 30);
   if (!r.shape) return r;
   r.row_tokens = 128 / G;
-  r.dual = p->head_dim == 128 && p->num_seqs > r.row_tokens;
+  r.dual = p->head_dim == 128 && seqs > r.row_tokens;
   r.lanes = p->head_dim == 128 && !r.dual ? 2 : 1;
   r.group_tokens = r.row_tokens * (r.dual ? 2 : 1);
-  r.row_groups = static_cast<int>(ceil_div(p->num_seqs, r.group_tokens));
-  const int k0 = static_cast<int>(ceil_div(r.row_groups, room));
-  double best = 0;
-  for (int k = k0; k < k0 + 4; ++k) {
-    const int blocks = k * room / r.row_groups;
-    const double cost = static_cast<double>(k) / blocks * (1.0 + 0.02 * k);
-    if (k == k0 || cost < best) {
-      best = cost;
-      r.key_blocks = blocks;
-    }
-  }
+  r.row_groups = static_cast<int>(ceil_div(seqs, r.group_tokens));
+  // never more than all SMs would get, which is what the workspace has room for
+  r.key_blocks = std::min(key_blocks(r.row_groups, room), key_blocks(r.row_groups, kSms));
   const int64_t tiles = ceil_div(x->max_prefix_len, 128);
   r.np = r.lanes * std::min<int64_t>(tiles, r.key_blocks / p->num_kv_heads + 2);
   return r;
@@ -89,12 +98,12 @@ struct PrefixLayout {
   size_t m[2], s[2], o[2], total;
 };
 
-PrefixLayout layout_of(const pa_params_t* p, const pa_prefix_t* x) {
+PrefixLayout layout_of(const pa_params_t* p, const pa_prefix_t* x, int seqs) {
   PrefixLayout w;
   w.np_prefix = std::max<int64_t>(std::max<int64_t>(1, ceil_div(x->max_prefix_len, kPortablePart)),
-                                  rows_plan(p, x).np);
+                                  rows_plan(p, x, seqs, true).np);
   w.np_own = std::max<int64_t>(1, ceil_div(p->max_seq_len, p->partition_size));
-  const size_t rows = static_cast<size_t>(p->num_seqs) * p->num_heads;
+  const size_t rows = static_cast<size_t>(seqs) * p->num_heads;
   size_t at = kCtrlBytes;
   const int64_t np[2] = {w.np_prefix, w.np_own};
   for (int i = 0; i < 2; ++i) {
@@ -118,7 +127,14 @@ extern "C" {
 
 size_t pa_prefix_workspace_size(const pa_params_t* p, const pa_prefix_t* prefix) {
   if (check_prefix(p, prefix) != PA_OK) return 0;
-  return layout_of(p, prefix).total;
+  size_t most = layout_of(p, prefix, p->num_seqs).total;
+  // Fewer sequences may have more partials in all.  Between them only the number
+  // of row tiles counts: so whole ones, of 128 / G sequences.
+  const int step = std::max(128 / (p->num_heads / p->num_kv_heads), 1);
+  if (rows_plan(p, prefix, p->num_seqs, true).shape)
+    for (int64_t s = step; s < p->num_seqs; s += step)
+      most = std::max(most, layout_of(p, prefix, static_cast<int>(s)).total);
+  return most;
 }
 
 pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, const void* q,
@@ -134,13 +150,13 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
   if (!aligned(prefix_len, 4) || !aligned(prefix_blocks, 4)) return PA_ERR_MISALIGNED;
   if (!workspace) return PA_ERR_INVALID_ARG;
   if (!aligned(workspace, kAlign)) return PA_ERR_MISALIGNED;
-  const PrefixLayout w = layout_of(p, prefix);
+  const PrefixLayout w = layout_of(p, prefix, p->num_seqs);
   if (workspace_bytes < w.total) return PA_ERR_WORKSPACE_TOO_SMALL;
   char* base = static_cast<char*>(workspace);
   int32_t* status = reinterpret_cast<int32_t*>(base);
   const auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
   JoinArgs j{};
-  const RowsPlan r = rows_plan(p, prefix);
+  const RowsPlan r = rows_plan(p, prefix, p->num_seqs, false);
   const int sms = r.shape ? rows_applicable(p->kv_dtype, p->num_heads, p->num_kv_heads,
                                             p->head_dim, p->block_size, p->num_blocks, p->num_seqs,
                                             p->scale)

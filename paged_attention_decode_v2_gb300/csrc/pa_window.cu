@@ -38,8 +38,8 @@ pa_status_t check_decode(const pa_params_t* p, const pa_window_t* w) {
   return PA_OK;
 }
 
-// Tokens of a partial on the tensor-core kernel, whose persistent grid has room
-// for 304 items (two CTAs on each of 152 SMs) at a time.
+// Parts of a list on the tensor-core kernel, whose persistent grid has room for
+// kRoom items (two CTAs on each of 152 SMs) at a time.
 //   * Many (sequence, KV head) pairs -- two rounds of them: partition_size,
 //     evened out over the list, so that short lists do not wait for long ones.
 //   * Fewer: the split that takes the least time, a round costing as much as
@@ -48,22 +48,31 @@ pa_status_t check_decode(const pa_params_t* p, const pa_window_t* w) {
 // Measured (window, heads 24 / 4 x 256, bf16; us with this split against parts of
 // 512): 1 sequence, 4096: 19.8 / 23.2; 4, 4096: 25 / 27; 16, 2048: 36 / 44; 64,
 // 1024: 52 / 55; 256 sequences, 8 KV heads of 128, 1024: 132, and 137 undivided.
-int32_t tc_part(const pa_params_t* p, int64_t len) {
-  constexpr int64_t kRoom = 304, kStart = 100, kJoin = 2, kLeast = 128;
-  const int64_t pairs = static_cast<int64_t>(p->num_seqs) * p->num_kv_heads;
+constexpr int64_t kRoom = 304;
+
+int64_t tc_parts(const pa_params_t* p, int64_t seqs, int64_t len) {
+  constexpr int64_t kStart = 100, kJoin = 2, kLeast = 128;
+  const int64_t pairs = seqs * p->num_kv_heads;
   int64_t parts = parts_of(len, p->partition_size);
   if (pairs < 2 * kRoom) {
-    int64_t best = -1;
+    // The cost of n parts is a line in len; the least of some lines falls to
+    // flatter ones, of more parts, as len grows: n never falls.
+    double best = -1;
     for (int64_t n = 1; n <= 64 && (n == 1 || n * kLeast <= len); ++n) {
-      const int64_t cost = (pairs * n + kRoom - 1) / kRoom * ((len + n - 1) / n + kStart) +
-                           (n > 1 ? n * kJoin : 0);
+      const double rounds = static_cast<double>((pairs * n + kRoom - 1) / kRoom);
+      const double cost = rounds / n * len + rounds * kStart + (n > 1 ? n * kJoin : 0);
       if (best < 0 || cost < best) {
         best = cost;
         parts = n;
       }
     }
   }
-  // whole blocks, of any size the kernel takes
+  return parts;
+}
+
+// Tokens of a part: whole blocks, of any size the kernel takes.
+int32_t tc_part(const pa_params_t* p, int64_t len) {
+  const int64_t parts = tc_parts(p, p->num_seqs, len);
   return static_cast<int32_t>(((len + parts - 1) / parts + 63) / 64 * 64);
 }
 
@@ -71,12 +80,12 @@ int64_t list_len(const pa_params_t* p, const pa_window_t& w) {
   return window_max_len(p->max_seq_len, w.window, w.num_sinks, p->block_size);
 }
 
-// Room for the partials of either kernel, whatever the device.
-WorkspaceLayout layout_of(const pa_params_t* p, const pa_window_t& w) {
+// Room for the partials of either kernel, whatever the device, of `seqs`
+// sequences.
+WorkspaceLayout layout_of(const pa_params_t* p, const pa_window_t& w, int64_t seqs) {
   const int64_t len = list_len(p, w);
-  return workspace_layout(p->num_seqs, p->num_heads, p->head_dim,
-                          std::max(parts_of(len, p->partition_size),
-                                   len > 0 ? parts_of(len, tc_part(p, len)) : 1));
+  return workspace_layout(static_cast<int32_t>(seqs), p->num_heads, p->head_dim,
+                          std::max(parts_of(len, p->partition_size), tc_parts(p, seqs, len)));
 }
 
 cudaError_t launch_list(const ListArgs& a, pa_dtype_t t, cudaStream_t s) {
@@ -96,7 +105,12 @@ extern "C" {
 
 size_t pa_window_workspace_size(const pa_params_t* p, const pa_window_t* window) {
   if (check_decode(p, window) != PA_OK) return 0;
-  return layout_of(p, clamped(window, p->max_seq_len)).total;
+  const pa_window_t w = clamped(window, p->max_seq_len);
+  size_t most = layout_of(p, w, p->num_seqs).total;
+  // fewer sequences may have more parts in all
+  for (int64_t s = 1; s < p->num_seqs && s * p->num_kv_heads < 2 * kRoom; ++s)
+    most = std::max(most, layout_of(p, w, s).total);
+  return most;
 }
 
 pa_status_t pa_decode_window(const pa_params_t* p, const pa_window_t* window, const void* q,
@@ -110,7 +124,7 @@ pa_status_t pa_decode_window(const pa_params_t* p, const pa_window_t* window, co
   if (!workspace) return PA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return PA_ERR_MISALIGNED;
   const pa_window_t w = clamped(window, p->max_seq_len);
-  const WorkspaceLayout lay = layout_of(p, w);
+  const WorkspaceLayout lay = layout_of(p, w, p->num_seqs);
   if (workspace_bytes < lay.total) return PA_ERR_WORKSPACE_TOO_SMALL;
   char* base = static_cast<char*>(workspace);
   float* part_max = reinterpret_cast<float*>(base + lay.max_logits_off);

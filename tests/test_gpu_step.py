@@ -808,3 +808,32 @@ def test_side_stream_and_shared_prefix_after_plan():
         out["query_start"], out["seq_lens"], out["positions"], out["slots"], out["free_left"],
         block_size=bs, num_blocks=p[1].k.shape[0], base_len=i32([prefix]))
     assert out["positions"].tolist()[:3] == [217, 201, 233]
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(32, 8, 128, 32), (24, 4, 256, 16), (8, 1, 128, 16)])
+def test_one_workspace_for_shrinking_batches(hq, hkv, d, bs):
+    """Sequences end and lengths are bounded tighter: the workspace stays."""
+    B, window, sinks, prefix = 40, 300, 3, 3000
+    r = np.random.RandomState(d)
+    lens = [int(x) for x in r.randint(1, 700, size=B)]
+    scale = d ** -0.5
+    q, pg, tables, gl, ref, mag = sr.window_decode_problem(lens, window, sinks, hq, hkv, d, bs,
+                                                           BF16, seed=1)
+    dev = [x.cuda() for x in (q, pg.k, pg.v, tables, gl)]
+    ws = pa.alloc_window_workspace(dev[0], dev[1], dev[3], window=window, num_sinks=sinks,
+                                   max_seq_len=700)
+    for n in (40, 33, 32, 16, 15, 4, 3, 1):
+        out = torch.empty((n, hq, d), device="cuda")
+        pa.decode_window(dev[0][:n], dev[1], dev[2], dev[3][:n], dev[4][:n], out, ws,
+                         window=window, num_sinks=sinks, max_seq_len=max(lens[:n]), scale=scale)
+        sr.assert_within(out, ref[:n], mag[:n], BF16, F32, False, f"window {n}")
+    p = sr.prefix_problem(prefix, lens, hq, hkv, d, bs, BF16, seed=2)
+    ref, mag = p[5:]
+    gq, kc, vc, shared, tab, gl = [x.cuda() for x in (p[0], p[1].k, p[1].v, *p[2:5])]
+    ws = pa.alloc_prefix_workspace(gq, kc, tab, max_seq_len=700, max_prefix_len=prefix)
+    for n in (40, 33, 32, 16, 15, 4, 3, 1):
+        out = torch.empty((n, hq, d), device="cuda")
+        pa.decode_prefix(gq[:n], kc, vc, shared, i32([prefix]), tab[:n], gl[:n], out, ws,
+                         max_seq_len=max(lens[:n]), max_prefix_len=prefix, scale=scale)
+        sr.assert_within(out, ref[:n], mag[:n], BF16, F32, True, f"prefix {n}")
+    assert pa.read_device_status(ws) == pa.PA_OK

@@ -177,3 +177,24 @@ def test_bindings_refuse_before_the_library():
     with pytest.raises(pa.PaError):
         pa.qk_norm_rope(q, q[:, :2], q[:, 2:], x, torch.zeros(2, dtype=torch.int64), None,
                         torch.zeros_like(q))
+
+
+@pytest.mark.parametrize("hq, hkv, d", [(8, 1, 128), (32, 8, 128), (24, 4, 256), (16, 16, 128)])
+def test_a_workspace_serves_smaller_batches(hq, hkv, d):
+    """The sizes never fall as sequences or lengths are added, so one workspace
+    for the largest step serves every step."""
+    def params(B, L):
+        return pa.Params(num_seqs=B, num_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=16,
+                         num_blocks=1 << 20, max_blocks_per_seq=1 << 16, max_seq_len=L,
+                         partition_size=512, scale=1.0, kv_dtype=pa.PA_BF16, out_dtype=pa.PA_BF16)
+
+    sizes = (lambda B, L: pa.window_workspace_size(params(B, L), 4096, 4),
+             lambda B, L: pa.prefix_workspace_size(params(B, 300), 20 * L, 20 * L // 16 + 1),
+             lambda B, L: pa.prefix_workspace_size(params(B, L), 32000, 2000))
+    for size in sizes:
+        for L in (1, 200, 4100):
+            got = [size(B, L) for B in range(1, 700)]
+            assert min(got) > 0 and got == sorted(got)
+        for B in (1, 3, 19, 40, 300):
+            got = [size(B, L) for L in range(1, 5000, 37)]
+            assert got == sorted(got)
