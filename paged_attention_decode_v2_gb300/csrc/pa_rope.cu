@@ -15,9 +15,9 @@
 // D < 256), everything that does not depend on the head -- the slot's place,
 // the angles, the weights -- done once per run, kUnroll rows loaded before the
 // first is used.  Measured on the device, bf16: 8192 rows of 24 / 4 heads of 256
-// (277 MB) 54 us = 5.1 TB/s, 76 % of the copy rate (115 us with one lane per 16
+// (277 MB) 47.5 us = 5.8 TB/s, 87 % of the copy rate (115 us with one lane per 16
 // bytes, pairs in two lanes and the set-up per head row); 32 rows of 32 / 8
-// heads of 128 2.4 us, a launch's latency.
+// heads of 128 2.5 us, a launch's latency.
 #include <cstdint>
 
 #include <cuda_runtime_api.h>
@@ -28,7 +28,10 @@ namespace pa {
 
 namespace {
 
-constexpr int kNT = 256;
+// A CTA is one warp: its registers are free for the next as soon as it is done,
+// and nothing waits for a slower neighbour.  Measured, 8192 rows of 24 / 4 heads of
+// 256, bf16: CTAs of 256 threads 54 us, 128 51, 64 49, 32 47.5.
+constexpr int kNT = 32;
 
 struct RopeArgs {
   const void* q;
@@ -114,7 +117,7 @@ __device__ __forceinline__ void store4(float* p, const F2* f) {
   float4 v;
   unpair(f[0], v.x, v.y);
   unpair(f[1], v.z, v.w);
-  *reinterpret_cast<float4*>(p) = v;
+  __stcs(reinterpret_cast<float4*>(p), v);
 }
 __device__ __forceinline__ uint32_t round2(F2 f, __nv_bfloat16*) {
   float x, y;
@@ -130,7 +133,7 @@ __device__ __forceinline__ uint32_t round2(F2 f, __half*) {
 }
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const F2* f) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(round2(f[0], p), round2(f[1], p));
+  __stcs(reinterpret_cast<uint2*>(p), make_uint2(round2(f[0], p), round2(f[1], p)));
 }
 
 __device__ __forceinline__ float round_elem(float x, float*) { return x; }
@@ -173,11 +176,11 @@ __device__ __forceinline__ void norm_rotate(F2 (&y)[4], const Lane& l, bool norm
 }
 
 // Head rows loaded at once, per side of the warp, and CTAs per SM that the
-// register budget is set for (64 registers, no spills).  Measured on GB300,
-// 8192 rows of 24 / 4 heads of 256, bf16: 4 rows and 4 CTAs 55 us, 4 and 3
-// 64 us, 2 and 5 58 us, 8 and 3 70 us.
+// register budget is set for (64 registers, no spills).  Measured on the same
+// rows with CTAs of 64 threads: 4 rows and 16 CTAs 48.6 us, 4 and 12 51.2 us,
+// 2 and 20 50.7 us, 6 and 12 53.3 us.
 constexpr int kUnroll = 4;
-constexpr int kCtas = 4;
+constexpr int kCtas = 32;
 
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
@@ -190,7 +193,10 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
   if (item >= a.items) return;
   const uint32_t per_row = a.q_runs + 2 * a.kv_runs;
   const int32_t t = static_cast<int32_t>(item / per_row);
-  const int k = static_cast<int>(item - t * per_row);
+  // the runs of a row t in an order that turns with t, or, where 152 is a multiple
+  // of per_row, some SMs would get all the runs of one kind (1001 rows, split-x
+  // values: 10.0 us, so 6.6)
+  const int k = static_cast<int>((item - t * per_row + t) % per_row);
   const int64_t slot = __ldg(a.slots + t);
   const int32_t pos = a.rot ? __ldg(a.positions + t) : 0;
   const int kind = k < a.q_runs ? 0 : k < a.q_runs + a.kv_runs ? 1 : 2;
