@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) pa_join_kernel(const JoinArgs 
       n[l] = (L + x.part_size - 1) / x.part_size;
     }
   }
+  // The partials were written while this kernel ran: coherent loads, no __ldg.
   cudaGridDependencySynchronize();
 
   float m = -INFINITY, w = 0.f, acc[E];
@@ -79,17 +80,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps) pa_join_kernel(const JoinArgs 
         for (int e = 0; e < E; ++e) o[i][e] = 0.f;
         if (p < n[l]) {
           const int64_t at = r + p;
-          mp[i] = __ldg(x.m + at);
-          sp[i] = __ldg(x.s + at);
+          mp[i] = __ldcg(x.m + at);
+          sp[i] = __ldcg(x.s + at);
           if constexpr (E == 2) {
-            const float2 v = __ldg(reinterpret_cast<const float2*>(x.o + at * D) + lane);
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(x.o + at * D) + lane);
             o[i][0] = v.x;
             o[i][1] = v.y;
           } else {
 #pragma unroll
             for (int g = 0; g < E / 4; ++g) {
               const float4 v =
-                  __ldg(reinterpret_cast<const float4*>(x.o + at * D) + g * 32 + lane);
+                  __ldcg(reinterpret_cast<const float4*>(x.o + at * D) + g * 32 + lane);
               o[i][4 * g] = v.x;
               o[i][4 * g + 1] = v.y;
               o[i][4 * g + 2] = v.z;

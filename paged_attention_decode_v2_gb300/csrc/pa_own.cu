@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(D, 512 / D)
     if (P < 0 || P > pre.max_len) poison = true;
     else if (pre.m) parts = prefix_split(P, a.num_kv_heads, pre.key_blocks).segments(kvh) * pre.lanes;
   }
+  // the partials were written while this kernel ran: coherent loads, no __ldg
   cudaGridDependencySynchronize();
   for (int i = tid; i < G * (D / 4); i += D) {
     const int h = i / (D / 4), d = i % (D / 4) * 4;
@@ -250,9 +251,9 @@ __global__ void __launch_bounds__(D, 512 / D)
         v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (base + x < parts) {
           const int64_t at = r * pre.stride + base + x;
-          mp[x] = __ldg(pre.m + at);
-          sp[x] = __ldg(pre.s + at);
-          v[x] = __ldg(reinterpret_cast<const float4*>(pre.o + at * D + d));
+          mp[x] = __ldcg(pre.m + at);
+          sp[x] = __ldcg(pre.s + at);
+          v[x] = __ldcg(reinterpret_cast<const float4*>(pre.o + at * D + d));
         }
       }
       float mb = M;

@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(kNT, kMinBlocks) pa_reduce_kernel(const Kernel
   // a sequence of one partition was finished by pass 1 (single_direct)
   if (a.single_direct && L >= 1 && L <= a.partition_size && seq_len_ok(a, L)) return;
 
-  // Wait for pass 1 (a no-op unless launched as a programmatic dependent).
+  // Wait for pass 1 (a no-op unless launched as a programmatic dependent).  Its
+  // results were written while this kernel ran: coherent loads, no __ldg.
   cudaGridDependencySynchronize();
 
   if (!seq_len_ok(a, L) || L == 0) {
@@ -71,9 +72,9 @@ __global__ void __launch_bounds__(kNT, kMinBlocks) pa_reduce_kernel(const Kernel
     return;
   }
   const int n = (L + a.partition_size - 1) / a.partition_size;
-  const float* __restrict__ ml = a.max_logits + row * a.num_partitions;
-  const float* __restrict__ es = a.exp_sums + row * a.num_partitions;
-  const float4* __restrict__ to =
+  const float* ml = a.max_logits + row * a.num_partitions;
+  const float* es = a.exp_sums + row * a.num_partitions;
+  const float4* to =
       reinterpret_cast<const float4*>(a.tmp_out + row * a.num_partitions * D + d0);
 
   const int col = tid % kCols, grp = tid / kCols;
@@ -87,9 +88,9 @@ __global__ void __launch_bounds__(kNT, kMinBlocks) pa_reduce_kernel(const Kernel
     for (int i = 0; i < kBatch; ++i) {
       const int p = base + i * kGroups;
       if (p < n) {
-        mp[i] = __ldg(ml + p);
-        sp[i] = __ldg(es + p);
-        o[i] = __ldg(to + static_cast<int64_t>(p) * (D / 4) + col);
+        mp[i] = __ldcg(ml + p);
+        sp[i] = __ldcg(es + p);
+        o[i] = __ldcg(to + static_cast<int64_t>(p) * (D / 4) + col);
       } else {
         mp[i] = -INFINITY;
         sp[i] = 0.f;
