@@ -145,10 +145,12 @@ __device__ __forceinline__ __half round_elem(float x, __half* p) { return round1
 // What a lane needs to norm and rotate its eight elements of any head row.
 // Element pairs y[0..3] hold elements oa .. oa + 3 and ob .. ob + 3; out =
 // y * c + other * s with `other` the pairs' other sides: y[2], y[3], y[0], y[1]
-// (halves), or each pair swapped (interleaved).  Lanes that do not rotate have
-// c = 1, s = 0.
+// (halves), or each pair swapped (interleaved).  Lanes that do not rotate leave
+// y alone: with c = 1 and s = 0 an infinite `other` would make y NaN, and -0
+// would become +0.
 struct Lane {
   F2 w[4], c[4], s[4];
+  bool turns;
 };
 
 template <int LPR, bool kInter>
@@ -169,6 +171,7 @@ __device__ __forceinline__ void norm_rotate(F2 (&y)[4], const Lane& l, bool norm
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(y[i], r2), l.w[i]);
   }
+  if (!l.turns) return;
   const F2 t[4] = {kInter ? swapped(y[0]) : y[2], kInter ? swapped(y[1]) : y[3],
                    kInter ? swapped(y[2]) : y[0], kInter ? swapped(y[3]) : y[1]};
 #pragma unroll
@@ -176,9 +179,10 @@ __device__ __forceinline__ void norm_rotate(F2 (&y)[4], const Lane& l, bool norm
 }
 
 // Head rows loaded at once, per side of the warp, and CTAs per SM that the
-// register budget is set for (64 registers, no spills).  Measured on the same
-// rows with CTAs of 64 threads: 4 rows and 16 CTAs 48.6 us, 4 and 12 51.2 us,
-// 2 and 20 50.7 us, 6 and 12 53.3 us.
+// register budget is set for (64 registers: two spilled at most for 16-bit
+// types, up to 40 for float32).  Measured on the same rows with CTAs of 64
+// threads: 4 rows and 16 CTAs 48.6 us, 4 and 12 51.2 us, 2 and 20 50.7 us, 6
+// and 12 53.3 us.
 constexpr int kUnroll = 4;
 constexpr int kCtas = 32;
 
@@ -241,6 +245,7 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
       s = __ldg(reinterpret_cast<const float4*>(row + half));
     }
     if (!pos_ok) c.x = c.y = c.z = c.w = qnan();      // the rows come out NaN
+    l.turns = rotates || !pos_ok;
     if (kInter) {
       l.c[0] = pair(c.x, c.x), l.c[1] = pair(c.y, c.y);
       l.c[2] = pair(c.z, c.z), l.c[3] = pair(c.w, c.w);

@@ -72,3 +72,94 @@ def test_decode_window_again_and_again_on_one_workspace():
     torch.cuda.synchronize()
     for i, out in enumerate(outs):
         assert torch.equal(out, first[i % 3]), i
+
+
+# ------------------------------------------------ norm + rotation: copied elements
+
+def _bits(x):
+    return x.contiguous().view(torch.int32 if x.dtype == F32 else torch.int16)
+
+
+def _same_bits(got, want):
+    got, want = got.cpu(), want.cpu()
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(_bits(got)[~nan], _bits(want)[~nan])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("d,rot,inter", [(64, 0, False), (128, 0, True), (256, 0, False),
+                                         (64, 32, True), (64, 16, False), (128, 64, False),
+                                         (256, 112, True), (256, 240, False)])
+def test_elements_outside_the_rotation_are_copied(dtype, d, rot, inter):
+    """Without weights they are the input's bits: infinities, NaN and -0 among
+    them, none of which reaches another element."""
+    T, hq, hkv, bs, sx = 21, 5, 2, 16, d == 64
+    g = torch.Generator().manual_seed(d + rot)
+    x = torch.randn(T, hq + 2 * hkv, d, generator=g).to(dtype)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0, 0.0]).to(dtype)
+    pick = torch.randint(0, 12, x.shape, generator=g)
+    pick[..., :rot] = 11                                   # the rotated part stays finite
+    pick[:, hq + hkv:] = torch.randint(0, 12, pick[:, hq + hkv:].shape, generator=g)  # values: any
+    x = torch.where(pick < 5, odd[pick.clamp(max=4)], x)
+    nb = 4
+    kc = torch.zeros(nb, hkv, bs, d, dtype=dtype)
+    vc = torch.zeros_like(kc)
+    slots = torch.randperm(nb * bs, generator=g)[:T]
+    gx = x.cuda()
+    gk, gv = [t.cuda() for t in (sr.split_x(kc, vc) if sx else (kc, vc))]
+    q_out = torch.empty(T, hq, d, dtype=dtype, device="cuda")
+    k_out, v_out = [torch.empty(T, hkv, d, dtype=dtype, device="cuda") for _ in range(2)]
+    status = i32([0])
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") if rot else None
+    pa.qk_norm_rope(gx[:, :hq], gx[:, hq:hq + hkv], gx[:, hq + hkv:], pos, slots.cuda(),
+                    _cos_sin(rot).cuda() if rot else None, q_out, gk, gv, interleaved=inter,
+                    k_out=k_out, v_out=v_out, split_x=sx, status=status)
+    assert int(status) == 0
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    _same_bits(q_out[..., rot:], q[..., rot:])
+    _same_bits(k_out[..., rot:], k[..., rot:])
+    _same_bits(v_out, v)
+    for got, src in ((q_out, q), (k_out, k)):
+        assert torch.isfinite(got[..., :rot]).all()
+        if rot:
+            want = sr.norm_rope(torch.where(torch.isfinite(src), src, 0), None, _cos_sin(rot),
+                                torch.arange(T), 0.0, 0.0, inter)[..., :rot]
+            # two products and a sum in float32, one rounding
+            size = src[..., :rot].double().abs().amax(-1, keepdim=True)
+            bound = sr.HALF_STEP[dtype] * want.abs() + 4 * 2.0 ** -24 * size + 2.0 ** -25
+            assert (got[..., :rot].double().cpu() - want).abs().le(bound).all()
+    ek, ev = kc.clone(), vc.clone()
+    ek[slots // bs, :, slots % bs] = k_out.cpu()
+    ev[slots // bs, :, slots % bs] = v
+    if sx:
+        ek, ev = sr.split_x(ek, ev)
+    _same_bits(gk, ek)
+    _same_bits(gv, ev)
+
+
+def test_zeros_outside_the_rotation_keep_their_sign_under_a_norm():
+    T, hq, hkv, d, rot = 3, 4, 1, 128, 32
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(T, hq + 2 * hkv, d, generator=g).to(BF16)
+    x[..., rot::3] = -0.0
+    w = (1 + 0.1 * torch.randn(d, generator=g)).to(BF16)
+    assert (w > 0).all()
+    gx, gw = x.cuda(), w.cuda()
+    q_out = torch.empty(T, hq, d, dtype=BF16, device="cuda")
+    pa.qk_norm_rope(gx[:, :hq], gx[:, hq:hq + hkv], gx[:, hq + hkv:], i32(range(T)),
+                    torch.arange(T, device="cuda"), _cos_sin(rot).cuda(), q_out, q_weight=gw,
+                    k_weight=gw)
+    assert torch.equal(torch.signbit(q_out).cpu()[..., rot:], torch.signbit(x[:, :hq])[..., rot:])
+
+
+def test_a_bad_position_makes_whole_rows_nan():
+    """The elements outside the rotation too."""
+    T, hq, hkv, d, rot = 5, 3, 2, 128, 32
+    x = torch.randn(T, hq + 2 * hkv, d, device="cuda").to(BF16)
+    q_out = torch.zeros(T, hq, d, dtype=BF16, device="cuda")
+    k_out = torch.zeros(T, hkv, d, dtype=BF16, device="cuda")
+    pa.qk_norm_rope(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], i32([0, -1, 2, 300, 4]),
+                    torch.arange(T, device="cuda"), _cos_sin(rot).cuda(), q_out, k_out=k_out)
+    for t in (q_out, k_out):
+        assert torch.isnan(t[[1, 3]]).all() and torch.isfinite(t[[0, 2, 4]]).all()
