@@ -195,7 +195,10 @@ __global__ void __launch_bounds__(256) pa_portable_kernel(const ListArgs a) {
         const float m_new = fmaxf(m_old, mx);
         float sum = 0.f;
         for (int tt = lane; tt < nt; tt += 32) {
-          const float pv = m_new == -INFINITY ? 0.f : exp2f(sm.p[tt][h] - m_new);
+          // a NaN logit goes on into the sum, also where none is above -inf
+          const float l = sm.p[tt][h];
+          const float pv =
+              l == -INFINITY ? 0.f : exp2f(l - (m_new == -INFINITY ? 0.f : m_new));
           sm.p[tt][h] = pv;
           sum += pv;
         }
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(256) pa_portable_kernel(const ListArgs a) {
     for (int i = tid; i < nh * D; i += C::NT) {
       const int hh = i / D, d = i % D;
       const float s = sm.s_run[hh];
-      const float o = bad ? qnan() : (s > 0.f ? sm.acc[hh][d] / s : 0.f);
+      const float o = bad ? qnan() : (s == 0.f ? 0.f : sm.acc[hh][d] / s);
       const int64_t r = row * Hq + h0 + hh;
       if (partial)
         a.part_out[(r * a.num_parts + part) * D + d] = o;

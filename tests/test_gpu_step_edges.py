@@ -163,3 +163,28 @@ def test_a_bad_position_makes_whole_rows_nan():
                     torch.arange(T, device="cuda"), _cos_sin(rot).cuda(), q_out, k_out=k_out)
     for t in (q_out, k_out):
         assert torch.isnan(t[[1, 3]]).all() and torch.isfinite(t[[0, 2, 4]]).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,dtype", [(8, 2, 128, 16, BF16), (6, 1, 256, 16, F16),
+                                               (4, 2, 64, 16, F16), (4, 2, 128, 8, F32)])
+@pytest.mark.parametrize("portable", [False, True])
+def test_prefill_window_with_nan(hq, hkv, d, bs, dtype, portable):
+    """A NaN query row is one row's; a NaN key those rows' that see it."""
+    G, C, n, window, sinks = hq // hkv, 300, 150, 40, 3
+    p = sr.window_prefill_problem((C,), (n,), window, sinks, hq, hkv, d, bs, dtype, seed=10)
+    q, k, v, pg, tables, start, ctx, ref, mag = p
+    q[7] = math.nan
+    k[50, 0, 3] = math.nan
+    pg.k[tables[0, 290 // bs], hkv - 1, 290 % bs, 1] = math.nan
+    out = _run_window_prefill(p, window, sinks, portable=portable)
+    bad = torch.zeros(n, hq, dtype=torch.bool)
+    bad[7] = True
+    for i in range(n):
+        see = sr.visible(C + i, window, sinks)
+        if C + 50 in see:
+            bad[i, :G] = True
+        if 290 in see:
+            bad[i, hq - G:] = True
+    assert torch.equal(torch.isnan(out).all(-1).cpu(), bad)
+    rounded = not portable and d > 64 and dtype != F32
+    sr.assert_within(out.cpu()[~bad], ref[~bad], mag[~bad], dtype, F32, rounded)
