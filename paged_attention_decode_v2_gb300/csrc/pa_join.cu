@@ -5,8 +5,9 @@
 // natural-log units, sum s_p of exp(l - m_p), normalised output o_p), and
 //   M = max m_p,  w_p = exp(m_p - M) s_p,  out = sum w_p o_p / sum w_p
 // over both: the log-sum-exp identity of the V2 reduce.  An empty partial has
-// m_p = -inf and s_p = 0 and weighs nothing; a NaN max makes the row NaN; a
-// row without a token is zeros.
+// m_p = -inf and s_p = 0 and weighs nothing; a NaN max (a bad block) or a NaN
+// sum (a NaN logit, beside a max of -inf where all are) makes the row NaN; a row
+// without a token is zeros.
 //
 // One CTA of `warps` warps per row; a warp folds every warps-th partial, four
 // loads in flight, D / 32 output elements a lane, and the warps are joined in
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) pa_join_kernel(const JoinArgs 
       float mb = m;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        nan_seen |= isnan(mp[i]);
+        nan_seen |= isnan(mp[i]) || isnan(sp[i]);
         mb = fmaxf(mb, mp[i]);
       }
       if (mb > m) {

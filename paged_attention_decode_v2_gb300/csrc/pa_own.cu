@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(D, 512 / D)
       float mb = M;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        nan_seen |= isnan(mp[x]);
+        nan_seen |= isnan(mp[x]) || isnan(sp[x]);  // a bad block, or a NaN logit
         mb = fmaxf(mb, mp[x]);
       }
       if (mb > M) {

@@ -165,6 +165,37 @@ def test_a_bad_position_makes_whole_rows_nan():
         assert torch.isnan(t[[1, 3]]).all() and torch.isfinite(t[[0, 2, 4]]).all()
 
 
+def test_decode_prefix_of_many_short_sequences_with_nan():
+    hq, hkv, d, bs = 8, 4, 128, 32
+    lens = [int(x) for x in np.random.RandomState(1).randint(0, 90, size=41)]
+    p = sr.prefix_problem(700, lens, hq, hkv, d, bs, BF16, seed=8)
+    empty = lens.index(0) if 0 in lens else 0
+    p[0][5] = math.nan
+    p[0][empty, 3] = math.nan
+    out, ws = _run_prefix(p, 700, check=False)
+    assert torch.isnan(out[5]).all() and torch.isnan(out[empty, 3]).all()
+    good = [i for i in range(41) if i not in (5, empty)]
+    sr.assert_within(out[good], p[5][good], p[6][good], BF16, F32, True)
+    assert pa.read_device_status(ws) == pa.PA_OK
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,dtype", [(8, 2, 128, 16, BF16), (24, 4, 256, 16, F16),
+                                               (4, 2, 64, 16, F16), (4, 2, 128, 8, F32)])
+@pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("window,P", [(1500, 128), (100, 512)])
+def test_decode_window_with_nan(hq, hkv, d, bs, dtype, portable, window, P):
+    G = hq // hkv
+    q, pg, tables, gl, ref, mag = sr.window_decode_problem([2500, 777, 60], window, 9, hq, hkv, d,
+                                                           bs, dtype, seed=9)
+    q[1] = math.nan
+    pg.k[tables[2, 1], 0, 3, 7] = math.nan
+    out, ws = _run_window(q, pg, tables, gl, window, 9, portable=portable, P=P, check=False)
+    assert torch.isnan(out[1]).all() and torch.isnan(out[2, :G]).all()
+    sr.assert_within(out[0], ref[0], mag[0], dtype, F32, False)
+    sr.assert_within(out[2, G:], ref[2, G:], mag[2, G:], dtype, F32, False)
+    assert pa.read_device_status(ws) == pa.PA_OK
+
+
 @pytest.mark.parametrize("hq,hkv,d,bs,dtype", [(8, 2, 128, 16, BF16), (6, 1, 256, 16, F16),
                                                (4, 2, 64, 16, F16), (4, 2, 128, 8, F32)])
 @pytest.mark.parametrize("portable", [False, True])
