@@ -1078,10 +1078,10 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         sync256();
         m_end = c.mref[r];
         if (m_end != m_ref) lsum *= m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_end);
-        c.lsum[slot][r] = bad ? qnan() : lsum;
+        c.lsum[slot][r] = bad ? -1.f : lsum;  // a sum is never negative: -1 is a bad block
         sync256();
         total = c.lsum[0][r] + c.lsum[1][r];
-        bad |= isnan(total);
+        bad |= c.lsum[0][r] == -1.f || c.lsum[1][r] == -1.f;
         c_lo = slot * (D / 2);
         c_hi = c_lo + D / 2;
         const int o = (K - 1) & 1;

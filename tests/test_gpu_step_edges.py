@@ -165,6 +165,39 @@ def test_a_bad_position_makes_whole_rows_nan():
         assert torch.isnan(t[[1, 3]]).all() and torch.isfinite(t[[0, 2, 4]]).all()
 
 
+# --------------------------------------------------- values that are not finite
+
+@pytest.mark.parametrize("hq,hkv,d,bs,dtype", [(8, 2, 128, 16, BF16), (24, 4, 256, 16, F16),
+                                               (4, 2, 64, 16, BF16), (4, 2, 128, 8, F32)])
+@pytest.mark.parametrize("portable", [False, True])
+def test_decode_prefix_with_nan(hq, hkv, d, bs, dtype, portable):
+    G = hq // hkv
+    fresh = lambda: sr.prefix_problem(900, (30, 0, 45), hq, hkv, d, bs, dtype, seed=7)
+    tc = not portable and d > 64 and dtype != F32
+    # a key of the prefix: the heads that see it, and no word of a bad block
+    p = fresh()
+    p[1].k[p[2][3], 1, 2, 5] = math.nan
+    out, ws = _run_prefix(p, 900, portable=portable, check=False)
+    assert torch.isnan(out[:, G:2 * G]).all()
+    rest = [h for h in range(hq) if h // G != 1]
+    sr.assert_within(out[:, rest], p[5][:, rest], p[6][:, rest], dtype, F32, tc)
+    assert pa.read_device_status(ws) == pa.PA_OK
+    # whole query rows, one with tokens of its own and one without
+    p = fresh()
+    p[0][0] = math.nan
+    p[0][1, 0] = math.nan
+    out, ws = _run_prefix(p, 900, portable=portable, check=False)
+    assert torch.isnan(out[0]).all() and torch.isnan(out[1, 0]).all()
+    sr.assert_within(out[1, 1:], p[5][1, 1:], p[6][1, 1:], dtype, F32, tc)
+    sr.assert_within(out[2], p[5][2], p[6][2], dtype, F32, tc)
+    assert pa.read_device_status(ws) == pa.PA_OK
+    # and beside a bad block the status names the block
+    p[2][1] = -1
+    out, ws = _run_prefix(p, 900, portable=portable, check=False)
+    assert torch.isnan(out).all()
+    assert pa.read_device_status(ws) == pa.PA_ERR_BAD_BLOCK_ID
+
+
 def test_decode_prefix_of_many_short_sequences_with_nan():
     hq, hkv, d, bs = 8, 4, 128, 32
     lens = [int(x) for x in np.random.RandomState(1).randint(0, 90, size=41)]
