@@ -35,10 +35,13 @@
 //   head_dim 256: one row tile and one accumulator (256 of the 512 columns);
 //     slots take the key tiles in turn and hand the row's reference maximum
 //     from one to the other through shared memory as soon as it is known.
-// The reference maximum moves only when a tile's maximum exceeds it by more
-// than 2^8 (then the sum and the accumulator are rescaled), so p <= 2^8.  Sums
-// and accumulators are float32; p alone is rounded to 16 bits (the operand
-// type of the MMA): at most half a step each, the sum adds the unrounded p.
+// The reference moves only when a tile's maximum exceeds it by more than 2^8
+// (then the sum and the accumulator are rescaled), so p <= 2^8.  For f16, whose
+// smallest step is 2^-24, it lies 2^7 below the maximum (p <= 2^15): with p <= 1
+// at first, 20000 keys of weight 2^-25.2 next to one of weight 1 were lost.  Sums
+// and accumulators are float32; p alone is rounded to 16 bits (the operand type
+// of the MMA): by half a step of the type, in f16 also by 2^-32 of the largest p
+// at most; the sum adds the unrounded p.
 //
 // Bound by the tensor core for many rows (4 * head_dim flops per row and key),
 // and by latency for few.  Measured: prefix of 32000 tokens, 256 sequences, 32 / 8
@@ -81,6 +84,8 @@ constexpr int kMaxStages = 5;
 constexpr int kTmemCols = 512;       // S slot 0 | S slot 1 | O (two of 128, or one of 256)
 constexpr int kOCol = 256;
 constexpr float kRescaleLog2 = 8.f;
+template <typename T>                // log2 of how far the reference lies below the maximum
+constexpr float kBelowLog2 = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr long long kWaitBudget = 4000000000LL;    // cycles (about 2 s)
 constexpr long long kSelftestBudget = 20000000LL;  // cycles (about 10 ms)
 constexpr int kSmemLimit = 227 * 1024;
@@ -291,7 +296,7 @@ __device__ __forceinline__ bool walk_next(const RowsArgs& a, const int* before, 
 }
 
 // 2^x by the hardware's approximate exponential: relative error well below the
-// 16-bit rounding that p goes through; inputs are at most 8 here.
+// 16-bit rounding that p goes through; inputs are at most 15 here.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -976,10 +981,10 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
         }
         // The row's reference maximum before this step: the slot's own, or the
         // other slot's after the step before.  P is computed against it at once,
-        // while the tile's maximum is still being found; only when that exceeds
-        // the reference by more than 2^8 (the first tile, rarely later) the
-        // reference moves, what the sum and the accumulator hold is rescaled, and
-        // the first keys are taken again.
+        // while the tile's maximum is still being found; only when that exceeds the
+        // one the reference was taken from by more than 2^8 (the first tile, rarely
+        // later) the reference moves, what the sum and the accumulator hold is
+        // rescaled, and the first keys are taken again.
         const float m_old = m_ref;
         if constexpr (kChain) {
           if (k > 0) {
@@ -995,8 +1000,8 @@ __global__ void __launch_bounds__(rw::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[e + 2 * x], s[e + 2 * x + 1]);
         const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;
-        const bool move = mt > m_in + kRescaleLog2;  // also from -inf
-        if (move) m_ref = mt;
+        const bool move = mt > m_in + (kRescaleLog2 + kBelowLog2<T>);  // also from -inf
+        if (move) m_ref = mt - kBelowLog2<T>;
         if constexpr (kChain) {
           c.mref[r] = m_ref;
           sm100::mbar_arrive(&c.m_next[slot]);

@@ -252,3 +252,57 @@ def test_prefill_window_with_nan(hq, hkv, d, bs, dtype, portable):
     assert torch.equal(torch.isnan(out).all(-1).cpu(), bad)
     rounded = not portable and d > 64 and dtype != F32
     sr.assert_within(out.cpu()[~bad], ref[~bad], mag[~bad], dtype, F32, rounded)
+
+
+# ------------------------------------------ many weights far below the largest
+
+def _faint(dtype, n, hkv, d, bs, below, seed):
+    """One token that outweighs each of the others by exp(below), its value 0 and
+    theirs 1: caches, table, the query row and the exact output."""
+    g = torch.Generator().manual_seed(seed)
+    blocks = -(-n // bs)
+    kc = torch.zeros(blocks, hkv, bs, d, dtype=dtype)
+    vc = torch.ones_like(kc)
+    table = torch.randperm(blocks, generator=g).to(torch.int32)
+    kc[table[0], :, 0, 0] = 16
+    vc[table[0], :, 0] = 0
+    q = torch.zeros(d, dtype=dtype)
+    q[0] = below * d ** 0.5 / 16
+    l0 = float(q[0].double()) * 16 * d ** -0.5
+    return kc, vc, table, q, l0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("hq,hkv,d,bs,rows", [(4, 1, 128, 32, 3), (8, 1, 128, 16, 70),
+                                              (6, 1, 256, 16, 5)])
+def test_many_faint_tokens(dtype, hq, hkv, d, bs, rows):
+    """20000 tokens of weight exp(-17.5) next to one of weight 1.  Each weight is
+    off by half a step of the element type, or, in f16, by half of its smallest
+    step 2^-24 at 2^7 below the largest weight's place: n 2^-32 in all."""
+    n = 20000
+    kc, vc, table, q1, l0 = _faint(dtype, n, hkv, d, bs, 17.5, 1)
+    u = sr.HALF_STEP[dtype]
+    extra = n * 2.0 ** -32 if dtype == F16 else 0.0
+
+    def check(out, others):
+        w = others * math.exp(-l0)
+        ref = w / (1 + w)
+        bound = (2e-5 + 2 * u) * ref + extra + 1e-6
+        assert float((out.double() - ref).abs().max()) <= bound
+
+    q = q1.expand(rows, hq, d).contiguous().cuda()
+    gk, gv, gt = kc.cuda(), vc.cuda(), table.cuda()
+    out = torch.empty(q.shape, device="cuda")
+    tables = torch.full((rows, 1), -1, dtype=torch.int32, device="cuda")
+    ws = pa.alloc_prefix_workspace(q, gk, tables, max_seq_len=bs, max_prefix_len=n)
+    pa.decode_prefix(q, gk, gv, gt, i32([n]), tables, i32([0] * rows), out, ws, max_seq_len=bs,
+                     max_prefix_len=n, scale=d ** -0.5)
+    check(out, n - 1)
+    # the same tokens as the context of a chunk, whose own are alike
+    k = torch.zeros(rows, hkv, d, dtype=dtype, device="cuda")
+    v = torch.ones_like(k)
+    out.fill_(math.nan)
+    pa.prefill_window(q, k, v, gk, gv, gt.view(1, -1), i32([0, rows]), i32([n]), out,
+                      window=2 * n, max_query_len=rows, max_ctx_len=n, scale=d ** -0.5)
+    for i in range(rows):
+        check(out[i], n + i)
