@@ -577,6 +577,8 @@ PA_API pa_status_t pa_prefill_window(const pa_prefill_params_t* params, const pa
  *   with no token at all is zeros).
  * A prefix length outside 0..max_prefix_len, or a prefix block id outside the
  * pool, makes every row NaN; a sequence's own bad length or block id its rows.
+ * The workspace's status word reads PA_ERR_BAD_SEQ_LEN or PA_ERR_BAD_BLOCK_ID,
+ * also where a bound is 0.
  * workspace: pa_prefix_workspace_size() bytes, initialised once by
  * pa_workspace_init; one for some num_seqs, max_seq_len and max_prefix_len
  * serves smaller ones.  Tensor-core kernel for the prefix where pa_decode_kernel()

@@ -204,6 +204,7 @@ struct JoinList {
 struct JoinArgs {
   JoinList list[2];
   void* out;
+  int32_t* status;              // may be null
   int64_t num_rows;             // num_seqs * num_heads
   int32_t num_heads, head_dim, group, out_dtype;
 };

@@ -42,7 +42,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps) pa_join_kernel(const JoinArgs 
     const JoinList& x = a.list[l];
     if (!x.lens) continue;
     int32_t L = __ldg(x.lens + (x.shared ? 0 : b));
-    ok = ok && L >= 0 && L <= x.max_len;
+    const bool in = L >= 0 && L <= x.max_len;
+    // a list with partials had its length checked by the kernel that made them
+    if (!in && !x.m && threadIdx.x == 0) set_status(a.status, PA_ERR_BAD_SEQ_LEN);
+    ok = ok && in;
     if (!ok || !x.m) continue;
     if (x.window > 0) {
       if (x.block_list) {

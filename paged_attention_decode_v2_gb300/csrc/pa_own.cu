@@ -216,8 +216,12 @@ __global__ void __launch_bounds__(D, 512 / D)
   bool poison = !ok || bad_s != 0;
   if (pre.lens) {
     const int32_t P = __ldg(pre.lens);
-    if (P < 0 || P > pre.max_len) poison = true;
-    else if (pre.m) parts = prefix_split(P, a.num_kv_heads, pre.key_blocks).segments(kvh) * pre.lanes;
+    if (P < 0 || P > pre.max_len) {
+      poison = true;
+      if (!pre.m && tid == 0) set_status(a.status, PA_ERR_BAD_SEQ_LEN);  // no prefix pass ran
+    } else if (pre.m) {
+      parts = prefix_split(P, a.num_kv_heads, pre.key_blocks).segments(kvh) * pre.lanes;
+    }
   }
   // the partials were written while this kernel ran: coherent loads, no __ldg
   cudaGridDependencySynchronize();

@@ -271,6 +271,7 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
                : PA_ERR_CUDA;
   }
   j.out = out;
+  j.status = status;
   j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;
   j.num_heads = p->num_heads;
   j.head_dim = p->head_dim;

@@ -306,3 +306,34 @@ def test_many_faint_tokens(dtype, hq, hkv, d, bs, rows):
                       window=2 * n, max_query_len=rows, max_ctx_len=n, scale=d ** -0.5)
     for i in range(rows):
         check(out[i], n + i)
+
+
+# --------------------------------------------------------------- bounds of zero
+
+@pytest.mark.parametrize("B,hkv", [(3, 2), (40, 4)])
+def test_lengths_past_bounds_of_zero_are_reported(B, hkv):
+    """Nothing promised and something there: NaN rows and the status, whichever
+    kernels run."""
+    p = sr.prefix_problem(16, [4] * B, 2 * hkv, hkv, 128, 16, BF16, seed=12)
+    q, pg, shared, tables, lens = [p[0].cuda(), p[1], p[2].cuda(), p[3].cuda(), p[4].cuda()]
+    kc, vc = pg.k.cuda(), pg.v.cuda()
+    out = torch.empty(q.shape, device="cuda")
+
+    def call(max_seq, max_prefix, n, sl):
+        ws = pa.alloc_prefix_workspace(q, kc, tables, max_seq_len=max_seq,
+                                       max_prefix_len=max_prefix)
+        out.fill_(3.0)
+        pa.decode_prefix(q, kc, vc, shared, i32([n]), tables, sl, out, ws, max_seq_len=max_seq,
+                         max_prefix_len=max_prefix, scale=1.0)
+        return pa.read_device_status(ws)
+
+    zero = torch.zeros_like(lens)
+    assert call(4, 0, 5, lens) == pa.PA_ERR_BAD_SEQ_LEN and torch.isnan(out).all()
+    assert call(0, 0, -1, zero) == pa.PA_ERR_BAD_SEQ_LEN and torch.isnan(out).all()
+    one = zero.clone()
+    one[1] = 2
+    for n in (0, 16):
+        assert call(0, n, n, one) == pa.PA_ERR_BAD_SEQ_LEN
+        assert torch.isnan(out[1]).all() and torch.isfinite(out[[0, 2]]).all()
+    assert call(0, 0, 0, zero) == pa.PA_OK and (out == 0).all()
+    assert call(0, 16, 16, zero) == pa.PA_OK and torch.isfinite(out).all()
