@@ -277,7 +277,10 @@ pa_status_t pa_decode_prefix(const pa_params_t* p, const pa_prefix_t* prefix, co
   j.head_dim = p->head_dim;
   j.group = p->num_heads / p->num_kv_heads;
   j.out_dtype = p->out_dtype;
-  return launch_join(j, stream, true) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  // a dependent of the kernels above, which read the same lengths; where none ran
+  // the kernel before may be the caller's, which still writes them
+  const bool dependent = j.list[0].m || j.list[1].m;
+  return launch_join(j, stream, dependent) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -337,3 +337,27 @@ def test_lengths_past_bounds_of_zero_are_reported(B, hkv):
         assert torch.isnan(out[1]).all() and torch.isfinite(out[[0, 2]]).all()
     assert call(0, 0, 0, zero) == pa.PA_OK and (out == 0).all()
     assert call(0, 16, 16, zero) == pa.PA_OK and torch.isfinite(out).all()
+
+
+def test_lengths_written_just_before_a_call_with_bounds_of_zero():
+    """The join is the call's only kernel then, and waits for whatever ran before."""
+    p = sr.prefix_problem(0, [0] * 5, 4, 2, 128, 16, BF16, seed=15)
+    q, kc, vc, shared, tables = [x.cuda() for x in (p[0], p[1].k, p[1].v, p[2], p[3])]
+    ws = pa.alloc_prefix_workspace(q, kc, tables, max_seq_len=0, max_prefix_len=0)
+    B, plen, free = 5, i32([0]), i32(range(8))
+    plan = dict(tables=torch.full((B, 4), -1, dtype=torch.int32, device="cuda"),
+                query_start=i32([0] * (B + 1)), seq_lens=i32([0] * B), positions=i32([0] * B),
+                slots=torch.zeros(B, dtype=torch.int64, device="cuda"), free_left=i32([0]))
+    outs, news = [], [i32([0, 1, 0, 0, 1]), i32([0] * B)]
+    for i in range(20):
+        pa.plan_step(i32([0] * B), news[i % 2], free, i32([8]), *plan.values(), block_size=16,
+                     num_blocks=8)
+        out = torch.full(q.shape, 3.0, device="cuda")
+        pa.decode_prefix(q, kc, vc, shared, plen, tables, plan["seq_lens"], out, ws, max_seq_len=0,
+                         max_prefix_len=0, scale=1.0)
+        outs.append(out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        bad = news[i % 2].bool()
+        assert torch.isnan(out[bad]).all() and (out[~bad] == 0).all()
+    assert pa.read_device_status(ws) == pa.PA_ERR_BAD_SEQ_LEN
