@@ -481,7 +481,7 @@ PA_API pa_status_t pa_plan_step(const pa_plan_params_t* params, const int32_t* c
  *   q_weight, k_weight [head_dim], element type as q; both null: no norm
  *   cos_sin float32 [max_position, rotary_dim]
  *   positions int32 [T], slots int64 [T]
- * A row with slot -1 is padding: nothing of it is written.  A slot
+ * A row with slot -1 is padding: nothing of it is written.  With caches a slot
  * outside the pool (below -1, or past num_blocks * block_size) writes no cache
  * and reads PA_ERR_BAD_SLOT in the status; a position outside
  * 0..max_position-1 makes the row's q_out and k_out NaN, writes no cache and

@@ -607,8 +607,8 @@ def qk_norm_rope(q, k, v, positions, slots, cos_sin, q_out, k_cache=None, v_cach
     ``q`` [T, Hq, D], ``k``, ``v`` [T, Hkv, D] may be slices of one projection
     (rows any 16-byte multiple apart, heads contiguous); ``q_out`` [T, Hq, D],
     ``k_out`` and ``v_out`` [T, Hkv, D] contiguous.  ``block_size`` and
-    ``num_blocks`` are read off ``k_cache``; without caches they only bound
-    the slots."""
+    ``num_blocks`` are read off ``k_cache``; without caches they are not used,
+    and ``slots`` only marks padding rows (-1)."""
     _done(_binding().qk_norm_rope(q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache,
                                    q_weight, k_weight, eps, weight_offset, interleaved, block_size,
                                    num_blocks, k_out, v_out, split_x, status, _handle(stream)),

@@ -277,9 +277,9 @@ int qk_norm_rope(Args& in) {
     require(c.heads == hkv && c.dim == d, "the caches' heads and head_dim must be k's");
     p.block_size = c.block_size;
     p.num_blocks = c.blocks;
-  } else {
+  } else {  // not used without caches
     if (p.block_size == 0) p.block_size = 1;
-    if (p.num_blocks == 0) p.num_blocks = 1 << 30;
+    if (p.num_blocks == 0) p.num_blocks = 1;
   }
   p.num_tokens = dim32(T);
   p.num_heads = dim32(hq);

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
   load(h0);
   if (slot == -1) return;                             // padding
   const bool pos_ok = !a.rot || (pos >= 0 && pos < a.max_position);
-  const bool slot_ok = slot >= 0 && slot < a.pool;
+  const bool slot_ok = !a.k_cache || (slot >= 0 && slot < a.pool);
   if (k == 0 && threadIdx.x % 32 == 0) {
     if (!slot_ok) set_status(a.status, PA_ERR_BAD_SLOT);
     if (!pos_ok) set_status(a.status, PA_ERR_BAD_POSITION);

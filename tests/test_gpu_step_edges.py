@@ -165,6 +165,18 @@ def test_a_bad_position_makes_whole_rows_nan():
         assert torch.isnan(t[[1, 3]]).all() and torch.isfinite(t[[0, 2, 4]]).all()
 
 
+def test_slots_without_caches_only_mark_padding():
+    T, hq, hkv, d = 4, 2, 1, 64
+    x = torch.randn(T, hq + 2 * hkv, d, device="cuda").to(BF16)
+    slots = torch.tensor([2 ** 30, 2 ** 31 + 7, -1, 2 ** 40], device="cuda")
+    q_out = torch.full((T, hq, d), 9.0, dtype=BF16, device="cuda")
+    status = i32([0])
+    pa.qk_norm_rope(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], None, slots, None, q_out,
+                    status=status)
+    assert int(status) == 0
+    assert torch.equal(q_out[[0, 1, 3]], x[[0, 1, 3], :hq]) and (q_out[2] == 9.0).all()
+
+
 # --------------------------------------------------- values that are not finite
 
 @pytest.mark.parametrize("hq,hkv,d,bs,dtype", [(8, 2, 128, 16, BF16), (24, 4, 256, 16, F16),
