@@ -471,8 +471,7 @@ PA_API pa_status_t pa_plan_step(const pa_plan_params_t* params, const int32_t* c
  *   q [T, num_heads, head_dim], k, v [T, num_kv_heads, head_dim]: rows
  *        q_stride / k_stride / v_stride elements apart (slices of one fused
  *        projection), heads contiguous within a row; 16-byte aligned rows
- *   q_out [T, num_heads, head_dim], contiguous; may be q itself when
- *        q is contiguous
+ *   q_out [T, num_heads, head_dim], contiguous
  *   k_out, v_out [T, num_kv_heads, head_dim], contiguous, may be null: the
  *        normed and rotated keys, and the values, as pa_prefill takes them
  *   k_cache, v_cache: the pools (standard layout, or PA_FLAG_SPLIT_X); row t
@@ -487,6 +486,8 @@ PA_API pa_status_t pa_plan_step(const pa_plan_params_t* params, const int32_t* c
  * 0..max_position-1 makes the row's q_out and k_out NaN, writes no cache and
  * reads PA_ERR_BAD_POSITION.  Rows must have distinct slots: where two rows
  * share one, what it holds afterwards is some mix of the two.
+ * No output may overlap an input or another output (PA_ERR_INVALID_ARG), but
+ * q_out may be q itself where q is contiguous, and so k_out and v_out.
  * rotary_dim is a multiple of 16, at most head_dim (0: no rotation).  One
  * launch; no workspace; status as for pa_plan_step.
  */

@@ -228,6 +228,24 @@ pa_status_t check_tensors(const void* q, const void* k, const void* v, const int
                           const int32_t* sl, const void* out);
 KernelArgs make_args(const pa_params_t* p, const void* q, const void* k, const void* v,
                      const int32_t* bt, const int32_t* sl, void* out);
+// The bytes of a tensor of a call, and whether the call writes it.
+struct Range {
+  const void* p;
+  size_t n;
+  bool out;
+};
+// Whether one that is written shares a byte with another (null and empty ones do not).
+inline bool outputs_overlap(const Range* r, int count) {
+  for (int i = 0; i < count; ++i)
+    for (int j = i + 1; j < count; ++j) {
+      if (!(r[i].out || r[j].out) || !r[i].p || !r[j].p || !r[i].n || !r[j].n) continue;
+      const uintptr_t x = reinterpret_cast<uintptr_t>(r[i].p);
+      const uintptr_t y = reinterpret_cast<uintptr_t>(r[j].p);
+      if (x <= y ? y - x < r[i].n : x - y < r[j].n) return true;
+    }
+  return false;
+}
+
 // Parameter checks of every decode entry point (`v2`: the partition rules too).
 pa_status_t check_params(const pa_params_t* p, bool v2);
 

@@ -189,11 +189,6 @@ __global__ void __launch_bounds__(kNT) pa_plan_kernel(const PlanArgs a) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace pa
 
@@ -226,7 +221,7 @@ extern "C" pa_status_t pa_plan_step(const pa_plan_params_t* p, const int32_t* ct
   if (!aligned(slots, 8)) return PA_ERR_MISALIGNED;
   {  // no output over an input, nor over another output
     const size_t B = static_cast<size_t>(p->num_seqs), T = static_cast<size_t>(p->max_tokens);
-    const struct { const void* p; size_t n; bool out; } r[] = {
+    const Range r[] = {
         {ctx_lens, 4 * B, false},
         {new_lens, 4 * B, false},
         {free_blocks, 4 * static_cast<size_t>(p->max_free), false},
@@ -239,11 +234,7 @@ extern "C" pa_status_t pa_plan_step(const pa_plan_params_t* p, const int32_t* ct
         {slots, 8 * T, true},
         {free_left, 4, true},
         {status, 4, true}};
-    constexpr int n = sizeof r / sizeof r[0];
-    for (int i = 0; i < n; ++i)
-      for (int j = i + 1; j < n; ++j)
-        if ((r[i].out || r[j].out) && r[i].n && r[j].n && overlap(r[i].p, r[i].n, r[j].p, r[j].n))
-          return PA_ERR_INVALID_ARG;
+    if (outputs_overlap(r, sizeof r / sizeof r[0])) return PA_ERR_INVALID_ARG;
   }
   PlanArgs a{ctx_lens,  new_lens,      free_blocks,   free_count,    base_len,
              block_tables, query_start, seq_lens,     positions,     slots,

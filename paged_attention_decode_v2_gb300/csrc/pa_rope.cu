@@ -18,6 +18,7 @@
 // (277 MB) 47.5 us = 5.8 TB/s, 87 % of the copy rate (115 us with one lane per 16
 // bytes, pairs in two lanes and the set-up per head row); 32 rows of 32 / 8
 // heads of 128 2.5 us, a launch's latency.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_runtime_api.h>
@@ -397,9 +398,42 @@ extern "C" pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q,
     if (!aligned(x, 16)) return PA_ERR_MISALIGNED;
   if (!aligned(positions, 4) || !aligned(slots, 8) || !aligned(status, 4))
     return PA_ERR_MISALIGNED;
-  // q_out in place only where rows coincide
-  if (q_out == q && p->num_tokens > 1 && p->q_stride != p->num_heads * D)
-    return PA_ERR_INVALID_ARG;
+  {
+    // No output over an input or over another output: other CTAs may still read
+    // the one, or write the other.  q, k and v may be replaced in place where the
+    // rows coincide: a lane stores the elements that it has loaded.
+    const int64_t T = p->num_tokens, nq = p->num_heads * D, nk = p->num_kv_heads * D;
+    const double most = 4e18;  // past any address space: sizes of wild parameters end here
+    const auto size = [&](double elements) {
+      return static_cast<size_t>(std::min(elements * esz, most));
+    };
+    const auto rows = [&](int64_t stride, int64_t n) {
+      return size(static_cast<double>(T - 1) * stride + n);
+    };
+    const auto in = [&](const void* x, int64_t stride, int64_t n, const void* out) {
+      const bool replaced = x == out && (T == 1 || stride == n);
+      return Range{replaced ? nullptr : x, rows(T > 1 ? stride : n, n), false};
+    };
+    const size_t pool = size(static_cast<double>(p->num_blocks) * p->block_size * nk);
+    const size_t D1 = static_cast<size_t>(D * esz);
+    const Range r[] = {
+        in(q, p->q_stride, nq, q_out),
+        in(k, p->k_stride, nk, k_out),
+        in(v, p->v_stride, nk, v_out),
+        {q_weight, D1, false},
+        {k_weight, D1, false},
+        {p->rotary_dim ? cos_sin : nullptr,
+         static_cast<size_t>(p->max_position) * p->rotary_dim * 4, false},
+        {p->rotary_dim ? positions : nullptr, static_cast<size_t>(T) * 4, false},
+        {slots, static_cast<size_t>(T) * 8, false},
+        {q_out, rows(nq, nq), true},
+        {k_out, rows(nk, nk), true},
+        {v_out, rows(nk, nk), true},
+        {k_cache, pool, true},
+        {v_cache, pool, true},
+        {status, 4, true}};
+    if (outputs_overlap(r, sizeof r / sizeof r[0])) return PA_ERR_INVALID_ARG;
+  }
   RopeArgs a{};
   a.q = q;
   a.k = k;

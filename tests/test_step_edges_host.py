@@ -6,6 +6,7 @@ import re
 
 import pytest
 
+import paged_attention_decode_v2_gb300 as pa
 from paged_attention_decode_v2_gb300 import build as pa_build
 
 
@@ -32,3 +33,44 @@ def test_results_of_the_grid_before_are_read_coherently(path):
         after = body.split("cudaGridDependencySynchronize();", 1)[1]
         assert "__ldg" not in after and "load_row" not in after
         assert "__ldcg" in after
+
+
+def test_qk_norm_rope_refuses_outputs_over_inputs():
+    """Addresses that are never dereferenced: every call is refused."""
+    from test_step_host import A, _rope
+    pa_build.build()
+    L, bad = pa.lib(), pa.PA_ERR_INVALID_ARG
+    T, hq, hkv, d = 5, 8, 2, 128
+    row, base = (hq + 2 * hkv) * d, 0x7000000
+    ok = dict(num_tokens=T, num_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=16,
+              num_blocks=10, rotary_dim=d, max_position=100, q_stride=row, k_stride=row,
+              v_stride=row, dtype=pa.PA_BF16, flags=0, eps=1e-6, weight_offset=0.0)
+    fused = dict(q=base, k=base + 2 * hq * d, v=base + 2 * (hq + hkv) * d)
+    span = 2 * T * row                                     # bytes of the projection
+
+    def call(params=(), **kw):
+        return _rope(L, pa.RopeParams(**{**ok, **dict(params)}), **{**fused, **kw})
+
+    # over the strided projection: in place, shifted, its first and last row
+    for name in ("qo", "ko", "vo", "kc", "vc"):
+        for at in (base, base + 2 * hq * d, base + 512, base + span - 256,
+                   base - 256, base + 2 * row):
+            assert call(**{name: at}) == bad, (name, at - base)
+    for name in ("ko", "vo"):
+        assert call(**{name: fused["k"]}) == bad and call(**{name: fused["v"]}) == bad
+    # contiguous q, k, v: shifted by a row, or one's output over another
+    flat = dict(q_stride=hq * d, k_stride=hkv * d, v_stride=hkv * d)
+    q, k, v = A[0], A[1], A[2]
+    for kw in (dict(qo=q + 2 * hq * d), dict(qo=q - 2 * hq * d), dict(ko=k + 512), dict(ko=v),
+               dict(vo=k), dict(ko=q, vo=0), dict(vo=v + 16), dict(qo=k)):
+        assert call(flat, **{**dict(q=q, k=k, v=v), **kw}) == bad, kw
+    # over the weights, the table, positions, slots; outputs over one another; the pools
+    names = ["q", "k", "v", "wq", "wk", "cs", "pos", "slots", "qo", "ko", "vo", "kc", "vc"]
+    at = dict(zip(names, A))
+    for out in ("qo", "ko", "vo", "kc", "vc"):
+        for other in names[3:]:
+            if other != out:
+                assert call(**{"ko": at["ko"], "vo": at["vo"], out: at[other]}) == bad, (out, other)
+    assert call(status=at["pos"] + 4) == bad and call(status=at["kc"] + 8) == bad
+    assert call(vc=at["kc"] + 10 * 16 * hkv * d * 2 - 16) == bad
+    assert call(dict(num_blocks=2 ** 31 - 1, block_size=2 ** 31 - 1), kc=256) == bad
