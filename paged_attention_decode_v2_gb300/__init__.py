@@ -561,7 +561,15 @@ def _binding():
     if _marshal_mod is None:
         lib()  # names what is missing where nothing has been built
         import torch  # noqa: F401  (the module links against its libraries)
-        from . import _marshal as m
+        from . import build
+        rebuild = "build it with `python -m paged_attention_decode_v2_gb300.build`"
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError(f"_marshal.so is missing or does not load: {rebuild}") from e
+        if not m.built_for.startswith(build.binding_stamp() + ";"):
+            raise RuntimeError(f"_marshal.so was compiled for {m.built_for}, not for "
+                               f"{build.binding_stamp()}: {rebuild}")
         m.set_error(PaError)
         _marshal_mod = m
     return _marshal_mod

@@ -17,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -48,26 +49,43 @@ def _flags(verbose: bool):
     return f
 
 
-def _build_marshal(force: bool) -> None:
-    """Compile and link ``csrc/marshal.cpp`` against torch's headers and libpa."""
-    import sysconfig
+def binding_stamp() -> str:
+    """What ``_marshal.so`` is compiled against: it reads tensors by the C++
+    layout of one torch and one Python, and fits no other."""
+    import torch
 
+    return (f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}, "
+            f"cxx11abi {int(torch.compiled_with_cxx11_abi())}")
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _build_marshal(force: bool) -> None:
+    """Compile and link ``csrc/marshal.cpp`` against torch's headers and libpa,
+    where it is out of date or was compiled against something else."""
     import torch
 
     src, header = os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "pa.h")
     newest = max(os.path.getmtime(src), os.path.getmtime(header))
+    version = subprocess.run([_cxx(), "-dumpfullversion"], capture_output=True, text=True).stdout
+    stamp = f"{binding_stamp()}; {_cxx()} {version.strip()}"  # kept in the binary
     if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
-        return
+        with open(MARSHAL, "rb") as f:
+            if stamp.encode() + b"\0" in f.read():
+                return
     troot = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
+    cmd = [_cxx(), "-std=c++17", "-O2", "-fPIC", "-shared",
            "-fvisibility=hidden", src, "-o", tmp, "-I", INCLUDE,
            "-isystem", os.path.join(troot, "include"),
            "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(cuda, "include"),
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DPA_MARSHAL_STAMP="{stamp}"',
            "-L", os.path.join(troot, "lib"), f"-Wl,-rpath,{os.path.join(troot, 'lib')}",
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
            "-L", PKG, "-l:libpa.so", "-Wl,-rpath,$ORIGIN"]

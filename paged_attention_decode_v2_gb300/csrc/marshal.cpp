@@ -459,6 +459,17 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal",
 
 }  // namespace
 
+// What this file was compiled against: the torch and Python whose layout of
+// tensors it reads, and the compiler.
+#ifndef PA_MARSHAL_STAMP
+#error "PA_MARSHAL_STAMP: the build's description of torch, Python and compiler"
+#endif
+
 extern "C" __attribute__((visibility("default"))) PyObject* PyInit__marshal() {
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", PA_MARSHAL_STAMP) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
 }

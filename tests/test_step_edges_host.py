@@ -74,3 +74,37 @@ def test_qk_norm_rope_refuses_outputs_over_inputs():
     assert call(status=at["pos"] + 4) == bad and call(status=at["kc"] + 8) == bad
     assert call(vc=at["kc"] + 10 * 16 * hkv * d * 2 - 16) == bad
     assert call(dict(num_blocks=2 ** 31 - 1, block_size=2 ** 31 - 1), kc=256) == bad
+
+
+def test_binding_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
+    """What _marshal.so was compiled against stands in the binary; a file that
+    names something else is out of date however new it is."""
+    pa_build.build()
+    so = tmp_path / "_marshal.so"
+    so.write_bytes(open(pa_build.MARSHAL, "rb").read())
+    monkeypatch.setattr(pa_build, "MARSHAL", str(so))
+    ran, run = [], pa_build.subprocess.run
+
+    def fake(cmd, **kw):
+        if "-o" not in cmd:
+            return run(cmd, **kw)
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "wb").write(b"new")
+        return pa_build.subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(pa_build.subprocess, "run", fake)
+    pa_build._build_marshal(False)
+    assert not ran                                         # up to date as it is
+    other = pa_build.binding_stamp().replace("torch ", "torch 1.")
+    monkeypatch.setattr(pa_build, "binding_stamp", lambda: other)
+    pa_build._build_marshal(False)
+    assert len(ran) == 1 and any(other in a for a in ran[0]) and so.read_bytes() == b"new"
+
+
+def test_binding_of_another_torch_is_not_used(monkeypatch):
+    pa_build.build()
+    assert pa._binding().built_for.startswith(pa_build.binding_stamp())
+    monkeypatch.setattr(pa, "_marshal_mod", None)
+    monkeypatch.setattr(pa_build, "binding_stamp", lambda: "torch 1.0, some Python, cxx11abi 0")
+    with pytest.raises(RuntimeError, match="compiled for.*not for torch 1.0"):
+        pa.plan_step(*[None] * 10, block_size=16, num_blocks=1)
