@@ -4,15 +4,19 @@
 Each ``csrc/*.cu`` file is compiled in parallel into ``_build/``, then the
 objects are linked into ``paged_attention_decode_v2_gb300/libpa.so``.  A file
 is recompiled only when it or a header under ``csrc/`` or ``include/`` is
-newer than its object.
+newer than its object.  ``_marshal.so`` serves Python callers only: where torch,
+its headers or the host compiler are missing, ``libpa.so`` alone is built and the
+reason goes to stderr.
 
-Usage: ``python -m paged_attention_decode_v2_gb300.build [--force] [--verbose]``
+Usage: ``python -m paged_attention_decode_v2_gb300.build [--force] [--verbose]
+[--no-binding]``
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -95,7 +99,24 @@ def _build_marshal(force: bool) -> None:
     os.replace(tmp, MARSHAL)
 
 
-def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
+def _no_binding() -> str | None:
+    """Why ``_marshal.so`` cannot be built here, if so."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(os.path.dirname(spec.origin), "include", "ATen", "core",
+                                       "Tensor.h")):
+        return "torch's headers are not installed"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers are not installed"
+    if shutil.which(_cxx()) is None:
+        return f"{_cxx()} is not installed"
+    return None
+
+
+def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
+          binding: bool = True) -> str:
+    """Build what is out of date and return the path of ``libpa.so``."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     newest_header = max((os.path.getmtime(h) for h in _headers()), default=0.0)
@@ -131,7 +152,12 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         if r.returncode != 0:
             raise RuntimeError(f"link of libpa.so failed:\n{r.stderr}")
         os.replace(tmp, LIB)
-    _build_marshal(force)
+    if binding:
+        why = _no_binding()
+        if why:
+            sys.stderr.write(f"_marshal.so is not built: {why}\n")
+        else:
+            _build_marshal(force)
     return LIB
 
 
@@ -139,5 +165,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
     ap.add_argument("--verbose", action="store_true", help="print ptxas register/spill reports")
+    ap.add_argument("--no-binding", action="store_true", help="libpa.so only (nvcc alone)")
     args = ap.parse_args()
-    print(build(force=args.force, verbose=args.verbose))
+    print(build(force=args.force, verbose=args.verbose, binding=not args.no_binding))

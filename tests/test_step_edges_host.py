@@ -3,6 +3,7 @@ sources must keep to, refusals, and the build of the two libraries."""
 import glob
 import os
 import re
+import sys
 
 import pytest
 
@@ -108,3 +109,25 @@ def test_binding_of_another_torch_is_not_used(monkeypatch):
     monkeypatch.setattr(pa_build, "binding_stamp", lambda: "torch 1.0, some Python, cxx11abi 0")
     with pytest.raises(RuntimeError, match="compiled for.*not for torch 1.0"):
         pa.plan_step(*[None] * 10, block_size=16, num_blocks=1)
+
+
+@pytest.mark.parametrize("missing", ["torch", "headers", "compiler"])
+def test_libpa_is_built_without_the_binding(monkeypatch, tmp_path, capsys, missing):
+    """nvcc alone builds libpa.so for callers in C."""
+    pa_build.build()                                       # libpa.so itself is up to date
+    monkeypatch.setattr(pa_build, "MARSHAL", str(tmp_path / "_marshal.so"))
+
+    class Spec:
+        origin = str(tmp_path / "torch" / "__init__.py")
+
+    if missing == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+        monkeypatch.setattr(pa_build.importlib.util, "find_spec", lambda name: None)
+    elif missing == "headers":
+        monkeypatch.setattr(pa_build.importlib.util, "find_spec", lambda name: Spec)
+    else:
+        monkeypatch.setenv("CXX", "no-such-compiler")
+    assert pa_build.build() == pa_build.LIB
+    assert "_marshal.so is not built" in capsys.readouterr().err
+    assert not os.path.exists(pa_build.MARSHAL)
+    assert pa_build.build(binding=False) == pa_build.LIB and capsys.readouterr().err == ""
