@@ -373,3 +373,82 @@ def test_lengths_written_just_before_a_call_with_bounds_of_zero():
         bad = news[i % 2].bool()
         assert torch.isnan(out[bad]).all() and (out[~bad] == 0).all()
     assert pa.read_device_status(ws) == pa.PA_ERR_BAD_SEQ_LEN
+
+
+# ----------------------------------------------- captured, and from two threads
+
+@pytest.mark.parametrize("hq,hkv,d,bs,lens", [
+    (8, 2, 128, 16, (700, 3, 0, 90)), (24, 4, 256, 16, tuple(range(0, 84, 2))), (4, 2, 64, 8, (9, 0))])
+def test_prefix_and_windowed_prefill_captured(hq, hkv, d, bs, lens):
+    """Captured once, replayed with other queries and lengths: the eager calls'
+    bits."""
+    p = sr.prefix_problem(600, lens, hq, hkv, d, bs, BF16, seed=13)
+    gq, kc, vc, shared, gt, gl = [x.cuda() for x in (p[0], p[1].k, p[1].v, *p[2:5])]
+    plen = i32([600])
+    ws = pa.alloc_prefix_workspace(gq, kc, gt, max_seq_len=max(lens), max_prefix_len=600)
+    w = sr.window_prefill_problem((300, 40), (90, 33), 70, 5, hq, hkv, d, bs, BF16, seed=14)
+    wq, wk, wv, wkc, wvc, wt, start, ctx = [x.cuda() for x in (*w[:3], w[3].k, w[3].v, *w[4:7])]
+    eager = [torch.empty(gq.shape, device="cuda"), torch.empty(wq.shape, device="cuda")]
+    replayed = [torch.empty_like(t) for t in eager]
+
+    def calls(outs):
+        pa.decode_prefix(gq, kc, vc, shared, plen, gt, gl, outs[0], ws, max_seq_len=max(lens),
+                         max_prefix_len=600, scale=d ** -0.5)
+        pa.prefill_window(wq, wk, wv, wkc, wvc, wt, start, ctx, outs[1], window=70, num_sinks=5,
+                          max_query_len=90, max_ctx_len=300, scale=d ** -0.5)
+
+    calls(eager)
+    sr.assert_within(eager[0], p[5], p[6], BF16, F32, d > 64)
+    sr.assert_within(eager[1], w[7], w[8], BF16, F32, d > 64)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(replayed)
+    for step in range(4):
+        gq.copy_(gq.roll(1, 0))
+        wq.neg_()
+        plen.sub_(37)
+        gl.copy_((gl - 1).clamp(min=0))
+        for t in replayed:
+            t.fill_(math.nan)
+        graph.replay()
+        calls(eager)
+        torch.cuda.synchronize()
+        for a, b in zip(eager, replayed):
+            assert torch.isfinite(a).all() and torch.equal(a, b), step
+    assert pa.read_device_status(ws) == pa.PA_OK
+
+
+def test_two_threads():
+    """Each on a stream of its own: the bindings and the library keep nothing
+    between calls that another thread's could reach."""
+    probs = [sr.window_decode_problem([900 + 100 * i, 50], 300 + i, 3, 8, 2, 128, 16, BF16, 30 + i)
+             for i in range(2)]
+    errors = []
+
+    def work(i):
+        try:
+            q, pg, tables, gl, ref, mag = probs[i]
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                g = [x.cuda() for x in (q, pg.k, pg.v, tables, gl)]
+                ws = pa.alloc_window_workspace(g[0], g[1], g[3], window=300 + i, num_sinks=3,
+                                               max_seq_len=900 + 100 * i)
+                for _ in range(200):
+                    out = torch.full(q.shape, math.nan, device="cuda")
+                    pa.decode_window(g[0], g[1], g[2], g[3], g[4], out, ws, window=300 + i,
+                                     num_sinks=3, max_seq_len=900 + 100 * i, scale=128 ** -0.5)
+                    with pytest.raises(pa.PaError):
+                        pa.decode_window(g[0], g[1], g[2], g[3], g[4], out, ws, window=-i,
+                                         num_sinks=3, max_seq_len=900 + 100 * i, scale=128 ** -0.5)
+                s.synchronize()
+                sr.assert_within(out, ref, mag, BF16, F32, False)
+                assert pa.read_device_status(ws) == pa.PA_OK
+        except BaseException as e:  # noqa: BLE001  (handed to the test's thread)
+            errors.append(e)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not errors, errors
