@@ -214,7 +214,10 @@ __global__ void __launch_bounds__(256) pa_generic_kernel(const KernelArgs a) {
         const float m_new = fmaxf(m_old, mx);
         float sum = 0.f;
         for (int tt = lane; tt < n; tt += 32) {
-          const float pv = m_new == -INFINITY ? 0.f : exp2f(sm.p[tt][h] - m_new);
+          // a NaN logit goes on into the sum, also where none is above -inf
+          const float l = sm.p[tt][h];
+          const float pv =
+              l == -INFINITY ? 0.f : exp2f(l - (m_new == -INFINITY ? 0.f : m_new));
           sm.p[tt][h] = pv;
           sum += pv;
         }
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(256) pa_generic_kernel(const KernelArgs a) {
     for (int i = tid; i < nh * D; i += C::NT) {
       const int hh = i / D, d = i % D;
       const float s = sm.s_run[hh];
-      const float o = bad ? qnan() : (s > 0.f ? sm.acc[hh][d] / s : 0.f);
+      const float o = bad ? qnan() : (s == 0.f ? 0.f : sm.acc[hh][d] / s);
       const int64_t row = static_cast<int64_t>(b) * Hq + h0 + hh;
       if (kV2 && !direct)
         a.tmp_out[(row * a.num_partitions + part) * D + d] = o;

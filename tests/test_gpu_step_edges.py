@@ -210,6 +210,46 @@ def test_decode_prefix_with_nan(hq, hkv, d, bs, dtype, portable):
     assert pa.read_device_status(ws) == pa.PA_ERR_BAD_BLOCK_ID
 
 
+@pytest.mark.parametrize("hq,hkv,d,bs,dtype,kw", [
+    (8, 2, 128, 16, BF16, {}), (8, 2, 128, 16, BF16, dict(portable=True)),
+    (8, 2, 128, 16, F16, dict(sx=True)), (4, 2, 64, 16, BF16, {}), (4, 2, 128, 8, F32, {})])
+def test_decode_prefix_with_nan_and_no_prefix(hq, hkv, d, bs, dtype, kw):
+    """Own lists alone, of one part and of three: every kernel that takes them."""
+    G = hq // hkv
+    p = sr.prefix_problem(0, (30, 300, 45), hq, hkv, d, bs, dtype, seed=16)
+    p[0][0] = math.nan
+    p[0][1, 0] = math.nan
+    p[1].k[p[3][2, 1], 1, 3, 7] = math.nan
+    out, ws = _run_prefix(p, 0, P=128, check=False, **kw)
+    assert torch.isnan(out[0]).all() and torch.isnan(out[1, 0]).all()
+    assert torch.isnan(out[2, G:2 * G]).all()
+    sr.assert_within(out[1, 1:], p[5][1, 1:], p[6][1, 1:], dtype, F32, False)
+    sr.assert_within(out[2, :G], p[5][2, :G], p[6][2, :G], dtype, F32, False)
+    assert pa.read_device_status(ws) == pa.PA_OK
+
+
+@pytest.mark.parametrize("path", ["v1", "v2"])
+def test_cuda_core_decode_with_nan(path):
+    """The same kernel behind pa_decode: as the tensor-core ones, NaN and not zeros."""
+    q, pg, tables, gl, ref, mag = sr.window_decode_problem([300, 77, 60], 10 ** 6, 0, 8, 2, 128, 16,
+                                                           BF16, seed=17)
+    q[1] = math.nan
+    pg.k[tables[2, 1], 0, 3, 7] = math.nan
+    g = [x.cuda() for x in (q, pg.k, pg.v, tables, gl)]
+    for portable in (False, True):
+        out = torch.empty(q.shape, device="cuda")
+        kw = dict(max_seq_len=300, scale=128 ** -0.5, portable=portable)
+        if path == "v1":
+            pa.decode_v1(*g, out, **kw)
+        else:
+            params = pa.make_params(g[0], g[1], g[3], max_seq_len=300, scale=1.0,
+                                    partition_size=128)
+            pa.decode_v2(*g, out, pa.alloc_workspace(params), partition_size=128, **kw)
+        assert torch.isnan(out[1]).all() and torch.isnan(out[2, :4]).all()
+        sr.assert_within(out[0], ref[0], mag[0], BF16, F32, False)
+        sr.assert_within(out[2, 4:], ref[2, 4:], mag[2, 4:], BF16, F32, False)
+
+
 def test_decode_prefix_of_many_short_sequences_with_nan():
     hq, hkv, d, bs = 8, 4, 128, 32
     lens = [int(x) for x in np.random.RandomState(1).randint(0, 90, size=41)]
