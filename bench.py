@@ -69,11 +69,11 @@ KERNEL_SOURCES = {
 NCU_TRAFFIC = {
     # (kernel, source hash, workload, partition size, path): bytes per launch
     # the one-launch V2 kernel (pass 1 and the in-grid reduce)
-    ("pa_tc_kernel", "8a5045d97b123fcf", "long_100k", 512, "v2"): 409_753_856 + 3_017_728,
+    ("pa_tc_kernel", "7ee010a591dac11b", "long_100k", 512, "v2"): 409_792_000 + 2_950_144,
     # the split-x kernel in one launch (its own pass 1 and the same in-grid reduce)
-    ("pa_sx_kernel", "c34260bcc25f78e6", "long_100k", 512, "v2"): 409_794_304 + 4_820_736,
-    ("pa_prefill_kernel", "805b531535404f7f", "prefill_32k", 0, "prefill"):
-        1_356_391_168 + 194_315_776,
+    ("pa_sx_kernel", "cb6e9dba05286304", "long_100k", 512, "v2"): 409_752_832 + 4_603_392,
+    ("pa_prefill_kernel", "a99874c019fd6c1b", "prefill_32k", 0, "prefill"):
+        1_353_717_504 + 192_799_232,
 }
 
 

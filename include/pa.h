@@ -557,6 +557,13 @@ PA_API pa_status_t pa_decode_window(const pa_params_t* params, const pa_window_t
  * (flags: PA_FLAG_PORTABLE, PA_FLAG_SPLIT_X for the caches,
  * PA_FLAG_SELFTEST_STALL).  Of the tokens that at least one row of the call
  * sees, values must be finite (a weight of zero times infinity is NaN).
+ * The call has no status word: what the device-side checks find shows as NaN
+ * rows, or as rows that are not written, only.
+ * Rounding: logits, maxima, sums and accumulators are float32.  The tensor-core
+ * kernel rounds each softmax weight once to the element type before the product
+ * with the values, as pa_prefill does (half a step: 2^-8 of the weight for bf16,
+ * 2^-11 for f16, and for f16 2^-32 of the row's largest); the sum takes it
+ * unrounded.  The CUDA-core kernel (PA_FLAG_PORTABLE) keeps it in float32.
  */
 PA_API pa_status_t pa_prefill_window(const pa_prefill_params_t* params, const pa_window_t* window,
                                      const void* q, const void* k, const void* v,
@@ -570,9 +577,11 @@ PA_API pa_status_t pa_prefill_window(const pa_prefill_params_t* params, const pa
  * last one possibly part full) and then to its own seq_lens[b] tokens (blocks
  * block_tables[b], which hold nothing of the prefix):
  *   out[b,h] = softmax over both lists of scale * q[b,h] . k, applied to v.
- * The prefix is read once for all sequences and heads of a KV group, as one
- * matrix product over the rows (b, h); the own tokens go through the paged
- * decode pass; a last kernel joins the partial results.
+ * On the tensor cores the prefix is read once for all sequences and heads of a
+ * KV group, as one matrix product over the rows (b, h); the CUDA-core kernel
+ * reads it for each sequence.  The own tokens go through the paged decode pass, or
+ * with the join through a kernel for many short lists; the last kernel joins the
+ * partial results.
  *   prefix_blocks [int32] [max_prefix_blocks], prefix_len [int32] [1], on the
  *   device; seq_lens[b] in 0..max_seq_len, and both lists may be empty (a row
  *   with no token at all is zeros).
@@ -582,8 +591,13 @@ PA_API pa_status_t pa_prefill_window(const pa_prefill_params_t* params, const pa
  * also where a bound is 0.
  * workspace: pa_prefix_workspace_size() bytes, initialised once by
  * pa_workspace_init; one for some num_seqs, max_seq_len and max_prefix_len
- * serves smaller ones.  Tensor-core kernel for the prefix where pa_decode_kernel()
- * says 2 and the layout is the standard one, else CUDA cores.
+ * serves smaller ones.  Tensor-core kernel for the prefix with the shapes that
+ * pa_prefill_window's has, else CUDA cores.
+ * Rounding: the tensor-core prefix pass rounds the weights as pa_prefill_window's
+ * kernel does, so the prefix's part of the result is off by about half a step of
+ * the element type where pa_decode, which keeps some 16 bits of each weight, is
+ * not: with a 16-bit output about 1.3 times pa_decode's error.  The own tokens keep
+ * 16 bits; PA_FLAG_PORTABLE keeps float32 weights throughout.
  */
 typedef struct pa_prefix {
   int32_t max_prefix_len;    /* host-known bound of *prefix_len              */

@@ -669,7 +669,8 @@ def prefill_window(q, k, v, k_cache, v_cache, block_tables, query_start, ctx_len
                    scale: float, portable: bool = False, split_x: bool = False, flags: int = 0,
                    stream=None):
     """``pa_prefill_window``: :func:`prefill` where the query at position p sees
-    tokens t <= p with t > p - ``window`` or t < ``num_sinks``."""
+    tokens t <= p with t > p - ``window`` or t < ``num_sinks``.  There is no
+    status word: bad lengths and block ids show as NaN rows."""
     _done(_binding().prefill_window(q, k, v, k_cache, v_cache, block_tables, query_start, ctx_lens,
                                      out, max_query_len, max_ctx_len, scale,
                                      _flags(portable, split_x, flags), window, num_sinks,
@@ -698,8 +699,9 @@ def decode_prefix(q, k_cache, v_cache, prefix_blocks, prefix_len, block_tables, 
                   flags: int = 0, stream=None):
     """``pa_decode_prefix``: decode of a batch whose sequences share the
     ``prefix_len`` [1] tokens in ``prefix_blocks`` [.] and own ``seq_lens`` [B]
-    further tokens in ``block_tables`` [B, .].  The prefix is read once for
-    the whole batch."""
+    further tokens in ``block_tables`` [B, .].  The tensor-core kernel reads
+    the prefix once for the whole batch (the CUDA-core one for each sequence)
+    and rounds its softmax weights to the element type."""
     _done(_binding().decode_prefix(q, k_cache, v_cache, block_tables, seq_lens, out, workspace,
                                     max_seq_len, scale, partition_size,
                                     _flags(portable, split_x, flags), prefix_blocks, prefix_len,

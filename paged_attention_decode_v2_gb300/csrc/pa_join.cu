@@ -14,7 +14,7 @@
 // shared memory.  The sums run in a fixed order.  Bound by the partials' bytes
 // (they are in L2, written just before) or, for few rows, by latency.  Measured
 // alone with cold caches (in the calls they are warm and the launch overlaps):
-// 8192 rows of 128 with 28 MB of partials 17.7 us, 24 rows of 256 6.5 us.  Two,
+// 8192 rows of 128 with 28 MB of partials 18.9 us, 24 rows of 256 6.6 us.  Two,
 // four or eight rows in a CTA changed whole calls by less than 1.5 %.
 #include "pa_device.cuh"
 #include "pa_span.cuh"

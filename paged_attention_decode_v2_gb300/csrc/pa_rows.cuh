@@ -45,7 +45,7 @@
 //
 // Bound by the tensor core for many rows (4 * head_dim flops per row and key),
 // and by latency for few.  Measured: prefix of 32000 tokens, 256 sequences, 32 / 8
-// heads of 128: 79 us at full clocks = 1700 TFLOP/s, tensor pipe 82 % busy (in a
+// heads of 128: 81 us at full clocks = 1660 TFLOP/s, tensor pipe 82 % busy (in a
 // loop the power cap holds 1.54 GHz: 93 us); windowed chunk of 4096 tokens,
 // window 2048, 24 / 4 heads of 256: 174 us for 213 visible GFLOP, tensor pipe
 // 68 % busy of the 86 % that 784 equal units leave on 152 SMs; 5 ragged chunks,
