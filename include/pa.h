@@ -518,6 +518,31 @@ PA_API pa_status_t pa_qk_norm_rope(const pa_rope_params_t* params, const void* q
                                    cudaStream_t stream);
 
 /*
+ * The same with several positions a row, one for each axis of an image or a video
+ * (time, height, width): pair j of the rotation turns by the angle of its own
+ * axis' position,
+ *   c_j = cos_sin[positions[axis_of[j]][t]][j], s_j likewise.
+ *   positions int32 [num_axes, T]; text has the same position on every axis
+ * A row with a position outside 0..max_position-1 on any axis is handled as
+ * pa_qk_norm_rope handles its one position.  Everything else is as there; with
+ * one axis so are the results.
+ */
+#define PA_ROPE_MAX_AXES 4
+#define PA_ROPE_MAX_PAIRS 128
+typedef struct pa_rope_axes {
+  int32_t num_axes;                   /* 1..PA_ROPE_MAX_AXES                   */
+  uint8_t axis_of[PA_ROPE_MAX_PAIRS]; /* axis of pair j < rotary_dim / 2       */
+} pa_rope_axes_t;
+
+PA_API pa_status_t pa_qk_norm_rope_axes(const pa_rope_params_t* params,
+                                        const pa_rope_axes_t* axes, const void* q, const void* k,
+                                        const void* v, const void* q_weight,
+                                        const void* k_weight, const float* cos_sin,
+                                        const int32_t* positions, const int64_t* slots,
+                                        void* q_out, void* k_out, void* v_out, void* k_cache,
+                                        void* v_cache, int32_t* status, cudaStream_t stream);
+
+/*
  * Attention with a sliding window and sinks.  A query at position p (0-based)
  * sees token t <= p when t < num_sinks (the sequence's first tokens, which stay
  * visible) or t > p - window (the last `window` tokens, itself included).
@@ -611,6 +636,110 @@ PA_API pa_status_t pa_decode_prefix(const pa_params_t* params, const pa_prefix_t
                                     const int32_t* block_tables, const int32_t* seq_lens,
                                     void* workspace, size_t workspace_bytes, void* out,
                                     cudaStream_t stream);
+
+/*
+ * The paged cache held in 4 bits.  A pool of num_blocks pages holds, for keys and
+ * for values each,
+ *   codes  [num_blocks, num_kv_heads, block_size, head_dim / 2] bytes: element 2i
+ *          of a head row is the low half of byte i, element 2i + 1 the high half;
+ *   scales [num_blocks, num_kv_heads, block_size, head_dim / group_size, 2] of the
+ *          model's element type: a scale and a minimum for each group of
+ *          group_size (32, 64 or 128, dividing head_dim) elements of a head row.
+ * A code c in 0..15 stands for the value c * scale + minimum.  dtype is the type of
+ * the scales, of the rows stored and of the queries: float32, bf16 or f16; head_dim
+ * is 64, 128 or 256.  Codes and scales are 16-byte aligned.  Block tables, lengths
+ * and slots are those of the other calls (pa_plan_step's).
+ *
+ * pa_store_kv4 writes the keys and values of T rows into such a pool.  For each
+ * group of a head row x, m = min x, s = (max x - m) / 15 rounded to the element
+ * type, and each element's code is (x - m) / s rounded to the nearest whole number
+ * (halves to even), at most 15, or 0 where s is 0.  A group with an element that is
+ * not finite, or a range past float32, gets NaN for both and reads back as NaN.
+ *   k, v [T, num_kv_heads, head_dim]: rows k_stride / v_stride elements apart,
+ *        heads contiguous within a row; 16-byte aligned rows
+ *   slots int64 [T]: slot block * block_size + place; -1 is padding (nothing of the
+ *        row is written); another slot outside the pool writes no cache and reads
+ *        PA_ERR_BAD_SLOT in the status.  Rows must have distinct slots.
+ *   k_out, v_out [T, num_kv_heads, head_dim], contiguous, may be null: the values
+ *        that the codes stand for, rounded to the element type -- the chunk's keys
+ *        and values for pa_prefill, as later steps will see them.
+ * No output may overlap an input or another output (PA_ERR_INVALID_ARG), but k_out
+ * may be k itself where k is contiguous, and so v_out.  One launch; no workspace;
+ * status as for pa_plan_step.
+ */
+typedef struct pa_store_kv4_params {
+  int32_t num_tokens;   /* T >= 0                                            */
+  int32_t num_kv_heads; /* Hkv >= 1                                          */
+  int32_t head_dim;     /* D: 64, 128 or 256                                 */
+  int32_t block_size;   /* tokens per page                                   */
+  int32_t num_blocks;   /* pages in the pool                                 */
+  int32_t group_size;   /* 32, 64 or 128, divides D                          */
+  int64_t k_stride;     /* elements from one row of k to the next            */
+  int64_t v_stride;
+  pa_dtype_t dtype;     /* k, v, k_out, v_out and the scales                 */
+} pa_store_kv4_params_t;
+
+PA_API pa_status_t pa_store_kv4(const pa_store_kv4_params_t* params, const void* k, const void* v,
+                                const int64_t* slots, void* k_codes, void* v_codes,
+                                void* k_scales, void* v_scales, void* k_out, void* v_out,
+                                int32_t* status, cudaStream_t stream);
+
+/*
+ * pa_load_kv4 widens pages of the 4-bit pool into pages of the element type
+ * (the standard layout [num_out_blocks, num_kv_heads, block_size, head_dim]), so that
+ * pa_prefill and pa_prefill_window can read a context that is held in 4 bits:
+ * for each sequence b and j < ceil(seq_lens[b] / block_size), page
+ * block_tables[b][j] becomes page out_tables[b][j] of k_out and v_out, each value
+ * rounded once.  Whole pages are written, places past the sequence's end included;
+ * no other page is touched.  Pages of out_tables must be distinct.
+ * A length outside 0..max_seq_len leaves the sequence out and reads
+ * PA_ERR_BAD_SEQ_LEN in the status; a page outside its pool reads
+ * PA_ERR_BAD_BLOCK_ID, and the page of out_tables becomes NaN (a bad source) or none
+ * is written (a bad destination).  No output may overlap an input or another output.
+ * One launch; no workspace; status as for pa_plan_step.
+ */
+typedef struct pa_load_kv4_params {
+  int32_t num_seqs;               /* B >= 0                                  */
+  int32_t num_kv_heads;           /* Hkv >= 1                                */
+  int32_t head_dim;               /* D: 64, 128 or 256                       */
+  int32_t block_size;             /* tokens per page, of both pools          */
+  int32_t num_blocks;             /* pages in the 4-bit pool                 */
+  int32_t max_blocks_per_seq;     /* row length of block_tables              */
+  int32_t num_out_blocks;         /* pages in k_out and v_out                */
+  int32_t max_out_blocks_per_seq; /* row length of out_tables                */
+  int32_t max_seq_len;            /* host-known bound of every seq_lens[b]   */
+  int32_t group_size;             /* 32, 64 or 128, divides D                */
+  pa_dtype_t dtype;               /* the scales, k_out and v_out             */
+} pa_load_kv4_params_t;
+
+PA_API pa_status_t pa_load_kv4(const pa_load_kv4_params_t* params, const void* k_codes,
+                               const void* v_codes, const void* k_scales, const void* v_scales,
+                               const int32_t* block_tables, const int32_t* seq_lens,
+                               const int32_t* out_tables, void* k_out, void* v_out,
+                               int32_t* status, cudaStream_t stream);
+
+/*
+ * Decode over the 4-bit cache: the step of pa_decode (same q, tables, lengths, out
+ * and checks; kv_dtype is the type of q and of the scales) with keys and values
+ * c * scale + minimum.  Scales and minima of visible tokens are finite, or NaN,
+ * which makes the rows that see them NaN; what the pools hold elsewhere does not
+ * matter.  The workspace holds pa_kv4_workspace_size() bytes, its control block
+ * initialised by pa_workspace_init; partition_size (>= 1, rounded
+ * up to whole tiles of 64) is about the tokens of one partial of a row where there
+ * are many sequences; for few the split is chosen to fill the GPU.  A workspace for some num_seqs and max_seq_len serves
+ * smaller ones.  v1_max_seq_len is not used; flags: PA_FLAG_PORTABLE.
+ * Tensor-core kernel for bf16 and f16, CUDA cores for float32 and PA_FLAG_PORTABLE.
+ */
+typedef struct pa_kv4 {
+  int32_t group_size; /* 32, 64 or 128, divides head_dim                     */
+} pa_kv4_t;
+
+PA_API size_t pa_kv4_workspace_size(const pa_params_t* params, const pa_kv4_t* kv4);
+PA_API pa_status_t pa_decode_kv4(const pa_params_t* params, const pa_kv4_t* kv4, const void* q,
+                                 const void* k_codes, const void* v_codes, const void* k_scales,
+                                 const void* v_scales, const int32_t* block_tables,
+                                 const int32_t* seq_lens, void* workspace,
+                                 size_t workspace_bytes, void* out, cudaStream_t stream);
 
 /* ABI version: major * 10000 + minor * 100 + patch. */
 PA_API int pa_version(void);

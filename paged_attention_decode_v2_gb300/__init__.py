@@ -11,8 +11,11 @@ Functions mirror the C entry points: :func:`workspace_size`,
 :func:`decode_path`, :func:`status_string`, :func:`workspace_init`,
 :func:`read_device_status`; and, in the order of a serving step,
 :func:`plan_step` (block tables, slots and positions from request lengths),
-:func:`qk_norm_rope` (norm, rotation, cache write), :func:`prefill`,
-:func:`prefill_window`, :func:`decode_window`, :func:`decode_prefix`.
+:func:`qk_norm_rope` (norm, rotation, cache write; :func:`qk_norm_rope_axes`
+with positions on several axes), :func:`prefill`,
+:func:`prefill_window`, :func:`decode_window`, :func:`decode_prefix`; and for a
+cache held in 4 bits :func:`alloc_kv4_cache`, :func:`store_kv4`, :func:`load_kv4`
+(pages widened for the prefill calls), :func:`decode_kv4`.
 """
 from __future__ import annotations
 
@@ -50,8 +53,10 @@ EXPORTS = ("pa_workspace_size", "pa_decode_v1", "pa_decode_v2", "pa_decode_v2_pa
            "pa_workspace_init", "pa_read_device_status", "pa_version", "pa_decode_v2_static",
            "pa_decode_kernel", "pa_host_staging_size", "pa_host_staging_offsets",
            "pa_decode_host", "pa_prefill", "pa_decode_launches", "pa_plan_step", "pa_qk_norm_rope",
+           "pa_qk_norm_rope_axes",
            "pa_window_workspace_size", "pa_decode_window", "pa_prefill_window",
-           "pa_prefix_workspace_size", "pa_decode_prefix")
+           "pa_prefix_workspace_size", "pa_decode_prefix", "pa_store_kv4", "pa_load_kv4",
+           "pa_kv4_workspace_size", "pa_decode_kv4")
 PA_STATIC_WORKSPACE_BYTES = 16 << 20
 
 
@@ -118,9 +123,36 @@ class RopeParams(ctypes.Structure):
                  ("weight_offset", ctypes.c_float)])
 
 
+class RopeAxes(ctypes.Structure):
+    """Mirror of ``pa_rope_axes_t``."""
+    _fields_ = [("num_axes", ctypes.c_int32), ("axis_of", ctypes.c_uint8 * 128)]
+
+
 class WindowParams(ctypes.Structure):
     """Mirror of ``pa_window_t``."""
     _fields_ = [("window", ctypes.c_int32), ("num_sinks", ctypes.c_int32)]
+
+
+class StoreKv4Params(ctypes.Structure):
+    """Mirror of ``pa_store_kv4_params_t``."""
+    _fields_ = ([(n, ctypes.c_int32) for n in
+                 ("num_tokens", "num_kv_heads", "head_dim", "block_size", "num_blocks",
+                  "group_size")] +
+                [("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                 ("dtype", ctypes.c_int32)])
+
+
+class LoadKv4Params(ctypes.Structure):
+    """Mirror of ``pa_load_kv4_params_t``."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_seqs", "num_kv_heads", "head_dim", "block_size", "num_blocks",
+                 "max_blocks_per_seq", "num_out_blocks", "max_out_blocks_per_seq", "max_seq_len",
+                 "group_size", "dtype")]
+
+
+class Kv4Params(ctypes.Structure):
+    """Mirror of ``pa_kv4_t``."""
+    _fields_ = [("group_size", ctypes.c_int32)]
 
 
 class PrefixParams(ctypes.Structure):
@@ -185,6 +217,9 @@ def lib() -> ctypes.CDLL:
             L.pa_plan_step.restype = ctypes.c_int
             L.pa_qk_norm_rope.argtypes = [ctypes.POINTER(RopeParams)] + [P] * 15
             L.pa_qk_norm_rope.restype = ctypes.c_int
+            L.pa_qk_norm_rope_axes.argtypes = [ctypes.POINTER(RopeParams),
+                                               ctypes.POINTER(RopeAxes)] + [P] * 15
+            L.pa_qk_norm_rope_axes.restype = ctypes.c_int
             L.pa_window_workspace_size.argtypes = [PP, PW]
             L.pa_window_workspace_size.restype = ctypes.c_size_t
             L.pa_decode_window.argtypes = [PP, PW] + [P] * 6 + [ctypes.c_size_t, P, P]
@@ -195,6 +230,15 @@ def lib() -> ctypes.CDLL:
             L.pa_prefix_workspace_size.restype = ctypes.c_size_t
             L.pa_decode_prefix.argtypes = [PP, PX] + [P] * 8 + [ctypes.c_size_t, P, P]
             L.pa_decode_prefix.restype = ctypes.c_int
+            L.pa_store_kv4.argtypes = [ctypes.POINTER(StoreKv4Params)] + [P] * 11
+            L.pa_store_kv4.restype = ctypes.c_int
+            L.pa_load_kv4.argtypes = [ctypes.POINTER(LoadKv4Params)] + [P] * 11
+            L.pa_load_kv4.restype = ctypes.c_int
+            P4 = ctypes.POINTER(Kv4Params)
+            L.pa_kv4_workspace_size.argtypes = [PP, P4]
+            L.pa_kv4_workspace_size.restype = ctypes.c_size_t
+            L.pa_decode_kv4.argtypes = [PP, P4] + [P] * 8 + [ctypes.c_size_t, P, P]
+            L.pa_decode_kv4.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -624,6 +668,47 @@ def qk_norm_rope(q, k, v, positions, slots, cos_sin, q_out, k_cache=None, v_cach
     return q_out
 
 
+def rope_axes(sections, alternate: bool = False) -> bytes:
+    """The axis of each pair of the rotation, for :func:`qk_norm_rope_axes`.
+
+    ``sections``: how many pairs each axis has.  They lie one after another, or
+    (``alternate``) are dealt out in turn: axis a > 0 has the pairs a, a + A,
+    a + 2 A, ... of A axes, the first axis what is left."""
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0:
+        raise PaError(PA_ERR_INVALID_ARG, "sections must be counts of pairs")
+    if not alternate:
+        return b"".join(bytes([a]) * n for a, n in enumerate(sections))
+    of = bytearray(sum(sections))
+    for a, n in enumerate(sections):
+        if a and n and a + len(sections) * (n - 1) >= len(of):
+            raise PaError(PA_ERR_INVALID_ARG, f"section {a} has too many pairs to alternate")
+        for i in range(n if a else 0):
+            of[a + i * len(sections)] = a
+    return bytes(of)
+
+
+def qk_norm_rope_axes(q, k, v, positions, slots, cos_sin, q_out, k_cache=None, v_cache=None, *,
+                      axis_of, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      weight_offset: float = 0.0, interleaved: bool = False, block_size: int = 0,
+                      num_blocks: int = 0, k_out=None, v_out=None, split_x: bool = False,
+                      status=None, stream=None):
+    """``pa_qk_norm_rope_axes``: :func:`qk_norm_rope` with ``positions`` int32
+    [axes, T], one row for each of up to four axes (time, height, width).
+    Pair j of the rotation turns by the position on axis ``axis_of[j]``
+    (``rotary_dim / 2`` whole numbers; see :func:`rope_axes`)."""
+    if not isinstance(axis_of, bytes):
+        try:
+            axis_of = bytes(list(axis_of))
+        except (TypeError, ValueError) as e:
+            raise PaError(PA_ERR_INVALID_ARG, "axis_of must be small whole numbers") from e
+    _done(_binding().qk_norm_rope_axes(q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache,
+                                        q_weight, k_weight, eps, weight_offset, interleaved,
+                                        block_size, num_blocks, k_out, v_out, split_x, status,
+                                        _handle(stream), axis_of), "pa_qk_norm_rope_axes")
+    return q_out
+
+
 def _alloc(n: int, where: str, device):
     import torch
     if n == 0:
@@ -706,4 +791,73 @@ def decode_prefix(q, k_cache, v_cache, prefix_blocks, prefix_len, block_tables, 
                                     max_seq_len, scale, partition_size,
                                     _flags(portable, split_x, flags), prefix_blocks, prefix_len,
                                     max_prefix_len, _handle(stream)), "pa_decode_prefix")
+    return out
+
+
+# ---- the paged cache held in 4 bits --------------------------------------------------------------
+
+def alloc_kv4_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int, *,
+                    group_size: int = 64, dtype=None, device="cuda"):
+    """Pools of a 4-bit cache: ``(k_cache, v_cache, k_scales, v_scales)``, codes
+    uint8 [NB, Hkv, BS, D / 2] and (scale, minimum) pairs [NB, Hkv, BS, D / group, 2]
+    of ``dtype`` (bfloat16 unless given)."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    _dtype_code(dtype)
+    if group_size not in (32, 64, 128) or head_dim % group_size:
+        raise PaError(PA_ERR_INVALID_ARG, "group_size must be 32, 64 or 128 and divide head_dim")
+    codes = (num_blocks, num_kv_heads, block_size, head_dim // 2)
+    scales = (num_blocks, num_kv_heads, block_size, head_dim // group_size, 2)
+    return (torch.empty(codes, dtype=torch.uint8, device=device),
+            torch.empty(codes, dtype=torch.uint8, device=device),
+            torch.empty(scales, dtype=dtype, device=device),
+            torch.empty(scales, dtype=dtype, device=device))
+
+
+def store_kv4(k, v, slots, k_cache, v_cache, k_scales, v_scales, *, k_out=None, v_out=None,
+              status=None, stream=None):
+    """``pa_store_kv4``: keys and values [T, Hkv, D] (rows any 16-byte multiple
+    apart) into a 4-bit cache at ``slots`` (int64 [T], -1: padding).  ``k_out``,
+    ``v_out`` [T, Hkv, D], if given, receive the values that the codes stand for:
+    the chunk's keys and values as later steps will see them."""
+    _done(_binding().store_kv4(k, v, slots, k_cache, v_cache, k_scales, v_scales, k_out, v_out,
+                                status, _handle(stream)), "pa_store_kv4")
+
+
+def load_kv4(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, out_tables, k_out,
+             v_out, *, max_seq_len: int, status=None, stream=None):
+    """``pa_load_kv4``: the pages of a 4-bit cache that ``seq_lens`` tokens of each
+    sequence take, widened into the pages ``out_tables`` of ``k_out`` and ``v_out``
+    [NB, Hkv, BS, D], for :func:`prefill` and :func:`prefill_window`."""
+    _done(_binding().load_kv4(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
+                               out_tables, k_out, v_out, max_seq_len, status, _handle(stream)),
+          "pa_load_kv4")
+
+
+def kv4_workspace_size(params: Params, group_size: int) -> int:
+    g = Kv4Params(int(group_size))
+    return int(lib().pa_kv4_workspace_size(ctypes.byref(params), ctypes.byref(g)))
+
+
+def alloc_kv4_workspace(q, k_cache, k_scales, block_tables, *, max_seq_len: int,
+                        partition_size: int = 1024):
+    """A workspace for :func:`decode_kv4` with these shapes, initialised."""
+    num_seqs, num_heads, head_dim = q.shape
+    if k_cache.dim() != 4 or k_scales.dim() != 5:
+        raise PaError(PA_ERR_INVALID_ARG, "k_cache must be 4-D and k_scales 5-D")
+    num_blocks, num_kv_heads, block_size, _ = k_cache.shape
+    p = Params(num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+               block_tables.shape[1], int(max_seq_len), int(partition_size), 0,
+               _dtype_code(q.dtype), _dtype_code(q.dtype), 1.0, 0)
+    return _alloc(kv4_workspace_size(p, head_dim // max(1, k_scales.shape[3])),
+                  "pa_kv4_workspace_size", q.device)
+
+
+def decode_kv4(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, out, workspace, *,
+               max_seq_len: int, scale: float, partition_size: int = 1024,
+               portable: bool = False, flags: int = 0, stream=None):
+    """``pa_decode_kv4``: the step of :func:`decode` over a 4-bit cache."""
+    _done(_binding().decode_kv4(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
+                                 out, workspace, max_seq_len, scale, partition_size,
+                                 _flags(portable, False, flags), _handle(stream)), "pa_decode_kv4")
     return out

@@ -12,6 +12,7 @@
 // do not leave it.
 #include <Python.h>
 
+#include <cstring>
 #include <exception>
 #include <initializer_list>
 #include <string>
@@ -73,6 +74,14 @@ struct Args {
       throw Refused(std::string(name) + " must be a number");
     }
     return static_cast<float>(v);
+  }
+  // a bytes object of at most `most` bytes; its length
+  int64_t bytes(const char* name, uint8_t* to, int64_t most) {
+    PyObject* o = next();
+    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) > most)
+      throw Refused(std::string(name) + " must be at most " + std::to_string(most) + " bytes");
+    std::memcpy(to, PyBytes_AS_STRING(o), static_cast<size_t>(PyBytes_GET_SIZE(o)));
+    return PyBytes_GET_SIZE(o);
   }
   bool flag() {
     const int v = PyObject_IsTrue(next());
@@ -166,6 +175,29 @@ Cache caches(const at::Tensor& k, const at::Tensor& v, bool split_x) {
   return c;
 }
 
+// Shapes of the pools of a 4-bit cache: codes [NB, Hkv, BS, D / 2], scales [NB, Hkv,
+// BS, D / group, 2].
+struct Kv4 {
+  Cache c;
+  int32_t group;
+};
+Kv4 kv4_pools(const at::Tensor& k, const at::Tensor& v, const at::Tensor& ks,
+              const at::Tensor& vs) {
+  require(k.dim() == 4 && k.scalar_type() == at::kByte && v.scalar_type() == at::kByte,
+          "k_cache and v_cache must be uint8 [NB, Hkv, BS, D / 2]");
+  require(v.sizes() == k.sizes(), "v_cache must match k_cache");
+  Kv4 x;
+  x.c = {dim32(k.size(0)), dim32(k.size(1)), dim32(k.size(2)), dim32(k.size(3) * 2)};
+  require(ks.dim() == 5 && ks.size(0) == k.size(0) && ks.size(1) == k.size(1) &&
+              ks.size(2) == k.size(2) && ks.size(4) == 2 && ks.size(3) >= 1 &&
+              x.c.dim % ks.size(3) == 0,
+          "k_scales must be [NB, Hkv, BS, D / group, 2]");
+  require(vs.sizes() == ks.sizes() && vs.scalar_type() == ks.scalar_type(),
+          "v_scales must match k_scales");
+  x.group = static_cast<int32_t>(x.c.dim / ks.size(3));
+  return x;
+}
+
 void status_word(const at::Tensor* status) {
   if (status)
     require(status->scalar_type() == at::kInt && status->numel() >= 1, "status must be int32");
@@ -218,7 +250,9 @@ int plan_step(Args& in) {
                       addr<int64_t>(slots), addr<int32_t>(left), addr<int32_t>(status), stream);
 }
 
-int qk_norm_rope(Args& in) {
+// qk_norm_rope and, with several axes, qk_norm_rope_axes
+template <bool kAxes>
+int norm_rope(Args& in) {
   const at::Tensor& q = in.tensor("q");
   const at::Tensor& k = in.tensor("k");
   const at::Tensor& v = in.tensor("v");
@@ -241,6 +275,14 @@ int qk_norm_rope(Args& in) {
   const bool split_x = in.flag();
   const at::Tensor* status = in.maybe("status");
   cudaStream_t stream = in.stream(q);
+  pa_rope_axes_t axes{1, {}};
+  int64_t pairs = 0;
+  if (kAxes) {
+    pairs = in.bytes("axis_of", axes.axis_of, PA_ROPE_MAX_PAIRS);
+    require(!pos || (pos->dim() == 2 && pos->size(0) >= 1 && pos->size(0) <= PA_ROPE_MAX_AXES),
+            "positions must be int32 [axes, T] with 1 to 4 axes");
+    if (pos) axes.num_axes = dim32(pos->size(0));
+  }
   require(q.dim() == 3 && k.dim() == 3, "q must be [T, Hq, D] and k, v [T, Hkv, D]");
   const int64_t T = q.size(0), hq = q.size(1), d = q.size(2), hkv = k.size(1);
   for (const at::Tensor* t : {&k, &v}) {
@@ -260,7 +302,12 @@ int qk_norm_rope(Args& in) {
             "q, k, v, weights, caches and outputs must share one dtype");
   require(q_out.sizes() == q.sizes(), "q_out must be [T, Hq, D]");
   require(slots.scalar_type() == at::kLong && is(slots, {T}), "slots must be int64 [T]");
-  require(!pos || (pos->scalar_type() == at::kInt && is(*pos, {T})), "positions must be int32 [T]");
+  if (kAxes)
+    require(!pos || (pos->scalar_type() == at::kInt && pos->size(1) == T),
+            "positions must be int32 [axes, T]");
+  else
+    require(!pos || (pos->scalar_type() == at::kInt && is(*pos, {T})),
+            "positions must be int32 [T]");
   require(!qw == !kw, "give both weights or neither");
   for (const at::Tensor* t : {qw, kw}) require(!t || is(*t, {d}), "weights must be [D]");
   for (const at::Tensor* t : {k_out, v_out})
@@ -271,6 +318,7 @@ int qk_norm_rope(Args& in) {
     p.max_position = dim32(cos_sin->size(0));
     p.rotary_dim = dim32(cos_sin->size(1));
   }
+  require(!kAxes || pairs == p.rotary_dim / 2, "axis_of must name an axis for each pair");
   require(!k_cache == !v_cache, "give both caches or neither");
   if (k_cache) {
     const Cache c = caches(*k_cache, *v_cache, split_x);
@@ -290,6 +338,11 @@ int qk_norm_rope(Args& in) {
   p.v_stride = v.stride(0);
   p.dtype = dtype_code(q);
   p.flags = (interleaved ? PA_ROPE_INTERLEAVED : 0) | (split_x ? PA_FLAG_SPLIT_X : 0);
+  if (kAxes)
+    return pa_qk_norm_rope_axes(&p, &axes, addr(q), addr(k), addr(v), addr(qw), addr(kw),
+                                addr<float>(cos_sin), addr<int32_t>(pos), addr<int64_t>(slots),
+                                addr(q_out), addr(k_out), addr(v_out), addr(k_cache),
+                                addr(v_cache), addr<int32_t>(status), stream);
   return pa_qk_norm_rope(&p, addr(q), addr(k), addr(v), addr(qw), addr(kw), addr<float>(cos_sin),
                          addr<int32_t>(pos), addr<int64_t>(slots), addr(q_out), addr(k_out),
                          addr(v_out), addr(k_cache), addr(v_cache), addr<int32_t>(status), stream);
@@ -406,6 +459,131 @@ int prefill_window(Args& in) {
                            stream);
 }
 
+int store_kv4(Args& in) {
+  const at::Tensor& k = in.tensor("k");
+  const at::Tensor& v = in.tensor("v");
+  const at::Tensor& slots = in.tensor("slots");
+  const at::Tensor& kc = in.tensor("k_cache");
+  const at::Tensor& vc = in.tensor("v_cache");
+  const at::Tensor& ks = in.tensor("k_scales");
+  const at::Tensor& vs = in.tensor("v_scales");
+  const at::Tensor* k_out = in.maybe("k_out");
+  const at::Tensor* v_out = in.maybe("v_out");
+  const at::Tensor* status = in.maybe("status");
+  cudaStream_t stream = in.stream(k);
+  require(v.device() == k.device(), "k and v must be on one device");
+  same_device(k, {{"slots", &slots}, {"k_cache", &kc}, {"v_cache", &vc}, {"k_scales", &ks},
+                  {"v_scales", &vs}, {"k_out", k_out}, {"v_out", v_out}, {"status", status}});
+  status_word(status);
+  const Kv4 x = kv4_pools(kc, vc, ks, vs);
+  require(k.dim() == 3 && k.size(1) == x.c.heads && k.size(2) == x.c.dim && v.sizes() == k.sizes(),
+          "k and v must be [T, Hkv, D] with the caches' heads and head_dim");
+  const int64_t T = k.size(0), d = k.size(2);
+  for (const at::Tensor* t : {&k, &v})
+    require((t->stride(2) == 1 || d == 1) && (t->stride(1) == d || t->size(1) == 1),
+            "heads must be contiguous within a row");
+  for (const at::Tensor* t : {&v, &ks, k_out, v_out})
+    require(!t || t->scalar_type() == k.scalar_type(),
+            "k, v, the scales and outputs must share one dtype");
+  for (const at::Tensor* t : {k_out, v_out})
+    require(!t || t->sizes() == k.sizes(), "k_out and v_out must be [T, Hkv, D]");
+  require(slots.scalar_type() == at::kLong && is(slots, {T}), "slots must be int64 [T]");
+  pa_store_kv4_params_t p{};
+  p.num_tokens = dim32(T);
+  p.num_kv_heads = x.c.heads;
+  p.head_dim = x.c.dim;
+  p.block_size = x.c.block_size;
+  p.num_blocks = x.c.blocks;
+  p.group_size = x.group;
+  p.k_stride = k.stride(0);
+  p.v_stride = v.stride(0);
+  p.dtype = dtype_code(k);
+  return pa_store_kv4(&p, addr(k), addr(v), addr<int64_t>(slots), addr(kc), addr(vc), addr(ks),
+                      addr(vs), addr(k_out), addr(v_out), addr<int32_t>(status), stream);
+}
+
+int load_kv4(Args& in) {
+  const at::Tensor& kc = in.tensor("k_cache");
+  const at::Tensor& vc = in.tensor("v_cache");
+  const at::Tensor& ks = in.tensor("k_scales");
+  const at::Tensor& vs = in.tensor("v_scales");
+  const at::Tensor& bt = in.tensor("block_tables");
+  const at::Tensor& sl = in.tensor("seq_lens");
+  const at::Tensor& to = in.tensor("out_tables");
+  const at::Tensor& k_out = in.tensor("k_out");
+  const at::Tensor& v_out = in.tensor("v_out");
+  pa_load_kv4_params_t p{};
+  p.max_seq_len = in.i32("max_seq_len");
+  const at::Tensor* status = in.maybe("status");
+  cudaStream_t stream = in.stream(kc);
+  same_device(kc, {{"k_cache", &kc}, {"v_cache", &vc}, {"k_scales", &ks}, {"v_scales", &vs},
+                   {"block_tables", &bt}, {"seq_lens", &sl}, {"out_tables", &to},
+                   {"k_out", &k_out}, {"v_out", &v_out}, {"status", status}});
+  status_word(status);
+  are_int32({{"block_tables", &bt}, {"seq_lens", &sl}, {"out_tables", &to}});
+  const Kv4 x = kv4_pools(kc, vc, ks, vs);
+  const Cache w = caches(k_out, v_out, false);
+  require(w.heads == x.c.heads && w.block_size == x.c.block_size && w.dim == x.c.dim,
+          "k_out and v_out must have the 4-bit caches' heads, block size and head_dim");
+  require(k_out.scalar_type() == ks.scalar_type(), "the scales and outputs must share one dtype");
+  require(bt.dim() == 2 && to.dim() == 2 && to.size(0) == bt.size(0) && is(sl, {bt.size(0)}),
+          "block_tables and out_tables must be [B, ..] and seq_lens [B]");
+  p.num_seqs = dim32(bt.size(0));
+  p.num_kv_heads = x.c.heads;
+  p.head_dim = x.c.dim;
+  p.block_size = x.c.block_size;
+  p.num_blocks = x.c.blocks;
+  p.max_blocks_per_seq = dim32(bt.size(1));
+  p.num_out_blocks = w.blocks;
+  p.max_out_blocks_per_seq = dim32(to.size(1));
+  p.group_size = x.group;
+  p.dtype = dtype_code(ks);
+  return pa_load_kv4(&p, addr(kc), addr(vc), addr(ks), addr(vs), addr<int32_t>(bt),
+                     addr<int32_t>(sl), addr<int32_t>(to), addr(k_out), addr(v_out),
+                     addr<int32_t>(status), stream);
+}
+
+int decode_kv4(Args& in) {
+  const at::Tensor& q = in.tensor("q");
+  const at::Tensor& kc = in.tensor("k_cache");
+  const at::Tensor& vc = in.tensor("v_cache");
+  const at::Tensor& ks = in.tensor("k_scales");
+  const at::Tensor& vs = in.tensor("v_scales");
+  const at::Tensor& bt = in.tensor("block_tables");
+  const at::Tensor& sl = in.tensor("seq_lens");
+  const at::Tensor& out = in.tensor("out");
+  const at::Tensor& ws = in.tensor("workspace");
+  pa_params_t p{};
+  p.max_seq_len = in.i32("max_seq_len");
+  p.scale = in.f32("scale");
+  p.partition_size = in.i32("partition_size");
+  p.flags = in.i32("flags");
+  cudaStream_t stream = in.stream(q);
+  same_device(q, {{"q", &q}, {"k_cache", &kc}, {"v_cache", &vc}, {"k_scales", &ks},
+                  {"v_scales", &vs}, {"block_tables", &bt}, {"seq_lens", &sl}, {"out", &out},
+                  {"workspace", &ws}});
+  are_int32({{"block_tables", &bt}, {"seq_lens", &sl}});
+  const Kv4 x = kv4_pools(kc, vc, ks, vs);
+  require(q.dim() == 3 && q.size(2) == x.c.dim, "q must be [B, Hq, D] with the caches' head_dim");
+  require(q.scalar_type() == ks.scalar_type(), "q and the scales must share one dtype");
+  require(out.sizes() == q.sizes(), "out must have q's shape");
+  require(bt.dim() == 2 && bt.size(0) == q.size(0) && is(sl, {q.size(0)}),
+          "block_tables must be [B, ..] and seq_lens [B]");
+  p.num_seqs = dim32(q.size(0));
+  p.num_heads = dim32(q.size(1));
+  p.num_kv_heads = x.c.heads;
+  p.head_dim = x.c.dim;
+  p.block_size = x.c.block_size;
+  p.num_blocks = x.c.blocks;
+  p.max_blocks_per_seq = dim32(bt.size(1));
+  p.kv_dtype = dtype_code(q);
+  p.out_dtype = dtype_code(out);
+  const pa_kv4_t kv4{x.group};
+  return pa_decode_kv4(&p, &kv4, addr(q), addr(kc), addr(vc), addr(ks), addr(vs),
+                       addr<int32_t>(bt), addr<int32_t>(sl), addr(ws), ws.nbytes(), addr(out),
+                       stream);
+}
+
 // ---- the module -----------------------------------------------------------------
 
 PyObject* refuse(int status, const char* why) {
@@ -446,10 +624,14 @@ constexpr PyCFunction fn() {
 
 PyMethodDef methods[] = {
     {"plan_step", fn<plan_step>(), METH_FASTCALL, nullptr},
-    {"qk_norm_rope", fn<qk_norm_rope>(), METH_FASTCALL, nullptr},
+    {"qk_norm_rope", fn<norm_rope<false>>(), METH_FASTCALL, nullptr},
+    {"qk_norm_rope_axes", fn<norm_rope<true>>(), METH_FASTCALL, nullptr},
     {"decode_window", fn<decode_window>(), METH_FASTCALL, nullptr},
     {"decode_prefix", fn<decode_prefix>(), METH_FASTCALL, nullptr},
     {"prefill_window", fn<prefill_window>(), METH_FASTCALL, nullptr},
+    {"store_kv4", fn<store_kv4>(), METH_FASTCALL, nullptr},
+    {"load_kv4", fn<load_kv4>(), METH_FASTCALL, nullptr},
+    {"decode_kv4", fn<decode_kv4>(), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, "The exception class that refusals raise."},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -216,6 +216,37 @@ bool own_applicable(const pa_params_t* p);
 cudaError_t launch_own(const KernelArgs& a, const JoinList& prefix, pa_dtype_t t, bool pdl,
                        cudaStream_t s);
 
+// Decode over the 4-bit cache (pa_kv4.cuh): query heads of a KV head are taken up
+// to kKv4Heads at a time.
+constexpr int kKv4Heads = 8;
+struct Kv4Args {
+  const void* q;
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const void* k_pairs;
+  const void* v_pairs;
+  const int32_t* block_tables;
+  const int32_t* lens;
+  void* out;
+  float* part_max;
+  float* part_sum;
+  float* part_out;
+  int32_t* status;
+  int32_t num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int32_t max_blocks_per_seq, max_len;
+  int32_t part_size, num_parts;  // tokens of a part; 1 part: results go to out
+  int32_t group, head_groups;    // query heads of a KV head; ceil(group / kKv4Heads)
+  int32_t group_size;            // elements of a head row that share a scale
+  int32_t block_shift;           // log2 of block_size, or -1
+  int32_t out_dtype;
+  float scale_log2;
+};
+cudaError_t launch_kv4_generic_f32(const Kv4Args& a, cudaStream_t s);
+cudaError_t launch_kv4_generic_bf16(const Kv4Args& a, cudaStream_t s);
+cudaError_t launch_kv4_generic_f16(const Kv4Args& a, cudaStream_t s);
+// What the calls on the 4-bit cache take in common.
+pa_status_t check_kv4(pa_dtype_t dtype, int head_dim, int group_size);
+
 // Launchers return cudaSuccess or the launch error.
 cudaError_t launch_generic_f32(const KernelArgs& a, bool v2, cudaStream_t s);
 cudaError_t launch_generic_bf16(const KernelArgs& a, bool v2, cudaStream_t s);

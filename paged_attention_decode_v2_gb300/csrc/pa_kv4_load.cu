@@ -1,0 +1,204 @@
+// pa_kv4_load.cu -- pa_load_kv4: pages of the 4-bit cache widened into pages of the
+// element type, for the calls that take such pages (pa_prefill, pa_prefill_window).
+//
+// value = c * scale + minimum, one float32 operation, rounded once.  A lane takes
+// eight codes (4 bytes) to eight elements (16 bytes, 32 in float32), so that a
+// warp's loads and stores are whole lines; a page is one run of memory on both
+// sides.  CTAs walk the list of pages that the sequences have (pa_kv4.cuh).
+// Bound by memory, mostly by the 16-bit pages written.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_runtime_api.h>
+
+#include "pa_kv4.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kNT = 256;
+constexpr int kUnroll = 4;  // loads of a lane in flight
+
+struct LoadArgs {
+  const uint8_t* codes[2];  // k, v
+  const void* pairs[2];
+  void* out[2];
+  const int32_t* tables;
+  const int32_t* lens;
+  const int32_t* out_tables;
+  int32_t* status;
+  int32_t num_seqs, block_size, num_blocks, num_out_blocks, width, out_width, max_len;
+  int32_t page;         // elements of a page: Hkv * block_size * D
+  int32_t group_shift;  // log2 of the group's size
+};
+
+struct Pages {
+  const LoadArgs& a;
+  __device__ __forceinline__ bool ok(int32_t L) const {
+    return L >= 0 && L <= a.max_len &&
+           L <= static_cast<int64_t>(min(a.width, a.out_width)) * a.block_size;
+  }
+  __device__ __forceinline__ uint32_t operator()(int b) const {
+    const int32_t L = __ldg(a.lens + b);
+    return ok(L) ? (L + a.block_size - 1) / a.block_size : 0;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void put8(T* p, const float (&f)[8]) {
+  if constexpr (std::is_same<T, float>::value) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = bits16(round16(f[2 * i], static_cast<T*>(nullptr))) |
+             static_cast<uint32_t>(bits16(round16(f[2 * i + 1], static_cast<T*>(nullptr)))) << 16;
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kNT) pa_load_kv4_kernel(const LoadArgs a) {
+  extern __shared__ uint32_t start[];
+  const Pages pages{a};
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.num_seqs; b += kNT)
+      if (!pages.ok(__ldg(a.lens + b))) set_status(a.status, PA_ERR_BAD_SEQ_LEN);
+  const uint32_t items = list_build(start, a.num_seqs, pages);
+  const int32_t units = a.page / 8;
+  for (uint32_t i = blockIdx.x; i < 2 * items; i += gridDim.x) {
+    const int kind = i & 1;
+    int b;
+    uint32_t j;
+    list_find(start, a.num_seqs, pages, i >> 1, b, j);
+    const int32_t from = __ldg(a.tables + static_cast<int64_t>(b) * a.width + j);
+    const int32_t to = __ldg(a.out_tables + static_cast<int64_t>(b) * a.out_width + j);
+    const bool from_ok = from >= 0 && from < a.num_blocks;
+    const bool to_ok = to >= 0 && to < a.num_out_blocks;
+    if ((!from_ok || !to_ok) && threadIdx.x == 0) set_status(a.status, PA_ERR_BAD_BLOCK_ID);
+    if (!to_ok) continue;
+    T* out = static_cast<T*>(a.out[kind]) + static_cast<int64_t>(to) * a.page;
+    const uint32_t* codes =
+        reinterpret_cast<const uint32_t*>(a.codes[kind]) + static_cast<int64_t>(from) * units;
+    const int64_t pair0 = static_cast<int64_t>(from) * (a.page >> a.group_shift);
+    for (int32_t u0 = threadIdx.x; u0 < units; u0 += kNT * kUnroll) {
+      uint32_t c[kUnroll];
+      float2 p[kUnroll];
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x) {
+        const int32_t u = u0 + x * kNT;
+        c[x] = 0;
+        p[x] = make_float2(qnan(), qnan());
+        if (from_ok && u < units) {
+          c[x] = __ldcs(codes + u);
+          p[x] = load_pair<T>(a.pairs[kind], pair0 + (u >> (a.group_shift - 3)));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x) {
+        const int32_t u = u0 + x * kNT;
+        if (u >= units) break;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          f[e] = fmaf(static_cast<float>(c[x] >> (4 * e) & 15), p[x].x, p[x].y);
+        put8(out + static_cast<int64_t>(u) * 8, f);
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const LoadArgs& a, int64_t most, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(2 * most, static_cast<int64_t>(sms) * 8);
+  pa_load_kv4_kernel<T>
+      <<<static_cast<unsigned>(grid), kNT, list_bytes(a.num_seqs), s>>>(a);
+  return cudaGetLastError();
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status_t pa_load_kv4(const pa_load_kv4_params_t* p, const void* k_codes,
+                                   const void* v_codes, const void* k_scales,
+                                   const void* v_scales, const int32_t* block_tables,
+                                   const int32_t* seq_lens, const int32_t* out_tables, void* k_out,
+                                   void* v_out, int32_t* status, cudaStream_t stream) {
+  using namespace pa;
+  if (!p || p->num_seqs < 0 || p->num_kv_heads < 1 || p->max_seq_len < 0) return PA_ERR_INVALID_ARG;
+  if (p->block_size < 1 || p->num_blocks < 1 || p->num_out_blocks < 1) return PA_ERR_INVALID_ARG;
+  if (p->max_blocks_per_seq < 1 || p->max_out_blocks_per_seq < 1) return PA_ERR_INVALID_ARG;
+  if (pa_status_t st = check_kv4(p->dtype, p->head_dim, p->group_size)) return st;
+  if (p->num_seqs > 65535 || p->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  const int64_t pages = (static_cast<int64_t>(p->max_seq_len) + p->block_size - 1) / p->block_size;
+  if (pages > p->max_blocks_per_seq || pages > p->max_out_blocks_per_seq) return PA_ERR_INVALID_ARG;
+  // units of a page and pages of a call are counted in 31 bits
+  const double page = static_cast<double>(p->num_kv_heads) * p->block_size * p->head_dim;
+  const int64_t most = p->num_seqs * pages;
+  if (page + 8.0 * kNT * kUnroll >= 2147483648.0 || 2 * most + 65536 >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(p->max_seq_len) + p->block_size >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;
+  if (p->num_seqs == 0) return PA_OK;
+  if (!k_codes || !v_codes || !k_scales || !v_scales || !block_tables || !seq_lens ||
+      !out_tables || !k_out || !v_out)
+    return PA_ERR_INVALID_ARG;
+  for (const void* x : {k_codes, v_codes, k_scales, v_scales, static_cast<const void*>(k_out),
+                        static_cast<const void*>(v_out)})
+    if (!aligned(x, 16)) return PA_ERR_MISALIGNED;
+  if (!aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(out_tables, 4) ||
+      !aligned(status, 4))
+    return PA_ERR_MISALIGNED;
+  {
+    const double esz = p->dtype == PA_F32 ? 4 : 2, all = 4e18;
+    const auto size = [&](double bytes) { return static_cast<size_t>(std::min(bytes, all)); };
+    const size_t codes = size(page * p->num_blocks / 2);
+    const size_t pairs = size(page * p->num_blocks / p->group_size * 2 * esz);
+    const size_t wide = size(page * p->num_out_blocks * esz);
+    const size_t B = static_cast<size_t>(p->num_seqs);
+    const Range r[] = {{k_codes, codes, false}, {v_codes, codes, false}, {k_scales, pairs, false},
+                       {v_scales, pairs, false},
+                       {block_tables, B * p->max_blocks_per_seq * 4, false},
+                       {seq_lens, B * 4, false},
+                       {out_tables, B * p->max_out_blocks_per_seq * 4, false},
+                       {k_out, wide, true}, {v_out, wide, true}, {status, 4, true}};
+    if (outputs_overlap(r, sizeof r / sizeof r[0])) return PA_ERR_INVALID_ARG;
+  }
+  LoadArgs a{};
+  a.codes[0] = static_cast<const uint8_t*>(k_codes);
+  a.codes[1] = static_cast<const uint8_t*>(v_codes);
+  a.pairs[0] = k_scales;
+  a.pairs[1] = v_scales;
+  a.out[0] = k_out;
+  a.out[1] = v_out;
+  a.tables = block_tables;
+  a.lens = seq_lens;
+  a.out_tables = out_tables;
+  a.status = status;
+  a.num_seqs = p->num_seqs;
+  a.block_size = p->block_size;
+  a.num_blocks = p->num_blocks;
+  a.num_out_blocks = p->num_out_blocks;
+  a.width = p->max_blocks_per_seq;
+  a.out_width = p->max_out_blocks_per_seq;
+  a.max_len = p->max_seq_len;
+  a.page = static_cast<int32_t>(page);
+  a.group_shift = __builtin_ctz(p->group_size);
+  // no page at all: the lengths are still looked at
+  const int64_t grid = std::max<int64_t>(most, 1);
+  cudaError_t e;
+  switch (p->dtype) {
+    case PA_F32: e = launch<float>(a, grid, stream); break;
+    case PA_BF16: e = launch<__nv_bfloat16>(a, grid, stream); break;
+    default: e = launch<__half>(a, grid, stream); break;
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}

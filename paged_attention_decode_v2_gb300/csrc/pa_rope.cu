@@ -1,5 +1,6 @@
-// pa_rope.cu -- pa_qk_norm_rope: norm of each query and key head, rotation by
-// position, and the write of keys and values into the paged cache.
+// pa_rope.cu -- pa_qk_norm_rope and pa_qk_norm_rope_axes: norm of each query and
+// key head, rotation by position, and the write of keys and values into the paged
+// cache.
 //
 // Row t has R = Hq + 2 Hkv head rows of D elements: queries, keys, values.  D / 8
 // lanes hold a head row in registers, each lane four pairs of the rotation:
@@ -18,8 +19,14 @@
 // (277 MB) 47.5 us = 5.8 TB/s, 87 % of the copy rate (115 us with one lane per 16
 // bytes, pairs in two lanes and the set-up per head row); 32 rows of 32 / 8
 // heads of 128 2.5 us, a launch's latency.
+//
+// With several axes (time, height, width) pair j turns by the angle of its own
+// axis' position: a lane's four pairs read their cosines and sines in up to four
+// rows of the table, once per run.  Two bits a pair say which axis it has; they
+// are kernel parameters, a byte a lane.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime_api.h>
 
@@ -58,6 +65,13 @@ struct RopeArgs {
   int32_t q_runs, kv_runs;     // runs of a row t: queries; keys, and as many values
   int64_t items;
   float eps, weight_offset;
+};
+
+// Several axes: a row of positions for each, and the axes of the pairs, two bits
+// a pair, four pairs a byte.
+struct RopeAxesArgs : RopeArgs {
+  int32_t num_axes;
+  uint8_t axes[PA_ROPE_MAX_PAIRS / 4];
 };
 
 // Two floats in one 64-bit register, for the packed float32 instructions.
@@ -187,8 +201,9 @@ __device__ __forceinline__ void norm_rotate(F2 (&y)[4], const Lane& l, bool norm
 constexpr int kUnroll = 4;
 constexpr int kCtas = 32;
 
-template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
+template <typename T, int D, bool kInter, typename Args>
+__global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const Args a) {
+  constexpr bool kAxes = std::is_same<Args, RopeAxesArgs>::value;
   constexpr int X = 16 / sizeof(T);                   // elements of a split-x key group
   constexpr int LPR = D / 8;                          // lanes of a head row
   constexpr int kSide = 32 / LPR;                     // head rows side by side in a warp
@@ -204,6 +219,13 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
   const int k = static_cast<int>((item - t * per_row + t) % per_row);
   const int64_t slot = __ldg(a.slots + t);
   const int32_t pos = a.rot ? __ldg(a.positions + t) : 0;
+  int32_t other[3] = {0, 0, 0};                       // the positions on further axes
+  if constexpr (kAxes) {
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      if (a.rot && x + 1 < a.num_axes)
+        other[x] = __ldg(a.positions + static_cast<int64_t>(x + 1) * a.num_tokens + t);
+  }
   const int kind = k < a.q_runs ? 0 : k < a.q_runs + a.kv_runs ? 1 : 2;
   const int h0 = (kind == 0 ? k : kind == 1 ? k - a.q_runs : k - a.q_runs - a.kv_runs) * a.run;
   const int heads = kind == 0 ? a.num_heads : a.num_kv_heads;
@@ -230,7 +252,12 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
   };
   load(h0);
   if (slot == -1) return;                             // padding
-  const bool pos_ok = !a.rot || (pos >= 0 && pos < a.max_position);
+  bool pos_ok = !a.rot || (pos >= 0 && pos < a.max_position);
+  if constexpr (kAxes) {
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      pos_ok = pos_ok && (!a.rot || (other[x] >= 0 && other[x] < a.max_position));
+  }
   const bool slot_ok = !a.k_cache || (slot >= 0 && slot < a.pool);
   if (k == 0 && threadIdx.x % 32 == 0) {
     if (!slot_ok) set_status(a.status, PA_ERR_BAD_SLOT);
@@ -240,7 +267,22 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
   const bool norm = a.qw != nullptr;
   if (kind < 2) {
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (rotates && pos_ok) {
+    if (kAxes && rotates && pos_ok) {
+      if constexpr (kAxes) {
+        // pairs j0 .. j0 + 3, each on its axis' row
+        const unsigned of = a.axes[lane];
+        const float* at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned x = of >> (2 * i) & 3;
+          const int32_t p = x == 0 ? pos : x == 1 ? other[0] : x == 2 ? other[1] : other[2];
+          at[i] = a.cos_sin + static_cast<int64_t>(p) * a.rot + j0 + i;
+        }
+        c = make_float4(__ldg(at[0]), __ldg(at[1]), __ldg(at[2]), __ldg(at[3]));
+        s = make_float4(__ldg(at[0] + half), __ldg(at[1] + half), __ldg(at[2] + half),
+                        __ldg(at[3] + half));
+      }
+    } else if (rotates && pos_ok) {
       const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot + j0;
       c = __ldg(reinterpret_cast<const float4*>(row));
       s = __ldg(reinterpret_cast<const float4*>(row + half));
@@ -324,8 +366,8 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_rope_kernel(const RopeArgs a) {
   }
 }
 
-template <typename T, int D, bool kInter>
-cudaError_t launch_i(RopeArgs a, int sms, cudaStream_t s) {
+template <typename T, int D, bool kInter, typename Args>
+cudaError_t launch_i(Args a, int sms, cudaStream_t s) {
   constexpr int kWarps = kNT / 32;
   constexpr int kSide = 32 / (D / 8);
   // two loads' worth of head rows a run, fewer while the runs do not fill the
@@ -339,18 +381,18 @@ cudaError_t launch_i(RopeArgs a, int sms, cudaStream_t s) {
   a.kv_runs = (a.num_kv_heads + a.run - 1) / a.run;
   a.items = static_cast<int64_t>(a.num_tokens) * (a.q_runs + 2 * a.kv_runs);
   if (a.items + kWarps >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  pa_rope_kernel<T, D, kInter>
+  pa_rope_kernel<T, D, kInter, Args>
       <<<static_cast<unsigned>((a.items + kWarps - 1) / kWarps), kNT, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t launch_d(const RopeArgs& a, int sms, cudaStream_t s) {
+template <typename T, int D, typename Args>
+cudaError_t launch_d(const Args& a, int sms, cudaStream_t s) {
   return a.interleaved ? launch_i<T, D, true>(a, sms, s) : launch_i<T, D, false>(a, sms, s);
 }
 
-template <typename T>
-cudaError_t launch_t(const RopeArgs& a, int D, int sms, cudaStream_t s) {
+template <typename T, typename Args>
+cudaError_t launch_t(const Args& a, int D, int sms, cudaStream_t s) {
   switch (D) {
     case 64: return launch_d<T, 64>(a, sms, s);
     case 128: return launch_d<T, 128>(a, sms, s);
@@ -358,18 +400,23 @@ cudaError_t launch_t(const RopeArgs& a, int D, int sms, cudaStream_t s) {
   }
 }
 
+template <typename Args>
+cudaError_t launch(const Args& a, pa_dtype_t dtype, int D, int sms, cudaStream_t s) {
+  switch (dtype) {
+    case PA_F32: return launch_t<float>(a, D, sms, s);
+    case PA_BF16: return launch_t<__nv_bfloat16>(a, D, sms, s);
+    default: return launch_t<__half>(a, D, sms, s);
+  }
+}
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-}  // namespace
-}  // namespace pa
-
-extern "C" pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q, const void* k,
-                                       const void* v, const void* q_weight, const void* k_weight,
-                                       const float* cos_sin, const int32_t* positions,
-                                       const int64_t* slots, void* q_out, void* k_out,
-                                       void* v_out, void* k_cache, void* v_cache, int32_t* status,
-                                       cudaStream_t stream) {
-  using namespace pa;
+// Both calls; `axes` null: one position a row.
+pa_status_t norm_rope(const pa_rope_params_t* p, const pa_rope_axes_t* axes, const void* q,
+                      const void* k, const void* v, const void* q_weight, const void* k_weight,
+                      const float* cos_sin, const int32_t* positions, const int64_t* slots,
+                      void* q_out, void* k_out, void* v_out, void* k_cache, void* v_cache,
+                      int32_t* status, cudaStream_t stream) {
   if (!p || p->num_tokens < 0 || p->num_heads < 1 || p->num_kv_heads < 1) return PA_ERR_INVALID_ARG;
   if (p->block_size < 1 || p->num_blocks < 1) return PA_ERR_INVALID_ARG;
   if (p->flags & ~(PA_ROPE_INTERLEAVED | PA_FLAG_SPLIT_X)) return PA_ERR_INVALID_ARG;
@@ -377,7 +424,12 @@ extern "C" pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q,
   if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return PA_ERR_UNSUPPORTED;
   if (p->rotary_dim < 0 || p->rotary_dim > p->head_dim || p->rotary_dim % 16)
     return PA_ERR_INVALID_ARG;
-  if (p->rotary_dim && (p->max_position < 1 || !cos_sin || !positions)) return PA_ERR_INVALID_ARG;
+  if (p->rotary_dim && p->max_position < 1) return PA_ERR_INVALID_ARG;
+  if (axes) {
+    if (axes->num_axes < 1 || axes->num_axes > PA_ROPE_MAX_AXES) return PA_ERR_INVALID_ARG;
+    for (int j = 0; j < p->rotary_dim / 2; ++j)
+      if (axes->axis_of[j] >= axes->num_axes) return PA_ERR_INVALID_ARG;
+  }
   if (p->num_heads > 65535 || p->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   if (!(p->eps >= 0.f)) return PA_ERR_INVALID_ARG;
   const int64_t D = p->head_dim, esz = p->dtype == PA_F32 ? 4 : 2;
@@ -387,6 +439,7 @@ extern "C" pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q,
     return PA_ERR_INVALID_ARG;
   if (p->num_tokens == 0) return PA_OK;
   if (!q || !k || !v || !slots || !q_out) return PA_ERR_INVALID_ARG;
+  if (p->rotary_dim && (!cos_sin || !positions)) return PA_ERR_INVALID_ARG;
   if (!q_weight != !k_weight || !k_cache != !v_cache) return PA_ERR_INVALID_ARG;
   if (p->num_tokens > 1 &&
       ((p->q_stride * esz) % 16 || (p->k_stride * esz) % 16 || (p->v_stride * esz) % 16))
@@ -424,7 +477,8 @@ extern "C" pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q,
         {k_weight, D1, false},
         {p->rotary_dim ? cos_sin : nullptr,
          static_cast<size_t>(p->max_position) * p->rotary_dim * 4, false},
-        {p->rotary_dim ? positions : nullptr, static_cast<size_t>(T) * 4, false},
+        {p->rotary_dim ? positions : nullptr, static_cast<size_t>(T) * 4 * (axes ? axes->num_axes : 1),
+         false},
         {slots, static_cast<size_t>(T) * 8, false},
         {q_out, rows(nq, nq), true},
         {k_out, rows(nk, nk), true},
@@ -466,10 +520,42 @@ extern "C" pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q,
   a.weight_offset = p->weight_offset;
   const int sms = sm100_num_sms();
   cudaError_t e;
-  switch (p->dtype) {
-    case PA_F32: e = launch_t<float>(a, p->head_dim, sms, stream); break;
-    case PA_BF16: e = launch_t<__nv_bfloat16>(a, p->head_dim, sms, stream); break;
-    default: e = launch_t<__half>(a, p->head_dim, sms, stream); break;
+  if (axes) {
+    RopeAxesArgs x{};
+    static_cast<RopeArgs&>(x) = a;
+    x.num_axes = axes->num_axes;
+    for (int i = 0; i < p->rotary_dim / 2; ++i)
+      x.axes[i / 4] = static_cast<uint8_t>(x.axes[i / 4] | axes->axis_of[i] << (2 * (i % 4)));
+    e = launch(x, p->dtype, p->head_dim, sms, stream);
+  } else {
+    e = launch(a, p->dtype, p->head_dim, sms, stream);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+pa_status_t pa_qk_norm_rope(const pa_rope_params_t* p, const void* q, const void* k,
+                            const void* v, const void* q_weight, const void* k_weight,
+                            const float* cos_sin, const int32_t* positions, const int64_t* slots,
+                            void* q_out, void* k_out, void* v_out, void* k_cache, void* v_cache,
+                            int32_t* status, cudaStream_t stream) {
+  return pa::norm_rope(p, nullptr, q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out,
+                       k_out, v_out, k_cache, v_cache, status, stream);
+}
+
+pa_status_t pa_qk_norm_rope_axes(const pa_rope_params_t* p, const pa_rope_axes_t* axes,
+                                 const void* q, const void* k, const void* v,
+                                 const void* q_weight, const void* k_weight, const float* cos_sin,
+                                 const int32_t* positions, const int64_t* slots, void* q_out,
+                                 void* k_out, void* v_out, void* k_cache, void* v_cache,
+                                 int32_t* status, cudaStream_t stream) {
+  if (!axes) return PA_ERR_INVALID_ARG;
+  return pa::norm_rope(p, axes, q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out,
+                       k_out, v_out, k_cache, v_cache, status, stream);
+}
+
+}  // extern "C"
