@@ -238,9 +238,15 @@ struct Kv4Args {
   int32_t group, head_groups;    // query heads of a KV head; ceil(group / kKv4Heads)
   int32_t group_size;            // elements of a head row that share a scale
   int32_t block_shift;           // log2 of block_size, or -1
+  int32_t paged16;               // block_size is a multiple of 16
   int32_t out_dtype;
   float scale_log2;
 };
+// CTAs of the tensor-core kernel that are resident on an SM.
+constexpr int kv4_tc_ctas(int head_dim) { return head_dim == 256 ? 3 : 4; }
+// `items`: at least the (part, KV head, query head group) triples that exist
+cudaError_t launch_kv4_tc_bf16(const Kv4Args& a, int64_t items, cudaStream_t s);
+cudaError_t launch_kv4_tc_f16(const Kv4Args& a, int64_t items, cudaStream_t s);
 cudaError_t launch_kv4_generic_f32(const Kv4Args& a, cudaStream_t s);
 cudaError_t launch_kv4_generic_bf16(const Kv4Args& a, cudaStream_t s);
 cudaError_t launch_kv4_generic_f16(const Kv4Args& a, cudaStream_t s);

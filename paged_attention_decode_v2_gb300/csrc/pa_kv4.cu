@@ -39,24 +39,24 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
 
 int64_t parts_of(int64_t len, int64_t size) { return std::max<int64_t>(1, (len + size - 1) / size); }
 
-// Parts of the longest of `seqs` sequences.  Room for kRoom work items -- (part,
-// KV head, eight query heads) -- at a time, three CTAs on each of 152 SMs.
+// Parts of the longest of `seqs` sequences.  There is room for some work items --
+// (part, KV head, eight query heads) -- at a time, a CTA each on 152 SMs.
 //   * Many sequences, two rounds of items undivided: partition_size.
 //   * Fewer: the split that takes the least time, as for the windowed decode: a
 //     round costs as much as its part is long plus a start, a partial the join.
-constexpr int64_t kRoom = 456;
-constexpr int64_t kMostParts = 512;
+int64_t room_for(const pa_params_t* p) { return 152 * kv4_tc_ctas(p->head_dim); }
+constexpr int64_t kMostParts = 640;
 
 int64_t parts_for(const pa_params_t* p, int64_t seqs) {
   constexpr int64_t kStart = 128, kJoin = 2, kLeast = 64;
-  const int64_t len = p->max_seq_len;
+  const int64_t len = p->max_seq_len, room = room_for(p);
   const int64_t pairs = seqs * p->num_kv_heads * head_groups(p);
-  if (pairs >= 2 * kRoom) return parts_of(len, p->partition_size);
+  if (pairs >= 2 * room) return parts_of(len, p->partition_size);
   // the cost of n parts is a line in len: n never falls as len grows
   int64_t parts = 1;
   double best = -1;
   for (int64_t n = 1; n <= kMostParts && (n == 1 || n * kLeast <= len); ++n) {
-    const double rounds = static_cast<double>((pairs * n + kRoom - 1) / kRoom);
+    const double rounds = static_cast<double>((pairs * n + room - 1) / room);
     const double cost = rounds / n * len + rounds * kStart + (n > 1 ? n * kJoin : 0);
     if (best < 0 || cost < best) {
       best = cost;
@@ -81,7 +81,7 @@ size_t pa_kv4_workspace_size(const pa_params_t* p, const pa_kv4_t* kv4) {
   if (check(p, kv4) != PA_OK) return 0;
   size_t most = layout_of(p, p->num_seqs).total;
   // fewer sequences may have more parts in all
-  for (int64_t s = 1; s < p->num_seqs && s * p->num_kv_heads < 2 * kRoom; ++s)
+  for (int64_t s = 1; s < p->num_seqs && s * p->num_kv_heads < 2 * room_for(p); ++s)
     most = std::max(most, layout_of(p, s).total);
   return most;
 }
@@ -126,6 +126,7 @@ pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void*
   a.head_groups = static_cast<int32_t>(head_groups(p));
   a.group_size = kv4->group_size;
   a.block_shift = (p->block_size & (p->block_size - 1)) ? -1 : __builtin_ctz(p->block_size);
+  a.paged16 = p->block_size % 16 == 0;
   a.out_dtype = p->out_dtype;
   a.scale_log2 = p->scale * 1.442695040888963407360f;
   // parts of whole tiles; evened out over the longest sequence
@@ -133,12 +134,19 @@ pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void*
   a.part_size = static_cast<int32_t>(
       std::max<int64_t>(64, ((p->max_seq_len + parts - 1) / parts + 63) / 64 * 64));
   a.num_parts = static_cast<int32_t>(parts_of(p->max_seq_len, a.part_size));
+  // work items, counted in 31 bits by the tensor-core kernel
+  const double items = static_cast<double>(a.num_seqs) * a.num_parts * a.num_kv_heads *
+                       a.head_groups;
+  const bool tc = p->kv_dtype != PA_F32 && !(p->flags & PA_FLAG_PORTABLE) && items < 2e9 &&
+                  sm100_num_sms() > 0;
   cudaError_t e;
-  switch (p->kv_dtype) {
-    case PA_F32: e = launch_kv4_generic_f32(a, stream); break;
-    case PA_BF16: e = launch_kv4_generic_bf16(a, stream); break;
-    default: e = launch_kv4_generic_f16(a, stream); break;
-  }
+  if (tc)
+    e = (p->kv_dtype == PA_BF16 ? launch_kv4_tc_bf16 : launch_kv4_tc_f16)(
+        a, static_cast<int64_t>(items), stream);
+  else
+    e = (p->kv_dtype == PA_F32    ? launch_kv4_generic_f32
+         : p->kv_dtype == PA_BF16 ? launch_kv4_generic_bf16
+                                  : launch_kv4_generic_f16)(a, stream);
   if (e != cudaSuccess) return PA_ERR_CUDA;
   if (a.num_parts == 1) return PA_OK;
   JoinArgs j{};
