@@ -11,7 +11,8 @@
 // float32, once per token, group and head.  With v = s (c - 8) + (m + 8 s),
 //   sum_t p v = sum_t (p s) c - 8 sum_t (p s) + sum_t p (m + 8 s),
 // so p s is what the second MMA multiplies by codes; its own sum comes from an MMA
-// with rows of eights, the last sum is float32 on the CUDA cores.
+// with rows of eights, and the last sum from one of scales and minima by p.  Those
+// take p in two parts of 16 bits, and the keys' minima the sums of q in two or three.
 //   * A code in the low half of a byte, masked, is the f16 subnormal c 2^-24, in the
 //     high half c 2^-20: one mask makes two operands of a 32-bit word, and the powers
 //     of two leave with the scales.
@@ -63,8 +64,8 @@ struct Cfg {
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQ = D / 32 * 512;       // q fragments
   static constexpr int kOffQ = kRing;
-  static constexpr int kOffQs = kOffQ + kQ;                  // sums of q: [NCH][8]
-  static constexpr int kOffP = kOffQs + NCH * 8 * 4;         // weights: [warp][8][PP]
+  static constexpr int kOffQs = kOffQ + kQ;                  // sums of q: [D / 32][8]
+  static constexpr int kOffP = kOffQs + D / 32 * 8 * 4;      // weights: [warp][8][PP]
   static constexpr int kOffW = kOffP + kWarps * 8 * PP * 4;  // statistics: [4][warp][8]
   static constexpr int kOffList = kOffW + 4 * kWarps * 8 * 4;
   static constexpr int kCtas = kv4_tc_ctas(D);  // resident on an SM
@@ -80,6 +81,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes));
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
+}
 template <int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
@@ -91,14 +95,35 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// c (16 x 8, f32) += a (16 x 16) * b (16 x 8), f16
+// c (16 x 8, f32) += a (16 x 16) * b (16 x 8), f16 or bf16
+template <typename T>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from zero.
+template <typename T>
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                     uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
@@ -112,9 +137,52 @@ __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) <
 __device__ __forceinline__ int exponent(float x) {
   return (__float_as_int(x) >> 23 & 255) - 127;
 }
-__device__ __forceinline__ uint32_t f16x2(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Two floats rounded to T, and what the rounding left, rounded too.
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t split(float& x, float& y) {
+  const uint32_t h = pack<T>(x, y);
+  const float2 f = widen_pair<T>(h);
+  x -= f.x;
+  y -= f.y;
+  return h;
+}
+// Two floats as one operand of the packed instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 unpair(F2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ F2 mul2(F2 x, F2 y) {
+  F2 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
+  return v;
+}
+__device__ __forceinline__ float low_half(const __nv_bfloat16*, uint32_t w) {
+  return __uint_as_float(w << 16);
+}
+__device__ __forceinline__ float low_half(const __half*, uint32_t w) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+}
+// The scale of a pair.
+template <typename T>
+__device__ __forceinline__ float scale_of(uint32_t w) {
+  return low_half(static_cast<const T*>(nullptr), w);
 }
 
 // The N pairs of a row in shared memory (N words, a power of two).
@@ -150,6 +218,10 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
   using C = Cfg<D, GS>;
   constexpr int NCH = C::NCH, MT = C::MT, W = C::W, NP = C::NP, CH = C::CH;
   constexpr int kTiles = CH / 16;  // MMA tiles of a chunk's values
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr int kParts = kHalf ? 2 : 3;                  // of the sums of q
+  constexpr float kMinUp = kHalf ? 0x1p16f : 1.f;        // powers of two that keep f16
+  constexpr float kWeightUp = kHalf ? 0x1p7f : 1.f;      // operands in its range
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int bad_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -180,8 +252,9 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
     const int h0 = kvh * a.group + hg * kKv4Heads;
     const int32_t L = __ldg(a.lens + b);
     if (!kv4_len_ok(a, L) || L == 0) {
+      const int64_t row = static_cast<int64_t>(b) * a.num_heads + h0;
       for (int i = threadIdx.x; i < nh * D; i += kNT)
-        kv4_finish(a, b, h0 + i / D, 0, i % D, D, true, L, L != 0, 0.f, 1.f, 0.f);
+        store_out(a.out, row * D + i, a.out_dtype, L == 0 ? 0.f : qnan());
       continue;
     }
     const int32_t t0 = part * a.part_size, t1 = min(L, t0 + a.part_size);
@@ -203,10 +276,38 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
           page[mt] = __ldg(table + (a.block_shift >= 0 ? t >> a.block_shift : t / BS));
       }
     };
-    const auto issue = [&](int i) {
-      const uint32_t dst = smem_addr(ring + i % C::kStages * C::kStage);
+    const auto issue = [&](int i, uint32_t dst) {
       const int32_t ts = t0 + (i * kWarps + warp) * C::ROWS;
-      if (a.paged16) {
+      bool whole = a.paged16 && ts + C::ROWS <= t1;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        whole = whole && static_cast<uint32_t>(page[mt]) < static_cast<uint32_t>(a.num_blocks);
+      if (whole) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int32_t t = ts + 16 * mt;
+          const int at = a.block_shift >= 0 ? t & (BS - 1) : t % BS;
+          const int64_t row =
+              static_cast<int64_t>(page[mt]) * a.num_kv_heads * BS + (kvh * BS + at);
+          const uint8_t* kc = a.k_codes + row * (D / 2) + lane * 16;
+          const uint8_t* vc = a.v_codes + row * (D / 2) + lane * 16;
+          const uint32_t to = dst + 16 * mt * C::KP + lane / (D / 32) * C::KP +
+                              lane % (D / 32) * 16;
+          const uint32_t vto = dst + C::kV + 16 * mt * C::VP + lane / (D / 32) * C::VP +
+                               lane % (D / 32) * 16;
+#pragma unroll
+          for (int u = 0; u < D / 64; ++u) {
+            copy16(to + u * (1024 / D) * C::KP, kc + u * 512);
+            copy16(vto + u * (1024 / D) * C::VP, vc + u * 512);
+          }
+          if (lane < C::SB) {
+            const int64_t from = row * C::SB + lane * 16;
+            const uint32_t pto = dst + C::kKs + 16 * mt * C::SB + lane * 16;
+            copy16(pto, static_cast<const uint8_t*>(a.k_pairs) + from);
+            copy16(pto + (C::kVs - C::kKs), static_cast<const uint8_t*>(a.v_pairs) + from);
+          }
+        }
+      } else if (a.paged16) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int32_t t = ts + 16 * mt;
@@ -274,7 +375,7 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
       if (i < stages) {
-        issue(i);
+        issue(i, smem_addr(ring + i * C::kStage));
         load_pages(i + 1);
       }
       copies_commit();
@@ -300,7 +401,6 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
     largest = fmaxf(largest, __shfl_xor_sync(kAll, largest, 2));
     if (c == 0) stat[warp * 8 + r] = largest;
     if (threadIdx.x == 0) bad_s = 0;
-    for (int i = threadIdx.x; i < NCH * 8; i += kNT) qs[i] = 0.f;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) largest = fmaxf(largest, stat[w * 8 + r]);
@@ -317,15 +417,12 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
       }
       // the high halves' elements meet codes 2^4 as large
       constexpr float k16 = 1.f / 16;
-      qf[u * 32 + lane] = make_uint4(f16x2(f[0], f[4]), f16x2(f[2], f[6]),
-                                     f16x2(f[1] * k16, f[5] * k16), f16x2(f[3] * k16, f[7] * k16));
+      qf[u * 32 + lane] =
+          make_uint4(pack<__half>(f[0], f[4]), pack<__half>(f[2], f[6]),
+                     pack<__half>(f[1] * k16, f[5] * k16), pack<__half>(f[3] * k16, f[7] * k16));
       sum += __shfl_xor_sync(kAll, sum, 1);
       sum += __shfl_xor_sync(kAll, sum, 2);
-      if constexpr (W == 1) {
-        if (c == 0) qs[u * 8 + r] = sum * 0x1p-24f;
-      } else {
-        if (c == 0) atomicAdd(&qs[u / W * 8 + r], sum * 0x1p-24f);  // two terms: any order
-      }
+      if (c == 0) qs[u * 8 + r] = sum;
     }
     // the factor of a logit of this lane's heads 2c, 2c + 1
     float lf[2];
@@ -333,30 +430,48 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
     for (int e = 0; e < 2; ++e)
       lf[e] = a.scale_log2 * pow2(min(24 - __shfl_sync(kAll, shift, (2 * c + e) * 4), 127));
     __syncthreads();
+    // The sums of q over groups 2c and 2c + 1 of head r, as B of the product with the
+    // minima: three bf16 or two f16 parts.  f16: times 2^16, at most 2^14.
+    uint32_t qb[kParts];
+    {
+      float g[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        g[e] = 0.f;
+        if (2 * c + e < NP)
+#pragma unroll
+          for (int u = 0; u < GS / 32; ++u) g[e] += qs[((2 * c + e) * (GS / 32) + u) * 8 + r];
+        g[e] *= 0x1p-24f * kMinUp;
+      }
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) qb[i] = split<T>(g[0], g[1]);
+    }
 
     // ---- the part -----------------------------------------------------------------------
-    float o[NCH][kTiles][4], eights[4], extra[NCH], lim = 0.f, up[NCH];
+    // eights: rows are chunks; sums: rows r are the minima of group r, r + 8 its scales
+    float o[NCH][kTiles][4], eights[4], sums[4], lim = 0.f, up[NCH];
     float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      extra[j] = up[j] = 0.f;
+      up[j] = 0.f;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][t][e] = 0.f;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) eights[e] = 0.f;
+    for (int e = 0; e < 4; ++e) eights[e] = sums[e] = 0.f;
 
+    uint8_t* st = ring;                                     // this stage, and
+    uint8_t* refill = ring + (C::kStages - 1) * C::kStage;  // the one before it
     for (int i = 0; i < stages; ++i) {
       copies_wait<C::kStages - 2>();
       __syncwarp();  // this stage has landed for all lanes, and the one to refill is read
       if (i + C::kStages - 1 < stages) {
-        issue(i + C::kStages - 1);
+        issue(i + C::kStages - 1, smem_addr(refill));
         load_pages(i + C::kStages);
       }
       copies_commit();
-      const uint8_t* st = ring + i % C::kStages * C::kStage;
       const int n = t1 - (t0 + (i * kWarps + warp) * C::ROWS);  // tokens, if fewer than ROWS
 
       // logits of rows r, r + 8 and heads 2c, 2c + 1
@@ -365,36 +480,57 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
         uint32_t kw[MT][2][NP];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          load_words(st + C::kKs + (16 * mt + r) * C::SB, kw[mt][0]);
-          load_words(st + C::kKs + (16 * mt + r + 8) * C::SB, kw[mt][1]);
+          const uint8_t* at = st + C::kKs + (16 * mt + r) * C::SB;
+          load_words(at, kw[mt][0]);
+          load_words(at + 8 * C::SB, kw[mt][1]);
+          // minima times the sums of q; groups past the last meet zeros
+          uint32_t m0, m1;
+          if constexpr (NP == 1) {
+            m0 = __byte_perm(kw[mt][0][0], 0, 0x3232);
+            m1 = __byte_perm(kw[mt][1][0], 0, 0x3232);
+          } else {
+            uint32_t w0[2], w1[2];
+            const int g = 2 * c % NP * 4;
+            load_words(at + g, w0);
+            load_words(at + 8 * C::SB + g, w1);
+            m0 = __byte_perm(w0[0], w0[1], 0x7632);
+            m1 = __byte_perm(w1[0], w1[1], 0x7632);
+          }
+          mma0<T>(l[mt], m0, m1, 0, 0, qb[0], 0);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) l[mt][e] = 0.f;
+          for (int i = 1; i < kParts; ++i) mma<T>(l[mt], m0, m1, 0, 0, qb[i], 0);
+          if constexpr (kMinUp != 1.f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l[mt][e] *= 1.f / kMinUp;
         }
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
           uint4 qv[W];
 #pragma unroll
           for (int w = 0; w < W; ++w) qv[w] = qf[(j * W + w) * 32 + lane];
-          const float2 s2 = *reinterpret_cast<const float2*>(qs + j * 8 + 2 * c);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const uint8_t* at = st + (16 * mt + r) * C::KP + j * (CH / 2) + c * (4 * W);
             uint32_t lo[W], hi[W];
             load_words(at, lo);
             load_words(at + 8 * C::KP, hi);
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float acc[4];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
               const uint32_t lo8 = lo[w] >> 8, hi8 = hi[w] >> 8;
-              mma(acc, lo[w] & kLow, hi[w] & kLow, lo8 & kLow, hi8 & kLow, qv[w].x, qv[w].y);
-              mma(acc, lo[w] & kHigh, hi[w] & kHigh, lo8 & kHigh, hi8 & kHigh, qv[w].z, qv[w].w);
+              const uint32_t a0 = lo[w] & kLow, a1 = hi[w] & kLow, a2 = lo8 & kLow,
+                             a3 = hi8 & kLow;
+              if (w == 0) mma0<__half>(acc, a0, a1, a2, a3, qv[w].x, qv[w].y);
+              else mma<__half>(acc, a0, a1, a2, a3, qv[w].x, qv[w].y);
+              mma<__half>(acc, lo[w] & kHigh, hi[w] & kHigh, lo8 & kHigh, hi8 & kHigh, qv[w].z,
+                          qv[w].w);
             }
-            const float2 p0 = widen_pair<T>(kw[mt][0][j * CH / GS]);
-            const float2 p1 = widen_pair<T>(kw[mt][1][j * CH / GS]);
-            l[mt][0] = fmaf(p0.y, s2.x, fmaf(p0.x, acc[0], l[mt][0]));
-            l[mt][1] = fmaf(p0.y, s2.y, fmaf(p0.x, acc[1], l[mt][1]));
-            l[mt][2] = fmaf(p1.y, s2.x, fmaf(p1.x, acc[2], l[mt][2]));
-            l[mt][3] = fmaf(p1.y, s2.y, fmaf(p1.x, acc[3], l[mt][3]));
+            const float s0 = scale_of<T>(kw[mt][0][j * CH / GS]);
+            const float s1 = scale_of<T>(kw[mt][1][j * CH / GS]);
+            l[mt][0] = fmaf(s0, acc[0], l[mt][0]);
+            l[mt][1] = fmaf(s0, acc[1], l[mt][1]);
+            l[mt][2] = fmaf(s1, acc[2], l[mt][2]);
+            l[mt][3] = fmaf(s1, acc[3], l[mt][3]);
           }
         }
       }
@@ -421,7 +557,7 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
 #pragma unroll
       for (int u = 0; u < (kScales + 31) / 32; ++u)
         if (kScales % 32 == 0 || u * 32 + lane < kScales)
-          moves = moves || fabsf(widen_pair<T>(vpairs[u * 32 + lane]).x) > lim;
+          moves = moves || fabsf(scale_of<T>(vpairs[u * 32 + lane])) > lim;
       if (__any_sync(kAll, moves)) {
         float f[2];
 #pragma unroll
@@ -436,15 +572,12 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
           if (m) ref[e] = top;
           sum[e] *= f[e];
         }
-        // head r's factor, for the sums that lie by head
-        const float f0 = __shfl_sync(kAll, f[0], r >> 1), f1 = __shfl_sync(kAll, f[1], r >> 1);
-        const float fr = r & 1 ? f1 : f0;
         // the groups' powers
         float most = 0.f;
 #pragma unroll
         for (int u = 0; u < (kScales + 31) / 32; ++u)
           if (kScales % 32 == 0 || u * 32 + lane < kScales)
-            most = fmaxf(most, fabsf(widen_pair<T>(vpairs[u * 32 + lane]).x));
+            most = fmaxf(most, fabsf(scale_of<T>(vpairs[u * 32 + lane])));
 #pragma unroll
         for (int s = NP; s <= 16; s <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, s));
         float g = 1.f;
@@ -460,7 +593,6 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
           const float lj = __shfl_sync(kAll, lim, j * CH / GS);
           up[j] = lj > 0.f ? pow2(7 - exponent(lj)) : 0.f;
           if (j == r) ge = gj;
-          extra[j] *= fr;
 #pragma unroll
           for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -468,6 +600,8 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
         }
         eights[0] *= f[0] * ge;
         eights[1] *= f[1] * ge;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[e] *= f[e & 1];
       }
 
       // weights, and their transposition: heads as rows, tokens as columns
@@ -483,8 +617,8 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
 
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const float2 pa = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c);
-        const float2 pb = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c + 8);
+        F2 pa = *reinterpret_cast<const F2*>(pt + r * C::PP + 16 * mt + 2 * c);
+        F2 pb = *reinterpret_cast<const F2*>(pt + r * C::PP + 16 * mt + 2 * c + 8);
         const uint8_t* at = st + C::kV + (16 * mt + 2 * c) * C::VP;
         const uint8_t* sc = st + C::kVs + (16 * mt + 2 * c) * C::SB;
         uint32_t vw[4][NP];
@@ -492,20 +626,39 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
         load_words(sc + C::SB, vw[1]);
         load_words(sc + 8 * C::SB, vw[2]);
         load_words(sc + 9 * C::SB, vw[3]);
+        {
+          // weights, in two parts of 16 bits, times minima and scales: group r % NP
+          uint32_t w[4];
+          const int g = r % NP;
+          if constexpr (NP == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = vw[e][0];
+          } else {
+            const uint32_t* x = reinterpret_cast<const uint32_t*>(sc) + g;
+            w[0] = x[0], w[1] = x[NP], w[2] = x[8 * NP], w[3] = x[9 * NP];
+          }
+          const uint32_t m0 = __byte_perm(w[0], w[1], 0x7632);
+          const uint32_t m1 = __byte_perm(w[0], w[1], 0x5410);
+          const uint32_t m2 = __byte_perm(w[2], w[3], 0x7632);
+          const uint32_t m3 = __byte_perm(w[2], w[3], 0x5410);
+          float2 x = unpair(pa), y = unpair(pb);
+          if constexpr (kWeightUp != 1.f)
+            x.x *= kWeightUp, x.y *= kWeightUp, y.x *= kWeightUp, y.y *= kWeightUp;
+          const uint32_t h0 = split<T>(x.x, x.y), h1 = split<T>(y.x, y.y);
+          mma<T>(sums, m0, m1, m2, m3, h0, h1);
+          mma<T>(sums, m0, m1, m2, m3, pack<T>(x.x, x.y), pack<T>(y.x, y.y));
+        }
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-          const float2 p0 = widen_pair<T>(vw[0][j * CH / GS]);
-          const float2 p1 = widen_pair<T>(vw[1][j * CH / GS]);
-          const float2 p2 = widen_pair<T>(vw[2][j * CH / GS]);
-          const float2 p3 = widen_pair<T>(vw[3][j * CH / GS]);
-          extra[j] = fmaf(pa.x, fmaf(8.f, p0.x, p0.y), extra[j]);
-          extra[j] = fmaf(pa.y, fmaf(8.f, p1.x, p1.y), extra[j]);
-          extra[j] = fmaf(pb.x, fmaf(8.f, p2.x, p2.y), extra[j]);
-          extra[j] = fmaf(pb.y, fmaf(8.f, p3.x, p3.y), extra[j]);
-          const uint32_t b0 = f16x2(pa.x * (p0.x * up[j]), pa.y * (p1.x * up[j]));
-          const uint32_t b1 = f16x2(pb.x * (p2.x * up[j]), pb.y * (p3.x * up[j]));
+          const F2 u2 = pair(up[j], up[j]);
+          const F2 s01 = pair(scale_of<T>(vw[0][j * CH / GS]), scale_of<T>(vw[1][j * CH / GS]));
+          const F2 s23 = pair(scale_of<T>(vw[2][j * CH / GS]), scale_of<T>(vw[3][j * CH / GS]));
+          const float2 q01 = unpair(mul2(pa, mul2(s01, u2)));
+          const float2 q23 = unpair(mul2(pb, mul2(s23, u2)));
+          const uint32_t b0 = pack<__half>(q01.x, q01.y);
+          const uint32_t b1 = pack<__half>(q23.x, q23.y);
           const uint32_t eight = j == r ? 0x00080008u : 0u;
-          mma(eights, eight, 0, eight, 0, b0, b1);
+          mma<__half>(eights, eight, 0, eight, 0, b0, b1);
           // a lane's word of the chunk, and for groups of 32 its half of it
           const int word = j * (CH / 8) + (W == 2 ? r : r >> 1);
           const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at + 4 * word);
@@ -516,13 +669,15 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
           for (int h = 0; h < W; ++h) {
             const uint32_t pick = (W == 2 ? h : r & 1) ? 0x7632u : 0x5410u;
             const uint32_t x0 = __byte_perm(w0, w1, pick), x1 = __byte_perm(w2, w3, pick);
-            mma(o[j][2 * h], x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh, b0, b1);
-            mma(o[j][2 * h + 1], x0 >> 8 & kLow, x0 >> 8 & kHigh, x1 >> 8 & kLow,
-                x1 >> 8 & kHigh, b0, b1);
+            mma<__half>(o[j][2 * h], x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh, b0, b1);
+            mma<__half>(o[j][2 * h + 1], x0 >> 8 & kLow, x0 >> 8 & kHigh, x1 >> 8 & kLow,
+                        x1 >> 8 & kHigh, b0, b1);
           }
         }
       }
       __syncwarp();  // pt is written again
+      refill = st;
+      st = st == ring + (C::kStages - 1) * C::kStage ? ring : st + C::kStage;
     }
     copies_wait<0>();
 
@@ -543,45 +698,64 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
     float* mine = reinterpret_cast<float*>(smem) + warp * (8 * D);  // [8][D]
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      extra[j] += __shfl_xor_sync(kAll, extra[j], 1);
-      extra[j] += __shfl_xor_sync(kAll, extra[j], 2);
       const float down = up[j] > 0.f ? 1.f / up[j] : 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ex = __shfl_sync(kAll, extra[j], (2 * c + e) * 4);
+        const int g = j * CH / GS * 4 + c;
+        const float ex = fmaf(8.f, __shfl_sync(kAll, sums[e + 2], g),
+                              __shfl_sync(kAll, sums[e], g)) * (1.f / kWeightUp);
         const float ei = __shfl_sync(kAll, eights[e], j * 4 + c) * 0x1p24f;
-        float* to = mine + (2 * c + e) * D + j * CH + r * (CH / 8);
+        float v[2 * kTiles];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           // rows r and r + 8 of the MMA: elements 2t and 2t + 1 of the lane's run
-          to[2 * t] = fmaf(o[j][t][e] * 0x1p24f - ei, down, ex);
-          to[2 * t + 1] = fmaf(o[j][t][e + 2] * 0x1p20f - ei, down, ex);
+          v[2 * t] = fmaf(o[j][t][e] * 0x1p24f - ei, down, ex);
+          v[2 * t + 1] = fmaf(o[j][t][e + 2] * 0x1p20f - ei, down, ex);
         }
+        float* to = mine + (2 * c + e) * D + j * CH + r * (CH / 8);
+#pragma unroll
+        for (int t = 0; t < kTiles / 2; ++t)
+          reinterpret_cast<float4*>(to)[t] =
+              make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
       }
     }
     __syncthreads();
-    // a warp's weight beside the largest reference; a warp without a token weighs nothing
-    if (threadIdx.x < kWarps * 8) {
-      const int h = threadIdx.x & 7;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w * 8 + h]);
-      const float m = stat[threadIdx.x], s = stat[kWarps * 8 + threadIdx.x];
-      stat[2 * kWarps * 8 + threadIdx.x] =
-          m == -INFINITY ? (s == 0.f ? 0.f : qnan()) : ex2(m - M);
-      if (threadIdx.x < 8) stat[3 * kWarps * 8 + h] = M;
+    if (warp == 0) {
+      // lane's warp and head: its weight beside the largest reference, over the sum of all;
+      // a warp without a token weighs nothing
+      const int w = lane >> 3, h = lane & 7;
+      const float m = stat[w * 8 + h], s = stat[(kWarps + w) * 8 + h];
+      float M = fmaxf(m, __shfl_xor_sync(kAll, m, 8));
+      M = fmaxf(M, __shfl_xor_sync(kAll, M, 16));
+      const float f = m == -INFINITY ? (s == 0.f ? 0.f : qnan()) : ex2(m - M);
+      float total = f * s;
+      total += __shfl_xor_sync(kAll, total, 8);
+      total += __shfl_xor_sync(kAll, total, 16);
+      stat[(2 * kWarps + w) * 8 + h] = bad_s ? qnan() : f / total;
+      if (!direct && w == 0 && h < nh) {
+        const int64_t at = (static_cast<int64_t>(b) * a.num_heads + h0 + h) * a.num_parts + part;
+        a.part_max[at] = bad_s ? qnan() : M * kLn2;
+        a.part_sum[at] = total;
+      }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nh * D; i += kNT) {
-      const int h = i / D, d = i % D;
-      float total = 0.f, v = 0.f;
+    for (int i = threadIdx.x; i < nh * (D / 4); i += kNT) {
+      const int h = i / (D / 4), d = i % (D / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = stat[(2 * kWarps + w) * 8 + h];
-        total = fmaf(stat[(kWarps + w) * 8 + h], f, total);
-        v = fmaf(reinterpret_cast<const float*>(smem)[(w * 8 + h) * D + d], f, v);
+        const float4 y = reinterpret_cast<const float4*>(smem)[(w * 8 + h) * (D / 4) + d];
+        v.x = fmaf(y.x, f, v.x);
+        v.y = fmaf(y.y, f, v.y);
+        v.z = fmaf(y.z, f, v.z);
+        v.w = fmaf(y.w, f, v.w);
       }
-      kv4_finish(a, b, h0 + h, part, d, D, direct, L, bad_s, stat[3 * kWarps * 8 + h], total, v);
+      const int64_t row = static_cast<int64_t>(b) * a.num_heads + h0 + h;
+      if (direct)
+        store_out4(a.out, row * D + 4 * d, a.out_dtype, v);
+      else
+        reinterpret_cast<float4*>(a.part_out)[(row * a.num_parts + part) * (D / 4) + d] = v;
     }
     if (bad_s && threadIdx.x == 0) set_status(a.status, PA_ERR_BAD_BLOCK_ID);
     __syncthreads();  // the ring, the statistics and q are written again
