@@ -58,6 +58,7 @@ struct KernelArgs {
 constexpr size_t kCtrlBytes = PA_WORKSPACE_CONTROL_BYTES;
 constexpr size_t kMarkerOffset = 4;
 constexpr size_t kSyncOffset = 256;
+constexpr size_t kPartOffset = 512;  // 4-bit decode: tokens of a part; the queue of items
 constexpr int kMarkerByte = 0x5A;
 constexpr int32_t kMarker = 0x5A5A5A5A;
 
@@ -195,6 +196,8 @@ struct JoinList {
   int32_t max_len;
   int32_t stride;
   int32_t part_size;            // tokens of a partial, unless key_blocks > 0
+  const int32_t* part_at;       // given: where the pass has left them; rows of one partial
+                                //   are written already
   int32_t window, num_sinks;    // window > 0: the length is the visible list's
   int32_t block_list;           //   the block list's (pa_span.cuh), else the plain list's
   int32_t block_size;
@@ -234,7 +237,12 @@ struct Kv4Args {
   int32_t* status;
   int32_t num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks;
   int32_t max_blocks_per_seq, max_len;
-  int32_t part_size, num_parts;  // tokens of a part; 1 part: results go to out
+  // The generic kernel's parts are part_size tokens.  The tensor-core kernel chooses the
+  // size from the lengths, at least part_floor, and leaves it at part_at.  num_parts:
+  // slots of a row for partials; 1: the kernel writes every row, and no join follows.
+  int32_t part_size, part_floor, num_parts;
+  int32_t* part_at;
+  int32_t room;                  // tensor-core kernel: CTAs that are resident
   int32_t group, head_groups;    // query heads of a KV head; ceil(group / kKv4Heads)
   int32_t group_size;            // elements of a head row that share a scale
   int32_t block_shift;           // log2 of block_size, or -1
@@ -242,8 +250,6 @@ struct Kv4Args {
   int32_t out_dtype;
   float scale_log2;
 };
-// CTAs of the tensor-core kernel that are resident on an SM.
-constexpr int kv4_tc_ctas(int head_dim) { return head_dim == 256 ? 3 : 4; }
 // `items`: at least the (part, KV head, query head group) triples that exist
 cudaError_t launch_kv4_tc_bf16(const Kv4Args& a, int64_t items, cudaStream_t s);
 cudaError_t launch_kv4_tc_f16(const Kv4Args& a, int64_t items, cudaStream_t s);

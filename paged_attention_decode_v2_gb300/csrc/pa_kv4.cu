@@ -37,37 +37,26 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
   return PA_OK;
 }
 
-int64_t parts_of(int64_t len, int64_t size) { return std::max<int64_t>(1, (len + size - 1) / size); }
+// Slots of a row of `seqs` sequences for partials.  The tensor-core kernel chooses the
+// parts from the lengths, which may all be the longest or one long among short ones: by
+// partition_size where there are many sequences, else up to kSplit items for each CTA
+// that may be resident (four on each of 152 SMs).
+constexpr int64_t kSplit = 8, kRoom = 608;
 
-// Parts of the longest of `seqs` sequences.  There is room for some work items --
-// (part, KV head, eight query heads) -- at a time, a CTA each on 152 SMs.
-//   * Many sequences, two rounds of items undivided: partition_size.
-//   * Fewer: the split that takes the least time, as for the windowed decode: a
-//     round costs as much as its part is long plus a start, a partial the join.
-int64_t room_for(const pa_params_t* p) { return 152 * kv4_tc_ctas(p->head_dim); }
-constexpr int64_t kMostParts = 640;
+int64_t pairs_of(const pa_params_t* p, int64_t seqs) {
+  return seqs * p->num_kv_heads * head_groups(p);
+}
+int64_t cover(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int64_t parts_for(const pa_params_t* p, int64_t seqs) {
-  constexpr int64_t kStart = 128, kJoin = 2, kLeast = 64;
-  const int64_t len = p->max_seq_len, room = room_for(p);
-  const int64_t pairs = seqs * p->num_kv_heads * head_groups(p);
-  if (pairs >= 2 * room) return parts_of(len, p->partition_size);
-  // the cost of n parts is a line in len: n never falls as len grows
-  int64_t parts = 1;
-  double best = -1;
-  for (int64_t n = 1; n <= kMostParts && (n == 1 || n * kLeast <= len); ++n) {
-    const double rounds = static_cast<double>((pairs * n + room - 1) / room);
-    const double cost = rounds / n * len + rounds * kStart + (n > 1 ? n * kJoin : 0);
-    if (best < 0 || cost < best) {
-      best = cost;
-      parts = n;
-    }
-  }
-  return parts;
+int64_t most_parts(const pa_params_t* p, int64_t seqs) {
+  const int64_t len = p->max_seq_len;
+  const int64_t by_size = cover(len, p->partition_size);
+  const int64_t by_room = cover(kSplit * kRoom, pairs_of(p, seqs));
+  return std::max<int64_t>(1, std::min(cover(len, 64), std::max(by_size, by_room)));
 }
 
 WorkspaceLayout layout_of(const pa_params_t* p, int64_t seqs) {
-  return workspace_layout(seqs, p->num_heads, p->head_dim, parts_for(p, seqs));
+  return workspace_layout(seqs, p->num_heads, p->head_dim, most_parts(p, seqs));
 }
 
 }  // namespace
@@ -81,7 +70,7 @@ size_t pa_kv4_workspace_size(const pa_params_t* p, const pa_kv4_t* kv4) {
   if (check(p, kv4) != PA_OK) return 0;
   size_t most = layout_of(p, p->num_seqs).total;
   // fewer sequences may have more parts in all
-  for (int64_t s = 1; s < p->num_seqs && s * p->num_kv_heads < 2 * room_for(p); ++s)
+  for (int64_t s = 1; s < p->num_seqs && pairs_of(p, s) < kSplit * kRoom; ++s)
     most = std::max(most, layout_of(p, s).total);
   return most;
 }
@@ -126,27 +115,34 @@ pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void*
   a.head_groups = static_cast<int32_t>(head_groups(p));
   a.group_size = kv4->group_size;
   a.block_shift = (p->block_size & (p->block_size - 1)) ? -1 : __builtin_ctz(p->block_size);
-  a.paged16 = p->block_size % 16 == 0;
+  // offsets within a page are 32 bits
+  a.paged16 = p->block_size % 16 == 0 &&
+              static_cast<double>(p->num_kv_heads) * p->block_size * p->head_dim < 2147483648.0;
   a.out_dtype = p->out_dtype;
   a.scale_log2 = p->scale * 1.442695040888963407360f;
-  // parts of whole tiles; evened out over the longest sequence
-  const int64_t parts = parts_for(p, p->num_seqs);
-  a.part_size = static_cast<int32_t>(
-      std::max<int64_t>(64, ((p->max_seq_len + parts - 1) / parts + 63) / 64 * 64));
-  a.num_parts = static_cast<int32_t>(parts_of(p->max_seq_len, a.part_size));
+  // whole tiles; slots as the parts of that size need them
+  a.part_floor = static_cast<int32_t>(
+      std::max<int64_t>(64, cover(cover(p->max_seq_len, most_parts(p, p->num_seqs)), 64) * 64));
+  a.part_at = reinterpret_cast<int32_t*>(base + kPartOffset);
+  a.num_parts = static_cast<int32_t>(
+      std::max<int64_t>(1, cover(p->max_seq_len, a.part_floor)));
   // work items, counted in 31 bits by the tensor-core kernel
   const double items = static_cast<double>(a.num_seqs) * a.num_parts * a.num_kv_heads *
                        a.head_groups;
   const bool tc = p->kv_dtype != PA_F32 && !(p->flags & PA_FLAG_PORTABLE) && items < 2e9 &&
                   sm100_num_sms() > 0;
   cudaError_t e;
-  if (tc)
+  if (tc) {
     e = (p->kv_dtype == PA_BF16 ? launch_kv4_tc_bf16 : launch_kv4_tc_f16)(
         a, static_cast<int64_t>(items), stream);
-  else
+  } else {
+    a.part_size = std::max(a.part_floor, 512);
+    a.num_parts = static_cast<int32_t>(
+        std::max<int64_t>(1, cover(p->max_seq_len, a.part_size)));
     e = (p->kv_dtype == PA_F32    ? launch_kv4_generic_f32
          : p->kv_dtype == PA_BF16 ? launch_kv4_generic_bf16
                                   : launch_kv4_generic_f16)(a, stream);
+  }
   if (e != cudaSuccess) return PA_ERR_CUDA;
   if (a.num_parts == 1) return PA_OK;
   JoinArgs j{};
@@ -158,6 +154,7 @@ pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void*
   l.max_len = p->max_seq_len;
   l.stride = a.num_parts;
   l.part_size = a.part_size;
+  l.part_at = tc ? a.part_at : nullptr;
   l.block_size = p->block_size;
   j.out = out;
   j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;

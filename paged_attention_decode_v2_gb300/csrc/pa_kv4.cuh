@@ -123,7 +123,7 @@ __device__ __forceinline__ void list_find(const uint32_t* start, int num_seqs, c
     const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  const uint32_t at = i - start[lo];
+  const uint32_t at = i - (lo > 0 ? start[lo] : 0);  // one span needs no list
   const int who = __ffs(__ballot_sync(0xffffffffu, at < x)) - 1;  // the first sum past it
   seq = lo * kListSpan + who;
   index = at - __shfl_sync(0xffffffffu, x - own, who);

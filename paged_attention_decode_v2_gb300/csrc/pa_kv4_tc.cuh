@@ -38,40 +38,37 @@
 namespace pa {
 namespace kv4 {
 
-constexpr int kWarps = 4;
-constexpr int kNT = kWarps * 32;
 constexpr unsigned kAll = 0xffffffffu;
 
-template <int D, int GS>
+template <int D, int GS, bool kWide>
 struct Cfg {
-  static constexpr int CH = GS < 64 ? GS : 64;  // elements that an accumulator sums
-  static constexpr int NCH = D / CH;
-  static constexpr int W = CH / 32;             // words of a chunk that a lane has
+  // warps of a CTA, and CTAs that are resident on an SM
+  static constexpr int kWarps = kWide ? (D == 256 ? 12 : 16) : 4;
+  static constexpr int kCtas = kWide ? 1 : D == 256 ? 3 : 4;
+  static constexpr int kNT = kWarps * 32;
+  static constexpr int kLeast = kWide ? 512 : 256;  // tokens of a part that pay for its join
+  static constexpr int NB = D / 32;             // blocks of 32 elements: a word of keys a lane
   static constexpr int NP = D / GS;             // pairs of a head row
   static constexpr int SB = NP * 4;             //   and their bytes
-  static constexpr int MT = D >= 128 ? 1 : 2;   // 16-token tiles of a stage
+  static constexpr int MT = D == 256 ? 1 : 2;   // 16-token tiles of a stage
   static constexpr int ROWS = 16 * MT;
-  // Pitches that spread a warp's reads over the banks: keys by 8-byte (4-byte for
-  // groups of 32) reads of 8 rows, values by 4-byte reads of rows 2 apart.
-  static constexpr int KP = CH == 32 ? D / 2 + 16 : D == 64 ? 32 : D / 2 + 32;
-  static constexpr int VP = D / 2 + 16;
+  static constexpr int KP = D / 2 + 16;         // pitch of codes: rows of LDSM in other banks
   static constexpr int kV = ROWS * KP;
-  static constexpr int kKs = kV + ROWS * VP;
+  static constexpr int kKs = kV + ROWS * KP;
   static constexpr int kVs = kKs + ROWS * SB;
   static constexpr int kStage = kVs + ROWS * SB;
-  static constexpr int kStages = D == 128 ? 4 : 3;
+  static constexpr int kStages = !kWide && D == 64 ? 3 : 2;
   static constexpr int PP = ROWS + 4;           // pitch of the weights' transposition
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQ = D / 32 * 512;       // q fragments
   static constexpr int kOffQ = kRing;
   static constexpr int kOffQs = kOffQ + kQ;                  // sums of q: [D / 32][8]
   static constexpr int kOffP = kOffQs + D / 32 * 8 * 4;      // weights: [warp][8][PP]
-  static constexpr int kOffW = kOffP + kWarps * 8 * PP * 4;  // statistics: [4][warp][8]
-  static constexpr int kOffList = kOffW + 4 * kWarps * 8 * 4;
-  static constexpr int kCtas = kv4_tc_ctas(D);  // resident on an SM
-  static_assert((kOffList + 1024 + 1024) * kCtas <= 228 * 1024, "resident CTAs");
-  static_assert(kRing >= kWarps * 8 * D * 4, "the join uses the ring");
-  static_assert(kStage % 16 == 0 && KP % 16 == 0 && VP % 16 == 0, "16-byte copies");
+  static constexpr int kOffW = kOffP + kWarps * 8 * PP * 4;  // statistics: [2][warp][8]
+  static constexpr int kOffList = kOffW + 2 * kWarps * 8 * 4;
+  static_assert((kOffList + 1024 + 128) * kCtas <= 228 * 1024, "resident CTAs");
+  static_assert(kStages * kStage >= 8 * D * 4, "a warp's results take its ring's place");
+  static_assert(kStage % 16 == 0 && KP % 16 == 0, "16-byte copies");
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -202,47 +199,143 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
+// Four 8 x 8 matrices of 16-bit units, lane's row at `addr`; kTrans: their transposes.
+template <bool kTrans>
+__device__ __forceinline__ void ldsm(uint32_t (&w)[4], uint32_t addr) {
+  if constexpr (kTrans)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // Parts of sequence b: those with a token; one for a row that the item itself has to
-// finish (direct: no join follows).
+// finish (no join follows).
 struct Parts {
   const Kv4Args& a;
-  __device__ __forceinline__ uint32_t operator()(int b) const {
-    const int32_t L = __ldg(a.lens + b);
-    const bool some = kv4_len_ok(a, L) && L > 0;
-    return some ? (L + a.part_size - 1) / a.part_size : a.num_parts == 1;
+  int32_t size;
+  __device__ __forceinline__ uint32_t of(int32_t L) const {
+    return kv4_len_ok(a, L) && L > 0 ? (static_cast<uint32_t>(L) + size - 1) / size
+                                     : a.num_parts == 1;
   }
+  __device__ __forceinline__ uint32_t operator()(int b) const { return of(__ldg(a.lens + b)); }
 };
 
-template <typename T, int D, int GS>
-__global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const Kv4Args a) {
-  using C = Cfg<D, GS>;
-  constexpr int NCH = C::NCH, MT = C::MT, W = C::W, NP = C::NP, CH = C::CH;
-  constexpr int kTiles = CH / 16;  // MMA tiles of a chunk's values
+// Tokens of a part, from the lengths of the call: all CTAs come to the same.
+//   * Few (sequence, KV head) pairs for the CTAs that are resident: one round, as even as
+//     parts of one size are: the least size that makes no more items than CTAs (32
+//     sequences or fewer), or one that does whatever the lengths are.
+//   * Many: a CTA's share of the work is w tokens; parts of n tokens cost it w / n starts,
+//     each worth some kStart tokens, and leave it waiting for about half a part at the end:
+//     n = sqrt(2 kStart w).
+// Never below `least` (nor below what the workspace has slots for).  In float32: nothing
+// depends on the size but speed.
+constexpr float kStart = 250.f;
+__device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, int32_t own,
+                                               int32_t least) {
+  const float per = static_cast<float>(a.num_kv_heads * a.head_groups);
+  const float pairs = per * a.num_seqs, room = a.room, share = tokens * per / room;
+  least = max(least, a.part_floor);
+  const int32_t most = max((a.max_len + 63) / 64 * 64, least);
+  const auto within = [&](float n) {  // whole tiles
+    return n >= static_cast<float>(most) ? most
+                                         : max((static_cast<int32_t>(ceilf(n)) + 63) / 64 * 64, least);
+  };
+  if (2.f * pairs > room) return within(sqrtf(2.f * kStart * share));
+  int32_t hi = within(tokens * per / (room - pairs));
+  if (a.num_seqs > 32) return hi;
+  // lanes hold the lengths: the fewest tokens, to some steps, with which all items have CTAs
+  int32_t lo = within(share) - 64;
+  const float fits = room / per;
+#pragma unroll 1
+  for (int i = 0; i < 5 && hi - lo > 64; ++i) {
+    const int32_t mid = lo + (hi - lo) / 128 * 64;
+    float n = ceilf(__fdividef(static_cast<float>(own), static_cast<float>(mid)));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+    if (n <= fits) hi = mid;
+    else lo = mid;
+  }
+  return hi;
+}
+
+// The queue of items, in the workspace's control block: CTAs take their first item by
+// number, further ones here.  The CTA that is done last leaves it as it was found, zeros.
+struct Queue {
+  uint32_t next, done;
+};
+
+template <typename T, int D, int GS, bool kWide>
+__global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCtas)
+    pa_kv4_tc_kernel(const Kv4Args a) {
+  using C = Cfg<D, GS, kWide>;
+  constexpr int NB = C::NB, MT = C::MT, NP = C::NP, kWarps = C::kWarps, kNT = C::kNT;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr int kParts = kHalf ? 2 : 3;                  // of the sums of q
   constexpr float kMinUp = kHalf ? 0x1p16f : 1.f;        // powers of two that keep f16
   constexpr float kWeightUp = kHalf ? 0x1p7f : 1.f;      // operands in its range
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int bad_s;
+  __shared__ uint32_t next_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;  // row of A, or head of B; column pair
   uint8_t* ring = smem + warp * (C::kStages * C::kStage);
   uint4* qf = reinterpret_cast<uint4*>(smem + C::kOffQ);
   float* qs = reinterpret_cast<float*>(smem + C::kOffQs);
   float* pt = reinterpret_cast<float*>(smem + C::kOffP) + warp * (8 * C::PP);
-  float* stat = reinterpret_cast<float*>(smem + C::kOffW);  // [4][kWarps][8]
+  float* stat = reinterpret_cast<float*>(smem + C::kOffW);  // [2][kWarps][8]
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + C::kOffList);
 
   cudaTriggerProgrammaticLaunchCompletion();  // the join waits for this grid's end itself
-  const Parts parts{a};
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.num_seqs; b += kNT)
       if (!kv4_len_ok(a, __ldg(a.lens + b))) set_status(a.status, PA_ERR_BAD_SEQ_LEN);
   const uint32_t per = a.num_kv_heads * a.head_groups;
-  const uint32_t items = list_build(list, a.num_seqs, parts) * per;
-  const bool direct = a.num_parts == 1;
+  Parts parts{a, 0};
+  uint32_t items;
+  if (a.num_seqs <= kListSpan) {  // a lane has a sequence, every warp the list
+    int32_t own = lane < a.num_seqs ? __ldg(a.lens + lane) : 0;
+    if (!kv4_len_ok(a, own)) own = 0;
+    float tokens = own;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) tokens += __shfl_xor_sync(kAll, tokens, o);
+    parts.size = choose_part(a, tokens, own, C::kLeast);
+    items = lane < a.num_seqs ? parts.of(own) : 0;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) items += __shfl_xor_sync(kAll, items, o);
+  } else {
+    // whole numbers: the sum has one order of addition
+    unsigned long long* all = reinterpret_cast<unsigned long long*>(stat);
+    if (threadIdx.x == 0) *all = 0;
+    __syncthreads();
+    unsigned long long tokens = 0;
+    for (int b = threadIdx.x; b < a.num_seqs; b += kNT) {
+      const int32_t L = __ldg(a.lens + b);
+      tokens += kv4_len_ok(a, L) ? L : 0;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) tokens += __shfl_xor_sync(kAll, tokens, o);
+    if (lane == 0) atomicAdd(all, tokens);
+    __syncthreads();
+    parts.size = choose_part(a, static_cast<float>(*all), 0, C::kLeast);
+    items = list_build(list, a.num_seqs, parts);
+  }
+  items *= per;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.part_at = parts.size;  // for the join
 
-  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+  // without the marker the control block may hold anything: items by number then
+  Queue* queue = reinterpret_cast<Queue*>(a.part_at + 1);
+  const bool queued = items > gridDim.x &&
+                      __ldg(a.status + kMarkerOffset / 4) == kMarker;
+
+  for (uint32_t item = blockIdx.x; item < items;) {
+    if (threadIdx.x == 0)  // for the next turn; read after barriers
+      next_s = queued ? gridDim.x + atomicAdd(&queue->next, 1u) : item + gridDim.x;
     int b;
     uint32_t part;
     const uint32_t sp = item / per, x = item - sp * per;
@@ -255,9 +348,14 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
       const int64_t row = static_cast<int64_t>(b) * a.num_heads + h0;
       for (int i = threadIdx.x; i < nh * D; i += kNT)
         store_out(a.out, row * D + i, a.out_dtype, L == 0 ? 0.f : qnan());
+      __syncthreads();
+      item = next_s;
+      __syncthreads();
       continue;
     }
-    const int32_t t0 = part * a.part_size, t1 = min(L, t0 + a.part_size);
+    const bool direct = L <= parts.size;  // the only part: no join
+    const int32_t t0 = part * parts.size;
+    const int32_t t1 = L - t0 > parts.size ? t0 + parts.size : L;
     const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq;
     const int BS = a.block_size;
 
@@ -276,6 +374,13 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
           page[mt] = __ldg(table + (a.block_shift >= 0 ? t >> a.block_shift : t / BS));
       }
     };
+    // bytes of a page in the pools, and this lane's 16 in a head's part and in a stage
+    const uint32_t page_rows = static_cast<uint32_t>(a.num_kv_heads) * BS;
+    const uint32_t page_codes = page_rows * (D / 2), page_pairs = page_rows * C::SB;
+    const uint32_t head_codes = kvh * BS * (D / 2) + lane * 16;
+    const uint32_t head_pairs = kvh * BS * C::SB + lane * 16;
+    const uint32_t copy_k = lane / (D / 32) * C::KP + lane % (D / 32) * 16;
+    const uint32_t copy_v = C::kV + lane / (D / 32) * C::KP + lane % (D / 32) * 16;
     const auto issue = [&](int i, uint32_t dst) {
       const int32_t ts = t0 + (i * kWarps + warp) * C::ROWS;
       bool whole = a.paged16 && ts + C::ROWS <= t1;
@@ -286,25 +391,25 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int32_t t = ts + 16 * mt;
-          const int at = a.block_shift >= 0 ? t & (BS - 1) : t % BS;
-          const int64_t row =
-              static_cast<int64_t>(page[mt]) * a.num_kv_heads * BS + (kvh * BS + at);
-          const uint8_t* kc = a.k_codes + row * (D / 2) + lane * 16;
-          const uint8_t* vc = a.v_codes + row * (D / 2) + lane * 16;
-          const uint32_t to = dst + 16 * mt * C::KP + lane / (D / 32) * C::KP +
-                              lane % (D / 32) * 16;
-          const uint32_t vto = dst + C::kV + 16 * mt * C::VP + lane / (D / 32) * C::VP +
-                               lane % (D / 32) * 16;
+          const uint32_t at = a.block_shift >= 0 ? t & (BS - 1) : t % BS;
+          // a page's part of a pool is below 2^32 bytes (paged16)
+          const uint64_t codes = static_cast<uint64_t>(static_cast<uint32_t>(page[mt])) *
+                                     page_codes + (at * (D / 2) + head_codes);
+          const uint8_t* kc = a.k_codes + codes;
+          const uint8_t* vc = a.v_codes + codes;
+          const uint32_t to = dst + copy_k + 16 * mt * C::KP;
+          const uint32_t vto = dst + copy_v + 16 * mt * C::KP;
 #pragma unroll
           for (int u = 0; u < D / 64; ++u) {
             copy16(to + u * (1024 / D) * C::KP, kc + u * 512);
-            copy16(vto + u * (1024 / D) * C::VP, vc + u * 512);
+            copy16(vto + u * (1024 / D) * C::KP, vc + u * 512);
           }
           if (lane < C::SB) {
-            const int64_t from = row * C::SB + lane * 16;
+            const uint64_t pairs = static_cast<uint64_t>(static_cast<uint32_t>(page[mt])) *
+                                       page_pairs + (at * C::SB + head_pairs);
             const uint32_t pto = dst + C::kKs + 16 * mt * C::SB + lane * 16;
-            copy16(pto, static_cast<const uint8_t*>(a.k_pairs) + from);
-            copy16(pto + (C::kVs - C::kKs), static_cast<const uint8_t*>(a.v_pairs) + from);
+            copy16(pto, static_cast<const uint8_t*>(a.k_pairs) + pairs);
+            copy16(pto + (C::kVs - C::kKs), static_cast<const uint8_t*>(a.v_pairs) + pairs);
           }
         }
       } else if (a.paged16) {
@@ -329,7 +434,7 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
             const int idx = u * 32 + lane, rr = idx / (D / 32), piece = idx % (D / 32);
             const int bytes = rr < n ? 16 : 0;
             copy16(dst + (16 * mt + rr) * C::KP + piece * 16, kc + idx * 16, bytes);
-            copy16(dst + C::kV + (16 * mt + rr) * C::VP + piece * 16, vc + idx * 16, bytes);
+            copy16(dst + C::kV + (16 * mt + rr) * C::KP + piece * 16, vc + idx * 16, bytes);
           }
           if (lane < C::SB) {  // SB pieces of 16 bytes are 16 rows of SB bytes
             const int bytes = min(max(n * C::SB - lane * 16, 0), 16);
@@ -357,7 +462,7 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
           bool ok;
           const int64_t at = place(rr, ok) * (D / 2) + piece * 16;
           copy16(dst + rr * C::KP + piece * 16, a.k_codes + at, ok ? 16 : 0);
-          copy16(dst + C::kV + rr * C::VP + piece * 16, a.v_codes + at, ok ? 16 : 0);
+          copy16(dst + C::kV + rr * C::KP + piece * 16, a.v_codes + at, ok ? 16 : 0);
         }
         constexpr int kPiece = C::SB < 16 ? C::SB : 16;
         for (int idx = lane; idx < C::ROWS * (C::SB / kPiece); idx += 32) {
@@ -371,7 +476,15 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
         }
       }
     };
+    // ---- q: a lane has eight elements of each block of head r; warps take blocks in turn ---
+    constexpr int kOwn = (NB + kWarps - 1) / kWarps;
+    const T* qrow = static_cast<const T*>(a.q) +
+                    (static_cast<int64_t>(b) * a.num_heads + h0 + min(r, nh - 1)) * D + 8 * c;
+    float f[kOwn][8];
     load_pages(0);
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (warp + i * kWarps < NB) load_row<T, 8>(qrow + 32 * (warp + i * kWarps), f[i]);
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
       if (i < stages) {
@@ -380,55 +493,47 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
       }
       copies_commit();
     }
-
-    // ---- q: fragments, and its sums over chunks ---------------------------------------
-    // Unit u = (chunk j, word i) holds a lane's elements d0 .. d0 + 7; warps take units in
-    // turn.  The largest |q| of each head first.
-    const T* qrow = static_cast<const T*>(a.q) +
-                    (static_cast<int64_t>(b) * a.num_heads + h0 + min(r, nh - 1)) * D;
-    const auto first = [&](int u) { return u / W * CH + c * (CH / 4) + u % W * 8; };
-    constexpr int kUnits = D / 32;
+    // the largest |q| of each head; fragments; sums over blocks
     float largest = 0.f;
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      if (u % kWarps != warp) continue;
-      float f[8];
-      load_row<T, 8>(qrow + first(u), f);
+    for (int i = 0; i < kOwn; ++i)
+      if (warp + i * kWarps < NB)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) largest = fmaxf(largest, fabsf(f[e]));
-    }
+        for (int e = 0; e < 8; ++e) largest = fmaxf(largest, fabsf(f[i][e]));
     largest = fmaxf(largest, __shfl_xor_sync(kAll, largest, 1));
     largest = fmaxf(largest, __shfl_xor_sync(kAll, largest, 2));
-    if (c == 0) stat[warp * 8 + r] = largest;
+    if (c == 0 && warp < NB) stat[warp * 8 + r] = largest;
     if (threadIdx.x == 0) bad_s = 0;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) largest = fmaxf(largest, stat[w * 8 + r]);
+    for (int w = 0; w < (kWarps < NB ? kWarps : NB); ++w)
+      largest = fmaxf(largest, stat[w * 8 + r]);
     const int shift = min(14 - exponent(largest), 126);
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      if (u % kWarps != warp) continue;
-      float f[8], sum = 0.f;
-      load_row<T, 8>(qrow + first(u), f);
+    for (int i = 0; i < kOwn; ++i) {
+      const int u = warp + i * kWarps;
+      if (u >= NB) break;
+      float total = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        f[e] = r < nh ? f[e] * pow2(shift) : 0.f;
-        sum += f[e];
+        f[i][e] = r < nh ? f[i][e] * pow2(shift) : 0.f;
+        total += f[i][e];
       }
       // the high halves' elements meet codes 2^4 as large
       constexpr float k16 = 1.f / 16;
-      qf[u * 32 + lane] =
-          make_uint4(pack<__half>(f[0], f[4]), pack<__half>(f[2], f[6]),
-                     pack<__half>(f[1] * k16, f[5] * k16), pack<__half>(f[3] * k16, f[7] * k16));
-      sum += __shfl_xor_sync(kAll, sum, 1);
-      sum += __shfl_xor_sync(kAll, sum, 2);
-      if (c == 0) qs[u * 8 + r] = sum;
+      qf[u * 32 + lane] = make_uint4(pack<__half>(f[i][0], f[i][4]), pack<__half>(f[i][2], f[i][6]),
+                                     pack<__half>(f[i][1] * k16, f[i][5] * k16),
+                                     pack<__half>(f[i][3] * k16, f[i][7] * k16));
+      total += __shfl_xor_sync(kAll, total, 1);
+      total += __shfl_xor_sync(kAll, total, 2);
+      if (c == 0) qs[u * 8 + r] = total;
     }
     // the factor of a logit of this lane's heads 2c, 2c + 1
     float lf[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      lf[e] = a.scale_log2 * pow2(min(24 - __shfl_sync(kAll, shift, (2 * c + e) * 4), 127));
+      lf[e] = fminf(fmaxf(a.scale_log2 * pow2(min(24 - __shfl_sync(kAll, shift, (2 * c + e) * 4),
+                                                  127)), 0x1p-126f), 0x1p127f);
     __syncthreads();
     // The sums of q over groups 2c and 2c + 1 of head r, as B of the product with the
     // minima: three bf16 or two f16 parts.  f16: times 2^16, at most 2^14.
@@ -448,20 +553,23 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
     }
 
     // ---- the part -----------------------------------------------------------------------
-    // eights: rows are chunks; sums: rows r are the minima of group r, r + 8 its scales
-    float o[NCH][kTiles][4], eights[4], sums[4], lim = 0.f, up[NCH];
-    float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    // o: tiles of a block, rows r and r + 8 the elements 4 r + 2 t and 4 r + 2 t + 1.  eights: row
+    // r is group r.  sums: rows r are the minima of group r, r + 8 its scales.
+    float o[NB][2][4], eights[4], sums[4], lim = 0.f, up[NP];
+    float ref[2] = {-INFINITY, -INFINITY}, bar[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      up[j] = 0.f;
+    for (int j = 0; j < NP; ++j) up[j] = 0.f;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][t][e] = 0.f;
-    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) eights[e] = sums[e] = 0.f;
 
+    // this lane's row and 16 bytes for LDSM: two blocks of 16 tokens
+    const uint32_t ldsm_at = (lane & 15) * C::KP + (lane >> 4) * 16;
     uint8_t* st = ring;                                     // this stage, and
     uint8_t* refill = ring + (C::kStages - 1) * C::kStage;  // the one before it
     for (int i = 0; i < stages; ++i) {
@@ -503,41 +611,39 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
 #pragma unroll
             for (int e = 0; e < 4; ++e) l[mt][e] *= 1.f / kMinUp;
         }
+        constexpr int kPer = GS < 64 ? 1 : 2;  // blocks that an accumulator sums
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          uint4 qv[W];
-#pragma unroll
-          for (int w = 0; w < W; ++w) qv[w] = qf[(j * W + w) * 32 + lane];
+        for (int j = 0; j < NB; j += 2) {
+          const uint4 q0 = qf[j * 32 + lane], q1 = qf[(j + 1) * 32 + lane];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const uint8_t* at = st + (16 * mt + r) * C::KP + j * (CH / 2) + c * (4 * W);
-            uint32_t lo[W], hi[W];
-            load_words(at, lo);
-            load_words(at + 8 * C::KP, hi);
-            float acc[4];
+            // words of blocks j (rows r, r + 8) and j + 1
+            uint32_t w[4];
+            ldsm<false>(w, smem_addr(st) + 16 * mt * C::KP + ldsm_at + 16 * j);
+            float acc[2][4];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-              const uint32_t lo8 = lo[w] >> 8, hi8 = hi[w] >> 8;
-              const uint32_t a0 = lo[w] & kLow, a1 = hi[w] & kLow, a2 = lo8 & kLow,
-                             a3 = hi8 & kLow;
-              if (w == 0) mma0<__half>(acc, a0, a1, a2, a3, qv[w].x, qv[w].y);
-              else mma<__half>(acc, a0, a1, a2, a3, qv[w].x, qv[w].y);
-              mma<__half>(acc, lo[w] & kHigh, hi[w] & kHigh, lo8 & kHigh, hi8 & kHigh, qv[w].z,
-                          qv[w].w);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t lo = w[2 * h], hi = w[2 * h + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+              const uint4 q = h ? q1 : q0;
+              float (&x)[4] = acc[kPer == 2 ? 0 : h];
+              if (h == 0 || kPer == 1)
+                mma0<__half>(x, lo & kLow, hi & kLow, lo8 & kLow, hi8 & kLow, q.x, q.y);
+              else
+                mma<__half>(x, lo & kLow, hi & kLow, lo8 & kLow, hi8 & kLow, q.x, q.y);
+              mma<__half>(x, lo & kHigh, hi & kHigh, lo8 & kHigh, hi8 & kHigh, q.z, q.w);
             }
-            const float s0 = scale_of<T>(kw[mt][0][j * CH / GS]);
-            const float s1 = scale_of<T>(kw[mt][1][j * CH / GS]);
-            l[mt][0] = fmaf(s0, acc[0], l[mt][0]);
-            l[mt][1] = fmaf(s0, acc[1], l[mt][1]);
-            l[mt][2] = fmaf(s1, acc[2], l[mt][2]);
-            l[mt][3] = fmaf(s1, acc[3], l[mt][3]);
+#pragma unroll
+            for (int h = 0; h < 2 / kPer; ++h) {
+              const float s0 = scale_of<T>(kw[mt][0][(j + h) * 32 / GS]);
+              const float s1 = scale_of<T>(kw[mt][1][(j + h) * 32 / GS]);
+              l[mt][0] = fmaf(s0, acc[h][0], l[mt][0]);
+              l[mt][1] = fmaf(s0, acc[h][1], l[mt][1]);
+              l[mt][2] = fmaf(s1, acc[h][2], l[mt][2]);
+              l[mt][3] = fmaf(s1, acc[h][3], l[mt][3]);
+            }
           }
         }
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) l[mt][e] *= lf[e & 1];
       if (n < C::ROWS) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -551,7 +657,7 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) moves = moves || l[mt][e] > ref[e & 1] + 8.f;
+        for (int e = 0; e < 4; ++e) moves = moves || l[mt][e] > bar[e & 1];
       constexpr int kScales = C::ROWS * NP;  // pairs of the stage; lane's are of group lane % NP
       const uint32_t* vpairs = reinterpret_cast<const uint32_t*>(st + C::kVs);
 #pragma unroll
@@ -564,12 +670,13 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
         for (int e = 0; e < 2; ++e) {
           float top = ref[e];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(l[mt][e], l[mt][e + 2]));
+          for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(l[mt][e], l[mt][e + 2]) * lf[e]);
 #pragma unroll
           for (int s = 4; s <= 16; s <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
           const bool m = top > ref[e] + 8.f;
           f[e] = m ? ex2(ref[e] - top) : 1.f;  // 0 where nothing has been seen
           if (m) ref[e] = top;
+          bar[e] = (ref[e] + 8.f) / lf[e];
           sum[e] *= f[e];
         }
         // the groups' powers
@@ -588,15 +695,16 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
         }
         float ge = 1.f;
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          const float gj = __shfl_sync(kAll, g, j * CH / GS);
-          const float lj = __shfl_sync(kAll, lim, j * CH / GS);
+        for (int j = 0; j < NP; ++j) {
+          const float gj = __shfl_sync(kAll, g, j), lj = __shfl_sync(kAll, lim, j);
           up[j] = lj > 0.f ? pow2(7 - exponent(lj)) : 0.f;
           if (j == r) ge = gj;
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t)
+          for (int i = j * (GS / 32); i < (j + 1) * (GS / 32); ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][t][e] *= f[e & 1] * gj;
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i][t][e] *= f[e & 1] * gj;
         }
         eights[0] *= f[0] * ge;
         eights[1] *= f[1] * ge;
@@ -609,7 +717,7 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p = ex2(l[mt][e] - ref[e & 1]);
+          const float p = ex2(fmaf(l[mt][e], lf[e & 1], -ref[e & 1]));
           sum[e & 1] += p;
           pt[(2 * c + (e & 1)) * C::PP + 16 * mt + r + (e & 2) * 4] = p;
         }
@@ -619,7 +727,7 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
       for (int mt = 0; mt < MT; ++mt) {
         F2 pa = *reinterpret_cast<const F2*>(pt + r * C::PP + 16 * mt + 2 * c);
         F2 pb = *reinterpret_cast<const F2*>(pt + r * C::PP + 16 * mt + 2 * c + 8);
-        const uint8_t* at = st + C::kV + (16 * mt + 2 * c) * C::VP;
+        const uint32_t at = smem_addr(st) + C::kV + 16 * mt * C::KP + ldsm_at;
         const uint8_t* sc = st + C::kVs + (16 * mt + 2 * c) * C::SB;
         uint32_t vw[4][NP];
         load_words(sc, vw[0]);
@@ -648,30 +756,29 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
           mma<T>(sums, m0, m1, m2, m3, h0, h1);
           mma<T>(sums, m0, m1, m2, m3, pack<T>(x.x, x.y), pack<T>(y.x, y.y));
         }
+        uint32_t b0 = 0, b1 = 0;  // p s of the group, by MMA columns
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          const F2 u2 = pair(up[j], up[j]);
-          const F2 s01 = pair(scale_of<T>(vw[0][j * CH / GS]), scale_of<T>(vw[1][j * CH / GS]));
-          const F2 s23 = pair(scale_of<T>(vw[2][j * CH / GS]), scale_of<T>(vw[3][j * CH / GS]));
-          const float2 q01 = unpair(mul2(pa, mul2(s01, u2)));
-          const float2 q23 = unpair(mul2(pb, mul2(s23, u2)));
-          const uint32_t b0 = pack<__half>(q01.x, q01.y);
-          const uint32_t b1 = pack<__half>(q23.x, q23.y);
-          const uint32_t eight = j == r ? 0x00080008u : 0u;
-          mma<__half>(eights, eight, 0, eight, 0, b0, b1);
-          // a lane's word of the chunk, and for groups of 32 its half of it
-          const int word = j * (CH / 8) + (W == 2 ? r : r >> 1);
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at + 4 * word);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(at + C::VP + 4 * word);
-          const uint32_t w2 = *reinterpret_cast<const uint32_t*>(at + 8 * C::VP + 4 * word);
-          const uint32_t w3 = *reinterpret_cast<const uint32_t*>(at + 9 * C::VP + 4 * word);
+        for (int j = 0; j < NB; j += 2) {
+          // two tokens' 16 bits of blocks j and j + 1: the transpose weaves them
+          uint32_t w[4];
+          ldsm<true>(w, at + 16 * j);
 #pragma unroll
-          for (int h = 0; h < W; ++h) {
-            const uint32_t pick = (W == 2 ? h : r & 1) ? 0x7632u : 0x5410u;
-            const uint32_t x0 = __byte_perm(w0, w1, pick), x1 = __byte_perm(w2, w3, pick);
-            mma<__half>(o[j][2 * h], x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh, b0, b1);
-            mma<__half>(o[j][2 * h + 1], x0 >> 8 & kLow, x0 >> 8 & kHigh, x1 >> 8 & kLow,
-                        x1 >> 8 & kHigh, b0, b1);
+          for (int h = 0; h < 2; ++h) {
+            if ((j + h) * 32 % GS == 0) {
+              const int g = (j + h) * 32 / GS;
+              const F2 u2 = pair(up[g], up[g]);
+              const F2 s01 = pair(scale_of<T>(vw[0][g]), scale_of<T>(vw[1][g]));
+              const F2 s23 = pair(scale_of<T>(vw[2][g]), scale_of<T>(vw[3][g]));
+              const float2 q01 = unpair(mul2(pa, mul2(s01, u2)));
+              const float2 q23 = unpair(mul2(pb, mul2(s23, u2)));
+              b0 = pack<__half>(q01.x, q01.y);
+              b1 = pack<__half>(q23.x, q23.y);
+              const uint32_t eight = g == r ? 0x00080008u : 0u;
+              mma<__half>(eights, eight, 0, eight, 0, b0, b1);
+            }
+            const uint32_t x0 = w[2 * h], x1 = w[2 * h + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+            mma<__half>(o[j + h][0], x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh, b0, b1);
+            mma<__half>(o[j + h][1], y0 & kLow, y0 & kHigh, y1 & kLow, y1 & kHigh, b0, b1);
           }
         }
       }
@@ -687,7 +794,6 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
 #pragma unroll
       for (int s = 4; s <= 16; s <<= 1) sum[e] += __shfl_xor_sync(kAll, sum[e], s);
     if (bad) bad_s = 1;
-    __syncthreads();  // all warps are done with the ring; bad_s
     if (r == 0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -695,93 +801,100 @@ __global__ void __launch_bounds__(kNT, Cfg<D, GS>::kCtas) pa_kv4_tc_kernel(const
         stat[(kWarps + warp) * 8 + 2 * c + e] = sum[e];
       }
     }
-    float* mine = reinterpret_cast<float*>(smem) + warp * (8 * D);  // [8][D]
+    __syncwarp();
+    float* mine = reinterpret_cast<float*>(ring);  // [8][D]: the warp is done with its ring
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const float down = up[j] > 0.f ? 1.f / up[j] : 0.f;
+    for (int g = 0; g < NP; ++g) {
+      const float down = up[g] > 0.f ? 1.f / up[g] : 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int g = j * CH / GS * 4 + c;
-        const float ex = fmaf(8.f, __shfl_sync(kAll, sums[e + 2], g),
-                              __shfl_sync(kAll, sums[e], g)) * (1.f / kWeightUp);
-        const float ei = __shfl_sync(kAll, eights[e], j * 4 + c) * 0x1p24f;
-        float v[2 * kTiles];
+        const float ex = fmaf(8.f, __shfl_sync(kAll, sums[e + 2], g * 4 + c),
+                              __shfl_sync(kAll, sums[e], g * 4 + c)) * (1.f / kWeightUp);
+        const float ei = __shfl_sync(kAll, eights[e], g * 4 + c) * 0x1p24f;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          // rows r and r + 8 of the MMA: elements 2t and 2t + 1 of the lane's run
-          v[2 * t] = fmaf(o[j][t][e] * 0x1p24f - ei, down, ex);
-          v[2 * t + 1] = fmaf(o[j][t][e + 2] * 0x1p20f - ei, down, ex);
-        }
-        float* to = mine + (2 * c + e) * D + j * CH + r * (CH / 8);
-#pragma unroll
-        for (int t = 0; t < kTiles / 2; ++t)
-          reinterpret_cast<float4*>(to)[t] =
-              make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
-      }
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // lane's warp and head: its weight beside the largest reference, over the sum of all;
-      // a warp without a token weighs nothing
-      const int w = lane >> 3, h = lane & 7;
-      const float m = stat[w * 8 + h], s = stat[(kWarps + w) * 8 + h];
-      float M = fmaxf(m, __shfl_xor_sync(kAll, m, 8));
-      M = fmaxf(M, __shfl_xor_sync(kAll, M, 16));
-      const float f = m == -INFINITY ? (s == 0.f ? 0.f : qnan()) : ex2(m - M);
-      float total = f * s;
-      total += __shfl_xor_sync(kAll, total, 8);
-      total += __shfl_xor_sync(kAll, total, 16);
-      stat[(2 * kWarps + w) * 8 + h] = bad_s ? qnan() : f / total;
-      if (!direct && w == 0 && h < nh) {
-        const int64_t at = (static_cast<int64_t>(b) * a.num_heads + h0 + h) * a.num_parts + part;
-        a.part_max[at] = bad_s ? qnan() : M * kLn2;
-        a.part_sum[at] = total;
+        for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j)
+          *reinterpret_cast<float4*>(mine + (2 * c + e) * D + 32 * j + 4 * r) =
+              make_float4(fmaf(o[j][0][e] * 0x1p24f - ei, down, ex),
+                          fmaf(o[j][0][e + 2] * 0x1p20f - ei, down, ex),
+                          fmaf(o[j][1][e] * 0x1p24f - ei, down, ex),
+                          fmaf(o[j][1][e + 2] * 0x1p20f - ei, down, ex));
       }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < nh * (D / 4); i += kNT) {
       const int h = i / (D / 4), d = i % (D / 4);
+      float M = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w * 8 + h]);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = stat[(2 * kWarps + w) * 8 + h];
-        const float4 y = reinterpret_cast<const float4*>(smem)[(w * 8 + h) * (D / 4) + d];
-        v.x = fmaf(y.x, f, v.x);
-        v.y = fmaf(y.y, f, v.y);
-        v.z = fmaf(y.z, f, v.z);
-        v.w = fmaf(y.w, f, v.w);
+        // a warp's weight beside the largest reference; one without a token weighs nothing
+        const float m = stat[w * 8 + h], s = stat[(kWarps + w) * 8 + h];
+        const float x = m == -INFINITY ? (s == 0.f ? 0.f : qnan()) : ex2(m - M);
+        const float4 y = *reinterpret_cast<const float4*>(
+            smem + w * (C::kStages * C::kStage) + (h * D + 4 * d) * 4);
+        total = fmaf(s, x, total);
+        v.x = fmaf(y.x, x, v.x);
+        v.y = fmaf(y.y, x, v.y);
+        v.z = fmaf(y.z, x, v.z);
+        v.w = fmaf(y.w, x, v.w);
       }
+      const float inv = bad_s ? qnan() : 1.f / total;
+      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
       const int64_t row = static_cast<int64_t>(b) * a.num_heads + h0 + h;
-      if (direct)
+      if (direct) {
         store_out4(a.out, row * D + 4 * d, a.out_dtype, v);
-      else
-        reinterpret_cast<float4*>(a.part_out)[(row * a.num_parts + part) * (D / 4) + d] = v;
+      } else {
+        const int64_t at = row * a.num_parts + part;
+        reinterpret_cast<float4*>(a.part_out)[at * (D / 4) + d] = v;
+        if (d == 0) {
+          a.part_max[at] = bad_s ? qnan() : M * kLn2;
+          a.part_sum[at] = total;
+        }
+      }
     }
     if (bad_s && threadIdx.x == 0) set_status(a.status, PA_ERR_BAD_BLOCK_ID);
+    item = next_s;
     __syncthreads();  // the ring, the statistics and q are written again
   }
+  if (queued && threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(&queue->done, 1u) == gridDim.x - 1) {
+      queue->next = 0;
+      queue->done = 0;
+    }
+  }
+}
+
+template <typename T, int D, int GS, bool kWide>
+cudaError_t launch_w(Kv4Args a, int64_t items, int dev, int sms, cudaStream_t s) {
+  using C = Cfg<D, GS, kWide>;
+  static std::atomic<bool> configured[128];
+  const auto kern = pa_kv4_tc_kernel<T, D, GS, kWide>;
+  constexpr int kMost = C::kOffList + (65536 / kListSpan + 1) * 4;  // the longest list
+  static_assert(kMost <= 227 * 1024, "shared memory of a CTA");
+  if (dev >= 128 || !configured[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+    if (dev < 128) configured[dev].store(true, std::memory_order_release);
+  }
+  a.room = sms * C::kCtas;
+  kern<<<static_cast<unsigned>(items < a.room ? items : a.room), C::kNT,
+         C::kOffList + list_bytes(a.num_seqs), s>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename T, int D, int GS>
 cudaError_t launch_d(const Kv4Args& a, int64_t items, cudaStream_t s) {
-  using C = Cfg<D, GS>;
-  static std::atomic<bool> configured[128];
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const auto kern = pa_kv4_tc_kernel<T, D, GS>;
-  // room for the longest list
-  constexpr int kMost = C::kOffList + (65536 / kListSpan + 1) * 4;
-  if (dev >= 128 || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-    if (e != cudaSuccess) return e;
-    if (dev < 128) configured[dev].store(true, std::memory_order_release);
-  }
-  const int64_t room = static_cast<int64_t>(sms) * C::kCtas;
-  kern<<<static_cast<unsigned>(items < room ? items : room), kNT,
-         C::kOffList + list_bytes(a.num_seqs), s>>>(a);
-  return cudaGetLastError();
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.head_groups;
+  return 2 * pairs <= sms ? launch_w<T, D, GS, true>(a, items, dev, sms, s)
+                          : launch_w<T, D, GS, false>(a, items, dev, sms, s);
 }
 
 template <typename T>
