@@ -30,6 +30,35 @@ __device__ __forceinline__ float2 load_pair(const void* pairs, int64_t i) {
     return widen_pair<T>(__ldg(static_cast<const uint32_t*>(pairs) + i));
 }
 
+// ---- two floats as one operand of the packed instructions -------------------------
+
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 unpair(F2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ F2 add2(F2 x, F2 y) {
+  F2 v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
+  return v;
+}
+__device__ __forceinline__ F2 mul2(F2 x, F2 y) {
+  F2 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
+  return v;
+}
+__device__ __forceinline__ F2 fma2(F2 x, F2 y, F2 z) {
+  F2 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(x), "l"(y), "l"(z));
+  return v;
+}
+
 // ---- decode -------------------------------------------------------------------------
 
 // Whether the call can serve this sequence length.

@@ -18,12 +18,17 @@ namespace pa {
 namespace {
 
 constexpr int kNT = 256;
+constexpr int kHalf = kNT / 2;
 constexpr int kUnroll = 4;  // loads of a lane in flight
+constexpr int kCtas = 6;    // resident on an SM
 
 struct LoadArgs {
-  const uint8_t* codes[2];  // k, v
-  const void* pairs[2];
-  void* out[2];
+  const void* k_codes;
+  const void* v_codes;
+  const void* k_pairs;
+  const void* v_pairs;
+  void* k_out;
+  void* v_out;
   const int32_t* tables;
   const int32_t* lens;
   const int32_t* out_tables;
@@ -60,54 +65,90 @@ __device__ __forceinline__ void put8(T* p, const float (&f)[8]) {
   }
 }
 
+// The values of eight codes.  Four bits at place 4e of a word are a whole number in the
+// mantissa of a float of exponent 23 - 4e: no shift and no conversion, one subtraction.
+__device__ __forceinline__ void widen_codes(uint32_t w, float2 p, float (&f)[8]) {
+  constexpr uint32_t kOne[4] = {0x4b000000u, 0x49000000u, 0x47000000u, 0x45000000u};
+  const F2 s = pair(p.x, p.x), m = pair(p.y, p.y);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const uint32_t x = h ? w >> 16 : w;
+      const F2 c = add2(pair(__uint_as_float((x & (15u << 4 * e)) | kOne[e]),
+                             __uint_as_float((x & (15u << 4 * (e + 1))) | kOne[e + 1])),
+                        pair(-__uint_as_float(kOne[e]), -__uint_as_float(kOne[e + 1])));
+      const float2 v = unpair(fma2(c, s, m));
+      f[4 * h + e] = v.x;
+      f[4 * h + e + 1] = v.y;
+    }
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kNT) pa_load_kv4_kernel(const LoadArgs a) {
+__global__ void __launch_bounds__(kNT, kCtas) pa_load_kv4_kernel(const LoadArgs a) {
   extern __shared__ uint32_t start[];
   const Pages pages{a};
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.num_seqs; b += kNT)
       if (!pages.ok(__ldg(a.lens + b))) set_status(a.status, PA_ERR_BAD_SEQ_LEN);
-  const uint32_t items = list_build(start, a.num_seqs, pages);
+  const uint32_t total = list_build(start, a.num_seqs, pages);
+  // this CTA's run of the list; one half of it takes keys, the other values
+  const uint32_t run = (total + gridDim.x - 1) / gridDim.x;
+  uint32_t i = blockIdx.x * run;
+  const uint32_t end = min(total, i + run);
+  if (i >= end) return;
+  const bool values = threadIdx.x >= kHalf;
   const int32_t units = a.page / 8;
-  for (uint32_t i = blockIdx.x; i < 2 * items; i += gridDim.x) {
-    const int kind = i & 1;
-    int b;
-    uint32_t j;
-    list_find(start, a.num_seqs, pages, i >> 1, b, j);
-    const int32_t from = __ldg(a.tables + static_cast<int64_t>(b) * a.width + j);
-    const int32_t to = __ldg(a.out_tables + static_cast<int64_t>(b) * a.out_width + j);
+  const uint32_t* pool = static_cast<const uint32_t*>(values ? a.v_codes : a.k_codes);
+  const void* pairs = values ? a.v_pairs : a.k_pairs;
+  T* wide = static_cast<T*>(values ? a.v_out : a.k_out);
+  int b;
+  uint32_t j;
+  list_find(start, a.num_seqs, pages, i, b, j);
+  uint32_t have = pages(b);
+  int32_t from = __ldg(a.tables + static_cast<int64_t>(b) * a.width + j);
+  int32_t to = __ldg(a.out_tables + static_cast<int64_t>(b) * a.out_width + j);
+  for (;;) {
     const bool from_ok = from >= 0 && from < a.num_blocks;
     const bool to_ok = to >= 0 && to < a.num_out_blocks;
     if ((!from_ok || !to_ok) && threadIdx.x == 0) set_status(a.status, PA_ERR_BAD_BLOCK_ID);
-    if (!to_ok) continue;
-    T* out = static_cast<T*>(a.out[kind]) + static_cast<int64_t>(to) * a.page;
-    const uint32_t* codes =
-        reinterpret_cast<const uint32_t*>(a.codes[kind]) + static_cast<int64_t>(from) * units;
-    const int64_t pair0 = static_cast<int64_t>(from) * (a.page >> a.group_shift);
-    for (int32_t u0 = threadIdx.x; u0 < units; u0 += kNT * kUnroll) {
+    const int64_t unit0 = from_ok ? static_cast<int64_t>(from) * units : 0;
+    const uint32_t* codes = pool + unit0;
+    const int64_t pair0 = unit0 >> (a.group_shift - 3);
+    T* out = wide + (to_ok ? static_cast<int64_t>(to) * a.page : 0);
+    // the next page's ids arrive while this page is widened
+    if (++i < end) {
+      if (++j >= have) {
+        do have = pages(++b); while (have == 0);  // the list holds another page
+        j = 0;
+      }
+      from = __ldg(a.tables + static_cast<int64_t>(b) * a.width + j);
+      to = __ldg(a.out_tables + static_cast<int64_t>(b) * a.out_width + j);
+    }
+    for (int32_t u0 = threadIdx.x % kHalf; u0 < units && to_ok; u0 += kHalf * kUnroll) {
       uint32_t c[kUnroll];
       float2 p[kUnroll];
 #pragma unroll
       for (int x = 0; x < kUnroll; ++x) {
-        const int32_t u = u0 + x * kNT;
+        const int32_t u = u0 + x * kHalf;
         c[x] = 0;
         p[x] = make_float2(qnan(), qnan());
         if (from_ok && u < units) {
           c[x] = __ldcs(codes + u);
-          p[x] = load_pair<T>(a.pairs[kind], pair0 + (u >> (a.group_shift - 3)));
+          p[x] = load_pair<T>(pairs, pair0 + (u >> (a.group_shift - 3)));
         }
       }
 #pragma unroll
       for (int x = 0; x < kUnroll; ++x) {
-        const int32_t u = u0 + x * kNT;
+        const int32_t u = u0 + x * kHalf;
         if (u >= units) break;
         float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          f[e] = fmaf(static_cast<float>(c[x] >> (4 * e) & 15), p[x].x, p[x].y);
+        widen_codes(c[x], p[x], f);
         put8(out + static_cast<int64_t>(u) * 8, f);
       }
     }
+    if (i >= end) break;
   }
 }
 
@@ -117,7 +158,7 @@ cudaError_t launch(const LoadArgs& a, int64_t most, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>(2 * most, static_cast<int64_t>(sms) * 8);
+  const int64_t grid = std::min<int64_t>(most, static_cast<int64_t>(sms) * kCtas);
   pa_load_kv4_kernel<T>
       <<<static_cast<unsigned>(grid), kNT, list_bytes(a.num_seqs), s>>>(a);
   return cudaGetLastError();
@@ -173,12 +214,12 @@ extern "C" pa_status_t pa_load_kv4(const pa_load_kv4_params_t* p, const void* k_
     if (outputs_overlap(r, sizeof r / sizeof r[0])) return PA_ERR_INVALID_ARG;
   }
   LoadArgs a{};
-  a.codes[0] = static_cast<const uint8_t*>(k_codes);
-  a.codes[1] = static_cast<const uint8_t*>(v_codes);
-  a.pairs[0] = k_scales;
-  a.pairs[1] = v_scales;
-  a.out[0] = k_out;
-  a.out[1] = v_out;
+  a.k_codes = k_codes;
+  a.v_codes = v_codes;
+  a.k_pairs = k_scales;
+  a.v_pairs = v_scales;
+  a.k_out = k_out;
+  a.v_out = v_out;
   a.tables = block_tables;
   a.lens = seq_lens;
   a.out_tables = out_tables;

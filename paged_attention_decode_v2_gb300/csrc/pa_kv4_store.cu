@@ -7,12 +7,13 @@
 // with it.  A group with a value that is not finite, or whose range is not, gets
 // NaN for both and reads back as NaN.
 //
-// D / 8 lanes hold a head row, eight elements each; a group's extremes are a
-// shuffle reduction over group / 8 of them.  One pass: 16 bytes a lane are read,
-// 4 bytes of codes written, and with k_out and v_out the values that the codes
-// stand for.
+// D / 16 lanes hold a head row, sixteen elements each; a group's extremes are a
+// shuffle reduction over group / 16 of them.  One pass: 32 bytes a lane are read, 8
+// bytes of codes written, and with k_out and v_out the values that the codes stand
+// for.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime_api.h>
 
@@ -28,17 +29,52 @@ struct StoreArgs {
   const void* k;
   const void* v;
   const int64_t* slots;
-  uint8_t* codes[2];  // k, v
-  void* pairs[2];
-  void* out[2];       // may be null
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  void* k_pairs;
+  void* v_pairs;
+  void* k_out;        // may be null, and
+  void* v_out;
   int32_t* status;
   int64_t k_stride, v_stride;
   int64_t pool;       // slots of the pool
-  int64_t rows;       // head rows of the call: keys and values
-  int32_t num_kv_heads, block_size, block_shift, group;
+  uint32_t rows;      // head rows of the call: keys and values
+  int32_t num_kv_heads, block_size;
+  int32_t span_shift;               // log2 of the lanes of a group, group_size / 16
+  int32_t head_shift, block_shift;  // log2, or -1
 };
 
-// Eight elements as they are in memory, and widened.
+// Minimum and maximum that are NaN where an operand is.
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float z;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, const __nv_bfloat16*) {
+  const __nv_bfloat162 z = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&x),
+                                       *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, const __nv_bfloat16*) {
+  const __nv_bfloat162 z = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&x),
+                                       *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, const __half*) {
+  const __half2 z = __hmin2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, const __half*) {
+  const __half2 z = __hmax2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+
+// Eight elements as they are in memory, widened, and their extremes.
 template <typename T>
 struct Raw8 {
   uint4 v;
@@ -52,6 +88,14 @@ struct Raw8 {
     widen2(t, v.z, f[4], f[5]);
     widen2(t, v.w, f[6], f[7]);
   }
+  __device__ __forceinline__ void extremes(float& lo, float& hi) const {
+    const T* t = nullptr;
+    float x, y;
+    widen2(t, min2(min2(v.x, v.y, t), min2(v.z, v.w, t), t), x, y);
+    lo = min_nan(x, y);
+    widen2(t, max2(max2(v.x, v.y, t), max2(v.z, v.w, t), t), x, y);
+    hi = max_nan(x, y);
+  }
 };
 template <>
 struct Raw8<float> {
@@ -64,7 +108,73 @@ struct Raw8<float> {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
+  __device__ __forceinline__ void extremes(float& lo, float& hi) const {
+    lo = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)),
+                 min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
+    hi = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)),
+                 max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
+  }
 };
+
+// range / 15, rounded to nearest: the quotient's remainder corrects the product with
+// 1 / 15.  (What float32 keeps less than whole, below 2^-100, takes the division.)
+__device__ __forceinline__ float fifteenth(float range) {
+  if (range < 0x1p-100f) return __fdiv_rn(range, 15.f);
+  const float q = range * (1.f / 15);
+  return fmaf(fmaf(-15.f, q, range), 1.f / 15, q);
+}
+
+// A code by the division.
+__device__ __noinline__ float divided(float d, float s) {
+  return s > 0.f ? fminf(rintf(__fdiv_rn(d, s)), 15.f) : 0.f;
+}
+
+// c = min(15, round(d / s)) of the eight d = x - lo, and the codes packed.  By the approximate
+// reciprocal the quotients are off by less than 2^-18 (15 times 2^-23, the reciprocal's and the
+// product's error), so a rounded one may differ only within that of a half; there d - c s, which
+// is exact, says on which side of the half d is.  (Rows of 16 bits come to a half often: some 1
+// in 500 elements.)  Scales that are subnormal or nearly so take the division.
+__device__ __forceinline__ uint32_t make_codes(const float (&x)[8], float lo, float s,
+                                               F2 (&c)[4]) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  if (!(s > 0.f)) inv = 0.f;  // no range: 0; NaN: the codes do not matter
+  constexpr float kMagic = 0x1.8p23f;  // adding it rounds to a whole number, to even
+  const F2 low = pair(-lo, -lo), by = pair(inv, inv), up = pair(kMagic, kMagic),
+           down = pair(-kMagic, -kMagic), minus = pair(-1.f, -1.f);
+  float far = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 q = unpair(mul2(add2(pair(x[2 * e], x[2 * e + 1]), low), by));
+    const F2 y = pair(fminf(q.x, 15.f), fminf(q.y, 15.f));
+    c[e] = add2(add2(y, up), down);
+    const float2 r = unpair(fma2(c[e], minus, y));
+    far = fmaxf(far, fmaxf(fabsf(r.x), fabsf(r.y)));
+  }
+  if (far > 0.5f - 0x1p-17f) {
+    const float half = 0.5f * s;
+    const auto settle = [&](float d, float k) {
+      const float r = fmaf(-k, s, d), other = k + copysignf(1.f, r);
+      const bool odd = (static_cast<int>(k) & 1) != 0;
+      return fabsf(r) > half || (fabsf(r) == half && odd) ? fminf(other, 15.f) : k;
+    };
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 k = unpair(c[e]);
+      c[e] = pair(settle(x[2 * e] - lo, k.x), settle(x[2 * e + 1] - lo, k.y));
+    }
+  }
+  if (s < 0x1p-100f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c[e] = pair(divided(x[2 * e] - lo, s), divided(x[2 * e + 1] - lo, s));
+  }
+  // four codes are 16 bits of a float's whole number
+  const float2 c0 = unpair(c[0]), c1 = unpair(c[1]), c2 = unpair(c[2]), c3 = unpair(c[3]);
+  const float a = fmaf(16.f, fmaf(16.f, fmaf(16.f, c1.y, c1.x), c0.y), c0.x) + 0x1p23f;
+  const float b = fmaf(16.f, fmaf(16.f, fmaf(16.f, c3.y, c3.x), c2.y), c2.x) + 0x1p23f;
+  return s >= 0.f ? __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410) : 0u;
+}
 
 template <typename T>
 __device__ __forceinline__ float rounded(float x) {
@@ -92,97 +202,115 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
 // kRows: head rows that a lane has in flight.
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(kNT) pa_store_kv4_kernel(const StoreArgs a) {
-  constexpr int LPR = D / 8;        // lanes of a head row
+  constexpr int LPR = D / 16;       // lanes of a head row
   constexpr int kSide = 32 / LPR;   // head rows side by side in a warp
   const int lane = threadIdx.x % LPR, side = threadIdx.x % 32 / LPR;
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kNT + threadIdx.x) / 32;
-  const int64_t r0 = warp * (kRows * kSide) + side;
-  const int H = a.num_kv_heads, span = a.group / 8;  // lanes of a group
+  const uint32_t warp = blockIdx.x * (kNT / 32) + threadIdx.x / 32;
+  const uint32_t r0 = warp * (kRows * kSide) + side;
+  const uint32_t H = a.num_kv_heads;
+  const int span = 1 << a.span_shift;  // lanes of a group
 
-  Raw8<T> raw[kRows];
+  Raw8<T> raw[kRows][2];
   int64_t slot[kRows];
-  int32_t t[kRows];
-  int kind[kRows], head[kRows];
+  uint32_t t[kRows], head[kRows];
+  int kind[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int64_t r = r0 + u * kSide;
+    const uint32_t r = r0 + u * kSide;
     slot[u] = -1;
     if (r >= a.rows) continue;
-    t[u] = static_cast<int32_t>(r / (2 * H));
-    const int x = static_cast<int>(r - static_cast<int64_t>(t[u]) * 2 * H);
-    kind[u] = x >= H;
-    head[u] = x - (kind[u] ? H : 0);
+    const uint32_t x = a.head_shift >= 0 ? r >> a.head_shift : r / H;  // 2 t + kind
+    t[u] = x / 2;
+    kind[u] = x & 1;
+    head[u] = r - x * H;
     slot[u] = __ldg(a.slots + t[u]);
-    const T* src = kind[u] ? static_cast<const T*>(a.v) + t[u] * a.v_stride
-                           : static_cast<const T*>(a.k) + t[u] * a.k_stride;
-    raw[u].load(src + head[u] * D + lane * 8);
+    const T* src = (kind[u] ? static_cast<const T*>(a.v) + t[u] * a.v_stride
+                            : static_cast<const T*>(a.k) + t[u] * a.k_stride) +
+                   head[u] * D + lane * 16;
+    raw[u][0].load(src);
+    raw[u][1].load(src + 8);
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     // every lane of the warp takes part in the reductions
-    float f[8];
-    raw[u].widen(f);
-    float lo = f[0], hi = f[0];
-    bool finite = true;
+    float lo, hi, x, y;
+    raw[u][0].extremes(lo, hi);
+    raw[u][1].extremes(x, y);
+    lo = min_nan(lo, x);
+    hi = max_nan(hi, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, f[e]);
-      hi = fmaxf(hi, f[e]);
-      finite = finite && isfinite(f[e]);
+    for (int o = 1; o < 8; o <<= 1) {
+      if (o >= span) break;
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    for (int o = span / 2; o >= 1; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const unsigned lanes = (1u << span) - 1;  // group / 8 is 16 at most
-    const unsigned all = __ballot_sync(0xffffffffu, finite) >> (threadIdx.x % 32 / span * span);
-    if (slot[u] == -1) continue;              // padding, or no such row
+    if (slot[u] == -1) continue;    // padding, or no such row
     float range = hi - lo;
-    if ((all & lanes) != lanes || !isfinite(range)) lo = range = qnan();
-    const float s = rounded<T>(__fdiv_rn(range, 15.f));
-    uint32_t codes = 0;
+    if (!isfinite(range)) lo = range = qnan();
+    const float s = rounded<T>(std::is_same<T, float>::value ? __fdiv_rn(range, 15.f)
+                                                             : fifteenth(range));
+    T* out = static_cast<T*>(kind[u] ? a.v_out : a.k_out);
+    if (out) out += (static_cast<uint64_t>(t[u]) * H + head[u]) * D + lane * 16;
+    uint2 codes;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float c = s > 0.f ? fminf(rintf(__fdiv_rn(f[e] - lo, s)), 15.f) : 0.f;
-      codes |= static_cast<uint32_t>(c) << (4 * e);
-      f[e] = fmaf(c, s, lo);
+    for (int h = 0; h < 2; ++h) {
+      float f[8];
+      F2 c[4];
+      raw[u][h].widen(f);
+      (h ? codes.y : codes.x) = make_codes(f, lo, s, c);
+      if (out) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = unpair(fma2(c[e], pair(s, s), pair(lo, lo)));
+          f[2 * e] = v.x;
+          f[2 * e + 1] = v.y;
+        }
+        store8(out + 8 * h, f);
+      }
     }
-    T* out = static_cast<T*>(a.out[kind[u]]);
-    if (out) store8(out + (static_cast<int64_t>(t[u]) * H + head[u]) * D + lane * 8, f);
     if (slot[u] < 0 || slot[u] >= a.pool) {
       if (lane == 0) set_status(a.status, PA_ERR_BAD_SLOT);
       continue;
     }
-    const int64_t block =
-        a.block_shift >= 0 ? slot[u] >> a.block_shift : slot[u] / a.block_size;
-    const int64_t row =
-        (block * H + head[u]) * a.block_size + (slot[u] - block * a.block_size);
-    *reinterpret_cast<uint32_t*>(a.codes[kind[u]] + row * (D / 2) + lane * 4) = codes;
-    if (lane % span == 0) {
-      const int64_t i = row * (D / a.group) + lane / span;
+    // block ids and rows of a page are 31 bits
+    const uint32_t block = static_cast<uint32_t>(
+        a.block_shift >= 0 ? slot[u] >> a.block_shift : slot[u] / a.block_size);
+    const uint32_t at = static_cast<uint32_t>(slot[u]) - block * a.block_size;
+    const uint64_t row = static_cast<uint64_t>(block) * (H * a.block_size) +
+                         (head[u] * a.block_size + at);
+    *reinterpret_cast<uint2*>((kind[u] ? a.v_codes : a.k_codes) + row * (D / 2) + lane * 8) =
+        codes;
+    if ((lane & (span - 1)) == 0) {
+      const uint64_t i = row * (LPR >> a.span_shift) + (lane >> a.span_shift);
+      void* pairs = kind[u] ? a.v_pairs : a.k_pairs;
       if constexpr (std::is_same<T, float>::value)
-        static_cast<float2*>(a.pairs[kind[u]])[i] = make_float2(s, lo);
+        static_cast<float2*>(pairs)[i] = make_float2(s, lo);
       else
-        static_cast<uint32_t*>(a.pairs[kind[u]])[i] = pack2<T>(s, lo);
+        static_cast<uint32_t*>(pairs)[i] = pack2<T>(s, lo);
     }
   }
 }
 
 template <typename T, int D, int kRows>
 cudaError_t launch_r(const StoreArgs& a, cudaStream_t s) {
-  constexpr int64_t kPer = kNT / 32 * kRows * (32 / (D / 8));
-  const int64_t ctas = (a.rows + kPer - 1) / kPer;
-  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  pa_store_kv4_kernel<T, D, kRows><<<static_cast<unsigned>(ctas), kNT, 0, s>>>(a);
+  constexpr uint32_t kPer = kNT / 32 * kRows * (32 / (D / 16));
+  pa_store_kv4_kernel<T, D, kRows><<<(a.rows + kPer - 1) / kPer, kNT, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+// Rows in flight for each lane: two, or one while two leave the GPU's SMs without some warps
+// each.
+template <typename T, int D>
+cudaError_t launch_d(const StoreArgs& a, cudaStream_t s) {
+  return a.rows / (32 / (D / 16)) < 152 * 32 ? launch_r<T, D, 1>(a, s) : launch_r<T, D, 2>(a, s);
 }
 
 template <typename T>
 cudaError_t launch(const StoreArgs& a, int D, cudaStream_t s) {
   switch (D) {
-    case 64: return launch_r<T, 64, 2>(a, s);
-    case 128: return launch_r<T, 128, 2>(a, s);
-    default: return launch_r<T, 256, 2>(a, s);
+    case 64: return launch_d<T, 64>(a, s);
+    case 128: return launch_d<T, 128>(a, s);
+    default: return launch_d<T, 256>(a, s);
   }
 }
 
@@ -200,6 +328,11 @@ extern "C" pa_status_t pa_store_kv4(const pa_store_kv4_params_t* p, const void* 
   if (p->block_size < 1 || p->num_blocks < 1) return PA_ERR_INVALID_ARG;
   if (pa_status_t st = check_kv4(p->dtype, p->head_dim, p->group_size)) return st;
   if (p->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->num_kv_heads) * p->block_size >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;
+  // head rows, and those of a CTA past the last, are counted in 31 bits
+  if (static_cast<int64_t>(p->num_tokens) * p->num_kv_heads * 2 + 1024 >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;
   const int64_t D = p->head_dim, T = p->num_tokens, n = p->num_kv_heads * D;
   const int64_t esz = p->dtype == PA_F32 ? 4 : 2;
   if (T > 1 && (p->k_stride < n || p->v_stride < n)) return PA_ERR_INVALID_ARG;
@@ -236,21 +369,23 @@ extern "C" pa_status_t pa_store_kv4(const pa_store_kv4_params_t* p, const void* 
   a.k = k;
   a.v = v;
   a.slots = slots;
-  a.codes[0] = static_cast<uint8_t*>(k_codes);
-  a.codes[1] = static_cast<uint8_t*>(v_codes);
-  a.pairs[0] = k_scales;
-  a.pairs[1] = v_scales;
-  a.out[0] = k_out;
-  a.out[1] = v_out;
+  a.k_codes = static_cast<uint8_t*>(k_codes);
+  a.v_codes = static_cast<uint8_t*>(v_codes);
+  a.k_pairs = k_scales;
+  a.v_pairs = v_scales;
+  a.k_out = k_out;
+  a.v_out = v_out;
   a.status = status;
   a.k_stride = p->k_stride;
   a.v_stride = p->v_stride;
   a.pool = static_cast<int64_t>(p->num_blocks) * p->block_size;
-  a.rows = T * p->num_kv_heads * 2;
+  a.rows = static_cast<uint32_t>(T * p->num_kv_heads * 2);
   a.num_kv_heads = p->num_kv_heads;
   a.block_size = p->block_size;
-  a.block_shift = (p->block_size & (p->block_size - 1)) ? -1 : __builtin_ctz(p->block_size);
-  a.group = p->group_size;
+  const auto shift = [](int n) { return (n & (n - 1)) ? -1 : __builtin_ctz(n); };
+  a.block_shift = shift(p->block_size);
+  a.head_shift = shift(p->num_kv_heads);
+  a.span_shift = shift(p->group_size / 16);
   cudaError_t e;
   switch (p->dtype) {
     case PA_F32: e = launch<float>(a, p->head_dim, stream); break;

@@ -153,23 +153,6 @@ __device__ __forceinline__ uint32_t split(float& x, float& y) {
   y -= f.y;
   return h;
 }
-// Two floats as one operand of the packed instructions.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pair(float x, float y) {
-  F2 v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-  return v;
-}
-__device__ __forceinline__ float2 unpair(F2 v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ F2 mul2(F2 x, F2 y) {
-  F2 v;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
-  return v;
-}
 __device__ __forceinline__ float low_half(const __nv_bfloat16*, uint32_t w) {
   return __uint_as_float(w << 16);
 }
