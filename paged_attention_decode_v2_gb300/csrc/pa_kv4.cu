@@ -37,26 +37,38 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
   return PA_OK;
 }
 
-// Slots of a row of `seqs` sequences for partials.  The tensor-core kernel chooses the
+// Slots of a row for partials.  The tensor-core kernel chooses the
 // parts from the lengths, which may all be the longest or one long among short ones: by
 // partition_size where there are many sequences, else up to kSplit items for each CTA
 // that may be resident (four on each of 152 SMs).
+// Up to single() tokens a row has one part, and the call one launch: a join costs about
+// the time that a CTA needs for them.
 constexpr int64_t kSplit = 8, kRoom = 608;
+int64_t single(const pa_params_t* p) { return 131072 / p->head_dim; }
 
 int64_t pairs_of(const pa_params_t* p, int64_t seqs) {
   return seqs * p->num_kv_heads * head_groups(p);
 }
 int64_t cover(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int64_t most_parts(const pa_params_t* p, int64_t seqs) {
+int64_t most_parts(const pa_params_t* p) {
   const int64_t len = p->max_seq_len;
+  if (len <= single(p)) return 1;
   const int64_t by_size = cover(len, p->partition_size);
-  const int64_t by_room = cover(kSplit * kRoom, pairs_of(p, seqs));
+  const int64_t by_room = cover(kSplit * kRoom, pairs_of(p, p->num_seqs));
   return std::max<int64_t>(1, std::min(cover(len, 64), std::max(by_size, by_room)));
 }
 
-WorkspaceLayout layout_of(const pa_params_t* p, int64_t seqs) {
-  return workspace_layout(seqs, p->num_heads, p->head_dim, most_parts(p, seqs));
+// The bytes of a workspace: room for the slots of this many sequences and of fewer, which
+// may have more parts in all (B * cover(n, B * h) <= n / h + B); never falls as sequences
+// or lengths are added.
+size_t workspace_bytes_of(const pa_params_t* p) {
+  const int64_t B = p->num_seqs, len = p->max_seq_len;
+  int64_t slots = B;
+  if (len > single(p))
+    slots = std::min(B * cover(len, 64), std::max(B * cover(len, p->partition_size),
+                                                  kSplit * kRoom / pairs_of(p, 1) + B));
+  return workspace_layout(1, p->num_heads, p->head_dim, slots).total;
 }
 
 }  // namespace
@@ -68,11 +80,7 @@ extern "C" {
 
 size_t pa_kv4_workspace_size(const pa_params_t* p, const pa_kv4_t* kv4) {
   if (check(p, kv4) != PA_OK) return 0;
-  size_t most = layout_of(p, p->num_seqs).total;
-  // fewer sequences may have more parts in all
-  for (int64_t s = 1; s < p->num_seqs && pairs_of(p, s) < kSplit * kRoom; ++s)
-    most = std::max(most, layout_of(p, s).total);
-  return most;
+  return workspace_bytes_of(p);
 }
 
 pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void* q,
@@ -86,8 +94,9 @@ pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void*
   if (!k_scales || !v_scales || !workspace) return PA_ERR_INVALID_ARG;
   if (!aligned(k_scales, 16) || !aligned(v_scales, 16) || !aligned(workspace, 256))
     return PA_ERR_MISALIGNED;
-  const WorkspaceLayout lay = layout_of(p, p->num_seqs);
-  if (workspace_bytes < lay.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < workspace_bytes_of(p)) return PA_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t parts = most_parts(p);
+  const WorkspaceLayout lay = workspace_layout(p->num_seqs, p->num_heads, p->head_dim, parts);
   char* base = static_cast<char*>(workspace);
 
   Kv4Args a{};
@@ -122,7 +131,7 @@ pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void*
   a.scale_log2 = p->scale * 1.442695040888963407360f;
   // whole tiles; slots as the parts of that size need them
   a.part_floor = static_cast<int32_t>(
-      std::max<int64_t>(64, cover(cover(p->max_seq_len, most_parts(p, p->num_seqs)), 64) * 64));
+      std::max<int64_t>(64, cover(cover(p->max_seq_len, parts), 64) * 64));
   a.part_at = reinterpret_cast<int32_t*>(base + kPartOffset);
   a.num_parts = static_cast<int32_t>(
       std::max<int64_t>(1, cover(p->max_seq_len, a.part_floor)));

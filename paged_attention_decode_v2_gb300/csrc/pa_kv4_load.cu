@@ -8,6 +8,7 @@
 // Bound by memory, mostly by the 16-bit pages written.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime_api.h>
 
@@ -19,8 +20,8 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr int kHalf = kNT / 2;
-constexpr int kUnroll = 4;  // loads of a lane in flight
-constexpr int kCtas = 6;    // resident on an SM
+constexpr int kUnroll = 8;  // loads of a lane in flight
+constexpr int kCtas = 4;    // resident on an SM
 
 struct LoadArgs {
   const void* k_codes;
@@ -35,7 +36,6 @@ struct LoadArgs {
   int32_t* status;
   int32_t num_seqs, block_size, num_blocks, num_out_blocks, width, out_width, max_len;
   int32_t page;         // elements of a page: Hkv * block_size * D
-  int32_t group_shift;  // log2 of the group's size
 };
 
 struct Pages {
@@ -85,7 +85,7 @@ __device__ __forceinline__ void widen_codes(uint32_t w, float2 p, float (&f)[8])
   }
 }
 
-template <typename T>
+template <typename T, int GS>
 __global__ void __launch_bounds__(kNT, kCtas) pa_load_kv4_kernel(const LoadArgs a) {
   extern __shared__ uint32_t start[];
   const Pages pages{a};
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_load_kv4_kernel(const LoadArgs 
     if ((!from_ok || !to_ok) && threadIdx.x == 0) set_status(a.status, PA_ERR_BAD_BLOCK_ID);
     const int64_t unit0 = from_ok ? static_cast<int64_t>(from) * units : 0;
     const uint32_t* codes = pool + unit0;
-    const int64_t pair0 = unit0 >> (a.group_shift - 3);
+    const int64_t pair0 = unit0 / (GS / 8);
     T* out = wide + (to_ok ? static_cast<int64_t>(to) * a.page : 0);
     // the next page's ids arrive while this page is widened
     if (++i < end) {
@@ -126,41 +126,53 @@ __global__ void __launch_bounds__(kNT, kCtas) pa_load_kv4_kernel(const LoadArgs 
       from = __ldg(a.tables + static_cast<int64_t>(b) * a.width + j);
       to = __ldg(a.out_tables + static_cast<int64_t>(b) * a.out_width + j);
     }
-    for (int32_t u0 = threadIdx.x % kHalf; u0 < units && to_ok; u0 += kHalf * kUnroll) {
+    // unit u has pair u / kPer; a lane's units are kHalf apart
+    constexpr int kPer = GS / 8;
+    const auto widen = [&](int32_t u0, auto whole) {
       uint32_t c[kUnroll];
       float2 p[kUnroll];
 #pragma unroll
       for (int x = 0; x < kUnroll; ++x) {
-        const int32_t u = u0 + x * kHalf;
         c[x] = 0;
         p[x] = make_float2(qnan(), qnan());
-        if (from_ok && u < units) {
-          c[x] = __ldcs(codes + u);
-          p[x] = load_pair<T>(pairs, pair0 + (u >> (a.group_shift - 3)));
+        if (whole.value || u0 + x * kHalf < units) {
+          if (whole.value || from_ok) {
+            c[x] = __ldcs(codes + u0 + x * kHalf);
+            p[x] = load_pair<T>(pairs, pair0 + u0 / kPer + x * (kHalf / kPer));
+          }
         }
       }
 #pragma unroll
       for (int x = 0; x < kUnroll; ++x) {
-        const int32_t u = u0 + x * kHalf;
-        if (u >= units) break;
+        if (!whole.value && u0 + x * kHalf >= units) break;
         float f[8];
         widen_codes(c[x], p[x], f);
-        put8(out + static_cast<int64_t>(u) * 8, f);
+        put8(out + static_cast<int64_t>(u0 + x * kHalf) * 8, f);
       }
-    }
+    };
+    if (to_ok)
+      for (int32_t u0 = threadIdx.x % kHalf; u0 < units; u0 += kHalf * kUnroll) {
+        if (from_ok && u0 + (kUnroll - 1) * kHalf < units) widen(u0, std::true_type{});
+        else widen(u0, std::false_type{});
+      }
     if (i >= end) break;
   }
 }
 
 template <typename T>
-cudaError_t launch(const LoadArgs& a, int64_t most, cudaStream_t s) {
+cudaError_t launch(const LoadArgs& a, int64_t most, int group, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>(most, static_cast<int64_t>(sms) * kCtas);
-  pa_load_kv4_kernel<T>
-      <<<static_cast<unsigned>(grid), kNT, list_bytes(a.num_seqs), s>>>(a);
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>(most, static_cast<int64_t>(sms) * kCtas));
+  const size_t smem = list_bytes(a.num_seqs);
+  switch (group) {
+    case 32: pa_load_kv4_kernel<T, 32><<<grid, kNT, smem, s>>>(a); break;
+    case 64: pa_load_kv4_kernel<T, 64><<<grid, kNT, smem, s>>>(a); break;
+    default: pa_load_kv4_kernel<T, 128><<<grid, kNT, smem, s>>>(a); break;
+  }
   return cudaGetLastError();
 }
 
@@ -232,14 +244,13 @@ extern "C" pa_status_t pa_load_kv4(const pa_load_kv4_params_t* p, const void* k_
   a.out_width = p->max_out_blocks_per_seq;
   a.max_len = p->max_seq_len;
   a.page = static_cast<int32_t>(page);
-  a.group_shift = __builtin_ctz(p->group_size);
   // no page at all: the lengths are still looked at
   const int64_t grid = std::max<int64_t>(most, 1);
   cudaError_t e;
   switch (p->dtype) {
-    case PA_F32: e = launch<float>(a, grid, stream); break;
-    case PA_BF16: e = launch<__nv_bfloat16>(a, grid, stream); break;
-    default: e = launch<__half>(a, grid, stream); break;
+    case PA_F32: e = launch<float>(a, grid, p->group_size, stream); break;
+    case PA_BF16: e = launch<__nv_bfloat16>(a, grid, p->group_size, stream); break;
+    default: e = launch<__half>(a, grid, p->group_size, stream); break;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

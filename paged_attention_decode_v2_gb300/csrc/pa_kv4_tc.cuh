@@ -46,7 +46,7 @@ struct Cfg {
   static constexpr int kWarps = kWide ? (D == 256 ? 12 : 16) : 4;
   static constexpr int kCtas = kWide ? 1 : D == 256 ? 3 : 4;
   static constexpr int kNT = kWarps * 32;
-  static constexpr int kLeast = kWide ? 512 : 256;  // tokens of a part that pay for its join
+  static constexpr int kLeast = 128;  // tokens of a part that pay for its join
   static constexpr int NB = D / 32;             // blocks of 32 elements: a word of keys a lane
   static constexpr int NP = D / GS;             // pairs of a head row
   static constexpr int SB = NP * 4;             //   and their bytes
@@ -219,8 +219,9 @@ struct Parts {
 // Never below `least` (nor below what the workspace has slots for).  In float32: nothing
 // depends on the size but speed.
 constexpr float kStart = 250.f;
-__device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, int32_t own,
-                                               int32_t least) {
+__device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, float longest,
+                                               int32_t own, int32_t least) {
+  if (a.num_parts == 1) return max((a.max_len + 63) / 64 * 64, 64);
   const float per = static_cast<float>(a.num_kv_heads * a.head_groups);
   const float pairs = per * a.num_seqs, room = a.room, share = tokens * per / room;
   least = max(least, a.part_floor);
@@ -229,7 +230,11 @@ __device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, i
     return n >= static_cast<float>(most) ? most
                                          : max((static_cast<int32_t>(ceilf(n)) + 63) / 64 * 64, least);
   };
-  if (2.f * pairs > room) return within(sqrtf(2.f * kStart * share));
+  if (2.f * pairs > room) {
+    const float n = sqrtf(2.f * kStart * share);
+    return within(pairs <= room && longest <= share + n ? longest : n);  // undivided if even
+  }
+  if (a.num_seqs == 1) return within(__fdividef(tokens, floorf(__fdividef(room, per))));
   int32_t hi = within(tokens * per / (room - pairs));
   if (a.num_seqs > 32) return hi;
   // lanes hold the lengths: the fewest tokens, to some steps, with which all items have CTAs
@@ -285,27 +290,41 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
     int32_t own = lane < a.num_seqs ? __ldg(a.lens + lane) : 0;
     if (!kv4_len_ok(a, own)) own = 0;
     float tokens = own;
+    int32_t longest = own;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) tokens += __shfl_xor_sync(kAll, tokens, o);
-    parts.size = choose_part(a, tokens, own, C::kLeast);
+    for (int o = 16; o >= 1; o >>= 1) {
+      tokens += __shfl_xor_sync(kAll, tokens, o);
+      longest = max(longest, __shfl_xor_sync(kAll, longest, o));
+    }
+    parts.size = choose_part(a, tokens, longest, own, C::kLeast);
     items = lane < a.num_seqs ? parts.of(own) : 0;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) items += __shfl_xor_sync(kAll, items, o);
   } else {
     // whole numbers: the sum has one order of addition
     unsigned long long* all = reinterpret_cast<unsigned long long*>(stat);
-    if (threadIdx.x == 0) *all = 0;
+    if (threadIdx.x == 0) all[0] = all[1] = 0;
     __syncthreads();
     unsigned long long tokens = 0;
+    int32_t longest = 0;
     for (int b = threadIdx.x; b < a.num_seqs; b += kNT) {
       const int32_t L = __ldg(a.lens + b);
-      tokens += kv4_len_ok(a, L) ? L : 0;
+      if (!kv4_len_ok(a, L)) continue;
+      tokens += L;
+      longest = max(longest, L);
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) tokens += __shfl_xor_sync(kAll, tokens, o);
-    if (lane == 0) atomicAdd(all, tokens);
+    for (int o = 16; o >= 1; o >>= 1) {
+      tokens += __shfl_xor_sync(kAll, tokens, o);
+      longest = max(longest, __shfl_xor_sync(kAll, longest, o));
+    }
+    if (lane == 0) {
+      atomicAdd(all, tokens);
+      atomicMax(all + 1, static_cast<unsigned long long>(longest));
+    }
     __syncthreads();
-    parts.size = choose_part(a, static_cast<float>(*all), 0, C::kLeast);
+    parts.size = choose_part(a, static_cast<float>(all[0]), static_cast<float>(all[1]), 0,
+                             C::kLeast);
     items = list_build(list, a.num_seqs, parts);
   }
   items *= per;
@@ -876,7 +895,12 @@ cudaError_t launch_d(const Kv4Args& a, int64_t items, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.head_groups;
-  return 2 * pairs <= sms ? launch_w<T, D, GS, true>(a, items, dev, sms, s)
+  // Wide CTAs: fewer, larger parts and one join of their warps where there are few pairs.
+  // Measured (24 / 4 heads of 256): one sequence of 100K 33.6 us, narrow 35.8; 8192 tokens 13.2
+  // and 14.5; four of 900 in one part each (32 / 8 of 128) 10.9 and 13.6.  32 pairs leave a
+  // third of a round idle: four of 20000 33.1, narrow 29.2.
+  const bool wide = 2 * pairs <= sms && (8 * pairs <= sms || a.num_parts == 1);
+  return wide ? launch_w<T, D, GS, true>(a, items, dev, sms, s)
                           : launch_w<T, D, GS, false>(a, items, dev, sms, s);
 }
 
