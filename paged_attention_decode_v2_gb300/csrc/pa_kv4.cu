@@ -31,8 +31,9 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
   if (static_cast<int64_t>(p->num_seqs) * p->num_heads >= (int64_t(1) << 31))
     return PA_ERR_UNSUPPORTED;  // a CTA of the join per row
   if (static_cast<int64_t>(p->num_kv_heads) * head_groups(p) > 65535) return PA_ERR_UNSUPPORTED;
-  // token positions up to two parts past the longest sequence are int32
-  if (static_cast<int64_t>(p->max_seq_len) + 2LL * p->partition_size + 256 >= (int64_t(1) << 31))
+  // token positions up to some tiles past the longest sequence are int32
+  if (static_cast<int64_t>(p->max_seq_len) + 4096 >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(p->partition_size) + 4096 >= (int64_t(1) << 31))
     return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }

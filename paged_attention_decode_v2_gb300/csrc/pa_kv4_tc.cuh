@@ -511,6 +511,10 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
     for (int w = 0; w < (kWarps < NB ? kWarps : NB); ++w)
       largest = fmaxf(largest, stat[w * 8 + r]);
     const int shift = min(14 - exponent(largest), 126);
+    // the sign of the logits' scale goes with q, so that larger products are larger logits
+    const float by = a.scale_log2 > 0.f   ? pow2(shift)
+                     : a.scale_log2 < 0.f ? -pow2(shift)
+                                          : a.scale_log2 * pow2(shift);
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       const int u = warp + i * kWarps;
@@ -518,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
       float total = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        f[i][e] = r < nh ? f[i][e] * pow2(shift) : 0.f;
+        f[i][e] = r < nh ? f[i][e] * by : 0.f;
         total += f[i][e];
       }
       // the high halves' elements meet codes 2^4 as large
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
     float lf[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      lf[e] = fminf(fmaxf(a.scale_log2 * pow2(min(24 - __shfl_sync(kAll, shift, (2 * c + e) * 4),
+      lf[e] = fminf(fmaxf(fabsf(a.scale_log2) * pow2(min(24 - __shfl_sync(kAll, shift, (2 * c + e) * 4),
                                                   127)), 0x1p-126f), 0x1p127f);
     __syncthreads();
     // The sums of q over groups 2c and 2c + 1 of head r, as B of the product with the

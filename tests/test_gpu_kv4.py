@@ -283,7 +283,7 @@ def run_decode(q, pool, tables, lens, scale=None, max_len=None, out_dtype=None, 
         ws.fill_(0xFF)                                      # NaN everywhere
         pa.workspace_init(ws)
     pa.decode_kv4(qg, kc, vc, ks, vs, bt, i32(lens), out, ws, max_seq_len=max_len,
-                  scale=scale or d ** -0.5, partition_size=partition_size, portable=portable)
+                  scale=d ** -0.5 if scale is None else scale, partition_size=partition_size, portable=portable)
     torch.cuda.synchronize()
     assert _guards_intact(whole, q.numel(), GUARD_F), "write outside out"
     if workspace is None:
@@ -312,6 +312,20 @@ def test_decode(hq, hkv, d, bs, group, lens, dtype, portable):
         kr.assert_decode(got, ref, mag, step, out_dtype, portable or dtype == F32)
 
 
+@pytest.mark.parametrize("hq,hkv,d,bs,group", [
+    (8, 2, 256, 16, 32), (8, 2, 256, 32, 64), (8, 2, 256, 16, 128), (8, 2, 128, 16, 32),
+    (8, 2, 128, 32, 64), (8, 2, 128, 20, 128), (8, 2, 64, 16, 32), (8, 2, 64, 48, 64)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_decode_batch(hq, hkv, d, bs, group, dtype):
+    """More pairs than half the SMs (80): narrow CTAs, sequences in one part and in several, rows
+    without a token among them."""
+    r = np.random.RandomState(d + group)
+    lens = [int(x) for x in np.exp(r.uniform(0, np.log(1000), size=36))] + [0, 2600, 1, 2176]
+    q, pool, tables, n, ref, mag, step = kr.decode_problem(lens, hq, hkv, d, bs, group, dtype, 3)
+    got = run_decode(q, pool, tables, n, out_dtype=F32)
+    kr.assert_decode(got, ref, mag, step, F32, False)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("portable", [False, True])
 def test_decode_long(dtype, portable):
@@ -322,13 +336,53 @@ def test_decode_long(dtype, portable):
 
 
 def test_decode_many_sequences():
-    """More sequences than the list's spans of 32, most of them short; small parts."""
+    """More sequences than the list's spans of 32 and more items than CTAs, so that they come from
+    the queue; most short, some without a token, some in several parts; the same workspace again
+    and again, in a graph, and one that has not been initialised (its items go by number)."""
     r = np.random.RandomState(1)
-    lens = tuple(int(x) for x in np.exp(r.uniform(0, np.log(700), size=301)))
+    lens = [int(x) for x in np.exp(r.uniform(0, np.log(600), size=301))]
+    lens[7] = lens[64] = lens[300] = 0
+    lens[33], lens[200] = 2900, 5000
     q, pool, tables, n, ref, mag, step = kr.decode_problem(lens, 8, 4, 64, 16, 32, BF16, 6)
+    first = None
     for size in (64, 100, 1024):
         got = run_decode(q, pool, tables, n, partition_size=size)
         kr.assert_decode(got, ref, mag, step, BF16, False)
+        first = got if first is None else first
+    qg, caches, bt, ng = q.cuda(), pool.cuda(), i32(tables), i32(n)
+    kc, vc, ks, vs = caches
+    for init in (True, False):
+        ws = pa.alloc_kv4_workspace(qg, kc, ks, bt, max_seq_len=5000, partition_size=64)
+        if not init:
+            ws.fill_(0x77)
+        out = torch.empty_like(qg)
+        call = lambda: pa.decode_kv4(qg, kc, vc, ks, vs, bt, ng, out, ws, max_seq_len=5000,
+                                     scale=64 ** -0.5, partition_size=64)
+        for _ in range(3):
+            out.fill_(math.nan)
+            call()
+            assert torch.equal(out, first)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+            call()
+        for _ in range(2):
+            out.fill_(math.nan)
+            graph.replay()
+            assert torch.equal(out, first)
+        if init:
+            assert pa.read_device_status(ws) == pa.PA_OK
+    # bad lengths and pages among them
+    m, t = n.clone(), tables.clone()
+    m[40], m[290] = -3, 5001
+    t[33, 100], t[250, 0] = -1, pool.k.shape[0]
+    bad = [33, 40, 290] + ([250] if lens[250] else [])
+    whole = run_decode(q, pool, tables, m, max_len=5000, status=pa.PA_ERR_BAD_SEQ_LEN)
+    assert torch.isnan(whole[[40, 290]]).all()
+    whole = run_decode(q, pool, t, n, status=pa.PA_ERR_BAD_BLOCK_ID)
+    assert torch.isnan(whole[[33] + ([250] if lens[250] else [])]).all()
+    keep = [b for b in range(301) if b not in bad]
+    kr.assert_decode(whole[keep], ref[keep], mag[keep], step[keep], BF16, False)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
@@ -373,6 +427,21 @@ def test_decode_queries_of_any_size():
         got = run_decode((q.float() * 2.0 ** e).to(BF16), pool, tables, n, out_dtype=F32,
                          scale=128 ** -0.5 * 2.0 ** -e)
         kr.assert_decode(got, ref, mag, step, F32, False)
+
+
+@pytest.mark.parametrize("portable", [False, True])
+def test_decode_scales_of_any_sign(portable):
+    q, pool, tables, n, ref, mag, step = kr.decode_problem((150, 9), 4, 2, 128, 16, 64, BF16, 12)
+    scale = 128 ** -0.5
+    got = run_decode(-q, pool, tables, n, scale=-scale, out_dtype=F32, portable=portable)
+    kr.assert_decode(got, ref, mag, step, F32, portable)
+    got = run_decode(q, pool, tables, n, scale=1e-40, out_dtype=F32, portable=portable)
+    zero = run_decode(0 * q, pool, tables, n, out_dtype=F32, portable=portable)
+    for b in range(2):                                      # equal weights: the mean
+        v = pool.rows(tables[b], int(n[b]))[1].mean(0).repeat_interleave(2, 0)
+        s = pool.rows(tables[b], int(n[b]))[2].mean(0).repeat_interleave(2, 0)
+        for x in (got, zero):
+            kr.assert_decode(x[b], v, v.abs() + 2, s, F32, portable)
 
 
 @pytest.mark.parametrize("portable", [False, True])
