@@ -286,9 +286,15 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
   const uint32_t per = a.num_kv_heads * a.head_groups;
   Parts parts{a, 0};
   uint32_t items;
-  if (a.num_seqs <= kListSpan) {  // a lane has a sequence, every warp the list
-    int32_t own = lane < a.num_seqs ? __ldg(a.lens + lane) : 0;
-    if (!kv4_len_ok(a, own)) own = 0;
+  // the item at hand: sequence, part, length; the first is found from registers where a lane
+  // has a sequence
+  int b = 0;
+  uint32_t part = 0;
+  int32_t L = 0;
+  bool found = a.num_seqs <= kListSpan;
+  if (found) {
+    const int32_t given = lane < a.num_seqs ? __ldg(a.lens + lane) : 0;
+    const int32_t own = kv4_len_ok(a, given) ? given : 0;
     float tokens = own;
     int32_t longest = own;
 #pragma unroll
@@ -297,9 +303,20 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
       longest = max(longest, __shfl_xor_sync(kAll, longest, o));
     }
     parts.size = choose_part(a, tokens, longest, own, C::kLeast);
-    items = lane < a.num_seqs ? parts.of(own) : 0;
+    const uint32_t n = lane < a.num_seqs ? parts.of(own) : 0;
+    uint32_t sums = n;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) items += __shfl_xor_sync(kAll, items, o);
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kAll, sums, o);
+      if (lane >= o) sums += y;
+    }
+    items = __shfl_sync(kAll, sums, 31);
+    const uint32_t sp = blockIdx.x / per;
+    if (sp < items) {
+      b = __ffs(__ballot_sync(kAll, sp < sums)) - 1;
+      part = sp - __shfl_sync(kAll, sums - n, b);
+      L = __shfl_sync(kAll, given, b);
+    }
   } else {
     // whole numbers: the sum has one order of addition
     unsigned long long* all = reinterpret_cast<unsigned long long*>(stat);
@@ -307,11 +324,11 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
     __syncthreads();
     unsigned long long tokens = 0;
     int32_t longest = 0;
-    for (int b = threadIdx.x; b < a.num_seqs; b += kNT) {
-      const int32_t L = __ldg(a.lens + b);
-      if (!kv4_len_ok(a, L)) continue;
-      tokens += L;
-      longest = max(longest, L);
+    for (int i = threadIdx.x; i < a.num_seqs; i += kNT) {
+      const int32_t one = __ldg(a.lens + i);
+      if (!kv4_len_ok(a, one)) continue;
+      tokens += one;
+      longest = max(longest, one);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
@@ -338,14 +355,15 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
   for (uint32_t item = blockIdx.x; item < items;) {
     if (threadIdx.x == 0)  // for the next turn; read after barriers
       next_s = queued ? gridDim.x + atomicAdd(&queue->next, 1u) : item + gridDim.x;
-    int b;
-    uint32_t part;
     const uint32_t sp = item / per, x = item - sp * per;
-    list_find(list, a.num_seqs, parts, sp, b, part);
+    if (!found) {
+      list_find(list, a.num_seqs, parts, sp, b, part);
+      L = __ldg(a.lens + b);
+    }
+    found = false;
     const int kvh = x / a.head_groups, hg = x - kvh * a.head_groups;
     const int nh = min(kKv4Heads, a.group - hg * kKv4Heads);
     const int h0 = kvh * a.group + hg * kKv4Heads;
-    const int32_t L = __ldg(a.lens + b);
     if (!kv4_len_ok(a, L) || L == 0) {
       const int64_t row = static_cast<int64_t>(b) * a.num_heads + h0;
       for (int i = threadIdx.x; i < nh * D; i += kNT)
