@@ -159,6 +159,10 @@ __device__ __forceinline__ float low_half(const __nv_bfloat16*, uint32_t w) {
 __device__ __forceinline__ float low_half(const __half*, uint32_t w) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
 }
+__device__ __forceinline__ uint32_t times(__half2 x, uint32_t y) {
+  const __half2 z = __hmul2(x, *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
 // The scale of a pair.
 template <typename T>
 __device__ __forceinline__ float scale_of(uint32_t w) {
@@ -265,8 +269,12 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
   constexpr int NB = C::NB, MT = C::MT, NP = C::NP, kWarps = C::kWarps, kNT = C::kNT;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr int kParts = kHalf ? 2 : 3;                  // of the sums of q
-  constexpr float kMinUp = kHalf ? 0x1p16f : 1.f;        // powers of two that keep f16
-  constexpr float kWeightUp = kHalf ? 0x1p7f : 1.f;      // operands in its range
+  constexpr float kMinUp = kHalf ? 0x1p16f : 1.f;        // keeps f16 operands in range
+  // Weights are taken times 2^kUp, and the reference moves when a logit passes it by 2^kBar;
+  // scales are taken times a power of two that leaves the largest below 2^kTop.  All are f16,
+  // their products below 2^15.  Weights 2^-33 of the largest, and scales 2^-28, are still there.
+  constexpr float kUp = 8.f, kBar = 4.f;
+  constexpr int kTop = 3;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int bad_s;
   __shared__ uint32_t next_s;
@@ -579,10 +587,9 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
     // ---- the part -----------------------------------------------------------------------
     // o: tiles of a block, rows r and r + 8 the elements 4 r + 2 t and 4 r + 2 t + 1.  eights: row
     // r is group r.  sums: rows r are the minima of group r, r + 8 its scales.
-    float o[NB][2][4], eights[4], sums[4], lim = 0.f, up[NP];
+    // lim, up: of group lane % NP, the bound of its scales and what they are taken times.
+    float o[NB][2][4], eights[4], sums[4], lim = 0.f, up = 0.f;
     float ref[2] = {-INFINITY, -INFINITY}, bar[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NP; ++j) up[j] = 0.f;
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
@@ -594,6 +601,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
 
     // this lane's row and 16 bytes for LDSM: two blocks of 16 tokens
     const uint32_t ldsm_at = (lane & 15) * C::KP + (lane >> 4) * 16;
+    // where this lane's scales go: token lane / NP (and on), group lane % NP
+    const int scale_at = (lane / (2 * NP) * NP + lane % NP) * 2 + lane / NP % 2;
     uint8_t* st = ring;                                     // this stage, and
     uint8_t* refill = ring + (C::kStages - 1) * C::kStage;  // the one before it
     for (int i = 0; i < stages; ++i) {
@@ -682,12 +691,14 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) moves = moves || l[mt][e] > bar[e & 1];
-      constexpr int kScales = C::ROWS * NP;  // pairs of the stage; lane's are of group lane % NP
+      constexpr int kScales = C::ROWS * NP / 32;  // of the stage, a lane's; of group lane % NP
       const uint32_t* vpairs = reinterpret_cast<const uint32_t*>(st + C::kVs);
+      float vs[kScales];
 #pragma unroll
-      for (int u = 0; u < (kScales + 31) / 32; ++u)
-        if (kScales % 32 == 0 || u * 32 + lane < kScales)
-          moves = moves || fabsf(scale_of<T>(vpairs[u * 32 + lane])) > lim;
+      for (int u = 0; u < kScales; ++u) {
+        vs[u] = scale_of<T>(vpairs[u * 32 + lane]);
+        moves = moves || fabsf(vs[u]) > lim;
+      }
       if (__any_sync(kAll, moves)) {
         float f[2];
 #pragma unroll
@@ -697,31 +708,29 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(l[mt][e], l[mt][e + 2]) * lf[e]);
 #pragma unroll
           for (int s = 4; s <= 16; s <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
-          const bool m = top > ref[e] + 8.f;
+          const bool m = top > ref[e] + kBar;
           f[e] = m ? ex2(ref[e] - top) : 1.f;  // 0 where nothing has been seen
           if (m) ref[e] = top;
-          bar[e] = (ref[e] + 8.f) / lf[e];
+          bar[e] = (ref[e] + kBar) / lf[e];
           sum[e] *= f[e];
         }
         // the groups' powers
         float most = 0.f;
 #pragma unroll
-        for (int u = 0; u < (kScales + 31) / 32; ++u)
-          if (kScales % 32 == 0 || u * 32 + lane < kScales)
-            most = fmaxf(most, fabsf(scale_of<T>(vpairs[u * 32 + lane])));
+        for (int u = 0; u < kScales; ++u) most = fmaxf(most, fabsf(vs[u]));
 #pragma unroll
         for (int s = NP; s <= 16; s <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, s));
         float g = 1.f;
         if (most > lim) {
-          const float to = pow2(min(max(exponent(most) + 1, -119), 127));
+          const float to = pow2(min(max(exponent(most) + 1, -120), 127));
           if (lim > 0.f) g = lim / to;
           lim = to;
+          up = pow2(kTop - exponent(to));
         }
         float ge = 1.f;
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          const float gj = __shfl_sync(kAll, g, j), lj = __shfl_sync(kAll, lim, j);
-          up[j] = lj > 0.f ? pow2(7 - exponent(lj)) : 0.f;
+          const float gj = __shfl_sync(kAll, g, j);
           if (j == r) ge = gj;
 #pragma unroll
           for (int i = j * (GS / 32); i < (j + 1) * (GS / 32); ++i)
@@ -741,44 +750,41 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p = ex2(fmaf(l[mt][e], lf[e & 1], -ref[e & 1]));
+          const float p = ex2(fmaf(l[mt][e], lf[e & 1], kUp - ref[e & 1]));
           sum[e & 1] += p;
           pt[(2 * c + (e & 1)) * C::PP + 16 * mt + r + (e & 2) * 4] = p;
         }
+      // the scales as f16, tokens side by side: [token pair][group], where the keys' pairs were
+      // (all lanes have used them: the vote is behind)
+      uint32_t* ts = reinterpret_cast<uint32_t*>(st + C::kKs);
+#pragma unroll
+      for (int u = 0; u < kScales; ++u)
+        reinterpret_cast<__half*>(ts)[scale_at + u * 32] = __float2half_rn(vs[u] * up);
       __syncwarp();
 
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        F2 pa = *reinterpret_cast<const F2*>(pt + r * C::PP + 16 * mt + 2 * c);
-        F2 pb = *reinterpret_cast<const F2*>(pt + r * C::PP + 16 * mt + 2 * c + 8);
+        float2 pa = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c);
+        float2 pb = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c + 8);
+        const __half2 ha = __floats2half2_rn(pa.x, pa.y), hb = __floats2half2_rn(pb.x, pb.y);
         const uint32_t at = smem_addr(st) + C::kV + 16 * mt * C::KP + ldsm_at;
         const uint8_t* sc = st + C::kVs + (16 * mt + 2 * c) * C::SB;
-        uint32_t vw[4][NP];
-        load_words(sc, vw[0]);
-        load_words(sc + C::SB, vw[1]);
-        load_words(sc + 8 * C::SB, vw[2]);
-        load_words(sc + 9 * C::SB, vw[3]);
+        uint32_t sa[NP], sb[NP];  // scales of tokens 2c, 2c + 1 and 2c + 8, 2c + 9
+        load_words(reinterpret_cast<const uint8_t*>(ts + (8 * mt + c) * NP), sa);
+        load_words(reinterpret_cast<const uint8_t*>(ts + (8 * mt + c + 4) * NP), sb);
         {
           // weights, in two parts of 16 bits, times minima and scales: group r % NP
           uint32_t w[4];
           const int g = r % NP;
-          if constexpr (NP == 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = vw[e][0];
-          } else {
-            const uint32_t* x = reinterpret_cast<const uint32_t*>(sc) + g;
-            w[0] = x[0], w[1] = x[NP], w[2] = x[8 * NP], w[3] = x[9 * NP];
-          }
+          const uint32_t* x = reinterpret_cast<const uint32_t*>(sc) + g;
+          w[0] = x[0], w[1] = x[NP], w[2] = x[8 * NP], w[3] = x[9 * NP];
           const uint32_t m0 = __byte_perm(w[0], w[1], 0x7632);
           const uint32_t m1 = __byte_perm(w[0], w[1], 0x5410);
           const uint32_t m2 = __byte_perm(w[2], w[3], 0x7632);
           const uint32_t m3 = __byte_perm(w[2], w[3], 0x5410);
-          float2 x = unpair(pa), y = unpair(pb);
-          if constexpr (kWeightUp != 1.f)
-            x.x *= kWeightUp, x.y *= kWeightUp, y.x *= kWeightUp, y.y *= kWeightUp;
-          const uint32_t h0 = split<T>(x.x, x.y), h1 = split<T>(y.x, y.y);
+          const uint32_t h0 = split<T>(pa.x, pa.y), h1 = split<T>(pb.x, pb.y);
           mma<T>(sums, m0, m1, m2, m3, h0, h1);
-          mma<T>(sums, m0, m1, m2, m3, pack<T>(x.x, x.y), pack<T>(y.x, y.y));
+          mma<T>(sums, m0, m1, m2, m3, pack<T>(pa.x, pa.y), pack<T>(pb.x, pb.y));
         }
         uint32_t b0 = 0, b1 = 0;  // p s of the group, by MMA columns
 #pragma unroll
@@ -790,13 +796,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           for (int h = 0; h < 2; ++h) {
             if ((j + h) * 32 % GS == 0) {
               const int g = (j + h) * 32 / GS;
-              const F2 u2 = pair(up[g], up[g]);
-              const F2 s01 = pair(scale_of<T>(vw[0][g]), scale_of<T>(vw[1][g]));
-              const F2 s23 = pair(scale_of<T>(vw[2][g]), scale_of<T>(vw[3][g]));
-              const float2 q01 = unpair(mul2(pa, mul2(s01, u2)));
-              const float2 q23 = unpair(mul2(pb, mul2(s23, u2)));
-              b0 = pack<__half>(q01.x, q01.y);
-              b1 = pack<__half>(q23.x, q23.y);
+              b0 = times(ha, sa[g]);
+              b1 = times(hb, sb[g]);
               const uint32_t eight = g == r ? 0x00080008u : 0u;
               mma<__half>(eights, eight, 0, eight, 0, b0, b1);
             }
@@ -829,11 +830,11 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
     float* mine = reinterpret_cast<float*>(ring);  // [8][D]: the warp is done with its ring
 #pragma unroll
     for (int g = 0; g < NP; ++g) {
-      const float down = up[g] > 0.f ? 1.f / up[g] : 0.f;
+      const float u = __shfl_sync(kAll, up, g), down = u > 0.f ? 1.f / u : 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float ex = fmaf(8.f, __shfl_sync(kAll, sums[e + 2], g * 4 + c),
-                              __shfl_sync(kAll, sums[e], g * 4 + c)) * (1.f / kWeightUp);
+                              __shfl_sync(kAll, sums[e], g * 4 + c));
         const float ei = __shfl_sync(kAll, eights[e], g * 4 + c) * 0x1p24f;
 #pragma unroll
         for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j)
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
         reinterpret_cast<float4*>(a.part_out)[at * (D / 4) + d] = v;
         if (d == 0) {
           a.part_max[at] = bad_s ? qnan() : M * kLn2;
-          a.part_sum[at] = total;
+          a.part_sum[at] = total * 0x1p-8f;  // 2^-kUp
         }
       }
     }

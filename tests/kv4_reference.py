@@ -112,13 +112,13 @@ def assert_decode(got, ref, mag, step, out_dtype, portable, logits=1.0, what="")
     by a few 2^-24 of sum |q k|, below 1e-5 where the logits are of order 1 (``logits``: how much
     larger they are here): the weights move by twice that, relatively, and a weighted mean with
     them.  The sums of codes and of minima cancel: each is at most 15 steps beyond the values.
-    The tensor-core kernel rounds weight * scale once to float16, half a step 2^-11, and it
-    multiplies c - 8, at most 8.  One rounding to the output type."""
+    The tensor-core kernel rounds the weight and its product with the scale to float16, half a
+    step 2^-11 each, and they multiply c - 8, at most 8.  One rounding to the output type."""
     got = got.double().cpu()
     assert torch.isfinite(got).all(), f"{what}: non-finite output"
     bound = 2e-5 * logits * (mag + 15 * step) + 1e-6
     if not portable:
-        bound = bound + 2.0 ** -11 * 8 * step
+        bound = bound + 2.0 ** -10 * 8 * step
     bound = bound + HALF_STEP[out_dtype] * (ref.abs() + bound)
     bad = (got - ref).abs() > bound
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
