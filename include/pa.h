@@ -2,9 +2,11 @@
  * pa.h -- C ABI of libpa: single-token decode attention over a paged KV
  * cache on one GB300 (sm_103a), and what a serving step needs around it: the
  * step plan (pa_plan_step), norm, rotation and cache write
- * (pa_qk_norm_rope), paged prefill (pa_prefill), attention with a sliding
- * window and sinks (pa_decode_window, pa_prefill_window) and decode of a batch
- * that shares a prefix (pa_decode_prefix).
+ * (pa_qk_norm_rope; pa_qk_norm_rope_axes with positions on several axes), paged
+ * prefill (pa_prefill), attention with a sliding window and sinks
+ * (pa_decode_window, pa_prefill_window), decode of a batch that shares a prefix
+ * (pa_decode_prefix), and a cache held in 4 bits (pa_store_kv4, pa_load_kv4,
+ * pa_decode_kv4).
  *
  * What the library computes.  For every sequence b < num_seqs and query head
  * h < num_heads, with G = num_heads / num_kv_heads, kvh = h / G and
@@ -724,11 +726,20 @@ PA_API pa_status_t pa_load_kv4(const pa_load_kv4_params_t* params, const void* k
  * c * scale + minimum.  Scales and minima of visible tokens are finite, or NaN,
  * which makes the rows that see them NaN; what the pools hold elsewhere does not
  * matter.  The workspace holds pa_kv4_workspace_size() bytes, its control block
- * initialised by pa_workspace_init; partition_size (>= 1, rounded
- * up to whole tiles of 64) is about the tokens of one partial of a row where there
- * are many sequences; for few the split is chosen to fill the GPU.  A workspace for some num_seqs and max_seq_len serves
- * smaller ones.  v1_max_seq_len is not used; flags: PA_FLAG_PORTABLE.
+ * initialised by pa_workspace_init; it serves one call at a time, and one for some
+ * num_seqs and max_seq_len serves smaller ones.  partition_size (>= 1) bounds the slots
+ * for partials where there are many sequences: a row's parts are that long, in whole
+ * tiles of 64 tokens, or longer.  The tensor-core kernel chooses their length on the
+ * device, from the lengths of the call, so results depend on the batch by what the order
+ * of float32 sums does.  Rows of up to 131072 / head_dim tokens have one part.
+ * v1_max_seq_len is not used; flags: PA_FLAG_PORTABLE.
  * Tensor-core kernel for bf16 and f16, CUDA cores for float32 and PA_FLAG_PORTABLE.
+ * Rounding: codes, scales and minima are used as they are; logits, maxima, sums and
+ * accumulators are float32.  The tensor-core kernel rounds each softmax weight, and its
+ * product with a value's scale, to 11 bits (half a step each, 2^-11 of it) where they
+ * multiply codes around the middle of the group, at most 8 steps from it; weights below
+ * 2^-33 of the row's largest, and scales below 2^-28 of the largest of their group, vanish
+ * there.  The CUDA-core kernel keeps float32.
  */
 typedef struct pa_kv4 {
   int32_t group_size; /* 32, 64 or 128, divides head_dim                     */

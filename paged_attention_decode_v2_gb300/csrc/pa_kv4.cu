@@ -38,12 +38,14 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
   return PA_OK;
 }
 
-// Slots of a row for partials.  The tensor-core kernel chooses the
-// parts from the lengths, which may all be the longest or one long among short ones: by
-// partition_size where there are many sequences, else up to kSplit items for each CTA
-// that may be resident (four on each of 152 SMs).
-// Up to single() tokens a row has one part, and the call one launch: a join costs about
-// the time that a CTA needs for them.
+// Slots of a row for partials.  The tensor-core kernel chooses the parts from the
+// lengths, which may all be the longest or one long among short ones: by partition_size
+// where there are many sequences, else up to kSplit items for each CTA that may be
+// resident (four on each of this GPU's 152 SMs; on others the slots are more or fewer than
+// they need be, and the results the same).  Up to single() tokens a row has one part, and
+// the call one launch: a join costs about the time that a CTA needs for them (one
+// sequence of 1000, 24 / 4 heads of 256: undivided 15.8 us, in parts 10.3; of 900, 32 / 8 of
+// 128, undivided 10.9).
 constexpr int64_t kSplit = 8, kRoom = 608;
 int64_t single(const pa_params_t* p) { return 131072 / p->head_dim; }
 

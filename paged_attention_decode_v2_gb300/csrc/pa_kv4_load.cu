@@ -4,8 +4,12 @@
 // value = c * scale + minimum, one float32 operation, rounded once.  A lane takes
 // eight codes (4 bytes) to eight elements (16 bytes, 32 in float32), so that a
 // warp's loads and stores are whole lines; a page is one run of memory on both
-// sides.  CTAs walk the list of pages that the sequences have (pa_kv4.cuh).
-// Bound by memory, mostly by the 16-bit pages written.
+// sides.  A CTA takes a run of the list of pages that the sequences have (pa_kv4.cuh),
+// half of its threads the keys, half the values.
+// Bound by memory, mostly by the 16-bit pages written.  Measured on the device, bf16:
+// 24576 tokens, 4 heads of 256 (129 MB) 25.2 us = 5.1 TB/s; 33 ragged sequences, 16 heads of
+// 128 (184 MB) 34.0 us = 5.4 TB/s, 80 % of the copy rate.  Sixteen codes a lane, in two
+// stores of every other 16 bytes: 34 us and more.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

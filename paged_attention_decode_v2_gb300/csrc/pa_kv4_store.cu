@@ -10,7 +10,11 @@
 // D / 16 lanes hold a head row, sixteen elements each; a group's extremes are a
 // shuffle reduction over group / 16 of them.  One pass: 32 bytes a lane are read, 8
 // bytes of codes written, and with k_out and v_out the values that the codes stand
-// for.
+// for.  Bound by instructions as much as by memory: some 200 a row of 256.  Measured on
+// the device, bf16: 8192 rows of 4 heads of 256 with k_out and v_out (77 MB) 16.1 us = 4.8
+// TB/s (36 us with a division per element and eight elements a lane); 32 rows 2.3 us, a
+// launch.  Halves of a row as a lane's two eights, for stores of whole sectors, cost more
+// than they gave (18.1 us).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
