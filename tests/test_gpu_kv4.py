@@ -514,6 +514,77 @@ def test_one_workspace_for_smaller_steps():
         kr.assert_decode(got, ref, mag, step, BF16, False)
 
 
+def test_two_graphs_that_share_a_workspace():
+    a = kr.decode_problem((3000, 40), 8, 2, 64, 16, 64, BF16, 30)
+    b = kr.decode_problem([int(x) for x in range(1, 400, 2)] + [2600], 8, 4, 64, 16, 64, BF16, 31)
+    runs = []
+    big = b[0].cuda()
+    ws = pa.alloc_kv4_workspace(big, b[1].k, b[1].ks, torch.zeros(201, 188), max_seq_len=3000)
+    for q, pool, tables, n, ref, mag, step in (a, b):
+        qg, caches, bt, ng = q.cuda(), pool.cuda(), i32(tables), i32(n)
+        bt = torch.nn.functional.pad(bt, (0, 188 - bt.shape[1]), value=-1).contiguous()
+        out = torch.empty_like(qg)
+
+        def call(qg=qg, caches=caches, bt=bt, ng=ng, out=out):
+            pa.decode_kv4(qg, *caches, bt, ng, out, ws, max_seq_len=3000, scale=64 ** -0.5)
+
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, out, ref, mag, step, (qg, caches, bt, ng)))
+    for _ in range(3):
+        for graph, out, ref, mag, step, _ in runs:
+            out.fill_(math.nan)
+            graph.replay()
+            kr.assert_decode(out, ref, mag, step, BF16, False)
+    assert pa.read_device_status(ws) == pa.PA_OK
+
+
+def random_pool(blocks, hkv, bs, d, group, seed):
+    """Codes at random, steps of 0.2 to 0.4, made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    kc, vc, ks, vs = pa.alloc_kv4_cache(blocks, hkv, bs, d, group_size=group)
+    for codes, pairs in ((kc, ks), (vc, vs)):
+        codes.copy_(torch.randint(0, 256, codes.shape, generator=g, device="cuda"))
+        pairs[..., 0] = 0.2 + 0.2 * torch.rand(pairs.shape[:-1], generator=g, device="cuda")
+        pairs[..., 1] = -8 * pairs[..., 0]
+    return (kc, vc, ks, vs), g
+
+
+@pytest.mark.parametrize("seqs,longest,hq,hkv", [(5000, 40, 2, 1), (1, 600000, 8, 1),
+                                                 (3, 250000, 10, 1), (700, 3000, 4, 2)])
+def test_many_sequences_and_long_ones_beside_the_portable_kernel(seqs, longest, hq, hkv):
+    d, bs, group = 64, 16, 32
+    lens = torch.randint(0, longest + 1, (seqs,), generator=torch.Generator().manual_seed(seqs))
+    lens[0] = longest
+    pages = (lens + bs - 1) // bs
+    total = int(pages.sum())
+    caches, g = random_pool(total + 1, hkv, bs, d, group, 1)
+    tables = torch.full((seqs, int(pages.max())), -1, dtype=torch.int32)
+    order = torch.randperm(total, generator=torch.Generator().manual_seed(2)).int()
+    at = torch.cumsum(pages, 0) - pages
+    col = torch.arange(tables.shape[1])[None, :]
+    live = col < pages[:, None]
+    tables[live] = order[(at[:, None] + col)[live]]
+    q = torch.randn(seqs, hq, d, generator=g, device="cuda").to(BF16)
+    bt, n = tables.cuda(), lens.int().cuda()
+    outs = []
+    ws = pa.alloc_kv4_workspace(q, caches[0], caches[2], bt, max_seq_len=longest)
+    for portable in (False, True):
+        out = torch.full(q.shape, math.nan, device="cuda")
+        pa.decode_kv4(q, *caches, bt, n, out, ws, max_seq_len=longest, scale=d ** -0.5,
+                      portable=portable)
+        assert pa.read_device_status(ws) == pa.PA_OK
+        outs.append(out.double())
+    # both within assert_decode's bounds of the same values: |v| below 8 steps, steps of 0.4
+    bound = 2 * 2e-5 * (3.2 + 15 * 0.4) + 2.0 ** -10 * 8 * 0.4 + 1e-5
+    assert torch.isfinite(outs[0]).all()
+    assert float((outs[0] - outs[1]).abs().max()) <= bound
+    assert (outs[0][(lens == 0).cuda()] == 0).all()
+
+
 def test_pools_past_32_bits():
     """Codes past 2^31 bytes and pages whose elements pass 2^32: store, load and decode there."""
     hkv, d, bs, group = 8, 256, 64, 128
