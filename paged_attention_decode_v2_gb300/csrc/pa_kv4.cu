@@ -43,20 +43,22 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
 // where there are many sequences, else up to kSplit items for each CTA that may be
 // resident (four on each of this GPU's 152 SMs; on others the slots are more or fewer than
 // they need be, and the results the same).  Up to single() tokens a row has one part, and
-// the call one launch: a join costs about the time that a CTA needs for them (one
-// sequence of 1000, 24 / 4 heads of 256: undivided 15.8 us, in parts 10.3; of 900, 32 / 8 of
-// 128, undivided 10.9).
+// the call one launch: a join costs about the time that a CTA needs for them.  Where the pairs
+// leave most SMs idle, parts pay from half as many on.  Measured, us, undivided and in parts,
+// 32 / 8 heads of 128: two sequences of 400 tokens 8.3 and 8.2, 600 9.4 and 8.4, 1000 11.3 and
+// 8.4; eight of 600 9.7 and 10.0, 800 10.2 and 11.2.
 constexpr int64_t kSplit = 8, kRoom = 608;
-int64_t single(const pa_params_t* p) { return 131072 / p->head_dim; }
-
 int64_t pairs_of(const pa_params_t* p, int64_t seqs) {
   return seqs * p->num_kv_heads * head_groups(p);
+}
+int64_t single(const pa_params_t* p, int64_t seqs) {
+  return (pairs_of(p, seqs) <= kRoom / 32 ? 65536 : 131072) / p->head_dim;
 }
 int64_t cover(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int64_t most_parts(const pa_params_t* p) {
   const int64_t len = p->max_seq_len;
-  if (len <= single(p)) return 1;
+  if (len <= single(p, p->num_seqs)) return 1;
   const int64_t by_size = cover(len, p->partition_size);
   const int64_t by_room = cover(kSplit * kRoom, pairs_of(p, p->num_seqs));
   return std::max<int64_t>(1, std::min(cover(len, 64), std::max(by_size, by_room)));
@@ -68,7 +70,7 @@ int64_t most_parts(const pa_params_t* p) {
 size_t workspace_bytes_of(const pa_params_t* p) {
   const int64_t B = p->num_seqs, len = p->max_seq_len;
   int64_t slots = B;
-  if (len > single(p))
+  if (len > single(p, 1))
     slots = std::min(B * cover(len, 64), std::max(B * cover(len, p->partition_size),
                                                   kSplit * kRoom / pairs_of(p, 1) + B));
   return workspace_layout(1, p->num_heads, p->head_dim, slots).total;

@@ -925,13 +925,15 @@ cudaError_t launch_d(const Kv4Args& a, int64_t items, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.head_groups;
-  // Wide CTAs: fewer, larger parts and one join of their warps where there are few pairs.
-  // Measured (24 / 4 heads of 256): one sequence of 100K 33.6 us, narrow 35.8; 8192 tokens 13.2
-  // and 14.5; four of 900 in one part each (32 / 8 of 128) 10.9 and 13.6.  32 pairs leave a
-  // third of a round idle: four of 20000 33.1, narrow 29.2.
-  const bool wide = 2 * pairs <= sms && (8 * pairs <= sms || a.num_parts == 1);
+  // Wide CTAs: fewer, larger parts and one join of their warps, where a pair is one part or
+  // the pairs are few and long.  Measured, us, wide and narrow: one part, 32 / 8 heads of 128,
+  // two sequences of 128 tokens 7.0 and 5.5, 256 7.6 and 7.0, 400 8.3 and 9.1, 1000 11.5 and
+  // 13.3; in parts, 24 / 4 of 256, one of 4000 11.7 and 10.5, 8000 13.2 and 13.6, 100K 33.6
+  // and 35.8; four of 32000 (16 pairs) 38.5 and 37.5, of 20000 with 32 pairs 33.1 and 29.2.
+  const bool wide = a.num_parts == 1 ? 2 * pairs <= sms && a.max_len > 320
+                                     : 16 * pairs <= sms && a.max_len > 6000;
   return wide ? launch_w<T, D, GS, true>(a, items, dev, sms, s)
-                          : launch_w<T, D, GS, false>(a, items, dev, sms, s);
+              : launch_w<T, D, GS, false>(a, items, dev, sms, s);
 }
 
 template <typename T>

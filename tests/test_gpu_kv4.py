@@ -326,6 +326,22 @@ def test_decode_batch(hq, hkv, d, bs, group, dtype):
     kr.assert_decode(got, ref, mag, step, F32, False)
 
 
+@pytest.mark.parametrize("hq,d,bs,group", [
+    (4, 256, 16, 32), (10, 256, 32, 64), (6, 256, 16, 128), (8, 128, 16, 32), (4, 128, 32, 64),
+    (12, 128, 20, 128), (6, 64, 16, 32), (16, 64, 48, 64)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("seqs", [1, 2, 24])
+def test_decode_few_pairs(hq, d, bs, group, dtype, seqs):
+    """Two KV heads of a sequence or two past 6000 tokens (wide CTAs, in parts), and of 24 of up to
+    131072 / head_dim (wide CTAs, one part each)."""
+    lens = [6007, 450][:seqs] if seqs < 24 else [131072 // d, 321, 0, 1] + [
+        64 * i + i % 3 - 1 for i in range(1, 7)] * 3 + [500, 130]
+    q, pool, tables, n, ref, mag, step = kr.decode_problem(lens, hq, 2, d, bs, group, dtype,
+                                                           d + group + seqs)
+    got = run_decode(q, pool, tables, n, out_dtype=F32)
+    kr.assert_decode(got, ref, mag, step, F32, False)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("portable", [False, True])
 def test_decode_long(dtype, portable):
