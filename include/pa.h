@@ -731,8 +731,9 @@ PA_API pa_status_t pa_load_kv4(const pa_load_kv4_params_t* params, const void* k
  * for partials where there are many sequences: a row's parts are that long, in whole
  * tiles of 64 tokens, or longer.  The tensor-core kernel chooses their length on the
  * device, from the lengths of the call, so results depend on the batch by what the order
- * of float32 sums does.  Where max_seq_len is at most 131072 / head_dim, rows have one
- * part and the call is one launch.
+ * of float32 sums does.  Where max_seq_len is at most 131072 / head_dim (half of that where
+ * num_seqs * num_kv_heads * ceil(num_heads / num_kv_heads / 8) is at most 19), rows have
+ * one part and the call is one launch.
  * v1_max_seq_len is not used; flags: PA_FLAG_PORTABLE.
  * Tensor-core kernel for bf16 and f16, CUDA cores for float32 and PA_FLAG_PORTABLE.
  * Rounding: codes, scales and minima are used as they are; logits, maxima, sums and
@@ -740,7 +741,9 @@ PA_API pa_status_t pa_load_kv4(const pa_load_kv4_params_t* params, const void* k
  * product with a value's scale, to 11 bits (half a step each, 2^-11 of it) where they
  * multiply codes around the middle of the group, at most 8 steps from it; weights below
  * 2^-33 of the row's largest, and scales below 2^-28 of the largest of their group, vanish
- * there.  The CUDA-core kernel keeps float32.
+ * there.  Queries of 2^116 and more make their row NaN, and the weighted sum of values is
+ * taken times up to 2^12: values whose sum over the row passes 2^115 overflow.  The
+ * CUDA-core kernel keeps float32.
  */
 typedef struct pa_kv4 {
   int32_t group_size; /* 32, 64 or 128, divides head_dim                     */

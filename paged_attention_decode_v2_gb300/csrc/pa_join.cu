@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) pa_join_kernel(const JoinArgs 
       const int kvh = static_cast<int>(row % a.num_heads) / a.group;
       n[l] = prefix_split(L, a.num_heads / a.group, x.key_blocks).segments(kvh) * x.lanes;
     } else {
-      n[l] = x.part_at ? L : (L + x.part_size - 1) / x.part_size;
+      n[l] = x.part_at ? L
+                       : static_cast<int>((static_cast<uint32_t>(L) + x.part_size - 1) / x.part_size);
     }
   }
   // The partials were written while this kernel ran: coherent loads, no __ldg.

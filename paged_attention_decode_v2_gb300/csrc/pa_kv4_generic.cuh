@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(256) pa_kv4_generic_kernel(const Kv4Args a) {
   const bool ok = kv4_len_ok(a, L);
   if (!ok && threadIdx.x == 0 && part == 0) set_status(a.status, PA_ERR_BAD_SEQ_LEN);
   const int32_t t0 = part * a.part_size;
-  const int32_t t1 = ok ? min(L, t0 + a.part_size) : 0;
+  // not past 31 bits in the last part of the longest rows
+  const int32_t t1 = !ok ? 0 : L - t0 > a.part_size ? t0 + a.part_size : L;
   const bool direct = a.num_parts == 1;
   if (t0 >= t1 && !direct) return;                     // the join knows these rows' lengths
   if (threadIdx.x == 0) bad_s = !ok;

@@ -227,16 +227,19 @@ struct Parts {
 //   * Many: a CTA's share of the work is w tokens; parts of n tokens cost it w / n starts,
 //     each worth some kStart tokens, and leave it waiting for about half a part at the end:
 //     n = sqrt(2 kStart w).
-// Never below `least` (nor below what the workspace has slots for).  In float32: nothing
-// depends on the size but speed.
+// Never below `least` (nor below what the workspace has slots for), nor above kLongest: the
+// tensor cores cut off what a sum cannot hold, up to 2^-23 of it with each product added, and
+// this keeps a warp's additions of a part to 2048.  In float32: nothing else depends on the
+// size but speed.
 constexpr float kStart = 250.f;
+constexpr int32_t kLongest = 1 << 17;
 __device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, float longest,
                                                int32_t own, int32_t least) {
   if (a.num_parts == 1) return max((a.max_len + 63) / 64 * 64, 64);
   const float per = static_cast<float>(a.num_kv_heads * a.head_groups);
   const float pairs = per * a.num_seqs, room = a.room, share = tokens * per / room;
   least = max(least, a.part_floor);
-  const int32_t most = max((a.max_len + 63) / 64 * 64, least);
+  const int32_t most = max(min((a.max_len + 63) / 64 * 64, kLongest), least);
   const auto within = [&](float n) {  // whole tiles
     return n >= static_cast<float>(most) ? most
                                          : max((static_cast<int32_t>(ceilf(n)) + 63) / 64 * 64, least);
@@ -543,7 +546,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
 #pragma unroll
     for (int w = 0; w < (kWarps < NB ? kWarps : NB); ++w)
       largest = fmaxf(largest, stat[w * 8 + r]);
-    const int shift = min(14 - exponent(largest), 126);
+    // queries of 2^116 and more become infinite in f16, and their rows NaN
+    const int shift = min(max(14 - exponent(largest), -100), 126);
     // the sign of the logits' scale goes with q, so that larger products are larger logits
     const float by = a.scale_log2 > 0.f   ? pow2(shift)
                      : a.scale_log2 < 0.f ? -pow2(shift)

@@ -437,12 +437,23 @@ def test_decode_steps_that_grow_and_shrink(factor, portable):
 
 
 def test_decode_queries_of_any_size():
-    """Queries up to 2^40 and down to 2^-60 (bf16): logits as with queries of order 1."""
-    for e in (40, 14, -20, -60):
+    """Queries up to 2^100 and down to 2^-60 (bf16): logits as with queries of order 1."""
+    for e in (100, 40, 14, -20, -60):
         q, pool, tables, n, ref, mag, step = kr.decode_problem((200,), 4, 2, 128, 16, 64, BF16, 12)
         got = run_decode((q.float() * 2.0 ** e).to(BF16), pool, tables, n, out_dtype=F32,
                          scale=128 ** -0.5 * 2.0 ** -e)
         kr.assert_decode(got, ref, mag, step, F32, False)
+
+
+def test_decode_queries_past_the_operands():
+    """From 2^116 on a head's row is NaN; the other rows are as they were."""
+    q, pool, tables, n, *_ = kr.decode_problem((200, 90), 8, 2, 128, 16, 64, BF16, 12)
+    want = run_decode(q, pool, tables, n, out_dtype=F32)
+    q[0, 3] *= 2.0 ** 120
+    got = run_decode(q, pool, tables, n, out_dtype=F32)
+    assert bool(got[0, 3].isnan().all())
+    want[0, 3] = got[0, 3] = 0.
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("portable", [False, True])
@@ -599,6 +610,29 @@ def test_many_sequences_and_long_ones_beside_the_portable_kernel(seqs, longest, 
     assert torch.isfinite(outs[0]).all()
     assert float((outs[0] - outs[1]).abs().max()) <= bound
     assert (outs[0][(lens == 0).cuda()] == 0).all()
+
+
+@pytest.mark.parametrize("portable", [False, True])
+def test_the_longest_sequence(portable):
+    """2^31 - 4097 tokens, in 4 pages taken over and over: positions, parts and their count stay
+    in their bits.  The reference counts each of the pages' tokens as often as the row has it."""
+    d, bs, blocks, n = 64, 65536, 4, 2 ** 31 - 4097
+    pool = kr.Pool(blocks, 1, bs, d, 32, BF16, seed=41)
+    pages = torch.empty(blocks, dtype=torch.int32)
+    pool.fill(pages, blocks * bs)
+    q = pool.randn(1, 2, d)
+    k, v, s = pool.rows(pages, blocks * bs)
+    table = pages[torch.arange(-(-n // bs)) % blocks]
+    times = torch.full((blocks * bs,), n // (blocks * bs), dtype=torch.float64)
+    times[:n % (blocks * bs)] += 1
+    ref, mag, step = (torch.empty(1, 2, d, dtype=torch.float64) for _ in range(3))
+    for h in range(2):
+        a = (k[:, 0] @ q[0, h].double()) * d ** -0.5
+        w = torch.softmax(a + times.log(), 0)
+        ref[0, h], mag[0, h], step[0, h] = w @ v[:, 0], w @ v[:, 0].abs(), w @ s[:, 0]
+    got = run_decode(q, pool, table[None], torch.tensor([n], dtype=torch.int32), out_dtype=F32,
+                     portable=portable, partition_size=1 << 18)
+    kr.assert_decode(got, ref, mag, step, F32, portable)
 
 
 def test_pools_past_32_bits():
