@@ -732,8 +732,8 @@ PA_API pa_status_t pa_load_kv4(const pa_load_kv4_params_t* params, const void* k
  * tiles of 64 tokens, or longer.  The tensor-core kernel chooses their length on the
  * device, from the lengths of the call, so results depend on the batch by what the order
  * of float32 sums does.  Where max_seq_len is at most 131072 / head_dim (half of that where
- * num_seqs * num_kv_heads * ceil(num_heads / num_kv_heads / 8) is at most 19), rows have
- * one part and the call is one launch.
+ * num_seqs * num_kv_heads * ceil(num_heads / num_kv_heads / 8) is at most 19, twice where
+ * it is above 1824), rows have one part and the call is one launch.
  * v1_max_seq_len is not used; flags: PA_FLAG_PORTABLE.
  * Tensor-core kernel for bf16 and f16, CUDA cores for float32 and PA_FLAG_PORTABLE.
  * Rounding: codes, scales and minima are used as they are; logits, maxima, sums and

@@ -196,8 +196,6 @@ struct JoinList {
   int32_t max_len;
   int32_t stride;
   int32_t part_size;            // tokens of a partial, unless key_blocks > 0
-  const int32_t* part_at;       // given: where the pass has left them; rows of one partial
-                                //   are written already
   int32_t window, num_sinks;    // window > 0: the length is the visible list's
   int32_t block_list;           //   the block list's (pa_span.cuh), else the plain list's
   int32_t block_size;
@@ -256,6 +254,8 @@ cudaError_t launch_kv4_tc_f16(const Kv4Args& a, int64_t items, cudaStream_t s);
 cudaError_t launch_kv4_generic_f32(const Kv4Args& a, cudaStream_t s);
 cudaError_t launch_kv4_generic_bf16(const Kv4Args& a, cudaStream_t s);
 cudaError_t launch_kv4_generic_f16(const Kv4Args& a, cudaStream_t s);
+// part_at null: parts of part_size, and no row is written yet
+cudaError_t launch_kv4_join(const Kv4Args& a, cudaStream_t s);
 // What the calls on the 4-bit cache take in common.
 pa_status_t check_kv4(pa_dtype_t dtype, int head_dim, int group_size);
 

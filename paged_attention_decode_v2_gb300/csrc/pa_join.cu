@@ -59,18 +59,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps) pa_join_kernel(const JoinArgs 
       const int kvh = static_cast<int>(row % a.num_heads) / a.group;
       n[l] = prefix_split(L, a.num_heads / a.group, x.key_blocks).segments(kvh) * x.lanes;
     } else {
-      n[l] = x.part_at ? L
-                       : static_cast<int>((static_cast<uint32_t>(L) + x.part_size - 1) / x.part_size);
+      n[l] = (L + x.part_size - 1) / x.part_size;
     }
   }
   // The partials were written while this kernel ran: coherent loads, no __ldg.
   cudaGridDependencySynchronize();
-  for (int l = 0; l < 2; ++l) {
-    if (!a.list[l].part_at || !ok) continue;
-    const int32_t size = __ldcg(a.list[l].part_at);
-    if (n[l] > 0 && n[l] <= size) return;
-    n[l] = static_cast<int>((static_cast<uint32_t>(n[l]) + size - 1) / size);
-  }
 
   float m = -INFINITY, w = 0.f, acc[E];
 #pragma unroll

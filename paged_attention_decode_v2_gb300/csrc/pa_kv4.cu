@@ -46,13 +46,17 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
 // the call one launch: a join costs about the time that a CTA needs for them.  Where the pairs
 // leave most SMs idle, parts pay from half as many on.  Measured, us, undivided and in parts,
 // 32 / 8 heads of 128: two sequences of 400 tokens 8.3 and 8.2, 600 9.4 and 8.4, 1000 11.3 and
-// 8.4; eight of 600 9.7 and 10.0, 800 10.2 and 11.2.
+// 8.4; eight of 600 9.7 and 10.0, 800 10.2 and 11.2.  Where they give every CTA several items
+// whatever happens, rows are undivided up to twice as many: 500 of 1200 162 and 167, of 50 to
+// 2000 107 and 113; 256 of 2000 129 and 132, of 50 to 2000 67 and 65; but 160 of 50 to 2000 55
+// and 48.
 constexpr int64_t kSplit = 8, kRoom = 608;
 int64_t pairs_of(const pa_params_t* p, int64_t seqs) {
   return seqs * p->num_kv_heads * head_groups(p);
 }
 int64_t single(const pa_params_t* p, int64_t seqs) {
-  return (pairs_of(p, seqs) <= kRoom / 32 ? 65536 : 131072) / p->head_dim;
+  const int64_t pairs = pairs_of(p, seqs);
+  return (pairs <= kRoom / 32 ? 65536 : pairs <= 3 * kRoom ? 131072 : 262144) / p->head_dim;
 }
 int64_t cover(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -159,24 +163,8 @@ pa_status_t pa_decode_kv4(const pa_params_t* p, const pa_kv4_t* kv4, const void*
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
   if (a.num_parts == 1) return PA_OK;
-  JoinArgs j{};
-  JoinList& l = j.list[0];
-  l.m = a.part_max;
-  l.s = a.part_sum;
-  l.o = a.part_out;
-  l.lens = seq_lens;
-  l.max_len = p->max_seq_len;
-  l.stride = a.num_parts;
-  l.part_size = a.part_size;
-  l.part_at = tc ? a.part_at : nullptr;
-  l.block_size = p->block_size;
-  j.out = out;
-  j.num_rows = static_cast<int64_t>(p->num_seqs) * p->num_heads;
-  j.num_heads = p->num_heads;
-  j.head_dim = p->head_dim;
-  j.group = a.group;
-  j.out_dtype = p->out_dtype;
-  return launch_join(j, stream, true) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (!tc) a.part_at = nullptr;
+  return launch_kv4_join(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -82,7 +82,7 @@ __device__ __forceinline__ void kv4_finish(const Kv4Args& a, int b, int h, int p
   const int64_t at = row * a.num_parts + part;
   a.part_out[at * D + d] = r;
   if (d == 0) {
-    a.part_max[at] = bad ? qnan() : M * kLn2;
+    a.part_max[at] = bad ? qnan() : M;
     a.part_sum[at] = bad ? qnan() : sum;
   }
 }

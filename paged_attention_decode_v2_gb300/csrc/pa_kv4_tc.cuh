@@ -224,14 +224,20 @@ struct Parts {
 //   * Few (sequence, KV head) pairs for the CTAs that are resident: one round, as even as
 //     parts of one size are: the least size that makes no more items than CTAs (32
 //     sequences or fewer), or one that does whatever the lengths are.
-//   * Many: a CTA's share of the work is w tokens; parts of n tokens cost it w / n starts,
-//     each worth some kStart tokens, and leave it waiting for about half a part at the end:
-//     n = sqrt(2 kStart w).
+//   * Many, of different lengths: a CTA's share of the work is w tokens; parts of n tokens cost
+//     it w / n starts, each worth some kStart tokens, and leave it waiting for about half a part
+//     at the end: n = sqrt(2 kStart w).
+//   * Many, most of them nearly as long as the longest: of 1 to 32 even parts of that, the number
+//     with the least rounds of items, the last one counted 0.7 (a CTA that has an SM for itself)
+//     to 1.  Measured, us, by w alone and so: 256 sequences of 2000, 32 / 8 heads of 128, 167 and
+//     132; 100 of 4000 122 and 114; 300 of 2000, 24 / 4 of 256, 176 and 140; 60 of 2000 52 and 45
+//     (40 of 4000, 32 / 8 of 128, 58 and 61).
 // Never below `least` (nor below what the workspace has slots for), nor above kLongest: the
 // tensor cores cut off what a sum cannot hold, up to 2^-23 of it with each product added, and
 // this keeps a warp's additions of a part to 2048.  In float32: nothing else depends on the
 // size but speed.
-constexpr float kStart = 250.f;
+constexpr float kStart = 250.f, kJoin = 350.f;  // the join's launch, too
+constexpr float kEven = 0.8f;
 constexpr int32_t kLongest = 1 << 17;
 __device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, float longest,
                                                int32_t own, int32_t least) {
@@ -245,8 +251,16 @@ __device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, f
                                          : max((static_cast<int32_t>(ceilf(n)) + 63) / 64 * 64, least);
   };
   if (2.f * pairs > room) {
-    const float n = sqrtf(2.f * kStart * share);
-    return within(pairs <= room && longest <= share + n ? longest : n);  // undivided if even
+    if (tokens < kEven * longest * a.num_seqs) return within(sqrtf(2.f * kStart * share));
+    // a lane for every number of parts
+    const int lane = threadIdx.x & 31;
+    const int32_t n = within(__fdividef(longest, lane + 1.f));
+    const float parts = ceilf(__fdividef(longest, static_cast<float>(n)));
+    const float rounds = __fdividef(pairs * parts, room), x = rounds - floorf(rounds);
+    const float cost = (floorf(rounds) + (x > 0.f ? 0.7f + 0.3f * x : 0.f)) * (n + kStart) +
+                       (parts > 1.f ? kJoin : 0.f);
+    const unsigned best = __reduce_min_sync(kAll, (__float_as_uint(cost) & ~31u) | lane);
+    return __shfl_sync(kAll, n, best & 31);
   }
   if (a.num_seqs == 1) return within(__fdividef(tokens, floorf(__fdividef(room, per))));
   int32_t hi = within(tokens * per / (room - pairs));
@@ -885,7 +899,7 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
         const int64_t at = row * a.num_parts + part;
         reinterpret_cast<float4*>(a.part_out)[at * (D / 4) + d] = v;
         if (d == 0) {
-          a.part_max[at] = bad_s ? qnan() : M * kLn2;
+          a.part_max[at] = bad_s ? qnan() : M;
           a.part_sum[at] = total * 0x1p-8f;  // 2^-kUp
         }
       }

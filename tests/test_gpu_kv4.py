@@ -342,6 +342,19 @@ def test_decode_few_pairs(hq, d, bs, group, dtype, seqs):
     kr.assert_decode(got, ref, mag, step, F32, False)
 
 
+@pytest.mark.parametrize("d,group,low,high,seqs", [
+    (64, 32, 2050, 2400, 200), (128, 128, 1025, 1280, 160), (256, 64, 513, 640, 160),
+    (256, 128, 900, 1000, 40), (64, 64, 2100, 2100, 160)])
+def test_decode_even_batch(d, group, low, high, seqs):
+    """Many sequences of about one length: even parts of the longest, or all of it; among them one
+    without a token and one that is short."""
+    r = np.random.RandomState(d + seqs)
+    lens = [int(x) for x in r.randint(low, high + 1, size=seqs - 2)] + [0, 77]
+    q, pool, tables, n, ref, mag, step = kr.decode_problem(lens, 6, 2, d, 16, group, BF16, 9)
+    got = run_decode(q, pool, tables, n, out_dtype=F32)
+    kr.assert_decode(got, ref, mag, step, F32, False)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("portable", [False, True])
 def test_decode_long(dtype, portable):
@@ -581,7 +594,8 @@ def random_pool(blocks, hkv, bs, d, group, seed):
 
 
 @pytest.mark.parametrize("seqs,longest,hq,hkv", [(5000, 40, 2, 1), (1, 600000, 8, 1),
-                                                 (3, 250000, 10, 1), (700, 3000, 4, 2)])
+                                                 (3, 250000, 10, 1), (700, 3000, 4, 2),
+                                                 (1000, 2500, 4, 2)])
 def test_many_sequences_and_long_ones_beside_the_portable_kernel(seqs, longest, hq, hkv):
     d, bs, group = 64, 16, 32
     lens = torch.randint(0, longest + 1, (seqs,), generator=torch.Generator().manual_seed(seqs))
