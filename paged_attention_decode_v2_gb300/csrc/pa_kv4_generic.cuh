@@ -8,8 +8,8 @@
 // all float32, joined in shared memory at the end.  A part that is the whole
 // sequence writes its output, others a partial for pa_kv4_join.cu.
 // Bound by instructions: 4 D operations a token and head, and a butterfly.  Measured, bf16:
-// one sequence of 100K, 24 / 4 heads of 256, 562 us (tensor cores 33); 256 sequences up to
-// 100K, 32 / 8 of 128, 12.1 ms (650 us).
+// one sequence of 100K, 24 / 4 heads of 256, 562 us (tensor cores 32); 256 sequences up to
+// 100K, 32 / 8 of 128, 12.1 ms (626 us).
 #pragma once
 
 #include "pa_kv4.cuh"

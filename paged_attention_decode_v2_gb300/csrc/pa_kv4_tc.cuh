@@ -32,10 +32,10 @@
 // Bound by instructions and by what waits on them, not by memory: a tile of 16 tokens of
 // 128 elements is some 290 warp instructions, 130 of them on the ALU pipe (64 masks and
 // 16 shifts), 22 MMAs.  Measured: 76 sequences of 8192, 32 / 8 heads of 128, one group a
-// row: 141 us = 4.8 TB/s, 71 % of the copy rate; the same kernel's copies alone take 119 us,
-// its arithmetic alone 122.  114 of 4096, 24 / 4 of 256: 101 us = 5.3 TB/s.  One sequence of
-// 100K 33 us with the join (5 us before the first stage, 20 of streaming, 2.5 to join the
-// warps), 256 sequences up to 100K 650 us.
+// row: 140 us = 4.8 TB/s, 72 % of the copy rate; the same kernel's copies alone take 119 us,
+// its arithmetic alone 122.  114 of 4096, 24 / 4 of 256: 99 us = 5.5 TB/s.  One sequence of
+// 100K 32 us with the join (5 us before the first stage, 20 of streaming, 2.5 to join the
+// warps), 256 sequences up to 100K 626 us.
 #pragma once
 
 #include <atomic>
@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
   constexpr int kTop = 3;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int bad_s;
-  __shared__ uint32_t next_s;
+  __shared__ uint32_t next_s, next_part_s;
+  __shared__ int next_b_s, next_len_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;  // row of A, or head of B; column pair
   uint8_t* ring = smem + warp * (C::kStages * C::kStage);
@@ -592,6 +593,15 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
       lf[e] = fminf(fmaxf(fabsf(a.scale_log2) * pow2(min(24 - __shfl_sync(kAll, shift, (2 * c + e) * 4),
                                                   127)), 0x1p-126f), 0x1p127f);
     __syncthreads();
+    // The warp with the fewest tiles looks the next item up (256 sequences up to 100K 640 to 628
+    // us, 500 up to 2000 107 to 105; with its pages' ids as well 632).  Wide CTAs have one, mostly.
+    if (!kWide && warp == kWarps - 1 && next_s < items) {
+      int nb;
+      uint32_t np;
+      list_find(list, a.num_seqs, parts, next_s / per, nb, np);
+      const int32_t nl = __ldg(a.lens + nb);
+      if (lane == 0) next_b_s = nb, next_part_s = np, next_len_s = nl;
+    }
     // The sums of q over groups 2c and 2c + 1 of head r, as B of the product with the
     // minima: three bf16 or two f16 parts.  f16: times 2^16, at most 2^14.
     uint32_t qb[kParts];
@@ -752,22 +762,27 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           lim = to;
           up = pow2(kTop - exponent(to));
         }
-        float ge = 1.f;
+        // The first stage has zeros to scale.  Passing them by, us: 64 sequences of 6000, 24 / 4
+        // heads of 256, 105.5 to 102.9; 33 sequences of bf16, groups of 32, 169.2 to 163.4; but
+        // of f16 161.0 to 163.9, from how it is compiled.
+        if (i > 0 || (kHalf && GS == 32)) {
+          float ge = 1.f;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const float gj = __shfl_sync(kAll, g, j);
-          if (j == r) ge = gj;
+          for (int j = 0; j < NP; ++j) {
+            const float gj = __shfl_sync(kAll, g, j);
+            if (j == r) ge = gj;
 #pragma unroll
-          for (int i = j * (GS / 32); i < (j + 1) * (GS / 32); ++i)
+            for (int i = j * (GS / 32); i < (j + 1) * (GS / 32); ++i)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+              for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[i][t][e] *= f[e & 1] * gj;
+                for (int e = 0; e < 4; ++e) o[i][t][e] *= f[e & 1] * gj;
+          }
+          eights[0] *= f[0] * ge;
+          eights[1] *= f[1] * ge;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sums[e] *= f[e & 1];
         }
-        eights[0] *= f[0] * ge;
-        eights[1] *= f[1] * ge;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sums[e] *= f[e & 1];
       }
 
       // weights, and their transposition: heads as rows, tokens as columns
@@ -906,6 +921,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
     }
     if (bad_s && threadIdx.x == 0) set_status(a.status, PA_ERR_BAD_BLOCK_ID);
     item = next_s;
+    if (!kWide) b = next_b_s, part = next_part_s, L = next_len_s;
+    found = !kWide;
     __syncthreads();  // the ring, the statistics and q are written again
   }
   if (queued && threadIdx.x == 0) {
