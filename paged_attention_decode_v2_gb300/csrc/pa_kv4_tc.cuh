@@ -236,7 +236,7 @@ struct Parts {
 // tensor cores cut off what a sum cannot hold, up to 2^-23 of it with each product added, and
 // this keeps a warp's additions of a part to 2048.  In float32: nothing else depends on the
 // size but speed.
-constexpr float kStart = 250.f, kJoin = 350.f;  // tokens that a start and the join are worth
+constexpr float kStart = 200.f, kJoin = 300.f;  // tokens that a start and the join are worth
 constexpr float kEven = 0.8f;                   // mean over longest
 constexpr int32_t kLongest = 1 << 17;
 __device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, float longest,
