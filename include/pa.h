@@ -737,13 +737,16 @@ PA_API pa_status_t pa_load_kv4(const pa_load_kv4_params_t* params, const void* k
  * v1_max_seq_len is not used; flags: PA_FLAG_PORTABLE.
  * Tensor-core kernel for bf16 and f16, CUDA cores for float32 and PA_FLAG_PORTABLE.
  * Rounding: codes, scales and minima are used as they are; logits, maxima, sums and
- * accumulators are float32.  The tensor-core kernel rounds each softmax weight, and its
- * product with a value's scale, to 11 bits (half a step each, 2^-11 of it) where they
- * multiply codes around the middle of the group, at most 8 steps from it; weights below
- * 2^-33 of the row's largest, and scales below 2^-28 of the largest of their group, vanish
- * there.  Queries of 2^116 and more make their row NaN, and the weighted sum of values is
- * taken times up to 2^12: values whose sum over the row passes 2^115 overflow.  The
- * CUDA-core kernel keeps float32.
+ * accumulators are float32.  With weights taken beside the row's largest, as 1, the
+ * tensor-core kernel rounds the product of a weight and a value's scale once, to 11 bits
+ * (half a step, 2^-11 of it, or 2^-35 of the largest scale of that group in the sequence where
+ * that is more), where it multiplies codes around the middle of the group, at most 8 steps
+ * from it; and the weights that meet the minima to 2^-17 (bf16) or 2^-22 (f16, or 2^-33 of a
+ * weight of 1).  So a token with scales up to 2^24 times another's costs that one no bits,
+ * however little weight it has.  Elements of a query head are whole to 2^-24 of its largest,
+ * below that off by up to 2^-35 of it.  Queries of 2^116 and more make their row NaN, and
+ * the weighted sum of values is taken times up to 2^12: values whose sum over the row passes
+ * 2^115 overflow.  The CUDA-core kernel keeps float32.
  */
 typedef struct pa_kv4 {
   int32_t group_size; /* 32, 64 or 128, divides head_dim                     */

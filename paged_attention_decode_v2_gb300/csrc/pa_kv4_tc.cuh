@@ -21,10 +21,13 @@
 //     The 16 elements of an MMA are those a lane finds in its words (LDSM), q in that
 //     order.
 //   * Values are A with rows d and columns t: LDSM's transpose brings two tokens' 16
-//     bits into one word.  B is p s: p rounded to f16, times s, which is exact there (a
-//     power of two per group, that follows the largest scale seen, keeps it in range),
-//     and the product rounded: two half steps, 2^-11 each of a weight, on c - 8 and not
-//     on c, since the eights are multiplied by the rounded weights too.
+//     bits into one word.  B is p s, multiplied in float32 (with a power of two per group
+//     that follows the largest scale seen) and rounded to f16 once: half a step, 2^-11 of
+//     it, on c - 8 and not on c, since the eights are multiplied by the rounded products
+//     too.  What is 2^-35 of the largest scale, for a weight of 1, is the least step: a token
+//     of the largest weight keeps all its bits while its scale is above 2^-24 of the largest.
+//     (The product in f16 instead, of both rounded, took 0 to 2 % less time, 3 to 5 % with
+//     groups of 32 of bf16, and lost what was below 2^-17 of the largest scale.)
 //   * The reference of the softmax moves when a logit passes it by 2^4, the scales'
 //     power when a scale passes it: one vote a tile, no reduction otherwise.
 // All sums are float32.
@@ -166,9 +169,10 @@ __device__ __forceinline__ float low_half(const __nv_bfloat16*, uint32_t w) {
 __device__ __forceinline__ float low_half(const __half*, uint32_t w) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
 }
-__device__ __forceinline__ uint32_t times(__half2 x, uint32_t y) {
-  const __half2 z = __hmul2(x, *reinterpret_cast<const __half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&z);
+// Two float32 products, rounded to f16.
+__device__ __forceinline__ uint32_t products(float2 x, float2 y) {
+  const float2 z = unpair(mul2(pair(x.x, x.y), pair(y.x, y.y)));
+  return pack<__half>(z.x, z.y);
 }
 // The scale of a pair.
 template <typename T>
@@ -295,8 +299,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
   constexpr int kParts = kHalf ? 2 : 3;                  // of the sums of q
   constexpr float kMinUp = kHalf ? 0x1p16f : 1.f;        // keeps f16 operands in range
   // Weights are taken times 2^kUp, and the reference moves when a logit passes it by 2^kBar;
-  // scales are taken times a power of two that leaves the largest below 2^kTop.  All are f16,
-  // their products below 2^15.  Weights 2^-33 of the largest, and scales 2^-28, are still there.
+  // scales are taken times a power of two that leaves the largest below 2^kTop.  The weights are
+  // split into two of T, and the products, at most 2^15, rounded to f16.
   constexpr float kUp = 8.f, kBar = 4.f;
   constexpr int kTop = 3;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -794,24 +798,22 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           sum[e & 1] += p;
           pt[(2 * c + (e & 1)) * C::PP + 16 * mt + r + (e & 2) * 4] = p;
         }
-      // the scales as f16, tokens side by side: [token pair][group], where the keys' pairs were
-      // (all lanes have used them: the vote is behind)
-      uint32_t* ts = reinterpret_cast<uint32_t*>(st + C::kKs);
+      // the scales, tokens side by side: [token pair][group][2], where the keys' pairs were (all
+      // lanes have used them: the vote is behind)
+      float* ts = reinterpret_cast<float*>(st + C::kKs);
 #pragma unroll
-      for (int u = 0; u < kScales; ++u)
-        reinterpret_cast<__half*>(ts)[scale_at + u * 32] = __float2half_rn(vs[u] * up);
+      for (int u = 0; u < kScales; ++u) ts[scale_at + u * 32] = vs[u] * up;
       __syncwarp();
 
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float2 pa = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c);
-        float2 pb = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c + 8);
-        const __half2 ha = __floats2half2_rn(pa.x, pa.y), hb = __floats2half2_rn(pb.x, pb.y);
+        const float2 pa = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c);
+        const float2 pb = *reinterpret_cast<const float2*>(pt + r * C::PP + 16 * mt + 2 * c + 8);
         const uint32_t at = smem_addr(st) + C::kV + 16 * mt * C::KP + ldsm_at;
         const uint8_t* sc = st + C::kVs + (16 * mt + 2 * c) * C::SB;
-        uint32_t sa[NP], sb[NP];  // scales of tokens 2c, 2c + 1 and 2c + 8, 2c + 9
-        load_words(reinterpret_cast<const uint8_t*>(ts + (8 * mt + c) * NP), sa);
-        load_words(reinterpret_cast<const uint8_t*>(ts + (8 * mt + c + 4) * NP), sb);
+        // scales of tokens 2c, 2c + 1 and 2c + 8, 2c + 9
+        const float2* sa = reinterpret_cast<const float2*>(ts) + (8 * mt + c) * NP;
+        const float2* sb = sa + 4 * NP;
         {
           // weights, in two parts of 16 bits, times minima and scales: group r % NP
           uint32_t w[4];
@@ -822,9 +824,10 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           const uint32_t m1 = __byte_perm(w[0], w[1], 0x5410);
           const uint32_t m2 = __byte_perm(w[2], w[3], 0x7632);
           const uint32_t m3 = __byte_perm(w[2], w[3], 0x5410);
-          const uint32_t h0 = split<T>(pa.x, pa.y), h1 = split<T>(pb.x, pb.y);
+          float2 la = pa, lb = pb;
+          const uint32_t h0 = split<T>(la.x, la.y), h1 = split<T>(lb.x, lb.y);
           mma<T>(sums, m0, m1, m2, m3, h0, h1);
-          mma<T>(sums, m0, m1, m2, m3, pack<T>(pa.x, pa.y), pack<T>(pb.x, pb.y));
+          mma<T>(sums, m0, m1, m2, m3, pack<T>(la.x, la.y), pack<T>(lb.x, lb.y));
         }
         uint32_t b0 = 0, b1 = 0;  // p s of the group, by MMA columns
 #pragma unroll
@@ -836,8 +839,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           for (int h = 0; h < 2; ++h) {
             if ((j + h) * 32 % GS == 0) {
               const int g = (j + h) * 32 / GS;
-              b0 = times(ha, sa[g]);
-              b1 = times(hb, sb[g]);
+              b0 = products(pa, sa[g]);
+              b1 = products(pb, sb[g]);
               const uint32_t eight = g == r ? 0x00080008u : 0u;
               mma<__half>(eights, eight, 0, eight, 0, b0, b1);
             }

@@ -1,0 +1,63 @@
+"""Decode over the 4-bit cache where a group's scales differ widely from token to token: the
+bounds that the header gives, against the float64 reference."""
+import math
+
+import pytest
+import torch
+
+import kv4_reference as kr
+import step_reference as sr
+from test_gpu_kv4 import run_decode
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def large_but_unseen(tokens, large, ratio, d, group, dtype, seed):
+    """Token ``large`` has values and steps ``ratio`` times the others', and a key against the
+    queries: a weight around 2^-45 of the largest.  Four query heads on one KV head."""
+    pool = kr.Pool(-(-tokens // 16) + 2, 1, 16, d, group, dtype, seed)
+    base = pool.randn(d).float()
+    q = (base + 0.1 * pool.randn(1, 4, d).float()).to(dtype)
+    k, v = pool.randn(tokens, 1, d).float(), pool.randn(tokens, 1, d).float()
+    k[large, 0] = -32 * math.sqrt(d) * base / (base @ base)
+    v[large] *= ratio
+    if dtype == F16:
+        v *= 2.0 ** -9
+    table = torch.tensor([pool.order.pop() for _ in range(-(-tokens // 16))], dtype=torch.int32)
+    t = torch.arange(tokens)
+    pool.put(table[t // 16].long(), t % 16, k.to(dtype), v.to(dtype))
+    return q, pool, table[None]
+
+
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128),
+                                     (256, 32), (256, 64), (256, 128)])
+@pytest.mark.parametrize("dtype,power", [(BF16, 10), (BF16, 16), (BF16, 20), (BF16, 24),
+                                         (F16, 10), (F16, 16), (F16, 20)])
+@pytest.mark.parametrize("tokens,large", [(20, 0), (20, 19), (300, 40)])
+@pytest.mark.parametrize("portable", [False, True])
+def test_a_large_token_that_no_query_sees(d, group, dtype, power, tokens, large, portable):
+    """The row is the other tokens' mean, to their own steps.  A weight times a scale is rounded
+    to float16, half a step 2^-11 of it, or 2^-35 of the largest scale where that is more (the
+    weight being at most 1), and multiplies c - 8, at most 8.  The minima meet the weights in two
+    parts: bf16 2^-17 of them; f16 2^-22, or 2^-33 of the largest weight.  Logits as in
+    assert_decode."""
+    q, pool, tables = large_but_unseen(tokens, large, 2.0 ** power, d, group, dtype, d + power)
+    k, v, s = pool.rows(tables[0], tokens)
+    got = run_decode(q, pool, tables, torch.tensor([tokens]), portable=portable,
+                     out_dtype=F32).double().cpu()
+    for h in range(4):
+        a = (k[:, 0] @ q[0, h].double()) * d ** -0.5
+        w = torch.softmax(a, 0)
+        assert float(w[large] / w.max()) < 2.0 ** -36
+        ref, mag, step = w @ v[:, 0], w @ v[:, 0].abs(), w @ s[:, 0]
+        bound = 2e-5 * (mag + 15 * step) + 1e-9
+        if not portable:
+            bound = bound + 2.0 ** -11 * 8 * step + 2.0 ** -17 * (mag + 15 * step)
+            few = tokens * w.max()         # tokens, each with an error beside a weight of 1
+            bound = bound + few * 2.0 ** -35 * 8 * s[:, 0].amax(0)
+            if dtype == F16:
+                bound = bound + few * 2.0 ** -33 * (v[:, 0].abs() + 15 * s[:, 0]).amax(0)
+        bound = bound + sr.HALF_STEP[F32] * (ref.abs() + bound)
+        bad = (got[0, h] - ref).abs() > bound
+        assert not bad.any(), (int(bad.sum()), float(((got[0, h] - ref).abs() / bound).max()))
