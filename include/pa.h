@@ -729,7 +729,7 @@ PA_API pa_status_t pa_load_kv4(const pa_load_kv4_params_t* params, const void* k
  * initialised by pa_workspace_init; it serves one call at a time, and one for some
  * num_seqs and max_seq_len serves smaller ones.  partition_size (>= 1) bounds the slots
  * for partials where there are many sequences: a row's parts are that long, in whole
- * tiles of 64 tokens, or longer.  The tensor-core kernel chooses their length on the
+ * tiles of 64 tokens, or longer, up to 2^17 tokens.  The tensor-core kernel chooses their length on the
  * device, from the lengths of the call, so results depend on the batch by what the order
  * of float32 sums does.  Where max_seq_len is at most 131072 / head_dim (half of that where
  * num_seqs * num_kv_heads * ceil(num_heads / num_kv_heads / 8) is at most 19, twice where

@@ -220,6 +220,9 @@ cudaError_t launch_own(const KernelArgs& a, const JoinList& prefix, pa_dtype_t t
 // Decode over the 4-bit cache (pa_kv4.cuh): query heads of a KV head are taken up
 // to kKv4Heads at a time.
 constexpr int kKv4Heads = 8;
+// The longest part of a row, in tokens: the tensor cores cut off what a sum cannot hold, up to
+// 2^-23 of it with each product added, and this keeps a warp's additions of a part to 2048.
+constexpr int32_t kKv4Longest = 1 << 17;
 struct Kv4Args {
   const void* q;
   const uint8_t* k_codes;

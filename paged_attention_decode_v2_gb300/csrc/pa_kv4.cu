@@ -39,10 +39,10 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
 }
 
 // Slots of a row for partials.  The tensor-core kernel chooses the parts from the
-// lengths, which may all be the longest or one long among short ones: by partition_size
-// where there are many sequences, else up to kSplit items for each CTA that may be
-// resident (four on each of this GPU's 152 SMs; on others the slots are more or fewer than
-// they need be, and the results the same).  Up to single() tokens a row has one part, and
+// lengths, which may all be the longest or one long among short ones: by partition_size, at
+// most kKv4Longest, where there are many sequences, else up to kSplit items for each CTA that
+// may be resident (four on each of this GPU's 152 SMs; on others the slots are more or fewer
+// than they need be, and the results the same).  Up to single() tokens a row has one part, and
 // the call one launch: a join costs about the time that a CTA needs for them.  Where the pairs
 // leave most SMs idle, parts pay from half as many on.  Measured, us, undivided and in parts,
 // 32 / 8 heads of 128: two sequences of 400 tokens 8.3 and 8.2, 600 9.4 and 8.4, 1000 11.3 and
@@ -59,13 +59,15 @@ int64_t single(const pa_params_t* p, int64_t seqs) {
   return (pairs <= kRoom / 32 ? 65536 : pairs <= 3 * kRoom ? 131072 : 262144) / p->head_dim;
 }
 int64_t cover(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t by_size(const pa_params_t* p) {
+  return cover(p->max_seq_len, std::min(p->partition_size, kKv4Longest));
+}
 
 int64_t most_parts(const pa_params_t* p) {
   const int64_t len = p->max_seq_len;
   if (len <= single(p, p->num_seqs)) return 1;
-  const int64_t by_size = cover(len, p->partition_size);
   const int64_t by_room = cover(kSplit * kRoom, pairs_of(p, p->num_seqs));
-  return std::max<int64_t>(1, std::min(cover(len, 64), std::max(by_size, by_room)));
+  return std::max<int64_t>(1, std::min(cover(len, 64), std::max(by_size(p), by_room)));
 }
 
 // The bytes of a workspace: room for the slots of this many sequences and of fewer, which
@@ -75,7 +77,7 @@ size_t workspace_bytes_of(const pa_params_t* p) {
   const int64_t B = p->num_seqs, len = p->max_seq_len;
   int64_t slots = B;
   if (len > single(p, 1))
-    slots = std::min(B * cover(len, 64), std::max(B * cover(len, p->partition_size),
+    slots = std::min(B * cover(len, 64), std::max(B * by_size(p),
                                                   kSplit * kRoom / pairs_of(p, 1) + B));
   return workspace_layout(1, p->num_heads, p->head_dim, slots).total;
 }

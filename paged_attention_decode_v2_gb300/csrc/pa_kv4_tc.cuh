@@ -236,20 +236,17 @@ struct Parts {
 //     to 1.  Measured, us, by w alone and so: 256 sequences of 2000, 32 / 8 heads of 128, 167 and
 //     132; 100 of 4000 122 and 114; 300 of 2000, 24 / 4 of 256, 176 and 140; 60 of 2000 52 and 45
 //     (40 of 4000, 32 / 8 of 128, 58 and 61).
-// Never below `least` (nor below what the workspace has slots for), nor above kLongest: the
-// tensor cores cut off what a sum cannot hold, up to 2^-23 of it with each product added, and
-// this keeps a warp's additions of a part to 2048.  In float32: nothing else depends on the
-// size but speed.
+// Never below `least` (nor below what the workspace has slots for, part_floor, which is at most
+// kKv4Longest), nor above kKv4Longest.  In float32: nothing else depends on the size but speed.
 constexpr float kStart = 200.f, kJoin = 300.f;  // tokens that a start and the join are worth
 constexpr float kEven = 0.8f;                   // mean over longest
-constexpr int32_t kLongest = 1 << 17;
 __device__ __forceinline__ int32_t choose_part(const Kv4Args& a, float tokens, float longest,
                                                int32_t own, int32_t least) {
   if (a.num_parts == 1) return max((a.max_len + 63) / 64 * 64, 64);
   const float per = static_cast<float>(a.num_kv_heads * a.head_groups);
   const float pairs = per * a.num_seqs, room = a.room, share = tokens * per / room;
   least = max(least, a.part_floor);
-  const int32_t most = max(min((a.max_len + 63) / 64 * 64, kLongest), least);
+  const int32_t most = max(min((a.max_len + 63) / 64 * 64, kKv4Longest), least);
   const auto within = [&](float n) {  // whole tiles
     return n >= static_cast<float>(most) ? most
                                          : max((static_cast<int32_t>(ceilf(n)) + 63) / 64 * 64, least);

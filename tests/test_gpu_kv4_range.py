@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import kv4_reference as kr
+import paged_attention_decode_v2_gb300 as pa
 import step_reference as sr
 from test_gpu_kv4 import run_decode
 
@@ -61,3 +62,30 @@ def test_a_large_token_that_no_query_sees(d, group, dtype, power, tokens, large,
         bound = bound + sr.HALF_STEP[F32] * (ref.abs() + bound)
         bad = (got[0, h] - ref).abs() > bound
         assert not bad.any(), (int(bad.sum()), float(((got[0, h] - ref).abs() / bound).max()))
+
+
+def test_parts_of_many_pairs_stay_below_the_longest():
+    """One row of 2^19 tokens among 4900 short ones and a partition size as large: its parts, whose
+    length the kernel leaves in the control block, are at most 2^17 tokens.  The pages are taken
+    over and over; a token counts as often as the row has it."""
+    d, bs, blocks, n, B = 64, 4096, 4, 1 << 19, 4900
+    pool = kr.Pool(blocks, 1, bs, d, 32, BF16, seed=3)
+    pages = torch.empty(blocks, dtype=torch.int32)
+    pool.fill(pages, blocks * bs)
+    q = pool.randn(B, 2, d)
+    k, v, s = pool.rows(pages, blocks * bs)
+    tables = torch.full((B, n // bs), -1, dtype=torch.int32)
+    tables[:, 0] = pages[0]
+    tables[5] = pages[torch.arange(n // bs) % blocks]
+    lens = torch.ones(B, dtype=torch.int32)
+    lens[5] = n
+    p = pa.Params(B, 2, 1, d, bs, blocks, n // bs, n, n, 0, pa.PA_BF16, pa.PA_F32, 1.0, 0)
+    ws = torch.empty(pa.kv4_workspace_size(p, 32), dtype=torch.uint8, device="cuda")
+    pa.workspace_init(ws)
+    got = run_decode(q, pool, tables, lens, out_dtype=F32, partition_size=n, workspace=ws)
+    assert 0 < int(ws[512:516].view(torch.int32)) <= 1 << 17
+    for b in (5, 6, B - 1):
+        m = blocks * bs if b == 5 else 1
+        for h in range(2):
+            w = torch.softmax((k[:m, 0] @ q[b, h].double()) * d ** -0.5, 0)
+            kr.assert_decode(got[b, h], w @ v[:m, 0], w @ v[:m, 0].abs(), w @ s[:m, 0], F32, False)
