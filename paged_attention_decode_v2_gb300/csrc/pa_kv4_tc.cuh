@@ -795,8 +795,8 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           sum[e & 1] += p;
           pt[(2 * c + (e & 1)) * C::PP + 16 * mt + r + (e & 2) * 4] = p;
         }
-      // the scales, tokens side by side: [token pair][group][2], where the keys' pairs were (all
-      // lanes have used them: the vote is behind)
+      // the scales, tokens side by side: [token pair][group][2], where the keys' pairs were
+      __syncwarp();  // that all lanes have read
       float* ts = reinterpret_cast<float*>(st + C::kKs);
 #pragma unroll
       for (int u = 0; u < kScales; ++u) ts[scale_at + u * 32] = vs[u] * up;

@@ -89,3 +89,16 @@ def test_parts_of_many_pairs_stay_below_the_longest():
         for h in range(2):
             w = torch.softmax((k[:m, 0] @ q[b, h].double()) * d ** -0.5, 0)
             kr.assert_decode(got[b, h], w @ v[:m, 0], w @ v[:m, 0].abs(), w @ s[:m, 0], F32, False)
+
+
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128),
+                                     (256, 32), (256, 64), (256, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_repeated_runs_are_bit_for_bit_the_same(d, group, dtype):
+    """The lanes of a warp hand scales and weights to one another in shared memory, many tiles a
+    row, with new references and powers on the way."""
+    lens = (1500, 37, 700) * 12
+    q, pool, tables, n, *_ = kr.decode_problem(lens, 4, 2, d, 16, group, dtype, 5, spread=3.0)
+    first = run_decode(q, pool, tables, n)
+    for _ in range(20):
+        assert torch.equal(run_decode(q, pool, tables, n), first)
