@@ -764,9 +764,9 @@ __global__ void __launch_bounds__(Cfg<D, GS, kWide>::kNT, Cfg<D, GS, kWide>::kCt
           up = pow2(kTop - exponent(to));
         }
         // The first stage has zeros to scale.  Passing them by, us: 64 sequences of 6000, 24 / 4
-        // heads of 256, 105.5 to 102.9; 33 sequences of bf16, groups of 32, 169.2 to 163.4; but
-        // of f16 161.0 to 163.9, from how it is compiled.
-        if (i > 0 || (kHalf && GS == 32)) {
+        // heads of 256, 105.5 to 102.9; 33 sequences of bf16, groups of 32, 169.2 to 163.4, of f16
+        // 160.6 to 161.1.
+        if (i > 0) {
           float ge = 1.f;
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
