@@ -759,7 +759,8 @@ PA_API pa_status_t pa_decode_kv4(const pa_params_t* params, const pa_kv4_t* kv4,
                                  const int32_t* seq_lens, void* workspace,
                                  size_t workspace_bytes, void* out, cudaStream_t stream);
 
-/* ABI version: major * 10000 + minor * 100 + patch. */
+/* ABI version: major * 10000 + minor * 100 + patch.  200: the serving-step calls; 300:
+ * pa_qk_norm_rope_axes and the calls on the 4-bit cache. */
 PA_API int pa_version(void);
 
 #ifdef __cplusplus
