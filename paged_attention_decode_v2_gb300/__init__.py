@@ -671,12 +671,12 @@ def qk_norm_rope(q, k, v, positions, slots, cos_sin, q_out, k_cache=None, v_cach
 def rope_axes(sections, alternate: bool = False) -> bytes:
     """The axis of each pair of the rotation, for :func:`qk_norm_rope_axes`.
 
-    ``sections``: how many pairs each axis has.  They lie one after another, or
+    ``sections``: how many pairs each of up to four axes has.  They lie one after another, or
     (``alternate``) are dealt out in turn: axis a > 0 has the pairs a, a + A,
     a + 2 A, ... of A axes, the first axis what is left."""
     sections = [int(n) for n in sections]
-    if not sections or min(sections) < 0:
-        raise PaError(PA_ERR_INVALID_ARG, "sections must be counts of pairs")
+    if not 1 <= len(sections) <= 4 or min(sections) < 0:
+        raise PaError(PA_ERR_INVALID_ARG, "sections must be counts of pairs of one to four axes")
     if not alternate:
         return b"".join(bytes([a]) * n for a, n in enumerate(sections))
     of = bytearray(sum(sections))
