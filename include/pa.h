@@ -146,8 +146,9 @@ typedef struct pa_params {
  * starting on a 256-byte boundary, in this order:
  *   control      1024 bytes (PA_WORKSPACE_CONTROL_BYTES), whatever the
  *                parameters: the int32 status word at offset 0, an
- *                initialisation marker at offset 4, and from offset 256 the
- *                counters of the one-launch V2 step
+ *                initialisation marker at offset 4, from offset 256 the
+ *                counters of the one-launch V2 step, and from offset 512 the
+ *                parts' length and the queue of pa_decode_kv4
  *   max_logits   float32 [num_seqs, num_heads, NP]   m_p, natural-log units
  *   exp_sums     float32 [num_seqs, num_heads, NP]   s_p = sum exp(l_t - m_p)
  *   tmp_output   float32 [num_seqs, num_heads, NP, head_dim]
@@ -490,8 +491,9 @@ PA_API pa_status_t pa_plan_step(const pa_plan_params_t* params, const int32_t* c
  * share one, what it holds afterwards is some mix of the two.
  * No output may overlap an input or another output (PA_ERR_INVALID_ARG), but
  * q_out may be q itself where q is contiguous, and so k_out and v_out.
- * rotary_dim is a multiple of 16, at most head_dim (0: no rotation).  One
- * launch; no workspace; status as for pa_plan_step.
+ * rotary_dim is a multiple of 16, at most head_dim (0: no rotation).  Without
+ * rows (num_tokens 0) no address is looked at: each may be null, as those of empty
+ * tensors are.  One launch; no workspace; status as for pa_plan_step.
  */
 #define PA_ROPE_INTERLEAVED 256 /* pa_rope_params_t.flags, beside PA_FLAG_SPLIT_X */
 typedef struct pa_rope_params {
@@ -656,7 +658,9 @@ PA_API pa_status_t pa_decode_prefix(const pa_params_t* params, const pa_prefix_t
  * group of a head row x, m = min x, s = (max x - m) / 15 rounded to the element
  * type, and each element's code is (x - m) / s rounded to the nearest whole number
  * (halves to even), at most 15, or 0 where s is 0.  A group with an element that is
- * not finite, or a range past float32, gets NaN for both and reads back as NaN.
+ * not finite, or a range past float32, gets NaN for both and reads back as NaN.  The
+ * rounding of s moves code 15's value by up to half a step, relative, of the group's range:
+ * where it passes the type's largest number it reads back as infinity.
  *   k, v [T, num_kv_heads, head_dim]: rows k_stride / v_stride elements apart,
  *        heads contiguous within a row; 16-byte aligned rows
  *   slots int64 [T]: slot block * block_size + place; -1 is padding (nothing of the

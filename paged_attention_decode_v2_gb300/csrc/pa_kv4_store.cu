@@ -2,9 +2,10 @@
 //
 // For each group of a head row: m = min x, s = (max x - m) / 15 rounded to the
 // element type, c = min(15, round((x - m) / s)), to even where it is halfway (0
-// where s is 0).  x - m and the quotients are float32, each rounded once; m is an
-// x, so the scale is all that is rounded to fewer bits, before the codes are made
-// with it.  A group with a value that is not finite, or whose range is not, gets
+// where s is 0).  x - m is float32, rounded once (exact for 16-bit rows of ordinary
+// spread); the code is that of its exact quotient by s, below s = 2^-100 of the quotient
+// rounded to float32.  m is an x, so the scale is all that is rounded to fewer bits, before
+// the codes are made with it.  A group with a value that is not finite, or whose range is not, gets
 // NaN for both and reads back as NaN.
 //
 // D / 16 lanes hold a head row, sixteen elements each; a group's extremes are a

@@ -102,3 +102,16 @@ def test_repeated_runs_are_bit_for_bit_the_same(d, group, dtype):
     first = run_decode(q, pool, tables, n)
     for _ in range(20):
         assert torch.equal(run_decode(q, pool, tables, n), first)
+
+
+def test_a_range_that_rounds_past_the_type():
+    """-65504 to 65504 of f16: s = 8733.9 rounds to 8736, and code 15 stands for 65536."""
+    x = torch.zeros(1, 1, 64, dtype=F16)
+    x[0, 0, 0], x[0, 0, 1] = 65504.0, -65504.0
+    pool = [t.cuda() for t in kr.Pool(1, 1, 16, 64, 64, F16, 1).cuda()]
+    k, v = x.cuda(), (x / 2).cuda()
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    pa.store_kv4(k, v, torch.zeros(1, dtype=torch.int64, device="cuda"), *pool, k_out=ko, v_out=vo)
+    assert pool[2][0, 0, 0, 0].tolist() == [8736.0, -65504.0]
+    assert ko[0, 0, 0] == math.inf and ko[0, 0, 1] == -65504.0
+    assert torch.isfinite(ko[0, 0, 1:]).all() and torch.isfinite(vo).all()
