@@ -45,11 +45,11 @@ pa_status_t check(const pa_params_t* p, const pa_kv4_t* kv4) {
 // than they need be, and the results the same).  Up to single() tokens a row has one part, and
 // the call one launch: a join costs about the time that a CTA needs for them.  Where the pairs
 // leave most SMs idle, parts pay from half as many on.  Measured, us, undivided and in parts,
-// 32 / 8 heads of 128: two sequences of 400 tokens 8.3 and 8.2, 600 9.4 and 8.4, 1000 11.3 and
-// 8.4; eight of 600 9.7 and 10.0, 800 10.2 and 11.2.  Where they give every CTA several items
-// whatever happens, rows are undivided up to twice as many: 500 of 1200 162 and 167, of 50 to
-// 2000 107 and 113; 256 of 2000 129 and 132, of 50 to 2000 67 and 65; but 160 of 50 to 2000 55
-// and 48.
+// 32 / 8 heads of 128: two sequences of 300 tokens 7.8 and 8.1, 600 9.4 and 8.2, 1000 11.2 and
+// 8.6; eight of 600 9.6 and 9.9, 1000 11.3 and 11.7, thirty of 1000 16.3 and 18.9.  Where they
+// give every CTA several items whatever happens, rows are undivided up to twice as many: 500 of
+// 1200 158 and 163, of 50 to 2000 104 and 108; 256 of 2000 125 and 128, of 50 to 2000 64 and 63;
+// but 160 of 50 to 2000 53 and 47 (of 1200 59 and 61).
 constexpr int64_t kSplit = 8, kRoom = 608;
 int64_t pairs_of(const pa_params_t* p, int64_t seqs) {
   return seqs * p->num_kv_heads * head_groups(p);

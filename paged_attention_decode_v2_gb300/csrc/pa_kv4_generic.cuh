@@ -9,7 +9,7 @@
 // sequence writes its output, others a partial for pa_kv4_join.cu.
 // Bound by instructions: 4 D operations a token and head, and a butterfly.  Measured, bf16:
 // one sequence of 100K, 24 / 4 heads of 256, 562 us (tensor cores 32); 256 sequences up to
-// 100K, 32 / 8 of 128, 12.1 ms (626 us).
+// 100K, 32 / 8 of 128, 12.1 ms (627 us).
 #pragma once
 
 #include "pa_kv4.cuh"

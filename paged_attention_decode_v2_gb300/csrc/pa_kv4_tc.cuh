@@ -35,10 +35,10 @@
 // Bound by instructions and by what waits on them, not by memory: a tile of 16 tokens of
 // 128 elements is some 290 warp instructions, 130 of them on the ALU pipe (64 masks and
 // 16 shifts), 22 MMAs.  Measured: 76 sequences of 8192, 32 / 8 heads of 128, one group a
-// row: 140 us = 4.8 TB/s, 72 % of the copy rate; the same kernel's copies alone take 119 us,
-// its arithmetic alone 122.  114 of 4096, 24 / 4 of 256: 99 us = 5.5 TB/s.  One sequence of
+// row: 141 us = 4.8 TB/s, 71 % of the copy rate; the same kernel's copies alone take 124 us,
+// its arithmetic alone 121.  114 of 4096, 24 / 4 of 256: 101 us = 5.3 TB/s.  One sequence of
 // 100K 32 us with the join (5 us before the first stage, 20 of streaming, 2.5 to join the
-// warps), 256 sequences up to 100K 626 us.
+// warps), 256 sequences up to 100K 627 us, 33 of f16 with groups of 32 161 us.
 #pragma once
 
 #include <atomic>
@@ -233,9 +233,9 @@ struct Parts {
 //     at the end: n = sqrt(2 kStart w).
 //   * Many, most of them nearly as long as the longest: of 1 to 32 even parts of that, the number
 //     with the least rounds of items, the last one counted 0.7 (a CTA that has an SM for itself)
-//     to 1.  Measured, us, by w alone and so: 256 sequences of 2000, 32 / 8 heads of 128, 167 and
-//     132; 100 of 4000 122 and 114; 300 of 2000, 24 / 4 of 256, 176 and 140; 60 of 2000 52 and 45
-//     (40 of 4000, 32 / 8 of 128, 58 and 61).
+//     to 1.  Measured, us, by w alone and so: 76 sequences of 8192, 32 / 8 heads of 128, 166 and
+//     141; 100 of 4000 116 and 113; 300 of 2000, 24 / 4 of 256, 169 and 137; 60 of 2000 50 and 44;
+//     114 of 4096 132 and 101 (but 128 of 2500, 32 / 8 of 128, 94 and 96; 40 of 4000 60.0 and 60.6).
 // Never below `least` (nor below what the workspace has slots for, part_floor, which is at most
 // kKv4Longest), nor above kKv4Longest.  In float32: nothing else depends on the size but speed.
 constexpr float kStart = 200.f, kJoin = 300.f;  // tokens that a start and the join are worth
@@ -962,9 +962,10 @@ cudaError_t launch_d(const Kv4Args& a, int64_t items, cudaStream_t s) {
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.head_groups;
   // Wide CTAs: fewer, larger parts and one join of their warps, where a pair is one part or
   // the pairs are few and long.  Measured, us, wide and narrow: one part, 32 / 8 heads of 128,
-  // two sequences of 128 tokens 7.0 and 5.5, 256 7.6 and 7.0, 400 8.3 and 9.1, 1000 11.5 and
-  // 13.3; in parts, 24 / 4 of 256, one of 4000 11.7 and 10.5, 8000 13.2 and 13.6, 100K 33.6
-  // and 35.8; four of 32000 (16 pairs) 38.5 and 37.5, of 20000 with 32 pairs 33.1 and 29.2.
+  // eight sequences of 128 tokens 6.9 and 5.5, 256 7.3 and 6.6, 320 7.6 and 7.7, 400 8.3 and
+  // 8.9, 1000 11.3 and 13.2; in parts, 24 / 4 of 256, one of 4000 11.1 and 10.3, 6000 11.8 and
+  // 12.0, 100K 32.3 and 34.0; two of 100K 50.9 and 51.6, four of 32000 (16 pairs) 38.7 and 37.1,
+  // eight of 20000 49.9 and 44.2.
   const bool wide = a.num_parts == 1 ? 2 * pairs <= sms && a.max_len > 320
                                      : 16 * pairs <= sms && a.max_len > 6000;
   return wide ? launch_w<T, D, GS, true>(a, items, dev, sms, s)

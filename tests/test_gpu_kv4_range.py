@@ -115,3 +115,35 @@ def test_a_range_that_rounds_past_the_type():
     assert pool[2][0, 0, 0, 0].tolist() == [8736.0, -65504.0]
     assert ko[0, 0, 0] == math.inf and ko[0, 0, 1] == -65504.0
     assert torch.isfinite(ko[0, 0, 1:]).all() and torch.isfinite(vo).all()
+
+
+def test_one_workspace_for_the_16_bit_and_the_4_bit_decode():
+    """Both keep their counters in the control block: calls in turn, on one workspace, each as if
+    it were alone; items from the queue, and a row reduced in one launch."""
+    lens = [1200, 40, 700] * 50
+    q, pool, tables, n, *_ = kr.decode_problem(lens, 8, 4, 64, 16, 32, BF16, 8)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kc, vc = (torch.randn(1300, 4, 16, 128, generator=g, device="cuda").to(BF16) for _ in range(2))
+    q16 = torch.randn(1, 24, 128, generator=g, device="cuda").to(BF16)
+    table = torch.randperm(1300, generator=g, device="cuda")[None, :1250].int()
+    n16 = torch.tensor([20000], dtype=torch.int32, device="cuda")
+    out16 = torch.empty_like(q16)
+    p = pa.make_params(q16, kc, table, max_seq_len=20000, scale=128 ** -0.5, partition_size=512)
+    p4 = pa.Params(150, 8, 4, 64, 16, pool.k.shape[0], tables.shape[1], 1200, 1024, 0, pa.PA_BF16,
+                   pa.PA_BF16, 1.0, 0)
+    ws = torch.empty(max(pa.workspace_size(p), pa.kv4_workspace_size(p4, 32)), dtype=torch.uint8,
+                     device="cuda")
+    pa.workspace_init(ws)
+
+    def decode16():
+        out16.fill_(math.nan)
+        pa.decode_v2(q16, kc, vc, table, n16, out16, ws, max_seq_len=20000, scale=128 ** -0.5,
+                     partition_size=512)
+        return out16.clone()
+
+    alone = run_decode(q, pool, tables, n), decode16()
+    assert torch.isfinite(alone[0]).all() and torch.isfinite(alone[1]).all()
+    for _ in range(5):
+        assert torch.equal(run_decode(q, pool, tables, n, workspace=ws), alone[0])
+        assert torch.equal(decode16(), alone[1])
+    assert pa.read_device_status(ws) == pa.PA_OK
